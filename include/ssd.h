@@ -312,6 +312,148 @@ int ssd_gated_rmsnorm_bwd(const ssd_norm_problem* prob, const void* y, const voi
                           float* dweight, void* workspace, size_t workspace_bytes,
                           ssd_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated delta rule: the recurrence of a layer whose state is corrected
+ * by what it already holds, instead of only added to.  Per batch row and
+ * head, with a state S (headdim x dstate), a log decay g and a strength beta:
+ *
+ *   S'  = exp(g_t) S_{t-1}
+ *   u_t = beta_t (v_t - S' k_t)
+ *   S_t = S' + u_t (outer) k_t
+ *   y_t = scale * S_t q_t
+ *
+ * with S_{-1} = initial_states (or 0).  q and k take the places of the SSD
+ * layer's C and B (ngroups heads of dstate values; head h reads group
+ * floor(h * ngroups / nheads)), v and y those of x and y.  A token whose
+ * seq_idx differs from its predecessor's starts from S' = 0.  Nothing is
+ * normalised inside: with |k| = 1 and 0 <= beta <= 2 the state stays bounded.
+ *
+ * Shapes (b = batch, L = seqlen, H = nheads, P = headdim, N = dstate,
+ * G = ngroups), device memory, 16-byte aligned:
+ *   q, k             (b, L, G, N)   dtype, q_stride / k_stride elements from
+ *                                   token to token (0: dense, G * N)
+ *   v                (b, L, H, P)   dtype, v_stride (0: dense, H * P)
+ *   g, beta          (b, L, H)      dtype
+ *   y, dy            (b, L, H, P)   dtype, dense; dq, dk, dv, dg, dbeta dense
+ *   initial_states, final_states, dfinal_states, dinitial_states
+ *                    (b, H, P, N)   state_dtype
+ *   seq_idx          (b, L)         int32
+ * The strides let q, k and v be column blocks of one projection's output.
+ * g may be -inf (the state is forgotten); a g below -100 counts as one.
+ *
+ * Precision: fp32 problems compute in fp32 throughout.  bf16 problems hold
+ * states, sums and decays in fp32; where the tensor cores form the products
+ * (headdim a multiple of 32, dstate 64 or 128, strides multiples of 8) their
+ * operands -- the carried state among them -- are rounded to bf16.
+ *
+ * Limits: headdim, dstate <= 256; nheads % ngroups == 0; ownership, errors
+ * and stream semantics as above; no device-side waits, no status word.
+ * Results are bitwise reproducible run to run. */
+typedef struct {
+  int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
+  int64_t q_stride, k_stride, v_stride; /* elements from token to token; 0 = dense */
+  float scale;
+  int32_t dtype;       /* ssd_dtype of q, k, v, g, beta, y and their gradients */
+  int32_t state_dtype; /* ssd_dtype of the states at the boundary */
+  int32_t flags;       /* SSD_HAS_INIT, SSD_HAS_SEQ_IDX, SSD_HAS_DFINAL, SSD_WANT_DINIT */
+} ssd_delta_problem;
+
+/* Device bytes of the workspaces and of the buffer in which the forward
+ * leaves what the backward reads (pure functions of the problem, whatever its
+ * flags; 0 if it is invalid). */
+size_t ssd_delta_fwd_workspace_bytes(const ssd_delta_problem* prob);
+size_t ssd_delta_bwd_workspace_bytes(const ssd_delta_problem* prob);
+size_t ssd_delta_saved_bytes(const ssd_delta_problem* prob);
+
+/* Forward over whole sequences.  Writes y and, if non-NULL, final_states;
+ * with `saved` (ssd_delta_saved_bytes) also what ssd_delta_bwd needs. */
+int ssd_delta_fwd(const ssd_delta_problem* prob, const void* q, const void* k, const void* v,
+                  const void* g, const void* beta, const void* initial_states,
+                  const int32_t* seq_idx, void* y, void* final_states, void* saved,
+                  size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                  ssd_stream_t stream);
+
+/* Backward of the forward that wrote `saved` from the same problem and
+ * inputs, for the upstream gradients dy and, if SSD_HAS_DFINAL,
+ * dfinal_states.  Gradients are overwritten; dq and dk are sums over the
+ * heads of their group, taken in a fixed order; dinitial_states iff
+ * SSD_WANT_DINIT.  `saved` is only read. */
+int ssd_delta_bwd(const ssd_delta_problem* prob, const void* q, const void* k, const void* v,
+                  const void* g, const void* beta, const int32_t* seq_idx, const void* dy,
+                  const void* dfinal_states, void* dq, void* dk, void* dv, void* dg, void* dbeta,
+                  void* dinitial_states, const void* saved, size_t saved_bytes, void* workspace,
+                  size_t workspace_bytes, ssd_stream_t stream);
+
+/* The recurrent form for serving: every sequence of the batch takes seqlen
+ * tokens (one, or a few drafted ones) from its state in a pool of nslots
+ * states (nslots, H, P, N), fp32 (state_dtype must be SSD_F32; flags 0).
+ * slots (b) int32 or NULL gives each sequence's place in the pool (NULL: b's
+ * own index, nslots >= batch); one outside [0, nslots) is padding: its y is
+ * zero and no state is read or written.  Writes y for all tokens unless y is
+ * NULL, and unless states_out is NULL the state after the first lengths[b]
+ * tokens of each sequence (lengths (b) int32 or NULL: all; clamped to
+ * [0, seqlen]).  states_out may be states_in.  Two sequences of one call must
+ * not write the same slot.  All arithmetic is fp32. */
+int ssd_delta_step(const ssd_delta_problem* prob, const void* q, const void* k, const void* v,
+                   const void* g, const void* beta, int64_t nslots, const float* states_in,
+                   float* states_out, const int32_t* slots, const int32_t* lengths, void* y,
+                   ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Verification of drafted tokens: which of a draft's tokens a sequence keeps,
+ * and the token that follows them, so that the result is distributed as the
+ * target's own samples.  With the target's probabilities p (b, ndraft + 1,
+ * vocab), the draft's q (b, ndraft, vocab), both dtype, and given random
+ * numbers: token i of a sequence's first lengths[b] is kept while
+ *   uniform[b, i] * q_i(token_i) < p_i(token_i)        (in fp32)
+ * and the first that fails ends the draft.  With n kept, the next token is
+ *   argmax_v  w(v) / noise[b, v],   w = max(p_n - q_n, 0)  after a refusal,
+ *                                   w = p_n                after a whole draft
+ * (noise (b, vocab) fp32: independent standard exponentials make that a draw
+ * from w; ties go to the lowest index).  Where no w is positive, w = p_n; if
+ * none of those is either, the token is 0.  NaN weights and ratios are passed
+ * over.  draft_probs may be NULL for drafts chosen without a distribution
+ * (q_i = 1 at the token, 0 elsewhere).  lengths (b) int32 or NULL (all
+ * ndraft), clamped to [0, ndraft]; a drafted token outside [0, vocab) is
+ * refused.  uniform (b, ndraft) fp32, draft_tokens (b, ndraft) int32.
+ * Writes out_tokens (b, ndraft + 1) int32 -- the kept tokens, the next one,
+ * then -1 -- and accepted (b) int32, the number kept.  ndraft may be 0 (then
+ * the draft's arrays may be NULL).  1 <= vocab < 2^31. */
+typedef struct {
+  int64_t batch, ndraft, vocab;
+  int32_t dtype; /* ssd_dtype of both probabilities */
+  int32_t flags; /* 0 */
+} ssd_verify_problem;
+
+int ssd_verify_draft(const ssd_verify_problem* prob, const void* target_probs,
+                     const void* draft_probs, const int32_t* draft_tokens, const int32_t* lengths,
+                     const float* uniform, const float* noise, int32_t* out_tokens,
+                     int32_t* accepted, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit cache of recurrent states: prefixes' states (of the SSD layer or
+ * of the delta rule) put away at a quarter of their size.  Each row of N
+ * values has one fp32 scale: with a = max |x| of the row and t = 127 (int8)
+ * or 448 (e4m3), scale = a / t and each value is x * (t / a) rounded to
+ * nearest, ties to even.  A row whose a is below 2^-118 (t / a is not finite
+ * for it) is stored as zeros with scale 0; a row that holds an infinity or a
+ * NaN reads back as NaN throughout.  cache (nslots, H, P, N) bytes, scales (nslots, H, P)
+ * fp32.  slots (b) int32 or NULL as for ssd_delta_step; the store passes over
+ * slots outside the pool (and must not get one twice), the load gives zeros
+ * for them (and may read one slot into many sequences). */
+typedef enum { SSD_CACHE_INT8 = 0, SSD_CACHE_E4M3 = 1 } ssd_cache_format;
+
+typedef struct {
+  int64_t batch, nheads, headdim, dstate, nslots;
+  int32_t format; /* ssd_cache_format */
+  int32_t flags;  /* 0 */
+} ssd_cache_problem;
+
+int ssd_state_cache_store(const ssd_cache_problem* prob, const float* states, const int32_t* slots,
+                          void* cache, float* scales, ssd_stream_t stream);
+int ssd_state_cache_load(const ssd_cache_problem* prob, const void* cache, const float* scales,
+                         const int32_t* slots, float* states, ssd_stream_t stream);
+
 /* Library build/version string, e.g. "libssd 0.1 sm_103a". */
 const char* ssd_version(void);
 

@@ -33,6 +33,8 @@ SSD_PATH_SINGLE_PASS = 1 << 18
 SSD_TEST_FEW_CTAS = 1 << 19
 SSD_SCAN_WARP_SHUFFLE = 1 << 20
 SSD_NORM_HAS_Z = 1
+SSD_CACHE_INT8 = 0
+SSD_CACHE_E4M3 = 1
 
 # every symbol include/ssd.h declares
 EXPORTS = ["ssd_fwd_workspace_bytes", "ssd_bwd_workspace_bytes", "ssd_fwd", "ssd_bwd",
@@ -40,7 +42,10 @@ EXPORTS = ["ssd_fwd_workspace_bytes", "ssd_bwd_workspace_bytes", "ssd_fwd", "ssd
            "ssd_profile_stop", "ssd_profile_count", "ssd_profile_get", "ssd_fwd_noalloc",
            "ssd_fwd_noalloc_read_device_status", "ssd_shard_decay", "ssd_shard_fold",
            "ssd_gated_rmsnorm_fwd", "ssd_gated_rmsnorm_bwd_workspace_bytes",
-           "ssd_gated_rmsnorm_bwd"]
+           "ssd_gated_rmsnorm_bwd", "ssd_delta_fwd_workspace_bytes",
+           "ssd_delta_bwd_workspace_bytes", "ssd_delta_saved_bytes", "ssd_delta_fwd",
+           "ssd_delta_bwd", "ssd_delta_step", "ssd_verify_draft", "ssd_state_cache_store",
+           "ssd_state_cache_load"]
 SSD_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -56,6 +61,27 @@ class ssd_norm_problem(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("group_size", ctypes.c_int64), ("eps", ctypes.c_float),
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class ssd_delta_problem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class ssd_verify_problem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("ndraft", ctypes.c_int64),
+                ("vocab", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class ssd_cache_problem(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("nheads", ctypes.c_int64),
+                ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("nslots", ctypes.c_int64), ("format", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -106,6 +132,23 @@ def _load():
     lib.ssd_gated_rmsnorm_bwd_workspace_bytes.restype = sz
     lib.ssd_gated_rmsnorm_bwd.argtypes = [npp] + [vp] * 8 + [sz, vp]
     lib.ssd_gated_rmsnorm_bwd.restype = i32
+    dpp = ctypes.POINTER(ssd_delta_problem)
+    for name in ("fwd_workspace", "bwd_workspace", "saved"):
+        fn = getattr(lib, f"ssd_delta_{name}_bytes")
+        fn.argtypes, fn.restype = [dpp], sz
+    lib.ssd_delta_fwd.argtypes = [dpp] + [vp] * 10 + [sz, vp, sz, vp]
+    lib.ssd_delta_fwd.restype = i32
+    lib.ssd_delta_bwd.argtypes = [dpp] + [vp] * 15 + [sz, vp, sz, vp]
+    lib.ssd_delta_bwd.restype = i32
+    lib.ssd_delta_step.argtypes = [dpp] + [vp] * 5 + [i64] + [vp] * 5 + [vp]
+    lib.ssd_delta_step.restype = i32
+    lib.ssd_verify_draft.argtypes = [ctypes.POINTER(ssd_verify_problem)] + [vp] * 8 + [vp]
+    lib.ssd_verify_draft.restype = i32
+    cpp = ctypes.POINTER(ssd_cache_problem)
+    lib.ssd_state_cache_store.argtypes = [cpp] + [vp] * 4 + [vp]
+    lib.ssd_state_cache_store.restype = i32
+    lib.ssd_state_cache_load.argtypes = [cpp] + [vp] * 4 + [vp]
+    lib.ssd_state_cache_load.restype = i32
     return lib
 
 
@@ -271,4 +314,111 @@ def ssd_gated_rmsnorm_bwd(prob, y, z, weight, dout, dy, dz, dweight, workspace,
                                    _stream(stream))
     if check and rc != SSD_OK:
         raise SSDError(rc, "ssd_gated_rmsnorm_bwd")
+    return rc
+
+
+def _dtype_code(dtype) -> int:
+    if isinstance(dtype, torch.dtype):
+        return SSD_BF16 if dtype == torch.bfloat16 else SSD_F32
+    return dtype
+
+
+def make_delta_problem(batch, seqlen, nheads, headdim, dstate, ngroups, scale, dtype,
+                       state_dtype=SSD_F32, flags=0, q_stride=0, k_stride=0,
+                       v_stride=0) -> ssd_delta_problem:
+    return ssd_delta_problem(batch, seqlen, nheads, headdim, dstate, ngroups, q_stride, k_stride,
+                             v_stride, scale, _dtype_code(dtype), _dtype_code(state_dtype), flags)
+
+
+def ssd_delta_fwd_workspace_bytes(prob: ssd_delta_problem) -> int:
+    return int(LIB.ssd_delta_fwd_workspace_bytes(ctypes.byref(prob)))
+
+
+def ssd_delta_bwd_workspace_bytes(prob: ssd_delta_problem) -> int:
+    return int(LIB.ssd_delta_bwd_workspace_bytes(ctypes.byref(prob)))
+
+
+def ssd_delta_saved_bytes(prob: ssd_delta_problem) -> int:
+    return int(LIB.ssd_delta_saved_bytes(ctypes.byref(prob)))
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def ssd_delta_fwd(prob, q, k, v, g, beta, initial_states, seq_idx, y, final_states, saved,
+                  workspace, saved_bytes=None, workspace_bytes=None, stream=None,
+                  check=True) -> int:
+    """Enqueue the gated delta rule's forward on ``stream`` (default: torch's
+    current stream); ``saved`` may be None when no backward follows."""
+    rc = LIB.ssd_delta_fwd(ctypes.byref(prob), _p(q), _p(k), _p(v), _p(g), _p(beta),
+                           _p(initial_states), _p(seq_idx), _p(y), _p(final_states), _p(saved),
+                           _nbytes(saved) if saved_bytes is None else saved_bytes, _p(workspace),
+                           _nbytes(workspace) if workspace_bytes is None else workspace_bytes,
+                           _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_delta_fwd")
+    return rc
+
+
+def ssd_delta_bwd(prob, q, k, v, g, beta, seq_idx, dy, dfinal_states, dq, dk, dv, dg, dbeta,
+                  dinitial_states, saved, workspace, saved_bytes=None, workspace_bytes=None,
+                  stream=None, check=True) -> int:
+    """Enqueue the gated delta rule's backward on ``stream``."""
+    rc = LIB.ssd_delta_bwd(ctypes.byref(prob), _p(q), _p(k), _p(v), _p(g), _p(beta), _p(seq_idx),
+                           _p(dy), _p(dfinal_states), _p(dq), _p(dk), _p(dv), _p(dg), _p(dbeta),
+                           _p(dinitial_states), _p(saved),
+                           _nbytes(saved) if saved_bytes is None else saved_bytes, _p(workspace),
+                           _nbytes(workspace) if workspace_bytes is None else workspace_bytes,
+                           _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_delta_bwd")
+    return rc
+
+
+def ssd_delta_step(prob, q, k, v, g, beta, nslots, states_in, states_out, slots, lengths, y,
+                   stream=None, check=True) -> int:
+    """Enqueue the gated delta rule's recurrent form on ``stream``."""
+    rc = LIB.ssd_delta_step(ctypes.byref(prob), _p(q), _p(k), _p(v), _p(g), _p(beta), nslots,
+                            _p(states_in), _p(states_out), _p(slots), _p(lengths), _p(y),
+                            _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_delta_step")
+    return rc
+
+
+def make_verify_problem(batch, ndraft, vocab, dtype) -> ssd_verify_problem:
+    return ssd_verify_problem(batch, ndraft, vocab, _dtype_code(dtype), 0)
+
+
+def ssd_verify_draft(prob, target_probs, draft_probs, draft_tokens, lengths, uniform, noise,
+                     out_tokens, accepted, stream=None, check=True) -> int:
+    """Enqueue the verification of drafted tokens on ``stream``."""
+    rc = LIB.ssd_verify_draft(ctypes.byref(prob), _p(target_probs), _p(draft_probs),
+                              _p(draft_tokens), _p(lengths), _p(uniform), _p(noise),
+                              _p(out_tokens), _p(accepted), _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_verify_draft")
+    return rc
+
+
+def make_cache_problem(batch, nheads, headdim, dstate, nslots, fmt) -> ssd_cache_problem:
+    return ssd_cache_problem(batch, nheads, headdim, dstate, nslots, fmt, 0)
+
+
+def ssd_state_cache_store(prob, states, slots, cache, scales, stream=None, check=True) -> int:
+    """Enqueue the quantisation of ``states`` into their slots on ``stream``."""
+    rc = LIB.ssd_state_cache_store(ctypes.byref(prob), _p(states), _p(slots), _p(cache),
+                                   _p(scales), _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_state_cache_store")
+    return rc
+
+
+def ssd_state_cache_load(prob, cache, scales, slots, states, stream=None, check=True) -> int:
+    """Enqueue the read-back of cached states on ``stream``."""
+    rc = LIB.ssd_state_cache_load(ctypes.byref(prob), _p(cache), _p(scales), _p(slots),
+                                  _p(states), _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_state_cache_load")
     return rc

@@ -123,3 +123,201 @@ class NormDevice:
         if self.dz is not None:
             out["dz"] = self.dz
         return {k: v.detach().to("cpu", torch.float64) for k, v in out.items()}
+
+
+def _token_stride(t, inner, what):
+    """Elements between the tokens of a (b, L, heads, d) tensor whose last two
+    axes are dense and whose rows are L tokens long (a column block of a
+    wider projection is one)."""
+    b, L, heads, d = t.shape
+    stride = t.stride(1) if L > 1 else t.stride(0) if b > 1 else inner
+    if ((d > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != d)
+            or (b > 1 and t.stride(0) != L * stride) or stride < inner):
+        raise ValueError(f"{what}: its heads must be dense and its tokens evenly spaced")
+    return stride
+
+
+def _dense(t, shape, dtype, what, device=None):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or \
+            (device is not None and t.device != device):
+        raise ValueError(f"{what}: expected a dense {tuple(shape)} {dtype} tensor on {device}")
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _delta_shape(q, k, v, g, beta):
+    if v.dim() != 4 or q.dim() != 4 or v.dtype not in _FLOATS:
+        raise ValueError("v must be (b, L, H, P) and q (b, L, G, N), both fp32 or bf16")
+    b, L, H, P = v.shape
+    G, N = q.shape[2:]
+    for t, what in ((q, "q"), (k, "k")):
+        if tuple(t.shape) != (b, L, G, N) or t.dtype != v.dtype or t.device != v.device:
+            raise ValueError(f"{what}: expected a {(b, L, G, N)} {v.dtype} tensor on {v.device}")
+    _dense(g, (b, L, H), v.dtype, "g", v.device)
+    _dense(beta, (b, L, H), v.dtype, "beta", v.device)
+    strides = dict(q_stride=_token_stride(q, G * N, "q"), k_stride=_token_stride(k, G * N, "k"),
+                   v_stride=_token_stride(v, H * P, "v"))
+    return (b, L, H, P, N, G), strides
+
+
+class DeltaDevice:
+    """One gated-delta-rule problem: the caller's device tensors, the outputs,
+    the gradients (when ``dy`` is given), the workspace, and the calls through
+    the C ABI.  q, k (b, L, G, N) and v (b, L, H, P) may be column blocks of
+    one projection's output; g (log decay), beta (b, L, H).  States
+    (b, H, P, N) are ``state_dtype``.  ``fwd`` fills y and final; ``bwd``,
+    after a ``fwd`` on the same inputs, dq, dk, dv, dg, dbeta and (with
+    initial states) dinit.  The tensors may be refilled between calls."""
+
+    def __init__(self, q, k, v, g, beta, scale=None, initial_states=None, seq_idx=None, dy=None,
+                 dfinal_states=None, state_dtype=torch.float32):
+        (b, L, H, P, N, G), strides = _delta_shape(q, k, v, g, beta)
+        if state_dtype not in _FLOATS:
+            raise ValueError("state_dtype must be fp32 or bf16")
+        if dfinal_states is not None and dy is None:
+            raise ValueError("dfinal_states needs dy")
+        _dense(initial_states, (b, H, P, N), state_dtype, "initial_states", v.device)
+        _dense(dfinal_states, (b, H, P, N), state_dtype, "dfinal_states", v.device)
+        _dense(seq_idx, (b, L), torch.int32, "seq_idx", v.device)
+        _dense(dy, (b, L, H, P), v.dtype, "dy", v.device)
+        self.q, self.k, self.v, self.g, self.beta = q, k, v, g, beta
+        self.init, self.seq_idx, self.dy, self.dfinal = initial_states, seq_idx, dy, dfinal_states
+        dev, dt = v.device, v.dtype
+        flags = ((_lib.SSD_HAS_INIT if initial_states is not None else 0)
+                 | (_lib.SSD_HAS_SEQ_IDX if seq_idx is not None else 0))
+        bflags = flags | (_lib.SSD_HAS_DFINAL if dfinal_states is not None else 0)
+        if initial_states is not None:
+            bflags |= _lib.SSD_WANT_DINIT
+        scale = N ** -0.5 if scale is None else scale
+        make = lambda f: _lib.make_delta_problem(  # noqa: E731
+            b, L, H, P, N, G, scale, dt, state_dtype, f, **strides)
+        self.fwd_prob, self.bwd_prob = make(flags), make(bflags)
+        self.y = torch.empty((b, L, H, P), dtype=dt, device=dev)
+        self.final = torch.empty((b, H, P, N), dtype=state_dtype, device=dev)
+        ws = _lib.ssd_delta_fwd_workspace_bytes(self.fwd_prob)
+        if ws == 0:
+            raise _lib.SSDError(_lib.SSD_ERR_INVALID_ARGUMENT, "delta workspace size")
+        self.saved = None
+        if dy is not None:
+            ws = max(ws, _lib.ssd_delta_bwd_workspace_bytes(self.bwd_prob))
+            self.saved = torch.empty(_lib.ssd_delta_saved_bytes(self.bwd_prob), dtype=torch.uint8,
+                                     device=dev)
+            self.dq = torch.empty((b, L, G, N), dtype=dt, device=dev)
+            self.dk = torch.empty((b, L, G, N), dtype=dt, device=dev)
+            self.dv = torch.empty((b, L, H, P), dtype=dt, device=dev)
+            self.dg, self.dbeta = torch.empty_like(g), torch.empty_like(beta)
+            self.dinit = None if initial_states is None else torch.empty_like(initial_states)
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+
+    def fwd(self, stream=None, check=True):
+        return _lib.ssd_delta_fwd(self.fwd_prob, self.q, self.k, self.v, self.g, self.beta,
+                                  self.init, self.seq_idx, self.y, self.final, self.saved,
+                                  self.workspace, stream=stream, check=check)
+
+    def bwd(self, stream=None, check=True):
+        if self.saved is None:
+            raise ValueError("built without dy: there is no backward")
+        return _lib.ssd_delta_bwd(self.bwd_prob, self.q, self.k, self.v, self.g, self.beta,
+                                  self.seq_idx, self.dy, self.dfinal, self.dq, self.dk, self.dv,
+                                  self.dg, self.dbeta, self.dinit, self.saved, self.workspace,
+                                  stream=stream, check=check)
+
+    def results(self) -> dict:
+        out = dict(y=self.y, final_states=self.final)
+        if self.dy is not None:
+            out.update(dq=self.dq, dk=self.dk, dv=self.dv, dg=self.dg, dbeta=self.dbeta)
+            if self.dinit is not None:
+                out["dinitial_states"] = self.dinit
+        return {k: v.detach().to("cpu", torch.float64) for k, v in out.items()}
+
+
+class DeltaStepDevice:
+    """Token generation with the gated delta rule on a pool of fp32 states
+    (nslots, H, P, N).  ``states_out`` defaults to ``states`` (updated in
+    place); another pool of the same shape keeps the old ones."""
+
+    def __init__(self, states, states_out=None):
+        if states.dim() != 4:
+            raise ValueError("states must be (nslots, H, P, N)")
+        _dense(states, states.shape, torch.float32, "states")
+        self.states = states
+        self.states_out = states if states_out is None else states_out
+        _dense(self.states_out, states.shape, torch.float32, "states_out", states.device)
+
+    def step(self, q, k, v, g, beta, scale=None, slots=None, lengths=None, update=True,
+             outputs=True, stream=None, check=True):
+        """All tokens of q, k (b, T, G, N), v (b, T, H, P), g, beta (b, T, H)
+        in order, from each sequence's slot; returns y (b, T, H, P), or None
+        without ``outputs``.  The states written are those after the first
+        ``lengths[b]`` tokens (default: all); ``update=False`` writes none."""
+        (b, T, H, P, N, G), strides = _delta_shape(q, k, v, g, beta)
+        nslots = self.states.shape[0]
+        if tuple(self.states.shape[1:]) != (H, P, N) or v.device != self.states.device:
+            raise ValueError("the tokens' heads do not fit the states")
+        _dense(slots, (b,), torch.int32, "slots", v.device)
+        _dense(lengths, (b,), torch.int32, "lengths", v.device)
+        scale = N ** -0.5 if scale is None else scale
+        prob = _lib.make_delta_problem(b, T, H, P, N, G, scale, v.dtype, **strides)
+        y = torch.empty((b, T, H, P), dtype=v.dtype, device=v.device) if outputs else None
+        _lib.ssd_delta_step(prob, q, k, v, g, beta, nslots, self.states,
+                            self.states_out if update else None, slots, lengths, y,
+                            stream=stream, check=check)
+        return y
+
+
+def verify_draft(target_probs, draft_probs, draft_tokens, uniform, noise, lengths=None,
+                 stream=None, check=True):
+    """Keep the drafted tokens that the target accepts and draw the next one:
+    (tokens (b, K + 1) int32, kept (b) int32) of target_probs (b, K + 1, V),
+    draft_probs (b, K, V) or None, draft_tokens (b, K), uniform (b, K) and
+    noise (b, V), standard exponentials."""
+    if target_probs.dim() != 3 or target_probs.dtype not in _FLOATS:
+        raise ValueError("target_probs must be (b, K + 1, V), fp32 or bf16")
+    b, K1, V = target_probs.shape
+    dev = target_probs.device
+    _dense(target_probs, (b, K1, V), target_probs.dtype, "target_probs", dev)
+    _dense(draft_probs, (b, K1 - 1, V), target_probs.dtype, "draft_probs", dev)
+    _dense(draft_tokens, (b, K1 - 1), torch.int32, "draft_tokens", dev)
+    _dense(uniform, (b, K1 - 1), torch.float32, "uniform", dev)
+    _dense(noise, (b, V), torch.float32, "noise", dev)
+    _dense(lengths, (b,), torch.int32, "lengths", dev)
+    tokens = torch.empty((b, K1), dtype=torch.int32, device=dev)
+    accepted = torch.empty(b, dtype=torch.int32, device=dev)
+    prob = _lib.make_verify_problem(b, K1 - 1, V, target_probs.dtype)
+    _lib.ssd_verify_draft(prob, target_probs, draft_probs, draft_tokens, lengths, uniform, noise,
+                          tokens, accepted, stream=stream, check=check)
+    return tokens, accepted
+
+
+class StateCache:
+    """An 8-bit cache of recurrent states (nslots, H, P, N): ``int8`` or
+    ``e4m3`` values with one fp32 scale for each row of N."""
+
+    FORMATS = {"int8": _lib.SSD_CACHE_INT8, "e4m3": _lib.SSD_CACHE_E4M3}
+
+    def __init__(self, nslots, nheads, headdim, dstate, form="int8", device="cuda"):
+        if form not in self.FORMATS:
+            raise ValueError(f"form must be one of {sorted(self.FORMATS)}")
+        self.shape, self.form = (nslots, nheads, headdim, dstate), form
+        self.values = torch.empty(self.shape, dtype=torch.uint8, device=device)
+        self.scales = torch.zeros(self.shape[:3], dtype=torch.float32, device=device)
+
+    def _prob(self, states, slots):
+        b = states.shape[0]
+        _dense(states, (b,) + self.shape[1:], torch.float32, "states", self.values.device)
+        _dense(slots, (b,), torch.int32, "slots", self.values.device)
+        return _lib.make_cache_problem(b, *self.shape[1:], self.shape[0], self.FORMATS[self.form])
+
+    def store(self, states, slots=None, stream=None, check=True):
+        """Quantise states (b, H, P, N) into their slots (default: 0 .. b-1)."""
+        return _lib.ssd_state_cache_store(self._prob(states, slots), states, slots, self.values,
+                                          self.scales, stream=stream, check=check)
+
+    def load(self, slots, out, stream=None, check=True):
+        """Read the slots' states (None: 0 .. b-1) into out (b, H, P, N); a
+        slot may be read many times, one outside the cache gives zeros."""
+        return _lib.ssd_state_cache_load(self._prob(out, slots), self.values, self.scales, slots,
+                                         out, stream=stream, check=check)
