@@ -35,9 +35,9 @@ struct DeltaPlan {
   int tc;                // the tensor-core kernels run this problem
   int C, nc;             // chunk length of the saved states, chunks per row
   // byte offsets in `saved`
-  size_t sv_S, sv_w, sv_T, sv_A, saved_bytes;
-  // forward workspace (T and A when there is no `saved`), backward workspace
-  size_t wf_T, wf_A, fwd_bytes;
+  size_t sv_S, sv_w, sv_T, sv_A, sv_e, saved_bytes;
+  // forward workspace (T, A and e when there is no `saved`), backward workspace
+  size_t wf_T, wf_A, wf_e, fwd_bytes;
   size_t wb_D, wb_r, bwd_bytes;
 };
 
@@ -52,9 +52,9 @@ struct DeltaBufs {
   void *dq, *dk, *dv, *dg, *dbeta, *dinit;
   // recurrent kernels (fp32): S (b,H,nc,P,N) states entering each chunk,
   // w (b,L,H,P), D (b,H,nc,P,N) gradients of the state after each chunk,
-  // r (b,L,H,P).  Tensor-core kernels (bf16): S, D (b,H,nc,N,P), w and r
-  // (b,H,nc,C,P), T and A (b,H,nc,C,C).
-  void *S, *w, *T, *A, *D, *r;
+  // r (b,L,H,P).  Tensor-core kernels (bf16): S, D (b,H,nc,N,P), w (b,H,nc,C,P),
+  // T and A (b,H,nc,C,C), and fp32 e (b,H,nc,2,C): e_i, then o_j beta_j; r is dv.
+  void *S, *w, *T, *A, *e, *D, *r;
 };
 
 // Pool arguments of the recurrent step.
@@ -80,10 +80,18 @@ __device__ __forceinline__ void st_state(void* p, long long i, int bf16, float v
 // and sums that held such a term would lose the digits of the others.
 constexpr float kForget = -100.0f;
 
+constexpr int kDeltaChunk = 64;  // tokens per chunk of the tensor-core kernels
+
 cudaError_t launch_delta_recurrent(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
 cudaError_t launch_delta_step(const DeltaPlan& p, const DeltaBufs& f, const DeltaStep& st, cudaStream_t s);
 cudaError_t launch_delta_reverse(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
 cudaError_t launch_delta_grad(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+
+// the tensor-core kernels
+cudaError_t launch_delta_prep(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+cudaError_t launch_delta_chain_fwd(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+cudaError_t launch_delta_chain_bwd(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+cudaError_t launch_delta_grad_tc(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
 
 int device_check();
 

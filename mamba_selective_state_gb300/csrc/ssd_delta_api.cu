@@ -52,8 +52,8 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
   p->scale = pr->scale;
   p->bf16 = pr->dtype == SSD_BF16;
   p->st_bf16 = pr->state_dtype == SSD_BF16;
-  p->tc = 0;
-  p->C = 32;
+  p->tc = p->bf16 && p->P % 32 == 0 && (p->N == 64 || p->N == 128) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0;
+  p->C = p->tc ? kDeltaChunk : 32;
   p->nc = (p->L + p->C - 1) / p->C;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -62,6 +62,24 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
     return o;
   };
   const size_t bh = (size_t)p->b * p->H, states = bh * p->nc * p->P * p->N, rows = bh * p->L * p->P;
+  if (p->tc) {
+    const size_t units = bh * p->nc, cc = (size_t)p->C * p->C * 2;
+    p->sv_S = take(states * 2);
+    p->sv_w = take(units * p->C * p->P * 2);
+    p->sv_T = take(units * cc);
+    p->sv_A = take(units * cc);
+    p->sv_e = take(units * 2 * p->C * 4);
+    p->saved_bytes = off;
+    off = 0;
+    p->wf_T = take(units * cc);
+    p->wf_A = take(units * cc);
+    p->wf_e = take(units * 2 * p->C * 4);
+    p->fwd_bytes = off;
+    off = 0;
+    p->wb_D = take(states * 2);
+    p->bwd_bytes = off;
+    return SSD_OK;
+  }
   p->sv_S = take(states * 4);
   p->sv_w = take(rows * 4);
   p->saved_bytes = off;
@@ -127,6 +145,15 @@ int ssd_delta_fwd(const ssd_delta_problem* prob, const void* q, const void* k, c
     f.w = sv + p.sv_w;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.tc) {
+    char* ws = static_cast<char*>(workspace);
+    f.T = sv ? sv + p.sv_T : ws + p.wf_T;
+    f.A = sv ? sv + p.sv_A : ws + p.wf_A;
+    f.e = sv ? sv + p.sv_e : ws + p.wf_e;
+    DELTA_LAUNCH(launch_delta_prep(p, f, s));
+    DELTA_LAUNCH(launch_delta_chain_fwd(p, f, s));
+    return SSD_OK;
+  }
   DELTA_LAUNCH(launch_delta_recurrent(p, f, s));
   return SSD_OK;
 }
@@ -162,6 +189,14 @@ int ssd_delta_bwd(const ssd_delta_problem* prob, const void* q, const void* k, c
   f.D = ws + p.wb_D;
   f.r = ws + p.wb_r;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.tc) {
+    f.T = sv + p.sv_T;
+    f.A = sv + p.sv_A;
+    f.e = sv + p.sv_e;
+    DELTA_LAUNCH(launch_delta_chain_bwd(p, f, s));
+    DELTA_LAUNCH(launch_delta_grad_tc(p, f, s));
+    return SSD_OK;
+  }
   DELTA_LAUNCH(launch_delta_reverse(p, f, s));
   DELTA_LAUNCH(launch_delta_grad(p, f, s));
   return SSD_OK;
