@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kAll, 1) delta_chain_fwd_kernel(DeltaPlan p, D
     load_state<N, PT>(S, f.init, state0, n0, pw, lane, p.st_bf16);
     publish_state<N, PT>(S, sm + L::oS, n0, pw, lane);
     constexpr int NH = PT / 16;  // 8-column tiles of half the columns
-    const int rb = w & 3, ch = w >> 2, c0 = ch * (PT / 2);
-    const int rbT = ch ? 3 - rb : rb;  // pairs long and short triangular rows on one sub-partition
+    // the two warps of a sub-partition take a long and a short row of the triangle
+    const int ch = w >> 2, rb = ch ? 3 - (w & 3) : (w & 3), c0 = ch * (PT / 2);
     for (int c = 0; c < p.nc; ++c) {
       const int st = c & 1;
       cp_wait<0>();
@@ -145,33 +145,32 @@ __global__ void __launch_bounds__(kAll, 1) delta_chain_fwd_kernel(DeltaPlan p, D
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int i = 16 * rb + g + 8 * r, col = c0 + j * 8 + 2 * t;
-          float2 v = unpack2(lds32(Vs + elem_off<UP>(i, col)));
-          if (e[i] != 0.f) {  // a sequence that starts here does not read the state, whatever it holds
-            v.x -= e[i] * x[j][2 * r];
-            v.y -= e[i] * x[j][2 * r + 1];
-          }
-          sts32(sm + L::oR + elem_off<UP>(i, col), pack2(v.x, v.y));
+          const float2 v = unpack2(lds32(Vs + elem_off<UP>(i, col)));
+          // a sequence that starts here does not read the state, whatever it holds
+          x[j][2 * r] = e[i] != 0.f ? v.x - e[i] * x[j][2 * r] : v.x;
+          x[j][2 * r + 1] = e[i] != 0.f ? v.y - e[i] * x[j][2 * r + 1] : v.y;
+          sts32(sm + L::oR + elem_off<UP>(i, col), pack2(x[j][2 * r], x[j][2 * r + 1]));
         }
       bar_sync(kBarChain, kChain);
-      float y[NH][4] = {};
-      for (int ks = 0; ks <= rbT; ++ks) {
+      // w = R + (T - I) R: the unit diagonal takes R as it is, in fp32
+      for (int ks = 0; ks <= rb; ++ks) {
         uint32_t a[4], b[4];
-        load_a<8>(a, Ts, 16 * rbT, 16 * ks, lane);
+        load_a<8>(a, Ts, 16 * rb, 16 * ks, lane);
 #pragma unroll
         for (int j = 0; j < NH; j += 2) {
           load_bt<UP>(b, sm + L::oR, c0 + j * 8, 16 * ks, lane);
-          mma(y[j], a, b[0], b[1]);
-          mma(y[j + 1], a, b[2], b[3]);
+          mma(x[j], a, b[0], b[1]);
+          mma(x[j + 1], a, b[2], b[3]);
         }
       }
 #pragma unroll
       for (int j = 0; j < NH; ++j)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int i = 16 * rbT + g + 8 * r, col = c0 + j * 8 + 2 * t;
+          const int i = 16 * rb + g + 8 * r, col = c0 + j * 8 + 2 * t;
           const float o = e[kC + i];
-          sts32(Ws + elem_off<UP>(i, col), pack2(y[j][2 * r], y[j][2 * r + 1]));
-          sts32(sm + L::oU + elem_off<UP>(i, col), pack2(o * y[j][2 * r], o * y[j][2 * r + 1]));
+          sts32(Ws + elem_off<UP>(i, col), pack2(x[j][2 * r], x[j][2 * r + 1]));
+          sts32(sm + L::oU + elem_off<UP>(i, col), pack2(o * x[j][2 * r], o * x[j][2 * r + 1]));
         }
       bar_arrive(kBarReady + st, kAll);
       bar_sync(kBarChain, kChain);
@@ -379,15 +378,15 @@ __global__ void __launch_bounds__(kChain, 1) delta_chain_bwd_kernel(DeltaPlan p,
       for (int r = 0; r < 2; ++r)
         sts32(sm + L::oR + elem_off<UP>(16 * rb + g + 8 * r, c0 + j * 8 + 2 * t), pack2(x[j][2 * r], x[j][2 * r + 1]));
     __syncthreads();
-    float y[NH][4] = {};
+    // r = R + (T - I)^T R, the unit diagonal in fp32
     for (int ks = rb; ks < 4; ++ks) {
       uint32_t a[4], b[4];
       load_at<8>(a, Ts, 16 * rb, 16 * ks, lane);
 #pragma unroll
       for (int j = 0; j < NH; j += 2) {
         load_bt<UP>(b, sm + L::oR, c0 + j * 8, 16 * ks, lane);
-        mma(y[j], a, b[0], b[1]);
-        mma(y[j + 1], a, b[2], b[3]);
+        mma(x[j], a, b[0], b[1]);
+        mma(x[j + 1], a, b[2], b[3]);
       }
     }
 #pragma unroll
@@ -398,8 +397,8 @@ __global__ void __launch_bounds__(kChain, 1) delta_chain_bwd_kernel(DeltaPlan p,
       __nv_bfloat16* dst = dvg + (long long)(c * kC + i) * vs + c0 + 2 * t;
 #pragma unroll
       for (int j = 0; j < NH; ++j) {
-        if (in) *reinterpret_cast<uint32_t*>(dst + j * 8) = pack2(y[j][2 * r], y[j][2 * r + 1]);
-        sts32(sm + L::oU + elem_off<UP>(i, c0 + j * 8 + 2 * t), pack2(s * y[j][2 * r], s * y[j][2 * r + 1]));
+        if (in) *reinterpret_cast<uint32_t*>(dst + j * 8) = pack2(x[j][2 * r], x[j][2 * r + 1]);
+        sts32(sm + L::oU + elem_off<UP>(i, c0 + j * 8 + 2 * t), pack2(s * x[j][2 * r], s * x[j][2 * r + 1]));
       }
     }
     __syncthreads();
