@@ -343,12 +343,16 @@ int ssd_gated_rmsnorm_bwd(const ssd_norm_problem* prob, const void* y, const voi
  *
  * Precision: fp32 problems compute in fp32 throughout.  bf16 problems hold
  * states, sums and decays in fp32; where the tensor cores form the products
- * (headdim a multiple of 32, dstate 64 or 128, strides multiples of 8) their
- * operands -- the carried state among them -- are rounded to bf16.
+ * (headdim a multiple of 64, dstate 64 or 128, strides multiples of 8) their
+ * operands -- the carried state among them -- are rounded to bf16.  There, and
+ * in the gradient of any problem, a value that is not finite may reach every
+ * token of its 64-token chunk, also across a sequence start.
  *
  * Limits: headdim, dstate <= 256; nheads % ngroups == 0; ownership, errors
- * and stream semantics as above; no device-side waits, no status word.
- * Results are bitwise reproducible run to run. */
+ * and stream semantics as above; device-side waits are bounded, and one that
+ * expired is recorded in the status word at the start of the call's workspace
+ * (ssd_read_device_status; the step has no waits and no workspace).  Results
+ * are bitwise reproducible run to run. */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
   int64_t q_stride, k_stride, v_stride; /* elements from token to token; 0 = dense */

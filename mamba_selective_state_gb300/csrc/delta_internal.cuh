@@ -52,9 +52,11 @@ struct DeltaBufs {
   void *dq, *dk, *dv, *dg, *dbeta, *dinit;
   // recurrent kernels (fp32): S (b,H,nc,P,N) states entering each chunk,
   // w (b,L,H,P), D (b,H,nc,P,N) gradients of the state after each chunk,
-  // r (b,L,H,P).  Tensor-core kernels (bf16): S, D (b,H,nc,N,P), w (b,H,nc,C,P),
-  // T and A (b,H,nc,C,C), and fp32 e (b,H,nc,2,C): e_i, then o_j beta_j; r is dv.
+  // r (b,L,H,P).  Tensor-core kernels: bf16 S, D (b,H,nc,P,N), w transposed
+  // (b,H,nc,P,C), T - I and A (b,H,nc,C,C), and fp32 gate records e
+  // (b,H,nc,kGateRows,C); r is dv.
   void *S, *w, *T, *A, *e, *D, *r;
+  int* status;  // device status word, at the start of the workspace
 };
 
 // Pool arguments of the recurrent step.
@@ -81,6 +83,9 @@ __device__ __forceinline__ void st_state(void* p, long long i, int bf16, float v
 constexpr float kForget = -100.0f;
 
 constexpr int kDeltaChunk = 64;  // tokens per chunk of the tensor-core kernels
+// rows of a chunk's gate record: e_i, o_j beta_j, gam, beta, o_j, and the
+// number of sequence starts up to the token (as an int)
+constexpr int kGateRows = 6;
 
 cudaError_t launch_delta_recurrent(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
 cudaError_t launch_delta_step(const DeltaPlan& p, const DeltaBufs& f, const DeltaStep& st, cudaStream_t s);

@@ -1,469 +1,558 @@
 // k_delta_chain.cu -- the state's way through the chunks of the gated delta
-// rule (see delta_internal.cuh for the formulas, k_delta_prep.cu for T, A, e
-// and o), one CTA per (batch row, head, 64 or 32 columns of headdim): the
-// columns of the state are independent, so a chain can be split over CTAs.
+// rule (see delta_internal.cuh for the formulas, k_delta_prep.cu for T, A and
+// the gates).
 //
-// Forward, eight chain warps per chunk:
-//   R = V - e (K S0)  ->  w = T R  ->  S = e_last S + K^T (o beta w)
-// with S in fp32 accumulators (each warp 16 of its dstate rows) and bf16
-// copies of S, R and w in shared memory as the next product's operands.
-// Four output warps follow a chunk behind the solve, off the chain's critical
-// path: y = scale e (Q S0) + A w; they also write S0 and w for the backward.
+// The columns of the state (values of headdim) are independent of each other,
+// and everything a column's chain needs besides its own v is shared: so one
+// warp keeps 16 columns, transposed, as the fp32 accumulators of a product
+// with 16 rows, and walks the chunks by itself.  Written transposed, every
+// product of the chain takes the last one's result as its left operand
+// straight from registers (an accumulator's layout is a left operand's
+// layout), and its right operand -- K, T, Q or A -- from shared memory:
 //
-// Reverse, given D = dL/dS after the chunk:
-//   R = o beta (K D) + A^T dY  ->  r = T^T R (= dv)
-//   D = e_last D + Q^T (scale e dY) - K^T (e r)
+//   forward   R' = V' - e (S' K')     w' = R' + R' (T-I)'    S' = e_last S' + (o beta w)' K
+//             y' = scale e (S' Q') + w' A'
+//   reverse   R' = o beta (D' K') + dY' A    r' = R' + R' (T-I)
+//             D' = e_last D' + (scale e dY)' Q - (e r)' K
+//
+// There is no barrier between warps on a chain and no state in shared memory.
+// The forward hands each chunk's S' and w' (bf16) to a second warp, which
+// forms y' off the chain's critical path; from the same tiles they leave for
+// the backward.  One more warp issues the TMA copies of the next chunks.
+// Bound by shared-memory reads of the right operands (about 70 KB per 16
+// columns and chunk) next to the tensor pipe (232 products of 16 x 8 x 16).
 #include "delta_internal.cuh"
 #include "mma_common.cuh"
+#include "tma_host.h"
 
 namespace ssd {
 namespace {
 
 using namespace mm;
+using namespace tc;
 
 constexpr int kC = kDeltaChunk;
-constexpr int kChain = 256;          // threads of the chain warps
-constexpr int kOut = 128;            // threads of the output warps
-constexpr int kAll = kChain + kOut;
-// named barriers: the chain's own, then "w of the chunk is written" and "the
-// output warps are done with it" for even and odd chunks
-constexpr int kBarChain = 1, kBarOut = 2, kBarReady = 3, kBarFree = 5;
+constexpr uint32_t kTile = kC * 128;  // a [64][64] bf16 tile, 128-byte swizzle
+constexpr int kGateBytes = 2 * kC * 4;  // the chains read e and o beta
 
-// The fp32 state rows of one warp: n0.. (16 rows) x NT 8-column tiles from
-// column p0w of this CTA's PT columns.
-template <int N, int PT>
-struct Split {
-  static constexpr int NT = N == 128 ? PT / 8 : PT / 16;
-  __device__ static int n0(int w) { return N == 128 ? 16 * w : 16 * (w & 3); }
-  __device__ static int p0(int w) { return N == 128 ? 0 : (w >> 2) * (PT / 2); }
+// Right operands from [64][64] tiles of a [64][64 * blocks] matrix.
+__device__ __forceinline__ void ld_b(uint32_t (&r)[4], uint32_t base, int n0, int k0, int lane) {
+  load_b<8>(r, base + (uint32_t)(k0 >> 6) * kTile, n0, k0 & 63, lane);
+}
+__device__ __forceinline__ void ld_bt(uint32_t (&r)[4], uint32_t base, int n0, int k0, int lane) {
+  load_bt<8>(r, base + (uint32_t)(n0 >> 6) * kTile, n0 & 63, k0, lane);
+}
+// The left operand of rows k0.. from two accumulators
+__device__ __forceinline__ void as_left(uint32_t (&a)[4], const float (&lo)[4], const float (&hi)[4]) {
+  a[0] = pack2(lo[0], lo[1]);
+  a[1] = pack2(lo[2], lo[3]);
+  a[2] = pack2(hi[0], hi[1]);
+  a[3] = pack2(hi[2], hi[3]);
+}
+// A [16][64 * blocks] bf16 tile (blocks of [16][64], 128-byte swizzle) in
+// shared memory: where the fragment of columns k0.. goes
+__device__ __forceinline__ uint32_t frag_at(uint32_t base, int k0, int lane) {
+  return base + (uint32_t)(k0 >> 6) * 2048u + tile_off<8>(lane & 15, ((k0 & 63) >> 3) + (lane >> 4));
+}
+// Where the transposed fragment of 16 tokens from tok0 goes in a [64][16]
+// tile of 32-byte rows
+__device__ __forceinline__ uint32_t token_at(uint32_t base, int tok0, int lane) {
+  return base + (uint32_t)(tok0 + ((lane >> 4) << 3) + (lane & 7)) * 32u + (uint32_t)((lane >> 3) & 1) * 16u;
+}
+
+template <int N>
+__device__ __forceinline__ void load_state(float (&S)[N / 8][4], const void* src, long long base, int lane, int bf16) {
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      S[i][j] = src ? ld_state(src, base + (long long)((lane >> 2) + (j >> 1) * 8) * N + i * 8 + 2 * (lane & 3) + (j & 1), bf16)
+                    : 0.f;
+}
+template <int N>
+__device__ __forceinline__ void store_state(const float (&S)[N / 8][4], void* dst, long long base, int lane, int bf16) {
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const long long o = base + (long long)((lane >> 2) + 8 * r) * N + i * 8 + 2 * (lane & 3);
+      if (bf16)
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(dst) + o) = pack2(S[i][2 * r], S[i][2 * r + 1]);
+      else
+        *reinterpret_cast<float2*>(static_cast<float*>(dst) + o) = make_float2(S[i][2 * r], S[i][2 * r + 1]);
+    }
+}
+
+struct ChainMaps {
+  CUtensorMap q, k, v, T, A, y, S, w;  // reverse: v is dy, y is dv, S is D
 };
 
-template <int N, int PT>
-__device__ __forceinline__ void load_state(float (&S)[Split<N, PT>::NT][4], const void* src, long long base, int n0,
-                                           int p0, int lane, int bf16) {
-#pragma unroll
-  for (int i = 0; i < Split<N, PT>::NT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + (lane >> 2) + (j >> 1) * 8, pp = p0 + i * 8 + 2 * (lane & 3) + (j & 1);
-      S[i][j] = src ? ld_state(src, base + (long long)pp * N + n, bf16) : 0.f;
-    }
-}
-template <int N, int PT>
-__device__ __forceinline__ void store_state(const float (&S)[Split<N, PT>::NT][4], void* dst, long long base, int n0,
-                                            int p0, int lane, int bf16) {
-#pragma unroll
-  for (int i = 0; i < Split<N, PT>::NT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + (lane >> 2) + (j >> 1) * 8, pp = p0 + i * 8 + 2 * (lane & 3) + (j & 1);
-      st_state(dst, base + (long long)pp * N + n, bf16, S[i][j]);
-    }
-}
-// the bf16 copy of the state, [n][p]
-template <int N, int PT>
-__device__ __forceinline__ void publish_state(const float (&S)[Split<N, PT>::NT][4], uint32_t dst, int n0, int p0,
-                                              int lane) {
-#pragma unroll
-  for (int i = 0; i < Split<N, PT>::NT; ++i)
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      sts32(dst + elem_off<PT / 8>(n0 + (lane >> 2) + 8 * r, p0 + i * 8 + 2 * (lane & 3)),
-            pack2(S[i][2 * r], S[i][2 * r + 1]));
-}
-
-template <int N, int PT>
+// NW column warps: 16 NW columns a CTA
+template <int N, int NW>
 struct FwdSmem {
-  static constexpr int kK = kC * N * 2, kV = kC * PT * 2, kT = kC * kC * 2, kS = N * PT * 2;
-  // two stages of K, V, T, e; two of Q, A, e; S0 and w for two chunks; R; o beta w
-  static constexpr int oK = 0, oT = oK + 2 * kK, oV = oT + 2 * kT, oQ = oV + 2 * kV, oA = oQ + 2 * kK,
-                       oS = oA + 2 * kT, oW = oS + 2 * kS, oR = oW + 2 * kV, oU = oR + kV, oE = oU + kV,
-                       bytes = oE + 4 * 2 * kC * 4;
+  static constexpr int kK = kC * N * 2, kV = kC * NW * 32;
+  // the chain's ring: K, T, V, gates; the output warps': Q, A, gates; each two deep
+  static constexpr int chain = kK + (int)kTile + kV, out = kK + (int)kTile;
+  static constexpr int oChain = 0, oOut = oChain + 2 * chain, oS = oOut + 2 * out,  // S' by warp, two each
+                       oW = oS + NW * 2 * N * 32, oY = oW + NW * 2 * 2048, oE = oY + NW * 2 * 2048,
+                       oBar = oE + 4 * kGateBytes, bytes = oBar + (8 + 4 * NW) * 8 + 1024;
 };
 
-template <int N, int PT>
-__global__ void __launch_bounds__(kAll, 1) delta_chain_fwd_kernel(DeltaPlan p, DeltaBufs f) {
-  using L = FwdSmem<N, PT>;
-  using Sp = Split<N, PT>;
-  constexpr int UN = N / 8, UP = PT / 8;
-  extern __shared__ __align__(128) unsigned char raw[];
+template <int N, int NW>
+__global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
+    delta_chain_fwd_kernel(DeltaPlan p, DeltaBufs f, const __grid_constant__ ChainMaps m) {
+  using L = FwdSmem<N, NW>;
+  extern __shared__ unsigned char raw_[];
+  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
   const uint32_t sm = smem_u32(raw);
-  const int ptiles = p.P / PT;
-  const int p0 = (int)(blockIdx.x % ptiles) * PT;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + L::oBar);
+  uint64_t *c_full = bars, *c_free = bars + 2, *o_full = bars + 4, *o_free = bars + 6;
+  uint64_t *h_full = bars + 8, *h_free = h_full + 2 * NW;  // [warp][2]
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+  const int ptiles = p.P / (16 * NW);
+  const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
   const int h = (int)((blockIdx.x / ptiles) % p.H), bi = (int)(blockIdx.x / ((long long)ptiles * p.H));
-  const int grp = h / p.hpg;
-  const long long row0 = (long long)bi * p.L;
-  const long long unit0 = ((long long)bi * p.H + h) * p.nc;
-  const long long state0 = (((long long)bi * p.H + h) * p.P + p0) * N;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const __nv_bfloat16* T = static_cast<const __nv_bfloat16*>(f.T) + unit0 * kC * kC;
-  const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(f.A) + unit0 * kC * kC;
-  const float* eg = static_cast<const float*>(f.e) + unit0 * 2 * kC;
-
-  if (threadIdx.x < kChain) {
-    const int tid = threadIdx.x, w = tid >> 5;
-    const __nv_bfloat16* kg = static_cast<const __nv_bfloat16*>(f.k) + row0 * p.ks + (long long)grp * N;
-    const __nv_bfloat16* vg = static_cast<const __nv_bfloat16*>(f.v) + row0 * p.vs + (long long)h * p.P + p0;
-    auto load = [&](int c) {
-      const int st = c & 1, n = min(kC, p.L - c * kC);
-      cp_tile<kC, UN>(sm + L::oK + st * L::kK, kg + (long long)c * kC * p.ks, p.ks, n, tid, kChain);
-      cp_tile<kC, 8>(sm + L::oT + st * L::kT, T + (long long)c * kC * kC, kC, kC, tid, kChain);
-      cp_tile<kC, UP>(sm + L::oV + st * L::kV, vg + (long long)c * kC * p.vs, p.vs, n, tid, kChain);
-      if (tid < 32) cp16(sm + L::oE + st * 2 * kC * 4 + tid * 16, eg + (long long)c * 2 * kC + tid * 4, true);
-      cp_commit();
-    };
-    load(0);
-    const int n0 = Sp::n0(w), pw = Sp::p0(w);
-    float S[Sp::NT][4];
-    load_state<N, PT>(S, f.init, state0, n0, pw, lane, p.st_bf16);
-    publish_state<N, PT>(S, sm + L::oS, n0, pw, lane);
-    constexpr int NH = PT / 16;  // 8-column tiles of half the columns
-    // the two warps of a sub-partition take a long and a short row of the triangle
-    const int ch = w >> 2, rb = ch ? 3 - (w & 3) : (w & 3), c0 = ch * (PT / 2);
+  const int grp = h / p.hpg, bh = bi * p.H + h;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(c_full + i, 1);
+      mbar_init(c_free + i, NW);
+      mbar_init(o_full + i, 1);
+      mbar_init(o_free + i, NW);
+    }
+    for (int i = 0; i < 2 * NW; ++i) {
+      mbar_init(h_full + i, 1);
+      mbar_init(h_free + i, 1);
+    }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  bool ok = true;
+  if (w == 2 * NW) {
+    if (lane == 0) {
+      const float* e = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+      for (int c = 0; c < p.nc; ++c) {
+        const int st = c & 1;
+        if (c >= 2) mbar_wait_flag(c_free + st, ((c >> 1) - 1) & 1, ok);
+        unsigned char* d = raw + L::oChain + st * L::chain;
+        mbar_expect_tx(c_full + st, L::chain + kGateBytes);
+        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, c_full + st, 64 * j, grp, c * kC, bi);
+        tma_load_4d(d + L::kK, &m.T, c_full + st, 0, 0, c, bh);
+        tma_load_4d(d + L::kK + kTile, &m.v, c_full + st, p0, h, c * kC, bi);
+        bulk_load(raw + L::oE + st * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, c_full + st);
+        if (c >= 2) mbar_wait_flag(o_free + st, ((c >> 1) - 1) & 1, ok);
+        d = raw + L::oOut + st * L::out;
+        mbar_expect_tx(o_full + st, L::out + kGateBytes);
+        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.q, o_full + st, 64 * j, grp, c * kC, bi);
+        tma_load_4d(d + L::kK, &m.A, o_full + st, 0, 0, c, bh);
+        bulk_load(raw + L::oE + (2 + st) * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, o_full + st);
+      }
+    }
+  } else if (w < NW) {
+    const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
+    float S[N / 8][4];
+    load_state<N>(S, f.init, state0, lane, p.st_bf16);
     for (int c = 0; c < p.nc; ++c) {
       const int st = c & 1;
-      cp_wait<0>();
-      bar_sync(kBarChain, kChain);  // this chunk's tiles and state are in place; the last chunk's have been read
-      if (c + 1 < p.nc) load(c + 1);
-      const float* e = reinterpret_cast<const float*>(raw + L::oE + st * 2 * kC * 4);
-      const uint32_t Ks = sm + L::oK + st * L::kK, Vs = sm + L::oV + st * L::kV, Ts = sm + L::oT + st * L::kT;
-      const uint32_t Ss = sm + L::oS + st * L::kS, Ws = sm + L::oW + st * L::kV;
-      float x[NH][4] = {};
+      const uint32_t Ks = sm + L::oChain + st * L::chain, Ts = Ks + L::kK, Vs = Ts + kTile;
+      const uint32_t Sd = sm + L::oS + (2 * w + st) * N * 32, Wd = sm + L::oW + (2 * w + st) * 2048;
+      const float* e = reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) + 2 * t;
+      if (c >= 2) mbar_wait_flag(h_free + 2 * w + st, ((c >> 1) - 1) & 1, ok);
+      mbar_wait_flag(c_full + st, (c >> 1) & 1, ok);
+      float x[8][4] = {};
 #pragma unroll
-      for (int ks = 0; ks < N; ks += 16) {
+      for (int ks = 0; ks < N / 16; ++ks) {
         uint32_t a[4], b[4];
-        load_a<UN>(a, Ks, 16 * rb, ks, lane);
+        as_left(a, S[2 * ks], S[2 * ks + 1]);
+        stsm4(frag_at(Sd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
 #pragma unroll
-        for (int j = 0; j < NH; j += 2) {
-          load_bt<UP>(b, Ss, c0 + j * 8, ks, lane);
+        for (int j = 0; j < 8; j += 2) {
+          ld_b(b, Ks, 8 * j, 16 * ks, lane);
           mma(x[j], a, b[0], b[1]);
           mma(x[j + 1], a, b[2], b[3]);
         }
       }
+      // R' = V' - e (S' K'); a sequence that starts here does not read the state, whatever it holds
+      uint32_t left[4][4];
 #pragma unroll
-      for (int j = 0; j < NH; ++j)
+      for (int k = 0; k < 4; ++k) {
+        uint32_t v[4];
+        if (NW == 4)
+          load_at<8>(v, Vs, 16 * w, 16 * k, lane);
+        else
+          load_at<4>(v, Vs, 16 * w, 16 * k, lane);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = 16 * rb + g + 8 * r, col = c0 + j * 8 + 2 * t;
-          const float2 v = unpack2(lds32(Vs + elem_off<UP>(i, col)));
-          // a sequence that starts here does not read the state, whatever it holds
-          x[j][2 * r] = e[i] != 0.f ? v.x - e[i] * x[j][2 * r] : v.x;
-          x[j][2 * r + 1] = e[i] != 0.f ? v.y - e[i] * x[j][2 * r + 1] : v.y;
-          sts32(sm + L::oR + elem_off<UP>(i, col), pack2(x[j][2 * r], x[j][2 * r + 1]));
+        for (int j = 0; j < 2; ++j) {
+          const float2 ej = *reinterpret_cast<const float2*>(e + 16 * k + 8 * j);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 vv = unpack2(v[2 * j + r]);
+            float(&xx)[4] = x[2 * k + j];
+            xx[2 * r] = ej.x != 0.f ? vv.x - ej.x * xx[2 * r] : vv.x;
+            xx[2 * r + 1] = ej.y != 0.f ? vv.y - ej.y * xx[2 * r + 1] : vv.y;
+          }
         }
-      bar_sync(kBarChain, kChain);
-      // w = R + (T - I) R: the unit diagonal takes R as it is, in fp32
-      for (int ks = 0; ks <= rb; ++ks) {
-        uint32_t a[4], b[4];
-        load_a<8>(a, Ts, 16 * rb, 16 * ks, lane);
-#pragma unroll
-        for (int j = 0; j < NH; j += 2) {
-          load_bt<UP>(b, sm + L::oR, c0 + j * 8, 16 * ks, lane);
-          mma(x[j], a, b[0], b[1]);
-          mma(x[j + 1], a, b[2], b[3]);
-        }
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
       }
+      // w' = R' + R' (T - I)': the unit diagonal takes R as it is, in fp32
 #pragma unroll
-      for (int j = 0; j < NH; ++j)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = 16 * rb + g + 8 * r, col = c0 + j * 8 + 2 * t;
-          const float o = e[kC + i];
-          sts32(Ws + elem_off<UP>(i, col), pack2(x[j][2 * r], x[j][2 * r + 1]));
-          sts32(sm + L::oU + elem_off<UP>(i, col), pack2(o * x[j][2 * r], o * x[j][2 * r + 1]));
+        for (int k = 0; k <= i; ++k) {
+          uint32_t b[4];
+          ld_b(b, Ts, 16 * i, 16 * k, lane);
+          mma(x[2 * i], left[k], b[0], b[1]);
+          mma(x[2 * i + 1], left[k], b[2], b[3]);
         }
-      bar_arrive(kBarReady + st, kAll);
-      bar_sync(kBarChain, kChain);
-      const float last = e[kC - 1];
 #pragma unroll
-      for (int i = 0; i < Sp::NT; ++i)
+      for (int k = 0; k < 4; ++k) {
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
+        stsm4(frag_at(Wd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
+      }
+      if (f.S) fence_async_smem();  // the tiles also leave through TMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(h_full + 2 * w + st);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 o = *reinterpret_cast<const float2*>(e + kC + 16 * k + 8 * j);
+          float(&xx)[4] = x[2 * k + j];
+          xx[0] *= o.x;
+          xx[1] *= o.y;
+          xx[2] *= o.x;
+          xx[3] *= o.y;
+        }
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
+      }
+      const float last = e[kC - 1 - 2 * t];
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) S[i][j] = last == 0.f ? 0.f : S[i][j] * last;
 #pragma unroll
-      for (int ks = 0; ks < kC; ks += 16) {
-        uint32_t a[4], b[4];
-        load_at<UN>(a, Ks, n0, ks, lane);
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int j = 0; j < Sp::NT; j += 2) {
-          load_bt<UP>(b, sm + L::oU, pw + j * 8, ks, lane);
-          mma(S[j], a, b[0], b[1]);
-          mma(S[j + 1], a, b[2], b[3]);
+        for (int i = 0; i < N / 8; i += 2) {
+          uint32_t b[4];
+          ld_bt(b, Ks, 8 * i, 16 * k, lane);
+          mma(S[i], left[k], b[0], b[1]);
+          mma(S[i + 1], left[k], b[2], b[3]);
         }
-      }
-      if (c + 1 < p.nc) {
-        // the output warps are done with chunk c - 1: its state and w make room
-        if (c >= 1) bar_sync(kBarFree + (st ^ 1), kAll);
-        publish_state<N, PT>(S, sm + L::oS + (st ^ 1) * L::kS, n0, pw, lane);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(c_free + st);
     }
-    if (f.fin) store_state<N, PT>(S, f.fin, state0, n0, pw, lane, p.st_bf16);
+    if (f.fin) store_state<N>(S, f.fin, state0, lane, p.st_bf16);
   } else {
-    const int tid = threadIdx.x - kChain, w = tid >> 5;
-    const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(f.q) + row0 * p.qs + (long long)grp * N;
-    __nv_bfloat16* yg = static_cast<__nv_bfloat16*>(f.y) + (row0 * p.H + h) * p.P + p0;
-    auto load = [&](int c) {
-      const int st = c & 1, n = min(kC, p.L - c * kC);
-      cp_tile<kC, UN>(sm + L::oQ + st * L::kK, qg + (long long)c * kC * p.qs, p.qs, n, tid, kOut);
-      cp_tile<kC, 8>(sm + L::oA + st * L::kT, A + (long long)c * kC * kC, kC, kC, tid, kOut);
-      if (tid < 32) cp16(sm + L::oE + (2 + st) * 2 * kC * 4 + tid * 16, eg + (long long)c * 2 * kC + tid * 4, true);
-      cp_commit();
-    };
-    load(0);
-    constexpr int NT = PT / 8;
+    const int cw = w - NW;
     for (int c = 0; c < p.nc; ++c) {
       const int st = c & 1;
-      cp_wait<0>();
-      bar_sync(kBarOut, kOut);
-      if (c + 1 < p.nc) load(c + 1);
-      const float* e = reinterpret_cast<const float*>(raw + L::oE + (2 + st) * 2 * kC * 4);
-      const uint32_t Qs = sm + L::oQ + st * L::kK, As = sm + L::oA + st * L::kT;
-      const uint32_t Ss = sm + L::oS + st * L::kS, Ws = sm + L::oW + st * L::kV;
-      bar_sync(kBarReady + st, kAll);
-      float y[NT][4] = {};
-#pragma unroll
-      for (int ks = 0; ks < N; ks += 16) {
-        uint32_t a[4], b[4];
-        load_a<UN>(a, Qs, 16 * w, ks, lane);
-#pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          load_bt<UP>(b, Ss, j * 8, ks, lane);
-          mma(y[j], a, b[0], b[1]);
-          mma(y[j + 1], a, b[2], b[3]);
-        }
+      const uint32_t Qs = sm + L::oOut + st * L::out, As = Qs + L::kK;
+      const uint32_t Sd = sm + L::oS + (2 * cw + st) * N * 32, Wd = sm + L::oW + (2 * cw + st) * 2048;
+      const uint32_t Yd = sm + L::oY + (2 * cw + st) * 2048;
+      const float* e = reinterpret_cast<const float*>(raw + L::oE + (2 + st) * kGateBytes) + 2 * t;
+      mbar_wait_flag(o_full + st, (c >> 1) & 1, ok);
+      mbar_wait_flag(h_full + 2 * cw + st, (c >> 1) & 1, ok);
+      if (f.S && lane == 0) {
+        for (int j = 0; j < N / 64; ++j)
+          tma_store_4d(&m.S, raw + (Sd - sm) + j * 2048, 64 * j, p0 + 16 * cw, c, bh);
+        tma_store_4d(&m.w, raw + (Wd - sm), 0, p0 + 16 * cw, c, bh);
+        bulk_commit();
       }
-      const float e0 = p.scale * e[16 * w + g], e1 = p.scale * e[16 * w + g + 8];
+      float y[8][4] = {};
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        y[j][0] = e0 == 0.f ? 0.f : y[j][0] * e0;
-        y[j][1] = e0 == 0.f ? 0.f : y[j][1] * e0;
-        y[j][2] = e1 == 0.f ? 0.f : y[j][2] * e1;
-        y[j][3] = e1 == 0.f ? 0.f : y[j][3] * e1;
-      }
-      for (int ks = 0; ks <= w; ++ks) {
+      for (int ks = 0; ks < N / 16; ++ks) {
         uint32_t a[4], b[4];
-        load_a<8>(a, As, 16 * w, 16 * ks, lane);
+        ldsm4(a, frag_at(Sd, 16 * ks, lane));
 #pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          load_bt<UP>(b, Ws, j * 8, 16 * ks, lane);
+        for (int j = 0; j < 8; j += 2) {
+          ld_b(b, Qs, 8 * j, 16 * ks, lane);
           mma(y[j], a, b[0], b[1]);
           mma(y[j + 1], a, b[2], b[3]);
         }
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int i = 16 * w + g + 8 * r;
-        if (c * kC + i < p.L) {
-          __nv_bfloat16* dst = yg + (long long)(c * kC + i) * p.H * p.P + 2 * t;
+      for (int j = 0; j < 8; ++j) {
+        const float2 ej = *reinterpret_cast<const float2*>(e + 8 * j);
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            *reinterpret_cast<uint32_t*>(dst + j * 8) = pack2(y[j][2 * r], y[j][2 * r + 1]);
+        for (int r = 0; r < 2; ++r) {
+          y[j][2 * r] = ej.x != 0.f ? p.scale * ej.x * y[j][2 * r] : 0.f;
+          y[j][2 * r + 1] = ej.y != 0.f ? p.scale * ej.y * y[j][2 * r + 1] : 0.f;
         }
       }
-      if (f.S) {
-        __nv_bfloat16* Sg = static_cast<__nv_bfloat16*>(f.S) + (unit0 + c) * N * p.P + p0;
-        __nv_bfloat16* Wg = static_cast<__nv_bfloat16*>(f.w) + (unit0 + c) * kC * p.P + p0;
-#pragma unroll 4
-        for (int i = tid; i < N * UP; i += kOut)
-          *reinterpret_cast<uint4*>(Sg + (long long)(i / UP) * p.P + (i % UP) * 8) = lds128(Ss + tile_off<UP>(i / UP, i % UP));
-#pragma unroll 4
-        for (int i = tid; i < kC * UP; i += kOut)
-          *reinterpret_cast<uint4*>(Wg + (long long)(i / UP) * p.P + (i % UP) * 8) = lds128(Ws + tile_off<UP>(i / UP, i % UP));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[4], b[4];
+        ldsm4(a, frag_at(Wd, 16 * k, lane));
+#pragma unroll
+        for (int i = k; i < 4; ++i) {
+          ld_b(b, As, 16 * i, 16 * k, lane);
+          mma(y[2 * i], a, b[0], b[1]);
+          mma(y[2 * i + 1], a, b[2], b[3]);
+        }
       }
-      // nobody waits for the last two chunks' buffers
-      if (c + 2 < p.nc) bar_arrive(kBarFree + st, kAll);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free + st);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[4];
+        as_left(a, y[2 * k], y[2 * k + 1]);
+        stsm4t(token_at(Yd, 16 * k, lane), a[0], a[1], a[2], a[3]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_4d(&m.y, raw + (Yd - sm), p0 + 16 * cw, h, c * kC, bi);
+        bulk_commit();
+        bulk_wait_read<1>();  // all but this chunk's y have been read: its S', w' and the last y's tile are free
+        mbar_arrive(h_free + 2 * cw + st);
+      }
+      __syncwarp();
     }
+    if (lane == 0) bulk_wait_all();
   }
+  if (!ok) atomicOr(f.status, kDevTimeout);
 }
 
-template <int N, int PT>
+template <int N, int NW>
 struct RevSmem {
-  static constexpr int kK = kC * N * 2, kV = kC * PT * 2, kT = kC * kC * 2;
-  // two stages of K, Q, T, A, dY, e; D; R; -e r; scale e dY
-  static constexpr int oK = 0, oQ = oK + 2 * kK, oT = oQ + 2 * kK, oA = oT + 2 * kT, oY = oA + 2 * kT,
-                       oD = oY + 2 * kV, oR = oD + N * PT * 2, oU = oR + kV, oP = oU + kV, oE = oP + kV,
-                       bytes = oE + 2 * 2 * kC * 4;
+  static constexpr int kK = kC * N * 2, kV = kC * NW * 32;
+  // a ring two deep of K, Q, T, A, dY, gates; D' and r by warp, two each
+  static constexpr int stage = 2 * kK + 2 * (int)kTile + kV;
+  static constexpr int oSt = 0, oD = oSt + 2 * stage, oR = oD + NW * 2 * N * 32, oE = oR + NW * 2 * 2048,
+                       oBar = oE + 2 * kGateBytes, bytes = oBar + 4 * 8 + 1024;
 };
 
-template <int N, int PT>
-__global__ void __launch_bounds__(kChain, 1) delta_chain_bwd_kernel(DeltaPlan p, DeltaBufs f) {
-  using L = RevSmem<N, PT>;
-  using Sp = Split<N, PT>;
-  constexpr int UN = N / 8, UP = PT / 8;
-  extern __shared__ __align__(128) unsigned char raw[];
+template <int N, int NW>
+__global__ void __launch_bounds__((NW + 1) * 32, 1)
+    delta_chain_bwd_kernel(DeltaPlan p, DeltaBufs f, const __grid_constant__ ChainMaps m) {
+  using L = RevSmem<N, NW>;
+  extern __shared__ unsigned char raw_[];
+  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
   const uint32_t sm = smem_u32(raw);
-  const int ptiles = p.P / PT;
-  const int p0 = (int)(blockIdx.x % ptiles) * PT;
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + L::oBar);
+  uint64_t* empty = full + 2;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+  const int ptiles = p.P / (16 * NW);
+  const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
   const int h = (int)((blockIdx.x / ptiles) % p.H), bi = (int)(blockIdx.x / ((long long)ptiles * p.H));
-  const int grp = h / p.hpg;
-  const long long row0 = (long long)bi * p.L;
-  const long long unit0 = ((long long)bi * p.H + h) * p.nc;
-  const long long state0 = (((long long)bi * p.H + h) * p.P + p0) * N;
-  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3, w = tid >> 5;
-  const __nv_bfloat16* T = static_cast<const __nv_bfloat16*>(f.T) + unit0 * kC * kC;
-  const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(f.A) + unit0 * kC * kC;
-  const float* eg = static_cast<const float*>(f.e) + unit0 * 2 * kC;
-  const __nv_bfloat16* kg = static_cast<const __nv_bfloat16*>(f.k) + row0 * p.ks + (long long)grp * N;
-  const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(f.q) + row0 * p.qs + (long long)grp * N;
-  const long long vs = (long long)p.H * p.P, v0 = row0 * vs + (long long)h * p.P + p0;
-  const __nv_bfloat16* yg = static_cast<const __nv_bfloat16*>(f.dy) + v0;
-  __nv_bfloat16* dvg = static_cast<__nv_bfloat16*>(f.dv) + v0;
-  auto load = [&](int c) {
-    const int st = c & 1, n = min(kC, p.L - c * kC);
-    cp_tile<kC, UN>(sm + L::oK + st * L::kK, kg + (long long)c * kC * p.ks, p.ks, n, tid, kChain);
-    cp_tile<kC, UN>(sm + L::oQ + st * L::kK, qg + (long long)c * kC * p.qs, p.qs, n, tid, kChain);
-    cp_tile<kC, 8>(sm + L::oT + st * L::kT, T + (long long)c * kC * kC, kC, kC, tid, kChain);
-    cp_tile<kC, 8>(sm + L::oA + st * L::kT, A + (long long)c * kC * kC, kC, kC, tid, kChain);
-    cp_tile<kC, UP>(sm + L::oY + st * L::kV, yg + (long long)c * kC * vs, vs, n, tid, kChain);
-    if (tid < 32) cp16(sm + L::oE + st * 2 * kC * 4 + tid * 16, eg + (long long)c * 2 * kC + tid * 4, true);
-    cp_commit();
-  };
-  load(p.nc - 1);
-  const int n0 = Sp::n0(w), pw = Sp::p0(w);
-  float D[Sp::NT][4];
-  load_state<N, PT>(D, f.dfin, state0, n0, pw, lane, p.st_bf16);
-  publish_state<N, PT>(D, sm + L::oD, n0, pw, lane);
-  constexpr int NH = PT / 16;
-  const int ch = w >> 2, rb = ch ? 3 - (w & 3) : (w & 3), c0 = ch * (PT / 2);
-  for (int c = p.nc - 1; c >= 0; --c) {
-    const int st = c & 1;
-    cp_wait<0>();
-    __syncthreads();
-    if (c > 0) load(c - 1);
-    const float* e = reinterpret_cast<const float*>(raw + L::oE + st * 2 * kC * 4);
-    const uint32_t Ks = sm + L::oK + st * L::kK, Qs = sm + L::oQ + st * L::kK, Ys = sm + L::oY + st * L::kV;
-    const uint32_t Ts = sm + L::oT + st * L::kT, As = sm + L::oA + st * L::kT, Ds = sm + L::oD;
-    __nv_bfloat16* Dg = static_cast<__nv_bfloat16*>(f.D) + (unit0 + c) * N * p.P + p0;
-#pragma unroll 4
-    for (int i = tid; i < N * UP; i += kChain)
-      *reinterpret_cast<uint4*>(Dg + (long long)(i / UP) * p.P + (i % UP) * 8) = lds128(Ds + tile_off<UP>(i / UP, i % UP));
-    for (int i = tid; i < kC * PT / 2; i += kChain) {
-      const int r = i / (PT / 2), col = 2 * (i % (PT / 2));
-      const float2 v = unpack2(lds32(Ys + elem_off<UP>(r, col)));
-      const float s = p.scale * e[r];
-      sts32(sm + L::oP + elem_off<UP>(r, col), pack2(s * v.x, s * v.y));
+  const int grp = h / p.hpg, bh = bi * p.H + h;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, NW);
     }
-    float x[NH][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < N; ks += 16) {
-      uint32_t a[4], b[4];
-      load_a<UN>(a, Ks, 16 * rb, ks, lane);
-#pragma unroll
-      for (int j = 0; j < NH; j += 2) {
-        load_bt<UP>(b, Ds, c0 + j * 8, ks, lane);
-        mma(x[j], a, b[0], b[1]);
-        mma(x[j + 1], a, b[2], b[3]);
-      }
-    }
-    const float o0 = e[kC + 16 * rb + g], o1 = e[kC + 16 * rb + g + 8];
-#pragma unroll
-    for (int j = 0; j < NH; ++j) {
-      x[j][0] = o0 == 0.f ? 0.f : x[j][0] * o0;
-      x[j][1] = o0 == 0.f ? 0.f : x[j][1] * o0;
-      x[j][2] = o1 == 0.f ? 0.f : x[j][2] * o1;
-      x[j][3] = o1 == 0.f ? 0.f : x[j][3] * o1;
-    }
-    for (int ks = rb; ks < 4; ++ks) {
-      uint32_t a[4], b[4];
-      load_at<8>(a, As, 16 * rb, 16 * ks, lane);
-#pragma unroll
-      for (int j = 0; j < NH; j += 2) {
-        load_bt<UP>(b, Ys, c0 + j * 8, 16 * ks, lane);
-        mma(x[j], a, b[0], b[1]);
-        mma(x[j + 1], a, b[2], b[3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NH; ++j)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-        sts32(sm + L::oR + elem_off<UP>(16 * rb + g + 8 * r, c0 + j * 8 + 2 * t), pack2(x[j][2 * r], x[j][2 * r + 1]));
-    __syncthreads();
-    // r = R + (T - I)^T R, the unit diagonal in fp32
-    for (int ks = rb; ks < 4; ++ks) {
-      uint32_t a[4], b[4];
-      load_at<8>(a, Ts, 16 * rb, 16 * ks, lane);
-#pragma unroll
-      for (int j = 0; j < NH; j += 2) {
-        load_bt<UP>(b, sm + L::oR, c0 + j * 8, 16 * ks, lane);
-        mma(x[j], a, b[0], b[1]);
-        mma(x[j + 1], a, b[2], b[3]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = 16 * rb + g + 8 * r;
-      const float s = -e[i];
-      const bool in = c * kC + i < p.L;
-      __nv_bfloat16* dst = dvg + (long long)(c * kC + i) * vs + c0 + 2 * t;
-#pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        if (in) *reinterpret_cast<uint32_t*>(dst + j * 8) = pack2(x[j][2 * r], x[j][2 * r + 1]);
-        sts32(sm + L::oU + elem_off<UP>(i, c0 + j * 8 + 2 * t), pack2(s * x[j][2 * r], s * x[j][2 * r + 1]));
-      }
-    }
-    __syncthreads();
-    const float last = e[kC - 1];
-#pragma unroll
-    for (int i = 0; i < Sp::NT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) D[i][j] = last == 0.f ? 0.f : D[i][j] * last;
-#pragma unroll
-    for (int ks = 0; ks < kC; ks += 16) {
-      uint32_t a[4], b[4], aq[4];
-      load_at<UN>(aq, Qs, n0, ks, lane);
-      load_at<UN>(a, Ks, n0, ks, lane);
-#pragma unroll
-      for (int j = 0; j < Sp::NT; j += 2) {
-        load_bt<UP>(b, sm + L::oP, pw + j * 8, ks, lane);
-        mma(D[j], aq, b[0], b[1]);
-        mma(D[j + 1], aq, b[2], b[3]);
-        load_bt<UP>(b, sm + L::oU, pw + j * 8, ks, lane);
-        mma(D[j], a, b[0], b[1]);
-        mma(D[j + 1], a, b[2], b[3]);
-      }
-    }
-    publish_state<N, PT>(D, Ds, n0, pw, lane);
+    mbar_fence_init();
   }
-  if (f.dinit) store_state<N, PT>(D, f.dinit, state0, n0, pw, lane, p.st_bf16);
+  __syncthreads();
+  bool ok = true;
+  if (w == NW) {
+    if (lane == 0) {
+      const float* e = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+      for (int k = 0; k < p.nc; ++k) {
+        const int c = p.nc - 1 - k, st = k & 1;
+        if (k >= 2) mbar_wait_flag(empty + st, ((k >> 1) - 1) & 1, ok);
+        unsigned char* d = raw + L::oSt + st * L::stage;
+        mbar_expect_tx(full + st, L::stage + kGateBytes);
+        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, full + st, 64 * j, grp, c * kC, bi);
+        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + L::kK + j * kTile, &m.q, full + st, 64 * j, grp, c * kC, bi);
+        d += 2 * L::kK;
+        tma_load_4d(d, &m.T, full + st, 0, 0, c, bh);
+        tma_load_4d(d + kTile, &m.A, full + st, 0, 0, c, bh);
+        tma_load_4d(d + 2 * kTile, &m.v, full + st, p0, h, c * kC, bi);
+        bulk_load(raw + L::oE + st * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, full + st);
+      }
+    }
+  } else {
+    const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
+    float D[N / 8][4];
+    load_state<N>(D, f.dfin, state0, lane, p.st_bf16);
+    for (int k0 = 0; k0 < p.nc; ++k0) {
+      const int c = p.nc - 1 - k0, st = k0 & 1;
+      const uint32_t Ks = sm + L::oSt + st * L::stage, Qs = Ks + L::kK, Ts = Qs + L::kK, As = Ts + kTile, Ys = As + kTile;
+      const uint32_t Dd = sm + L::oD + (2 * w + st) * N * 32, Rd = sm + L::oR + (2 * w + st) * 2048;
+      const float* e = reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) + 2 * t;
+      mbar_wait_flag(full + st, (k0 >> 1) & 1, ok);
+      float x[8][4] = {};
+#pragma unroll
+      for (int ks = 0; ks < N / 16; ++ks) {
+        uint32_t a[4], b[4];
+        as_left(a, D[2 * ks], D[2 * ks + 1]);
+        stsm4(frag_at(Dd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          ld_b(b, Ks, 8 * j, 16 * ks, lane);
+          mma(x[j], a, b[0], b[1]);
+          mma(x[j + 1], a, b[2], b[3]);
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        for (int j = 0; j < N / 64; ++j)
+          tma_store_4d(&m.S, raw + (Dd - sm) + j * 2048, 64 * j, p0 + 16 * w, c, bh);
+        bulk_commit();
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 o = *reinterpret_cast<const float2*>(e + kC + 8 * j);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          x[j][2 * r] = o.x != 0.f ? o.x * x[j][2 * r] : 0.f;
+          x[j][2 * r + 1] = o.y != 0.f ? o.y * x[j][2 * r + 1] : 0.f;
+        }
+      }
+      const float last = e[kC - 1 - 2 * t];
+#pragma unroll
+      for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) D[i][j] = last == 0.f ? 0.f : D[i][j] * last;
+      // R' += dY' A, and the part of D' that does not wait for r: (scale e dY)' Q
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t y[4], b[4];
+        if (NW == 4)
+          load_at<8>(y, Ys, 16 * w, 16 * i, lane);
+        else
+          load_at<4>(y, Ys, 16 * w, 16 * i, lane);
+#pragma unroll
+        for (int j = 0; j <= i; ++j) {
+          load_bt<8>(b, As, 16 * j, 16 * i, lane);
+          mma(x[2 * j], y, b[0], b[1]);
+          mma(x[2 * j + 1], y, b[2], b[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 ej = *reinterpret_cast<const float2*>(e + 16 * i + 8 * j);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 v = unpack2(y[2 * j + r]);
+            y[2 * j + r] = pack2(p.scale * ej.x * v.x, p.scale * ej.y * v.y);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < N / 8; n += 2) {
+          ld_bt(b, Qs, 8 * n, 16 * i, lane);
+          mma(D[n], y, b[0], b[1]);
+          mma(D[n + 1], y, b[2], b[3]);
+        }
+      }
+      uint32_t left[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) as_left(left[k], x[2 * k], x[2 * k + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) {
+          uint32_t b[4];
+          load_bt<8>(b, Ts, 16 * j, 16 * i, lane);
+          mma(x[2 * j], left[i], b[0], b[1]);
+          mma(x[2 * j + 1], left[i], b[2], b[3]);
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
+        stsm4t(token_at(Rd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_4d(&m.y, raw + (Rd - sm), p0 + 16 * w, h, c * kC, bi);
+        bulk_commit();
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 ej = *reinterpret_cast<const float2*>(e + 16 * k + 8 * j);
+          float(&xx)[4] = x[2 * k + j];
+          xx[0] *= -ej.x;
+          xx[1] *= -ej.y;
+          xx[2] *= -ej.x;
+          xx[3] *= -ej.y;
+        }
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int n = 0; n < N / 8; n += 2) {
+          uint32_t b[4];
+          ld_bt(b, Ks, 8 * n, 16 * k, lane);
+          mma(D[n], left[k], b[0], b[1]);
+          mma(D[n + 1], left[k], b[2], b[3]);
+        }
+      if (lane == 0) bulk_wait_read<2>();  // the last chunk's two tiles have been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + st);
+    }
+    if (f.dinit) store_state<N>(D, f.dinit, state0, lane, p.st_bf16);
+    if (lane == 0) bulk_wait_all();
+  }
+  if (!ok) atomicOr(f.status, kDevTimeout);
 }
 
-// 32 columns a CTA when 64 would leave SMs idle, else 64
-int chain_cols(const DeltaPlan& p) {
-  return p.P % 64 != 0 || (long long)p.b * p.H * (p.P / 64) * 2 <= device_sm_count() ? 32 : 64;
+// 64 columns a CTA, or 32 where 64 would leave half the SMs idle
+bool narrow(const DeltaPlan& p) { return (long long)p.b * p.H * (p.P / 64) * 2 <= device_sm_count(); }
+
+bool chain_maps(const DeltaPlan& p, const DeltaBufs& f, bool reverse, int nw, ChainMaps* m) {
+  const uint64_t N = p.N, P = p.P, H = p.H, G = p.G, Ln = p.L, b = p.b, nc = p.nc, e = 2;
+  auto tokens = [&](CUtensorMap* t, const void* base, uint64_t width, uint64_t heads, uint64_t stride, uint32_t cols,
+                    int swizzle) {
+    const uint64_t d[4] = {width, heads, Ln, b}, s[3] = {width * e, stride * e, Ln * stride * e};
+    const uint32_t box[4] = {cols, 1, (uint32_t)kC, 1};
+    return encode_tmap_bf16_4d(t, base, d, s, box, swizzle);
+  };
+  auto chunks = [&](CUtensorMap* t, const void* base, uint64_t width, uint64_t rows, uint32_t box_rows) {
+    const uint64_t d[4] = {width, rows, nc, b * H}, s[3] = {width * e, rows * width * e, nc * rows * width * e};
+    const uint32_t box[4] = {64, box_rows, 1, 1};
+    return encode_tmap_bf16_4d(t, base, d, s, box, 128);
+  };
+  const uint32_t cols = 16 * nw;
+  bool good = tokens(&m->q, f.q, N, G, p.qs, 64, 128) && tokens(&m->k, f.k, N, G, p.ks, 64, 128) &&
+              tokens(&m->v, reverse ? f.dy : f.v, P, H, reverse ? H * P : p.vs, cols, (int)cols * 2) &&
+              tokens(&m->y, reverse ? f.dv : f.y, P, H, H * P, 16, 0) && chunks(&m->T, f.T, 64, 64, 64) &&
+              chunks(&m->A, f.A, 64, 64, 64);
+  if (good && (reverse || f.S)) good = chunks(&m->S, reverse ? f.D : f.S, N, P, 16);
+  if (good && !reverse && f.S) good = chunks(&m->w, f.w, 64, P, 16);
+  return good;
 }
 
-template <int N, int PT>
-cudaError_t launch_fwd_t(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
-  auto kern = delta_chain_fwd_kernel<N, PT>;
-  constexpr int smem = FwdSmem<N, PT>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  set_kernel_name("delta_chain_fwd");
-  kern<<<(unsigned)((long long)(p.P / PT) * p.H * p.b), kAll, smem, s>>>(p, f);
+template <int N, int NW>
+cudaError_t launch_chain_t(const DeltaPlan& p, const DeltaBufs& f, bool reverse, cudaStream_t s) {
+  ChainMaps m = {};
+  if (!chain_maps(p, f, reverse, NW, &m)) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)((long long)(p.P / (16 * NW)) * p.H * p.b);
+  if (reverse) {
+    auto kern = delta_chain_bwd_kernel<N, NW>;
+    constexpr int smem = RevSmem<N, NW>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    set_kernel_name("delta_chain_bwd");
+    kern<<<grid, (NW + 1) * 32, smem, s>>>(p, f, m);
+  } else {
+    auto kern = delta_chain_fwd_kernel<N, NW>;
+    constexpr int smem = FwdSmem<N, NW>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    set_kernel_name("delta_chain_fwd");
+    kern<<<grid, (2 * NW + 1) * 32, smem, s>>>(p, f, m);
+  }
   return cudaGetLastError();
 }
 
-template <int N, int PT>
-cudaError_t launch_bwd_t(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
-  auto kern = delta_chain_bwd_kernel<N, PT>;
-  constexpr int smem = RevSmem<N, PT>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  set_kernel_name("delta_chain_bwd");
-  kern<<<(unsigned)((long long)(p.P / PT) * p.H * p.b), kChain, smem, s>>>(p, f);
-  return cudaGetLastError();
+cudaError_t launch_chain(const DeltaPlan& p, const DeltaBufs& f, bool reverse, cudaStream_t s) {
+  if (narrow(p)) return p.N == 128 ? launch_chain_t<128, 2>(p, f, reverse, s) : launch_chain_t<64, 2>(p, f, reverse, s);
+  return p.N == 128 ? launch_chain_t<128, 4>(p, f, reverse, s) : launch_chain_t<64, 4>(p, f, reverse, s);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_chain_bwd(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
-  if (chain_cols(p) == 64) return p.N == 128 ? launch_bwd_t<128, 64>(p, f, s) : launch_bwd_t<64, 64>(p, f, s);
-  return p.N == 128 ? launch_bwd_t<128, 32>(p, f, s) : launch_bwd_t<64, 32>(p, f, s);
-}
-
 cudaError_t launch_delta_chain_fwd(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
-  if (chain_cols(p) == 64) return p.N == 128 ? launch_fwd_t<128, 64>(p, f, s) : launch_fwd_t<64, 64>(p, f, s);
-  return p.N == 128 ? launch_fwd_t<128, 32>(p, f, s) : launch_fwd_t<64, 32>(p, f, s);
+  return launch_chain(p, f, false, s);
+}
+cudaError_t launch_delta_chain_bwd(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
+  return launch_chain(p, f, true, s);
 }
 
 }  // namespace ssd

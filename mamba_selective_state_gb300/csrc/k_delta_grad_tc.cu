@@ -2,400 +2,455 @@
 // tensor cores, chunk by chunk: the formulas at the head of
 // k_delta_grad_simt.cu, with bf16 S0, D1, w and r = dv from the chains.
 //
-// One CTA takes a chunk of a group and walks its heads, so that q k^T, k k^T
-// and the sums over heads stay on chip: dq and dk accumulate in registers, and
-// of the pairs' part only Z and M are summed per head, their products with k
-// and q taken once per group.  Per head the tensor cores form dY S0^T, r S0^T,
-// w D1^T (64 x dstate) and dY w^T, r w^T (64 x 64) from a double-buffered
-// stage.  The pairs' contributions to dgam are formed once in fp32 and summed
-// by rows and by columns, so that what cancels in their running difference
-// cancels exactly.
+// One CTA takes a chunk of a group and walks its heads.  Per head, with the
+// tokens of dY and of r as the 128 rows of one left operand,
+//
+//   [dY ; r] [S0 | w']  ->  dY S0, r S0 (64 x dstate) and dY w', r w' (64 x 64)
+//   [.. ; w]  D1        ->  w D1
+//
+// come from tcgen05 products into tensor memory (S0, D1 and w' are stored with
+// headdim as rows, as the chains write them, and enter as MN-major operands).
+// Sixteen warps read them back: a thread owns one token's row -- of dY and dq
+// in the lower 64 lanes, of r, w and dk in the upper -- and a quarter of the
+// columns, so the dot products with q and k and the sums over heads stay in
+// its registers.  q k^T and k k^T do not depend on the head, and the pairs'
+// part of dq and dk is summed over the heads before its products with k and
+// q: both are one more product of 128 rows per group.  The pairs'
+// contributions to dgam are formed once in fp32 and summed by rows and by
+// columns, so that what cancels in their running difference cancels exactly.
 #include "delta_internal.cuh"
 #include "mma_common.cuh"
+#include "tma_host.h"
 
 namespace ssd {
 namespace {
 
 using namespace mm;
+using namespace tc;
 
 constexpr int kC = kDeltaChunk;
-constexpr int kThreads = 256;
-constexpr int kPs = 72;     // row stride of the fp32 q k^T and k k^T
-constexpr int kGate = 8;    // heads whose gates are prepared together, one a warp
+constexpr int kWarps = 16;                    // epilogue warps
+constexpr int kEpi = kWarps * 32;
+constexpr int kThreads = kEpi + 32;           // and the control warp
+constexpr uint32_t kTile = 8192;              // [64][64] bf16, 128-byte swizzle
+constexpr int kGate = kGateRows * kC * 4;
 
-template <int N, int PC>
-struct GradSmem {
-  static constexpr int kK = kC * N * 2, kS = N * PC * 2, kV = kC * PC * 2;
-  static constexpr int stage = 2 * kS + 3 * kV;  // S0, D1, w, r, dY
-  static constexpr int pair = kC * kPs * 4;
-  static constexpr int oK = 0, oQ = oK + kK, oSt = oQ + kK, oQK = oSt + 2 * stage, oKK = oQK + pair,
-                       oGate = oKK + pair,                       // gam, beta, e, o of kGate heads
-                       oSeg = oGate + kGate * 4 * kC * 4, oCol = oSeg + kGate * kC * 4,  // [4][64]
-                       oRow = oCol + 4 * kC * 4, oOut = oRow + 2 * kC * 4, oDiag = oOut + 2 * kC * 4, oRed = oDiag + kC * 4,
-                       bytes = oRed + 8 * 4;
-  static_assert(2 * stage >= 2 * kC * kC * 2, "Z and M reuse the stage");
+struct GradMaps {
+  CUtensorMap q, k, S, D, w, dv, dy;
 };
 
-template <int N, int PC>
-__global__ void __launch_bounds__(kThreads, 1) delta_grad_tc_kernel(DeltaPlan p, DeltaBufs f) {
-  using L = GradSmem<N, PC>;
-  constexpr int UN = N / 8, UP = PC / 8;
-  constexpr int NT = N / 16;  // 8-column tiles of half of dstate
-  extern __shared__ __align__(128) unsigned char raw[];
+template <int N>
+struct GradSmem {
+  static constexpr int NB = N / 64;
+  // per head and 64 columns of headdim: dY, r, S0, w, D1
+  static constexpr int stage = (2 + 2 * NB + 1) * (int)kTile;
+  static constexpr int kStages = N == 128 ? 3 : 4;
+  // q and k: for each 64 columns of dstate the tile of q above that of k
+  static constexpr int oQK = 0, oSt = NB * 2 * (int)kTile, oGate = oSt + kStages * stage,  // four gate records
+                       oCol = oGate + 4 * kGate,       // [2][4][64] column sums by lane quarter
+                       oRow = oCol + 2 * 4 * kC * 4,   // [2][4][128] row sums by column quarter
+                       oOut = oRow + 2 * 4 * 128 * 4,  // [2][4][64] k.(D1 w)
+                       oDiag = oOut + 2 * 4 * kC * 4, oRed = oDiag + 2 * kC * 4, oBar = oRed + 2 * kWarps * 4,
+                       bytes = oBar + 256 + 1024;
+  static_assert(kStages * stage >= 4 * (int)kTile, "the pairs' operand reuses the ring");
+};
+
+// Sum over the warp's lanes of v[0..15]: lane l returns the total of v[l >> 1].
+__device__ __forceinline__ float sum16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int half = 8; half >= 1; half >>= 1) {
+    const bool up = lane & (2 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half];
+      const float keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * half);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    delta_grad_tc_kernel(DeltaPlan p, DeltaBufs f, const __grid_constant__ GradMaps m) {
+  using L = GradSmem<N>;
+  constexpr int NB = L::NB, NC = N / 4;        // columns of dstate per thread
+  constexpr uint32_t kX = N + 64;              // columns of [dY ; r] [S0 | w']
+  constexpr uint32_t kX3 = 2 * kX;             // tensor-memory column of w D1
+  constexpr uint32_t kCols = 512;
+  extern __shared__ unsigned char raw_[];
+  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
   const uint32_t sm = smem_u32(raw);
-  float* qk_s = reinterpret_cast<float*>(raw + L::oQK);
-  float* kk_s = reinterpret_cast<float*>(raw + L::oKK);
-  float* colp = reinterpret_cast<float*>(raw + L::oCol);
-  float* rowp = reinterpret_cast<float*>(raw + L::oRow);
-  float* outp = reinterpret_cast<float*>(raw + L::oOut);
-  float* diag = reinterpret_cast<float*>(raw + L::oDiag);
-  float* red = reinterpret_cast<float*>(raw + L::oRed);
-  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3, w = tid >> 5;
-  const int rb = w & 3, ch = w >> 2, i0 = 16 * rb + g;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + L::oBar);
+  uint64_t *s_full = bars, *s_free = bars + 4, *g_full = bars + 8, *g_free = bars + 12, *x_full = bars + 16,
+           *x_free = bars + 18, *x3_free = bars + 20, *qk_full = bars + 21, *qk_done = bars + 22, *z_done = bars + 23;
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int c = (int)(blockIdx.x % p.nc);
   const int grp = (int)((blockIdx.x / p.nc) % p.G);
   const int bi = (int)(blockIdx.x / ((long long)p.nc * p.G));
   const int t0 = c * kC, n = min(kC, p.L - t0);
   const long long tok0 = (long long)bi * p.L + t0;
-  const int npc = p.P / PC, steps = p.hpg * npc;
-  const long long vs = (long long)p.H * p.P;
+  const int npc = p.P / 64, h0 = grp * p.hpg;
 
-  auto load = [&](int s) {
-    const int h = grp * p.hpg + s / npc, p0 = (s % npc) * PC;
-    const uint32_t st = sm + L::oSt + (s & 1) * L::stage;
-    const long long unit = ((long long)bi * p.H + h) * p.nc + c;
-    cp_tile<N, UP>(st, static_cast<const __nv_bfloat16*>(f.S) + unit * N * p.P + p0, p.P, N, tid, kThreads);
-    cp_tile<N, UP>(st + L::kS, static_cast<const __nv_bfloat16*>(f.D) + unit * N * p.P + p0, p.P, N, tid, kThreads);
-    cp_tile<kC, UP>(st + 2 * L::kS, static_cast<const __nv_bfloat16*>(f.w) + unit * kC * p.P + p0, p.P, kC, tid, kThreads);
-    const long long o = tok0 * vs + (long long)h * p.P + p0;
-    cp_tile<kC, UP>(st + 2 * L::kS + L::kV, static_cast<const __nv_bfloat16*>(f.dv) + o, vs, n, tid, kThreads);
-    cp_tile<kC, UP>(st + 2 * L::kS + 2 * L::kV, static_cast<const __nv_bfloat16*>(f.dy) + o, vs, n, tid, kThreads);
-    cp_commit();
-  };
-  // gam, beta, e, o and the sequence starts of head hh, by one warp
-  auto gates = [&](int hh) {
-    float* ga = reinterpret_cast<float*>(raw + L::oGate) + (hh % kGate) * 4 * kC;
-    int* sg = reinterpret_cast<int*>(raw + L::oSeg) + (hh % kGate) * kC;
-    const int h = grp * p.hpg + hh;
-    float gv[2], be[2];
-    int rs[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 2 * lane + j;
-      gv[j] = be[j] = 0.f;
-      rs[j] = 0;
-      if (i < n) {
-        const long long o = (tok0 + i) * p.H + h;
-        gv[j] = to_f(static_cast<const __nv_bfloat16*>(f.g)[o]);
-        be[j] = to_f(static_cast<const __nv_bfloat16*>(f.beta)[o]);
-        rs[j] = (f.seq != nullptr && t0 + i > 0 && f.seq[tok0 + i] != f.seq[tok0 + i - 1]) || gv[j] < kForget;
-        if (rs[j]) gv[j] = 0.f;
-      }
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, kWarps + 1);
     }
-    float sum = gv[0] + gv[1];
-    int cnt = rs[0] + rs[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float us = __shfl_up_sync(0xffffffffu, sum, o);
-      const int uc = __shfl_up_sync(0xffffffffu, cnt, o);
-      if (lane >= o) {
-        sum += us;
-        cnt += uc;
-      }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(g_full + i, 1);
+      mbar_init(g_free + i, kWarps);
     }
-    const float last = __shfl_sync(0xffffffffu, sum, 31);
-    const int slast = __shfl_sync(0xffffffffu, cnt, 31);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 2 * lane + j;
-      const float gam = j ? sum : sum - gv[1];
-      const int s = j ? cnt : cnt - rs[1];
-      ga[i] = gam;
-      ga[kC + i] = be[j];
-      ga[2 * kC + i] = s == 0 ? expf(gam) : 0.f;
-      ga[3 * kC + i] = s == slast ? expf(last - gam) : 0.f;
-      sg[i] = s;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(x_full + i, 1);
+      mbar_init(x_free + i, kWarps);
     }
-  };
-
-  cp_tile<kC, UN>(sm + L::oK, static_cast<const __nv_bfloat16*>(f.k) + tok0 * p.ks + (long long)grp * N, p.ks, n, tid, kThreads);
-  cp_tile<kC, UN>(sm + L::oQ, static_cast<const __nv_bfloat16*>(f.q) + tok0 * p.qs + (long long)grp * N, p.qs, n, tid, kThreads);
-  cp_commit();
-  load(0);
-  if (w < p.hpg) gates(w);
-  cp_wait<1>();
-  __syncthreads();
-  {
-    float a1[4][4] = {}, a2[4][4] = {};
-#pragma unroll 2
-    for (int ks = 0; ks < N; ks += 16) {
-      uint32_t ka[4], qa[4], b[4];
-      load_a<UN>(ka, sm + L::oK, 16 * rb, ks, lane);
-      load_a<UN>(qa, sm + L::oQ, 16 * rb, ks, lane);
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        load_b<UN>(b, sm + L::oK, 32 * ch + j * 8, ks, lane);
-        mma(a1[j], qa, b[0], b[1]);
-        mma(a1[j + 1], qa, b[2], b[3]);
-        mma(a2[j], ka, b[0], b[1]);
-        mma(a2[j + 1], ka, b[2], b[3]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int o = (i0 + 8 * r) * kPs + 32 * ch + j * 8 + 2 * t;
-        *reinterpret_cast<float2*>(&qk_s[o]) = make_float2(a1[j][2 * r], a1[j][2 * r + 1]);
-        *reinterpret_cast<float2*>(&kk_s[o]) = make_float2(a2[j][2 * r], a2[j][2 * r + 1]);
-      }
+    mbar_init(x3_free, kWarps);
+    mbar_init(qk_full, 1);
+    mbar_init(qk_done, 1);
+    mbar_init(z_done, 1);
+    mbar_fence_init();
   }
-  float dq[NT][4] = {}, dk[NT][4] = {}, Z[4][4] = {}, M[4][4] = {};
-  float m1[4][4], m2[4][4], row[2], out[2], sd;
-  for (int s = 0; s < steps; ++s) {
-    const int hh = s / npc, pc = s % npc;
-    cp_wait<0>();
-    __syncthreads();
-    if (s + 1 < steps) load(s + 1);
-    const float* ga = reinterpret_cast<const float*>(raw + L::oGate) + (hh % kGate) * 4 * kC;
-    const int* sg = reinterpret_cast<const int*>(raw + L::oSeg) + (hh % kGate) * kC;
-    const uint32_t Ss = sm + L::oSt + (s & 1) * L::stage, Ds = Ss + L::kS, Ws = Ss + 2 * L::kS, Rs = Ws + L::kV,
-                   Ys = Rs + L::kV;
-    if (pc == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) m1[j][x] = m2[j][x] = 0.f;
-      row[0] = row[1] = out[0] = out[1] = sd = 0.f;
-    }
-    for (int i = tid; i < N * UP; i += kThreads) {
-      const uint4 a = lds128(Ss + i * 16), b = lds128(Ds + i * 16);
-      const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 u = unpack2(av[j]), v = unpack2(bv[j]);
-        sd += u.x * v.x + u.y * v.y;
-      }
-    }
-    // which: 0 dY S0^T, 1 r S0^T, 2 w D1^T; the first two also against w
-#pragma unroll
-    for (int which = 0; which < 3; ++which) {
-      const uint32_t As = which == 0 ? Ys : which == 1 ? Rs : Ws, Bs = which == 2 ? Ds : Ss;
-      float x[NT][4] = {};
-#pragma unroll
-      for (int ks = 0; ks < PC; ks += 16) {
-        uint32_t a[4], b[4];
-        load_a<UP>(a, As, 16 * rb, ks, lane);
-#pragma unroll
-        for (int j = 0; j < NT; j += 2) {
-          load_b<UP>(b, Bs, ch * (N / 2) + j * 8, ks, lane);
-          mma(x[j], a, b[0], b[1]);
-          mma(x[j + 1], a, b[2], b[3]);
+  if (w == kWarps) tmem_alloc(tm_slot, kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tm_slot;
+  bool ok = true;
+
+  if (w == kWarps) {
+    if (lane == 0) {
+      const int steps = p.hpg * npc;
+      auto load = [&](int s) {
+        const int hh = s / npc, pc = s % npc, st = s % L::kStages, use = s / L::kStages;
+        const int h = h0 + hh, bh = bi * p.H + h;
+        if (pc == 0) {
+          // four records: this runs up to three heads ahead of the products
+          const int gb = hh & 3;
+          if (hh >= 4) mbar_wait_flag(g_free + gb, ((hh >> 2) - 1) & 1, ok);
+          mbar_expect_tx(g_full + gb, kGate);
+          bulk_load(raw + L::oGate + gb * kGate,
+                    static_cast<const float*>(f.e) + ((long long)bh * p.nc + c) * kGateRows * kC, kGate, g_full + gb);
         }
-        if (which < 2) {
+        if (use > 0) mbar_wait_flag(s_free + st, (use - 1) & 1, ok);
+        unsigned char* d = raw + L::oSt + st * L::stage;
+        mbar_expect_tx(s_full + st, L::stage);
+        tma_load_4d(d, &m.dy, s_full + st, 64 * pc, h, t0, bi);
+        tma_load_4d(d + kTile, &m.dv, s_full + st, 64 * pc, h, t0, bi);
+        for (int j = 0; j < NB; ++j) tma_load_4d(d + (2 + j) * kTile, &m.S, s_full + st, 64 * j, 64 * pc, c, bh);
+        tma_load_4d(d + (2 + NB) * kTile, &m.w, s_full + st, 0, 64 * pc, c, bh);
+        for (int j = 0; j < NB; ++j) tma_load_4d(d + (3 + NB + j) * kTile, &m.D, s_full + st, 64 * j, 64 * pc, c, bh);
+      };
+      mbar_expect_tx(qk_full, NB * 2 * kTile);
+      for (int j = 0; j < NB; ++j) {
+        tma_load_4d(raw + L::oQK + 2 * j * kTile, &m.q, qk_full, 64 * j, grp, t0, bi);
+        tma_load_4d(raw + L::oQK + (2 * j + 1) * kTile, &m.k, qk_full, 64 * j, grp, t0, bi);
+      }
+      int loaded = 0;
+      for (; loaded < L::kStages - 1 && loaded < steps; ++loaded) load(loaded);
+      // [q ; k] k^T into the first columns
+      mbar_wait_flag(qk_full, 0, ok);
+      tc_fence_after();
+      for (int ks = 0; ks < N / 16; ++ks) {
+        const uint32_t a = sm + L::oQK + (ks >> 2) * 2 * kTile + (ks & 3) * 32;
+        mma_bf16(tm, smem_desc(a, 16, 1024, kSwz128), smem_desc(a + kTile, 16, 1024, kSwz128),
+                 idesc_bf16(128, 64, 0, 0), ks > 0);
+      }
+      mma_commit(qk_done);
+      for (int s = 0; s < steps; ++s) {
+        const int hh = s / npc, pc = s % npc, st = s % L::kStages, use = s / L::kStages, buf = hh & 1;
+        if (loaded < steps) load(loaded++);
+        mbar_wait_flag(s_full + st, use & 1, ok);
+        if (pc == 0) {
+          // the buffer's last head has been read (the first head's: q k^T)
+          if (hh >= 2) mbar_wait_flag(x_free + buf, ((hh >> 1) - 1) & 1, ok);
+          if (hh == 0) mbar_wait_flag(z_done, 0, ok);
+        }
+        tc_fence_after();
+        const uint32_t base = sm + L::oSt + st * L::stage, S0 = base + 2 * kTile, D1 = base + (3 + NB) * kTile;
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16(tm + buf * kX, smem_desc(base + ks * 32, 16, 1024, kSwz128),
+                   smem_desc(S0 + ks * 2048, kTile, 1024, kSwz128), idesc_bf16(128, N + 64, 0, 1), pc > 0 || ks > 0);
+        if (pc == 0 && hh >= 1) {
+          mbar_wait_flag(x3_free, (hh - 1) & 1, ok);
+          tc_fence_after();
+        }
+        // rows 64.. are w: the tile before it only fills the product's 128 rows
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16(tm + kX3, smem_desc(S0 + (NB - 1) * kTile + ks * 2048, kTile, 1024, kSwz128),
+                   smem_desc(D1 + ks * 2048, kTile, 1024, kSwz128), idesc_bf16(128, N, 1, 1), pc > 0 || ks > 0);
+        mma_commit(s_free + st);
+        if (pc == npc - 1) mma_commit(x_full + buf);
+      }
+      // the pairs' part, once its operand is in place (the epilogue's arrivals on qk_full)
+      mbar_wait_flag(qk_full, 1, ok);
+      tc_fence_after();
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t a = sm + L::oSt + (ks >> 2) * 2 * kTile + (ks & 3) * 32;
+        mma_bf16(tm, smem_desc(a, 16, 1024, kSwz128), smem_desc(sm + L::oQK + ks * 2048, 2 * kTile, 1024, kSwz128),
+                 idesc_bf16(128, N, 0, 1), ks > 0);
+      }
+      mma_commit(qk_done);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = w & 3, cq = w >> 2;          // tensor-memory lanes, columns
+    const int row = 32 * quarter + lane, i = row & 63;
+    const bool lower = quarter < 2;                  // dY, dq, q k^T; else r, w, dk, k k^T
+    const uint32_t tlane = tmem_addr(tm, 32 * quarter, 0);
+    float acc[NC], pair[16], qk[16];
+    uint32_t own[NC / 2];                            // this row of q or k
+    {
+      mbar_wait_flag(qk_full, 0, ok);
+      // element (i, col): tile col / 64, q's or k's half of it
+      const uint32_t base = sm + L::oQK + ((cq * NC) >> 6) * 2 * kTile + (lower ? 0 : kTile);
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            load_b<UP>(b, Ws, 32 * ch + j * 8, ks, lane);
-            if (which == 0) {
-              mma(m1[j], a, b[0], b[1]);
-              mma(m1[j + 1], a, b[2], b[3]);
-            } else {
-              mma(m2[j], a, b[0], b[1]);
-              mma(m2[j + 1], a, b[2], b[3]);
-            }
+      for (int u = 0; u < NC / 8; ++u) {
+        const uint4 v = lds128(base + tile_off<8>(i, (((cq * NC) & 63) >> 3) + u));
+        own[4 * u] = v.x;
+        own[4 * u + 1] = v.y;
+        own[4 * u + 2] = v.z;
+        own[4 * u + 3] = v.w;
+      }
+      mbar_wait_flag(qk_done, 0, ok);
+      tc_fence_after();
+      tmem_ld16(tlane + cq * 16, qk);
+      tc_fence_before();
+      // every warp has read q k^T before the first head's product takes its place
+      bar_sync(1, kEpi);
+      if (tid == 0) mbar_arrive(z_done);
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) acc[j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) pair[j] = 0.f;
+    for (int hh = 0; hh < p.hpg; ++hh) {
+      const int buf = hh & 1;
+      const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
+      const int* sg = reinterpret_cast<const int*>(ga + 5 * kC);
+      float* colp = reinterpret_cast<float*>(raw + L::oCol) + buf * 4 * kC;
+      float* rowp = reinterpret_cast<float*>(raw + L::oRow) + buf * 4 * 128;
+      float* outp = reinterpret_cast<float*>(raw + L::oOut) + buf * 4 * kC;
+      float* diag = reinterpret_cast<float*>(raw + L::oDiag) + buf * kC;
+      float* red = reinterpret_cast<float*>(raw + L::oRed) + buf * kWarps;
+      mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
+      // <S0, D1>, a few elements a thread
+      float sd = 0.f;
+      for (int pc = 0; pc < npc; ++pc) {
+        const int s = hh * npc + pc, st = s % L::kStages;
+        mbar_wait_flag(s_full + st, (s / L::kStages) & 1, ok);
+        const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 1) * kTile;
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          const uint4 a = lds128(S0 + (tid + u * kEpi) * 16), b = lds128(D1 + (tid + u * kEpi) * 16);
+          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 y = unpack2(av[x]), z = unpack2(bv[x]);
+            sd += y.x * z.x + y.y * z.y;
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free + st);
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int i = i0 + 8 * r;
-        const float fac = which == 0 ? p.scale * ga[2 * kC + i] : which == 1 ? -ga[2 * kC + i] : ga[3 * kC + i];
-        const float be = ga[kC + i];
+      for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+      if (lane == 0) red[w] = sd;
+      const float ei = ga[i], be = ga[3 * kC + i], oi = ga[4 * kC + i], gi = ga[2 * kC + i];
+      const int si = sg[i];
+      mbar_wait_flag(x_full + buf, (hh >> 1) & 1, ok);
+      tc_fence_after();
+      if (!lower) {  // w D1: dk_i += o_i beta_i D1 w_i
+        const float fac = oi * be;
         float dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int col = ch * (N / 2) + j * 8 + 2 * t;
-          const float2 v = unpack2(lds32(sm + (which == 0 ? L::oQ : L::oK) + elem_off<UN>(i, col)));
-          const float x0 = fac == 0.f ? 0.f : fac * x[j][2 * r], x1 = fac == 0.f ? 0.f : fac * x[j][2 * r + 1];
-          dot += v.x * x0 + v.y * x1;
-          if (which == 0) {
-            dq[j][2 * r] += x0;
-            dq[j][2 * r + 1] += x1;
-          } else {
-            dk[j][2 * r] += which == 2 ? be * x0 : x0;
-            dk[j][2 * r + 1] += which == 2 ? be * x1 : x1;
+        for (int j0 = 0; j0 < NC; j0 += 16) {
+          float x[16];
+          tmem_ld16(tlane + kX3 + cq * NC + j0, x);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 v = unpack2(own[(j0 + j) / 2]);
+            const float x0 = oi == 0.f ? 0.f : x[j], x1 = oi == 0.f ? 0.f : x[j + 1];
+            acc[j0 + j] += fac * x0;
+            acc[j0 + j + 1] += fac * x1;
+            dot += v.x * x0 + v.y * x1;
           }
         }
-        if (which == 2) out[r] += dot; else row[r] += dot;
+        outp[cq * kC + i] = oi * dot;
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x3_free);
+      // dY S0 or r S0: dq_i += scale e_i ..., dk_i -= e_i ...
+      const float fac = lower ? p.scale * ei : -ei;
+      float rsum = 0.f;
+#pragma unroll
+      for (int j0 = 0; j0 < NC; j0 += 16) {
+        float x[16];
+        tmem_ld16(tlane + buf * kX + cq * NC + j0, x);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 v = unpack2(own[(j0 + j) / 2]);
+          const float x0 = ei == 0.f ? 0.f : x[j], x1 = ei == 0.f ? 0.f : x[j + 1];
+          acc[j0 + j] += fac * x0;
+          acc[j0 + j + 1] += fac * x1;
+          rsum += v.x * x0 + v.y * x1;
+        }
+      }
+      rsum *= fac;
+      // the pairs (i, 16 cq + j)
+      float x[16];
+      tmem_ld16(tlane + buf * kX + N + cq * 16, x);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_free + buf);
+      const float sign = lower ? p.scale : -1.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int jj = 16 * cq + j;
+        const float bj = ga[3 * kC + jj];
+        const bool in = jj <= i && sg[jj] == si && (lower || jj < i);
+        const float z = in ? sign * __expf(gi - ga[2 * kC + jj]) * x[j] : 0.f;
+        const float both = z * qk[j];
+        pair[j] += bj * z;
+        if (jj == i) {
+          if (lower) diag[i] = both;  // a token's own pair does not depend on the decays
+          x[j] = 0.f;
+        } else {
+          rsum += bj * both;
+          x[j] = both;
+        }
+      }
+      rowp[cq * 128 + row] = rsum;
+      const float cs = sum16(x, lane);
+      if ((lane & 1) == 0) colp[quarter * kC + 16 * cq + (lane >> 1)] = cs;
+      bar_sync(1, kEpi);
+      if (w == (hh & (kWarps - 1))) {
+        // this head's dbeta, and dg as the reverse cumulative sum of dgam
+        float d[2], all = 0.f, sdot = 0.f;
+#pragma unroll
+        for (int x2 = 0; x2 < kWarps; ++x2) sdot += red[x2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int a = 2 * lane + j;
+          const float o = (outp[a] + outp[kC + a]) + (outp[2 * kC + a] + outp[3 * kC + a]);
+          const float cj = (colp[a] + colp[kC + a]) + (colp[2 * kC + a] + colp[3 * kC + a]);
+          float r = 0.f;
+#pragma unroll
+          for (int x2 = 0; x2 < 4; ++x2) r += rowp[x2 * 128 + a] + rowp[x2 * 128 + 64 + a];
+          const float b2 = ga[3 * kC + a];
+          d[j] = r - b2 * (cj + o);
+          all += b2 * o;
+          if (a < n)
+            static_cast<__nv_bfloat16*>(f.dbeta)[(tok0 + a) * p.H + h0 + hh] = __float2bfloat16_rn(cj + diag[a] + o);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const float el = ga[kC - 1];
+        if (lane == 31) d[1] += all + (el == 0.f ? 0.f : el * sdot);
+        float sum = d[0] + d[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float dn = __shfl_down_sync(0xffffffffu, sum, o);
+          if (lane + o < 32) sum += dn;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int a = 2 * lane + j;
+          const bool starts = a > 0 ? sg[a] != sg[a - 1] : sg[0] != 0;
+          const float v = starts ? 0.f : j ? sum - d[0] : sum;
+          if (a < n) static_cast<__nv_bfloat16*>(f.dg)[(tok0 + a) * p.H + h0 + hh] = __float2bfloat16_rn(v);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(g_free + (hh & 3));
     }
-    if (pc + 1 < npc) continue;
-    // the pairs of this head
-    float col[4][2] = {};
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = i0 + 8 * r;
-      const float gi = ga[i];
-      const int si = sg[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int jj = 32 * ch + j * 8 + 2 * t;
-        const float2 qk = *reinterpret_cast<const float2*>(&qk_s[i * kPs + jj]);
-        const float2 kk = *reinterpret_cast<const float2*>(&kk_s[i * kPs + jj]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (jj + x <= i && sg[jj + x] == si) {
-            const float E = __expf(gi - ga[jj + x]), be = ga[kC + jj + x];
-            const float z = p.scale * E * m1[j][2 * r + x];
-            const float m = jj + x < i ? -E * m2[j][2 * r + x] : 0.f;
-            const float both = z * (x ? qk.y : qk.x) + m * (x ? kk.y : kk.x);
-            if (jj + x < i) {
-              col[j][x] += both;
-              row[r] += be * both;
-            } else {
-              diag[i] = both;  // a token's own pair does not depend on the decays
-            }
-            Z[j][2 * r + x] += be * z;
-            M[j][2 * r + x] += be * m;
-          }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float v = col[j][x];
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 16);
-        if (g == 0) colp[rb * kC + 32 * ch + j * 8 + 2 * t + x] = v;
-      }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float v = row[r], o = out[r];
-      v += __shfl_xor_sync(0xffffffffu, v, 1);
-      v += __shfl_xor_sync(0xffffffffu, v, 2);
-      o += __shfl_xor_sync(0xffffffffu, o, 1);
-      o += __shfl_xor_sync(0xffffffffu, o, 2);
-      if (t == 0) {
-        rowp[ch * kC + i0 + 8 * r] = v;
-        outp[ch * kC + i0 + 8 * r] = o;
-      }
-    }
-    float v = sd;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) red[w] = v;
-    __syncthreads();
-    if (w == (hh & 7)) {
-      // this head's dbeta, and dg as the reverse cumulative sum of dgam
-      float d[2], all = 0.f, sdot = 0.f;
-      for (int i = 0; i < 8; ++i) sdot += red[i];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * lane + j;
-        const float o = outp[i] + outp[kC + i], be = ga[kC + i];
-        const float cs = (colp[i] + colp[kC + i]) + (colp[2 * kC + i] + colp[3 * kC + i]);
-        d[j] = rowp[i] + rowp[kC + i] - be * (cs + o);
-        all += be * o;
-        if (i < n) static_cast<__nv_bfloat16*>(f.dbeta)[(tok0 + i) * p.H + grp * p.hpg + hh] = __float2bfloat16_rn(cs + diag[i] + o);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-      const float el = ga[2 * kC + kC - 1];
-      if (lane == 31) d[1] += all + (el == 0.f ? 0.f : el * sdot);
-      float sum = d[0] + d[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float dn = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += dn;
-      }
-      // `sum` runs from this lane's first token to the end
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int i = 2 * lane + j;
-        const bool starts = i > 0 ? sg[i] != sg[i - 1] : sg[0] != 0;
-        const float v2 = starts ? 0.f : j ? sum - d[0] : sum;
-        if (i < n) static_cast<__nv_bfloat16*>(f.dg)[(tok0 + i) * p.H + grp * p.hpg + hh] = __float2bfloat16_rn(v2);
-      }
-    }
-    if ((hh + 1) % kGate == 0 && hh + 1 < p.hpg) {
-      __syncthreads();  // the gates of these heads have been read
-      if (hh + 1 + w < p.hpg) gates(hh + 1 + w);
-    }
-  }
-  // the pairs' part of dq and dk, once for all heads
-  __syncthreads();
-  const uint32_t Zs = sm + L::oSt, Ms = Zs + kC * kC * 2;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint32_t o = elem_off<8>(i0 + 8 * r, 32 * ch + j * 8 + 2 * t);
-      sts32(Zs + o, pack2(Z[j][2 * r], Z[j][2 * r + 1]));
-      sts32(Ms + o, pack2(M[j][2 * r], M[j][2 * r + 1]));
-    }
-  __syncthreads();
-#pragma unroll
-  for (int ks = 0; ks < kC; ks += 16) {
-    uint32_t a[4], b[4], bq[4], am[4], amt[4], azt[4];
-    const bool lower = ks <= 16 * rb, upper = ks >= 16 * rb;
+    // The pairs' part for all heads: rows of [0 | Z ; Z^T | M + M^T] against
+    // [q ; k], Z (i, j) and M (i, j) summed over the heads.  All of the ring's
+    // products are done: the last head's x_full followed them.
+    bar_sync(1, kEpi);
+    const uint32_t Zb = sm + L::oSt;  // 128 rows x 64 columns of q's tokens, then of k's
     if (lower) {
-      load_a<8>(a, Zs, 16 * rb, ks, lane);
-      load_a<8>(am, Ms, 16 * rb, ks, lane);
-    }
-    if (upper) {
-      load_at<8>(azt, Zs, 16 * rb, ks, lane);
-      load_at<8>(amt, Ms, 16 * rb, ks, lane);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(Zb + tile_off<8>(i, 2 * cq + u)), "r"(0), "r"(0),
+                     "r"(0), "r"(0)
+                     : "memory");
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(Zb + 2 * kTile + tile_off<8>(i, 2 * cq + u)),
+                     "r"(pack2(pair[8 * u], pair[8 * u + 1])), "r"(pack2(pair[8 * u + 2], pair[8 * u + 3])),
+                     "r"(pack2(pair[8 * u + 4], pair[8 * u + 5])), "r"(pack2(pair[8 * u + 6], pair[8 * u + 7]))
+                     : "memory");
     }
 #pragma unroll
-    for (int j = 0; j < NT; j += 2) {
-      load_bt<UN>(b, sm + L::oK, ch * (N / 2) + j * 8, ks, lane);
-      if (lower) {
-        mma(dq[j], a, b[0], b[1]);
-        mma(dq[j + 1], a, b[2], b[3]);
-        mma(dk[j], am, b[0], b[1]);
-        mma(dk[j + 1], am, b[2], b[3]);
+    for (int j = 0; j < 16; ++j) {
+      const int jj = 16 * cq + j;
+      const __nv_bfloat16 v = __float2bfloat16_rn(pair[j]);
+      const uint16_t b = *reinterpret_cast<const uint16_t*>(&v);
+      if (lower) {  // Z^T below the zeros
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(Zb + elem_off<8>(64 + jj, i)), "h"(b) : "memory");
+      } else if (jj <= i) {  // M is zero on its diagonal
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(Zb + 2 * kTile + elem_off<8>(64 + i, jj)), "h"(b) : "memory");
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(Zb + 2 * kTile + elem_off<8>(64 + jj, i)), "h"(b) : "memory");
       }
-      if (upper) {
-        load_bt<UN>(bq, sm + L::oQ, ch * (N / 2) + j * 8, ks, lane);
-        mma(dk[j], azt, bq[0], bq[1]);
-        mma(dk[j + 1], azt, bq[2], bq[3]);
-        mma(dk[j], amt, b[0], b[1]);
-        mma(dk[j + 1], amt, b[2], b[3]);
+    }
+    fence_async_smem();
+    bar_sync(1, kEpi);
+    if (tid == 0) mbar_arrive(qk_full);
+    mbar_wait_flag(qk_done, 1, ok);
+    tc_fence_after();
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(lower ? f.dq : f.dk) + ((tok0 + i) * p.G + grp) * N + cq * NC;
+#pragma unroll
+    for (int j0 = 0; j0 < NC; j0 += 16) {
+      float x[16];
+      tmem_ld16(tlane + cq * NC + j0, x);
+      uint32_t o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = pack2(acc[j0 + 2 * j] + x[2 * j], acc[j0 + 2 * j + 1] + x[2 * j + 1]);
+      if (i < n) {
+        reinterpret_cast<uint4*>(dst + j0)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(dst + j0)[1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
   }
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int i = i0 + 8 * r;
-    if (i < n) {
-      const long long o = ((tok0 + i) * p.G + grp) * N + ch * (N / 2) + 2 * t;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(f.dq) + o + j * 8) = pack2(dq[j][2 * r], dq[j][2 * r + 1]);
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(f.dk) + o + j * 8) = pack2(dk[j][2 * r], dk[j][2 * r + 1]);
-      }
-    }
-  }
+  if (!ok) atomicOr(f.status, kDevTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (w == kWarps) tmem_dealloc(tm, kCols);
 }
 
-template <int N, int PC>
+template <int N>
 cudaError_t launch_t(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
-  auto kern = delta_grad_tc_kernel<N, PC>;
-  constexpr int smem = GradSmem<N, PC>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  const uint64_t P = p.P, H = p.H, G = p.G, Ln = p.L, b = p.b, nc = p.nc, e = 2;
+  GradMaps m = {};
+  auto tokens = [&](CUtensorMap* t, const void* base, uint64_t width, uint64_t heads, uint64_t stride) {
+    const uint64_t d[4] = {width, heads, Ln, b}, st[3] = {width * e, stride * e, Ln * stride * e};
+    const uint32_t box[4] = {64, 1, (uint32_t)kC, 1};
+    return encode_tmap_bf16_4d(t, base, d, st, box, 128);
+  };
+  auto chunks = [&](CUtensorMap* t, const void* base, uint64_t width) {
+    const uint64_t d[4] = {width, P, nc, b * H}, st[3] = {width * e, P * width * e, nc * P * width * e};
+    const uint32_t box[4] = {64, 64, 1, 1};
+    return encode_tmap_bf16_4d(t, base, d, st, box, 128);
+  };
+  if (!tokens(&m.q, f.q, N, G, p.qs) || !tokens(&m.k, f.k, N, G, p.ks) || !tokens(&m.dy, f.dy, P, H, H * P) ||
+      !tokens(&m.dv, f.dv, P, H, H * P) || !chunks(&m.S, f.S, N) || !chunks(&m.D, f.D, N) || !chunks(&m.w, f.w, 64))
+    return cudaErrorInvalidValue;
+  auto kern = delta_grad_tc_kernel<N>;
+  constexpr int smem = GradSmem<N>::bytes;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
   set_kernel_name("delta_grad_tc");
-  kern<<<(unsigned)((long long)p.nc * p.G * p.b), kThreads, smem, s>>>(p, f);
+  kern<<<(unsigned)((long long)p.nc * p.G * p.b), kThreads, smem, s>>>(p, f, m);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_delta_grad_tc(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
-  if (p.P % 64 == 0) return p.N == 128 ? launch_t<128, 64>(p, f, s) : launch_t<64, 64>(p, f, s);
-  return p.N == 128 ? launch_t<128, 32>(p, f, s) : launch_t<64, 32>(p, f, s);
+  return p.N == 128 ? launch_t<128>(p, f, s) : launch_t<64>(p, f, s);
 }
 
 }  // namespace ssd

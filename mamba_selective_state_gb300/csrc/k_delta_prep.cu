@@ -3,7 +3,7 @@
 //
 //   T = (I + M)^-1, M_ij = E_ij (k_i.k_j) beta_j (j < i)
 //   A_ij = scale E_ij (q_i.k_j) beta_j (j <= i)
-//   e_i, and o_j beta_j            (see delta_internal.cuh)
+//   the gates' records: e_i, o_j beta_j, ...   (see delta_internal.cuh)
 //
 // One CTA takes a chunk of a group: k k^T and q k^T do not depend on the head
 // and stay in registers while the CTA walks its heads.  The triangular
@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(DeltaPlan p, De
   const int bi = (int)(idx / p.G);
   const int t0 = c * kC, n = min(kC, p.L - t0);
   const long long tok0 = (long long)bi * p.L + t0;
+  if (blockIdx.x == 0 && tid == 0) *f.status = 0;
   const int h0 = grp * p.hpg + sp * heads_per_cta;
   const int h1 = min(h0 + heads_per_cta, (grp + 1) * p.hpg);
 
@@ -113,15 +114,19 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(DeltaPlan p, De
     *reinterpret_cast<float2*>(gam + 2 * lane) = make_float2(ga[0], ga[1]);
     *reinterpret_cast<float2*>(gam + kC + 2 * lane) = make_float2(be[0], be[1]);
     *reinterpret_cast<int2*>(seg + 2 * lane) = make_int2(sg[0], sg[1]);
-    float* eg = static_cast<float*>(f.e) + (((long long)bi * p.H + h) * p.nc + c) * 2 * kC + 2 * lane;
+    float* eg = static_cast<float*>(f.e) + (((long long)bi * p.H + h) * p.nc + c) * kGateRows * kC + 2 * lane;
     float e[2], o[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       e[j] = sg[j] == 0 ? expf(ga[j]) : 0.f;
-      o[j] = sg[j] == slast ? expf(last - ga[j]) * be[j] : 0.f;
+      o[j] = sg[j] == slast ? expf(last - ga[j]) : 0.f;
     }
     *reinterpret_cast<float2*>(eg) = make_float2(e[0], e[1]);
-    *reinterpret_cast<float2*>(eg + kC) = make_float2(o[0], o[1]);
+    *reinterpret_cast<float2*>(eg + kC) = make_float2(o[0] * be[0], o[1] * be[1]);
+    *reinterpret_cast<float2*>(eg + 2 * kC) = make_float2(ga[0], ga[1]);
+    *reinterpret_cast<float2*>(eg + 3 * kC) = make_float2(be[0], be[1]);
+    *reinterpret_cast<float2*>(eg + 4 * kC) = make_float2(o[0], o[1]);
+    *reinterpret_cast<int2*>(eg + 5 * kC) = make_int2(sg[0], sg[1]);
   };
 
   cp_tile<kC, U>(k_s, static_cast<const __nv_bfloat16*>(f.k) + tok0 * p.ks + (long long)grp * N, p.ks, n, tid, kThreads);

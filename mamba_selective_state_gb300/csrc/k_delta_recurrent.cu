@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaPlan p, 
   const int lane = threadIdx.x % kLanes, c = threadIdx.x / kLanes;
   const int col = p0 + c;
   const bool live = col < p.P;
+  if (!kStep && blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
   float S[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) S[i] = 0.f;
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_kernel(DeltaPlan p, De
   const int col = p0 + c;
   const bool live = col < p.P;
   const long long state_row = (((long long)bi * p.H + h) * p.P + col) * p.N;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *f.status = 0;
   float D[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) D[i] = 0.f;

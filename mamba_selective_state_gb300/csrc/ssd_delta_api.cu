@@ -7,6 +7,8 @@
 namespace ssd {
 namespace {
 
+constexpr size_t kStatusBytes = 256;  // the device status word's place in the workspaces
+
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool misaligned(const void* ptr) { return ptr && (reinterpret_cast<uintptr_t>(ptr) & 15u); }
 
@@ -52,7 +54,7 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
   p->scale = pr->scale;
   p->bf16 = pr->dtype == SSD_BF16;
   p->st_bf16 = pr->state_dtype == SSD_BF16;
-  p->tc = p->bf16 && p->P % 32 == 0 && (p->N == 64 || p->N == 128) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0;
+  p->tc = p->bf16 && p->P % 64 == 0 && (p->N == 64 || p->N == 128) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0;
   p->C = p->tc ? kDeltaChunk : 32;
   p->nc = (p->L + p->C - 1) / p->C;
   size_t off = 0;
@@ -68,14 +70,14 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
     p->sv_w = take(units * p->C * p->P * 2);
     p->sv_T = take(units * cc);
     p->sv_A = take(units * cc);
-    p->sv_e = take(units * 2 * p->C * 4);
+    p->sv_e = take(units * kGateRows * p->C * 4);
     p->saved_bytes = off;
-    off = 0;
+    off = kStatusBytes;
     p->wf_T = take(units * cc);
     p->wf_A = take(units * cc);
-    p->wf_e = take(units * 2 * p->C * 4);
+    p->wf_e = take(units * kGateRows * p->C * 4);
     p->fwd_bytes = off;
-    off = 0;
+    off = kStatusBytes;
     p->wb_D = take(states * 2);
     p->bwd_bytes = off;
     return SSD_OK;
@@ -83,8 +85,8 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
   p->sv_S = take(states * 4);
   p->sv_w = take(rows * 4);
   p->saved_bytes = off;
-  p->fwd_bytes = 256;
-  off = 0;
+  p->fwd_bytes = kStatusBytes;
+  off = kStatusBytes;
   p->wb_D = take(states * 4);
   p->wb_r = take(rows * 4);
   p->bwd_bytes = off;
@@ -144,9 +146,10 @@ int ssd_delta_fwd(const ssd_delta_problem* prob, const void* q, const void* k, c
     f.S = sv + p.sv_S;
     f.w = sv + p.sv_w;
   }
+  char* ws = static_cast<char*>(workspace);
+  f.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p.tc) {
-    char* ws = static_cast<char*>(workspace);
     f.T = sv ? sv + p.sv_T : ws + p.wf_T;
     f.A = sv ? sv + p.sv_A : ws + p.wf_A;
     f.e = sv ? sv + p.sv_e : ws + p.wf_e;
@@ -188,11 +191,13 @@ int ssd_delta_bwd(const ssd_delta_problem* prob, const void* q, const void* k, c
   f.w = sv + p.sv_w;
   f.D = ws + p.wb_D;
   f.r = ws + p.wb_r;
+  f.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p.tc) {
     f.T = sv + p.sv_T;
     f.A = sv + p.sv_A;
     f.e = sv + p.sv_e;
+    if (cudaMemsetAsync(f.status, 0, sizeof(int), s) != cudaSuccess) return SSD_ERR_CUDA;
     DELTA_LAUNCH(launch_delta_chain_bwd(p, f, s));
     DELTA_LAUNCH(launch_delta_grad_tc(p, f, s));
     return SSD_OK;

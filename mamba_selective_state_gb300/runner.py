@@ -225,6 +225,10 @@ class DeltaDevice:
                                   self.dg, self.dbeta, self.dinit, self.saved, self.workspace,
                                   stream=stream, check=check)
 
+    def device_status(self, stream=None):
+        """Synchronises; the status word of the last call."""
+        return _lib.ssd_read_device_status(self.workspace, stream)
+
     def results(self) -> dict:
         out = dict(y=self.y, final_states=self.final)
         if self.dy is not None:

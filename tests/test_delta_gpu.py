@@ -90,7 +90,7 @@ def check(d, scale=None, state_dtype=None, grad=True, **over):
     dev.fwd()
     if grad:
         dev.bwd()
-    torch.cuda.synchronize()
+    assert dev.device_status() == 0
     got = dev.results()
     ref = reference(d, scale or d["q"].shape[-1] ** -0.5, grad)
     tol = TOL[d["v"].dtype]
@@ -123,6 +123,10 @@ F, B = torch.float32, torch.bfloat16
     (2, 190, 6, 128, 128, 3, B, 3, True, True),     # wide values
     (1, 150, 2, 96, 64, 1, B, 2, True, True),
     (1, 321, 24, 64, 128, 2, B, 1, True, True),     # twelve heads share
+    (1, 129, 40, 64, 64, 1, B, 1, False, True),     # forty
+    (1, 100, 2, 256, 128, 1, B, 2, True, False),    # the widest values
+    (3, 70, 30, 128, 64, 30, B, 1, True, True),     # enough chains for 64 columns a CTA
+    (20, 66, 8, 64, 128, 4, B, 1, True, True),
 ])
 def test_forward_and_gradient(b, L, H, P, N, G, dtype, nseq, init, dfinal):
     check(draw(b, L, H, P, N, G, dtype, seed=L, nseq=nseq, init=init, dfinal=dfinal))
