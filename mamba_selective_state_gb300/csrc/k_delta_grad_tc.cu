@@ -31,7 +31,14 @@ using namespace tc;
 constexpr int kC = kDeltaChunk;
 constexpr int kWarps = 16;                    // epilogue warps
 constexpr int kEpi = kWarps * 32;
-constexpr int kThreads = kEpi + 32;           // and the control warp
+constexpr int kThreads = kEpi + 128;          // and the control warp with three idle ones: registers
+                                              // are handed over by groups of four warps
+// Registers a thread: 640 threads are launched with 96; the control warps keep
+// 32 and the epilogue warps take 112 (4 x 112 + 32 = 5 x 96).  Without that
+// the epilogue spills, and the ring leaves the L1 cache too small for it.
+// named barriers: the epilogue's own; a head's sums are written (by parity), and have been used
+constexpr int kBarSums = 2, kBarFree = 4;
+constexpr int kRegsEpi = 112, kRegsCtl = 32;
 constexpr uint32_t kTile = 8192;              // [64][64] bf16, 128-byte swizzle
 constexpr int kGate = kGateRows * kC * 4;
 
@@ -100,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(g_full + i, 1);
-      mbar_init(g_free + i, kWarps);
+      mbar_init(g_free + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(x_full + i, 1);
@@ -119,8 +126,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tm = *tm_slot;
   bool ok = true;
 
-  if (w == kWarps) {
-    if (lane == 0) {
+  if (w >= kWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtl));
+    if (w == kWarps && lane == 0) {
       const int steps = p.hpg * npc;
       auto load = [&](int s) {
         const int hh = s / npc, pc = s % npc, st = s % L::kStages, use = s / L::kStages;
@@ -194,139 +202,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(qk_done);
     }
     __syncwarp();
-  } else {
-    const int quarter = w & 3, cq = w >> 2;          // tensor-memory lanes, columns
-    const int row = 32 * quarter + lane, i = row & 63;
-    const bool lower = quarter < 2;                  // dY, dq, q k^T; else r, w, dk, k k^T
-    const uint32_t tlane = tmem_addr(tm, 32 * quarter, 0);
-    float acc[NC], pair[16], qk[16];
-    uint32_t own[NC / 2];                            // this row of q or k
-    {
-      mbar_wait_flag(qk_full, 0, ok);
-      // element (i, col): tile col / 64, q's or k's half of it
-      const uint32_t base = sm + L::oQK + ((cq * NC) >> 6) * 2 * kTile + (lower ? 0 : kTile);
-#pragma unroll
-      for (int u = 0; u < NC / 8; ++u) {
-        const uint4 v = lds128(base + tile_off<8>(i, (((cq * NC) & 63) >> 3) + u));
-        own[4 * u] = v.x;
-        own[4 * u + 1] = v.y;
-        own[4 * u + 2] = v.z;
-        own[4 * u + 3] = v.w;
-      }
-      mbar_wait_flag(qk_done, 0, ok);
-      tc_fence_after();
-      tmem_ld16(tlane + cq * 16, qk);
-      tc_fence_before();
-      // every warp has read q k^T before the first head's product takes its place
-      bar_sync(1, kEpi);
-      if (tid == 0) mbar_arrive(z_done);
-    }
-#pragma unroll
-    for (int j = 0; j < NC; ++j) acc[j] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) pair[j] = 0.f;
-    for (int hh = 0; hh < p.hpg; ++hh) {
-      const int buf = hh & 1;
-      const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
-      const int* sg = reinterpret_cast<const int*>(ga + 5 * kC);
-      float* colp = reinterpret_cast<float*>(raw + L::oCol) + buf * 4 * kC;
-      float* rowp = reinterpret_cast<float*>(raw + L::oRow) + buf * 4 * 128;
-      float* outp = reinterpret_cast<float*>(raw + L::oOut) + buf * 4 * kC;
-      float* diag = reinterpret_cast<float*>(raw + L::oDiag) + buf * kC;
-      float* red = reinterpret_cast<float*>(raw + L::oRed) + buf * kWarps;
-      mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
-      // <S0, D1>, a few elements a thread
-      float sd = 0.f;
-      for (int pc = 0; pc < npc; ++pc) {
-        const int s = hh * npc + pc, st = s % L::kStages;
-        mbar_wait_flag(s_full + st, (s / L::kStages) & 1, ok);
-        const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 1) * kTile;
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const uint4 a = lds128(S0 + (tid + u * kEpi) * 16), b = lds128(D1 + (tid + u * kEpi) * 16);
-          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 y = unpack2(av[x]), z = unpack2(bv[x]);
-            sd += y.x * z.x + y.y * z.y;
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free + st);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-      if (lane == 0) red[w] = sd;
-      const float ei = ga[i], be = ga[3 * kC + i], oi = ga[4 * kC + i], gi = ga[2 * kC + i];
-      const int si = sg[i];
-      mbar_wait_flag(x_full + buf, (hh >> 1) & 1, ok);
-      tc_fence_after();
-      if (!lower) {  // w D1: dk_i += o_i beta_i D1 w_i
-        const float fac = oi * be;
-        float dot = 0.f;
-#pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 16) {
-          float x[16];
-          tmem_ld16(tlane + kX3 + cq * NC + j0, x);
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 v = unpack2(own[(j0 + j) / 2]);
-            const float x0 = oi == 0.f ? 0.f : x[j], x1 = oi == 0.f ? 0.f : x[j + 1];
-            acc[j0 + j] += fac * x0;
-            acc[j0 + j + 1] += fac * x1;
-            dot += v.x * x0 + v.y * x1;
-          }
-        }
-        outp[cq * kC + i] = oi * dot;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x3_free);
-      // dY S0 or r S0: dq_i += scale e_i ..., dk_i -= e_i ...
-      const float fac = lower ? p.scale * ei : -ei;
-      float rsum = 0.f;
-#pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += 16) {
-        float x[16];
-        tmem_ld16(tlane + buf * kX + cq * NC + j0, x);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 v = unpack2(own[(j0 + j) / 2]);
-          const float x0 = ei == 0.f ? 0.f : x[j], x1 = ei == 0.f ? 0.f : x[j + 1];
-          acc[j0 + j] += fac * x0;
-          acc[j0 + j + 1] += fac * x1;
-          rsum += v.x * x0 + v.y * x1;
-        }
-      }
-      rsum *= fac;
-      // the pairs (i, 16 cq + j)
-      float x[16];
-      tmem_ld16(tlane + buf * kX + N + cq * 16, x);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x_free + buf);
-      const float sign = lower ? p.scale : -1.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int jj = 16 * cq + j;
-        const float bj = ga[3 * kC + jj];
-        const bool in = jj <= i && sg[jj] == si && (lower || jj < i);
-        const float z = in ? sign * __expf(gi - ga[2 * kC + jj]) * x[j] : 0.f;
-        const float both = z * qk[j];
-        pair[j] += bj * z;
-        if (jj == i) {
-          if (lower) diag[i] = both;  // a token's own pair does not depend on the decays
-          x[j] = 0.f;
-        } else {
-          rsum += bj * both;
-          x[j] = both;
-        }
-      }
-      rowp[cq * 128 + row] = rsum;
-      const float cs = sum16(x, lane);
-      if ((lane & 1) == 0) colp[quarter * kC + 16 * cq + (lane >> 1)] = cs;
-      bar_sync(1, kEpi);
-      if (w == (hh & (kWarps - 1))) {
+    if (w == kWarps + 1 || w == kWarps + 2) {
+      // the even or the odd heads' sums over a chunk, beside the next head's epilogue
+      for (int hh = w - kWarps - 1; hh < p.hpg; hh += 2) {
+        const int buf = hh & 1;
+        const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
+        const int* sg = reinterpret_cast<const int*>(ga + 5 * kC);
+        const float* colp = reinterpret_cast<const float*>(raw + L::oCol) + buf * 4 * kC;
+        const float* rowp = reinterpret_cast<const float*>(raw + L::oRow) + buf * 4 * 128;
+        const float* outp = reinterpret_cast<const float*>(raw + L::oOut) + buf * 4 * kC;
+        const float* diag = reinterpret_cast<const float*>(raw + L::oDiag) + buf * kC;
+        const float* red = reinterpret_cast<const float*>(raw + L::oRed) + buf * kWarps;
+        mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
+        bar_sync(kBarSums + buf, kEpi + 32);
         // this head's dbeta, and dg as the reverse cumulative sum of dgam
         float d[2], all = 0.f, sdot = 0.f;
 #pragma unroll
@@ -362,9 +250,141 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float v = starts ? 0.f : j ? sum - d[0] : sum;
           if (a < n) static_cast<__nv_bfloat16*>(f.dg)[(tok0 + a) * p.H + h0 + hh] = __float2bfloat16_rn(v);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_free + (hh & 3));
+        if (hh + 2 < p.hpg) bar_arrive(kBarFree + buf, kEpi + 32);
       }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    const int quarter = w & 3, cq = w >> 2;          // tensor-memory lanes, columns
+    const int row = 32 * quarter + lane, i = row & 63;
+    const bool lower = quarter < 2;                  // dY, dq, q k^T; else r, w, dk, k k^T
+    const uint32_t tlane = tmem_addr(tm, 32 * quarter, 0);
+    float acc[NC], pair[16], qk[16];
+    // acc[j0 ..] += fac x over 16 columns of a product; returns the dot product with this row of q or k
+    const uint32_t own = sm + L::oQK + ((cq * NC) >> 6) * 2 * kTile + (lower ? 0 : kTile);
+    auto add16 = [&](float (&a)[NC], int j0, uint32_t col, float fac, bool on) {
+      float x[16], dot = 0.f;
+      tmem_ld16(col, x);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 v4 = lds128(own + tile_off<8>(i, (((cq * NC) & 63) + j0) / 8 + u));
+        const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = unpack2(v[j]);
+          const float x0 = on ? x[8 * u + 2 * j] : 0.f, x1 = on ? x[8 * u + 2 * j + 1] : 0.f;
+          a[j0 + 8 * u + 2 * j] += fac * x0;
+          a[j0 + 8 * u + 2 * j + 1] += fac * x1;
+          dot += y.x * x0 + y.y * x1;
+        }
+      }
+      return dot;
+    };
+    {
+      mbar_wait_flag(qk_full, 0, ok);
+      mbar_wait_flag(qk_done, 0, ok);
+      tc_fence_after();
+      tmem_ld16(tlane + cq * 16, qk);
+      tc_fence_before();
+      // every warp has read q k^T before the first head's product takes its place
+      bar_sync(1, kEpi);
+      if (tid == 0) mbar_arrive(z_done);
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) acc[j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) pair[j] = 0.f;
+    for (int hh = 0; hh < p.hpg; ++hh) {
+      const int buf = hh & 1;
+      const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
+      const int* sg = reinterpret_cast<const int*>(ga + 5 * kC);
+      float* colp = reinterpret_cast<float*>(raw + L::oCol) + buf * 4 * kC;
+      float* rowp = reinterpret_cast<float*>(raw + L::oRow) + buf * 4 * 128;
+      float* outp = reinterpret_cast<float*>(raw + L::oOut) + buf * 4 * kC;
+      float* diag = reinterpret_cast<float*>(raw + L::oDiag) + buf * kC;
+      float* red = reinterpret_cast<float*>(raw + L::oRed) + buf * kWarps;
+      if (hh >= 2) bar_sync(kBarFree + buf, kEpi + 32);  // head hh - 2's sums have been used
+      mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
+      // <S0, D1>, a few elements a thread
+      float sd = 0.f;
+      for (int pc = 0; pc < npc; ++pc) {
+        const int s = hh * npc + pc, st = s % L::kStages;
+        mbar_wait_flag(s_full + st, (s / L::kStages) & 1, ok);
+        const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 1) * kTile;
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+          const uint4 a = lds128(S0 + (tid + u * kEpi) * 16), b = lds128(D1 + (tid + u * kEpi) * 16);
+          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 y = unpack2(av[x]), z = unpack2(bv[x]);
+            sd += y.x * z.x + y.y * z.y;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free + st);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+      if (lane == 0) red[w] = sd;
+      const float ei = ga[i], be = ga[3 * kC + i], oi = ga[4 * kC + i], gi = ga[2 * kC + i];
+      const int si = sg[i];
+      mbar_wait_flag(x_full + buf, (hh >> 1) & 1, ok);
+      tc_fence_after();
+      if (!lower) {  // w D1: dk_i += o_i beta_i D1 w_i
+        float dot = 0.f;
+#pragma unroll
+        for (int j0 = 0; j0 < NC; j0 += 16) dot += add16(acc, j0, tlane + kX3 + cq * NC + j0, oi * be, oi != 0.f);
+        outp[cq * kC + i] = oi * dot;
+      }
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(g_free + (hh & 3));
+      if (lane == 0) mbar_arrive(x3_free);
+      // dY S0 or r S0: dq_i += scale e_i ..., dk_i -= e_i ...
+      const float fac = lower ? p.scale * ei : -ei;
+      float rsum = 0.f;
+#pragma unroll
+      for (int j0 = 0; j0 < NC; j0 += 16) rsum += add16(acc, j0, tlane + buf * kX + cq * NC + j0, fac, ei != 0.f);
+      rsum *= fac;
+      // the pairs (i, 16 cq + j)
+      float x[16];
+      tmem_ld16(tlane + buf * kX + N + cq * 16, x);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_free + buf);
+      const float sign = lower ? p.scale : -1.f;
+      const int most = lower ? i : i - 1;
+      float own_pair = 0.f;
+      // (no branches: each pair's chain of loads and exponential has its latency, and sixteen overlap)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j0 = 16 * cq + 4 * u;
+        const float4 g4 = *reinterpret_cast<const float4*>(ga + 2 * kC + j0);
+        const float4 b4 = *reinterpret_cast<const float4*>(ga + 3 * kC + j0);
+        const int4 s4 = *reinterpret_cast<const int4*>(sg + j0);
+        const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
+        const int sj[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int j = 4 * u + v;
+          const bool in = (j0 + v <= most) & (sj[v] == si);
+          const float Ez = sign * __expf(gi - gj[v]) * x[j];
+          const float z = in ? Ez : 0.f;
+          const float both = z * qk[j];
+          pair[j] += bj[v] * z;
+          own_pair = j0 + v == i ? both : own_pair;
+          x[j] = j0 + v == i ? 0.f : both;
+          rsum += bj[v] * x[j];
+        }
+      }
+      if (lower && (i >> 4) == cq) diag[i] = own_pair;  // a token's own pair does not depend on the decays
+      rowp[cq * 128 + row] = rsum;
+      const float cs = sum16(x, lane);
+      if ((lane & 1) == 0) colp[quarter * kC + 16 * cq + (lane >> 1)] = cs;
+      __syncwarp();
+      bar_arrive(kBarSums + buf, kEpi + 32);
     }
     // The pairs' part for all heads: rows of [0 | Z ; Z^T | M + M^T] against
     // [q ; k], Z (i, j) and M (i, j) summed over the heads.  All of the ring's

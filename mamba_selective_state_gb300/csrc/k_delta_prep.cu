@@ -179,8 +179,10 @@ __global__ void __launch_bounds__(kThreads, 4) delta_prep_kernel(DeltaPlan p, De
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int i = i0 + 8 * r;
-          const float E0 = j <= i && sj.x == si[r] ? __expf(gi[r] - gj.x) * bj.x : 0.f;
-          const float E1 = j + 1 <= i && sj.y == si[r] ? __expf(gi[r] - gj.y) * bj.y : 0.f;
+          // (no branches: the exponentials' latencies overlap)
+          const float e0 = __expf(gi[r] - gj.x) * bj.x, e1 = __expf(gi[r] - gj.y) * bj.y;
+          const float E0 = (j <= i) & (sj.x == si[r]) ? e0 : 0.f;
+          const float E1 = (j + 1 <= i) & (sj.y == si[r]) ? e1 : 0.f;
           *reinterpret_cast<float2*>(&M_s[i * kMs + j]) =
               make_float2(j < i ? E0 * kk[nt][2 * r] : 0.f, j + 1 < i ? E1 * kk[nt][2 * r + 1] : 0.f);
           sts32(A_s + elem_off<8>(i, j), pack2(p.scale * E0 * qk[nt][2 * r], p.scale * E1 * qk[nt][2 * r + 1]));
