@@ -53,7 +53,7 @@ struct DeltaBufs {
   // recurrent kernels (fp32): S (b,H,nc,P,N) states entering each chunk,
   // w (b,L,H,P), D (b,H,nc,P,N) gradients of the state after each chunk,
   // r (b,L,H,P).  Tensor-core kernels: bf16 S, D (b,H,nc,P,N), w transposed
-  // (b,H,nc,P,C), T - I and A (b,H,nc,C,C), and fp32 gate records e
+  // (b,H,nc,P,C), T and A (b,H,nc,C,C), and fp32 gate records e
   // (b,H,nc,kGateRows,C); r is dv.
   void *S, *w, *T, *A, *e, *D, *r;
   int* status;  // device status word, at the start of the workspace
@@ -83,9 +83,11 @@ __device__ __forceinline__ void st_state(void* p, long long i, int bf16, float v
 constexpr float kForget = -100.0f;
 
 constexpr int kDeltaChunk = 64;  // tokens per chunk of the tensor-core kernels
-// rows of a chunk's gate record: e_i, o_j beta_j, gam, beta, o_j, and the
-// number of sequence starts up to the token (as an int)
-constexpr int kGateRows = 6;
+// Rows of a chunk's gate record (fp32): e_i; o_j beta_j; gam_i log2(e); beta;
+// o_j; the decay between token 32 and the token (of the second half's rows
+// from it, of the first half's columns to it; 0 across a sequence start); and
+// the number of sequence starts up to the token (an int).
+enum { kGateE, kGateOB, kGateGam, kGateBeta, kGateO, kGateHalf, kGateSeg, kGateRows };
 
 cudaError_t launch_delta_recurrent(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
 cudaError_t launch_delta_step(const DeltaPlan& p, const DeltaBufs& f, const DeltaStep& st, cudaStream_t s);

@@ -10,10 +10,17 @@
 // straight from registers (an accumulator's layout is a left operand's
 // layout), and its right operand -- K, T, Q or A -- from shared memory:
 //
-//   forward   R' = V' - e (S' K')     w' = R' + R' (T-I)'    S' = e_last S' + (o beta w)' K
+//   forward   R' = V' - e (S' K')    w' = R' (I + M)'^-1    S' = e_last S' + (o beta w)' K
 //             y' = scale e (S' Q') + w' A'
-//   reverse   R' = o beta (D' K') + dY' A    r' = R' + R' (T-I)
+//   reverse   R' = o beta (D' K') + dY' A    r' = R' (I + M)^-1
 //             D' = e_last D' + (scale e dY)' Q - (e r)' K
+//
+// The solves go by blocks of 16 tokens: each block takes the earlier (reverse:
+// later) ones' share of M, then its own inverse; T holds -M and those inverses
+// less their unit diagonals, which pass the accumulators through in fp32.
+// The state's update and the next chunk's product with it are one stream of
+// products, state tile by state tile, so that neither waits for the other's
+// end.
 //
 // There is no barrier between warps on a chain and no state in shared memory.
 // The forward hands each chunk's S' and w' (bf16) to a second warp, which
@@ -91,11 +98,12 @@ struct ChainMaps {
 template <int N, int NW>
 struct FwdSmem {
   static constexpr int kK = kC * N * 2, kV = kC * NW * 32;
-  // the chain's ring: K, T, V, gates; the output warps': Q, A, gates; each two deep
+  // the chain's ring: K, T, V, gates, three deep (a chunk's K is in use until
+  // the next one's has been); the output warps': Q, A, gates, two deep
   static constexpr int chain = kK + (int)kTile + kV, out = kK + (int)kTile;
-  static constexpr int oChain = 0, oOut = oChain + 2 * chain, oS = oOut + 2 * out,  // S' by warp, two each
+  static constexpr int oChain = 0, oOut = oChain + 3 * chain, oS = oOut + 2 * out,  // S' by warp, two each
                        oW = oS + NW * 2 * N * 32, oY = oW + NW * 2 * 2048, oE = oY + NW * 2 * 2048,
-                       oBar = oE + 4 * kGateBytes, bytes = oBar + (8 + 4 * NW) * 8 + 1024;
+                       oBar = oE + 5 * kGateBytes, bytes = oBar + (10 + 4 * NW) * 8 + 1024;
 };
 
 template <int N, int NW>
@@ -106,17 +114,19 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
   unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
   const uint32_t sm = smem_u32(raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(raw + L::oBar);
-  uint64_t *c_full = bars, *c_free = bars + 2, *o_full = bars + 4, *o_free = bars + 6;
-  uint64_t *h_full = bars + 8, *h_free = h_full + 2 * NW;  // [warp][2]
+  uint64_t *c_full = bars, *c_free = bars + 3, *o_full = bars + 6, *o_free = bars + 8;
+  uint64_t *h_full = bars + 10, *h_free = h_full + 2 * NW;  // [warp][2]
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
   const int ptiles = p.P / (16 * NW);
   const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
   const int h = (int)((blockIdx.x / ptiles) % p.H), bi = (int)(blockIdx.x / ((long long)ptiles * p.H));
   const int grp = h / p.hpg, bh = bi * p.H + h;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(c_full + i, 1);
       mbar_init(c_free + i, NW);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(o_full + i, 1);
       mbar_init(o_free + i, NW);
     }
@@ -131,49 +141,61 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
   if (w == 2 * NW) {
     if (lane == 0) {
       const float* e = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+      int cs = 0, cph = 0;  // the chain's ring position and phase
       for (int c = 0; c < p.nc; ++c) {
         const int st = c & 1;
-        if (c >= 2) mbar_wait_flag(c_free + st, ((c >> 1) - 1) & 1, ok);
-        unsigned char* d = raw + L::oChain + st * L::chain;
-        mbar_expect_tx(c_full + st, L::chain + kGateBytes);
-        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, c_full + st, 64 * j, grp, c * kC, bi);
-        tma_load_4d(d + L::kK, &m.T, c_full + st, 0, 0, c, bh);
-        tma_load_4d(d + L::kK + kTile, &m.v, c_full + st, p0, h, c * kC, bi);
-        bulk_load(raw + L::oE + st * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, c_full + st);
+        if (c >= 3) mbar_wait_flag(c_free + cs, cph ^ 1, ok);
+        unsigned char* d = raw + L::oChain + cs * L::chain;
+        mbar_expect_tx(c_full + cs, L::chain + kGateBytes);
+        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, c_full + cs, 64 * j, grp, c * kC, bi);
+        tma_load_4d(d + L::kK, &m.T, c_full + cs, 0, 0, c, bh);
+        tma_load_4d(d + L::kK + kTile, &m.v, c_full + cs, p0, h, c * kC, bi);
+        bulk_load(raw + L::oE + cs * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, c_full + cs);
+        if (++cs == 3) cs = 0, cph ^= 1;
         if (c >= 2) mbar_wait_flag(o_free + st, ((c >> 1) - 1) & 1, ok);
         d = raw + L::oOut + st * L::out;
         mbar_expect_tx(o_full + st, L::out + kGateBytes);
         for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.q, o_full + st, 64 * j, grp, c * kC, bi);
         tma_load_4d(d + L::kK, &m.A, o_full + st, 0, 0, c, bh);
-        bulk_load(raw + L::oE + (2 + st) * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, o_full + st);
+        bulk_load(raw + L::oE + (3 + st) * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, o_full + st);
       }
     }
   } else if (w < NW) {
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
-    float S[N / 8][4];
+    float S[N / 8][4], x[8][4];
     load_state<N>(S, f.init, state0, lane, p.st_bf16);
-    for (int c = 0; c < p.nc; ++c) {
-      const int st = c & 1;
-      const uint32_t Ks = sm + L::oChain + st * L::chain, Ts = Ks + L::kK, Vs = Ts + kTile;
-      const uint32_t Sd = sm + L::oS + (2 * w + st) * N * 32, Wd = sm + L::oW + (2 * w + st) * 2048;
-      const float* e = reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) + 2 * t;
-      if (c >= 2) mbar_wait_flag(h_free + 2 * w + st, ((c >> 1) - 1) & 1, ok);
-      mbar_wait_flag(c_full + st, (c >> 1) & 1, ok);
-      float x[8][4] = {};
+    int cs = 0, cph = 0;
+    // S' K' of the chunk at ring position `pos` for one 16-row step of K, and
+    // the step's bf16 copy for the output warps
+    auto state_product = [&](int ks, uint32_t Ks, uint32_t Sd) {
+      uint32_t a[4], b[4];
+      as_left(a, S[2 * ks], S[2 * ks + 1]);
+      stsm4(frag_at(Sd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int ks = 0; ks < N / 16; ++ks) {
-        uint32_t a[4], b[4];
-        as_left(a, S[2 * ks], S[2 * ks + 1]);
-        stsm4(frag_at(Sd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          ld_b(b, Ks, 8 * j, 16 * ks, lane);
-          mma(x[j], a, b[0], b[1]);
-          mma(x[j + 1], a, b[2], b[3]);
-        }
+      for (int j = 0; j < 8; j += 2) {
+        ld_b(b, Ks, 8 * j, 16 * ks, lane);
+        mma(x[j], a, b[0], b[1]);
+        mma(x[j + 1], a, b[2], b[3]);
       }
-      // R' = V' - e (S' K'); a sequence that starts here does not read the state, whatever it holds
-      uint32_t left[4][4];
+    };
+    auto zero = [](float(&v)[8][4]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
+    };
+    mbar_wait_flag(c_full, 0, ok);
+    zero(x);
+#pragma unroll
+    for (int ks = 0; ks < N / 16; ++ks) state_product(ks, sm + L::oChain, sm + L::oS + 2 * w * N * 32);
+    // from x = S' K' of a chunk its w', handed to the output warp, and (o beta w)' as left operands
+    uint32_t left[4][4];
+    auto solve = [&](int c) {
+      const int st = c & 1;
+      const uint32_t Ts = sm + L::oChain + cs * L::chain + L::kK, Vs = Ts + kTile;
+      const uint32_t Wd = sm + L::oW + (2 * w + st) * 2048;
+      const float* e = reinterpret_cast<const float*>(raw + L::oE + cs * kGateBytes) + 2 * t;
+      // R' = V' - e (S' K')
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t v[4];
@@ -188,26 +210,27 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
           for (int r = 0; r < 2; ++r) {
             const float2 vv = unpack2(v[2 * j + r]);
             float(&xx)[4] = x[2 * k + j];
-            xx[2 * r] = ej.x != 0.f ? vv.x - ej.x * xx[2 * r] : vv.x;
-            xx[2 * r + 1] = ej.y != 0.f ? vv.y - ej.y * xx[2 * r + 1] : vv.y;
+            xx[2 * r] = vv.x - ej.x * xx[2 * r];
+            xx[2 * r + 1] = vv.y - ej.y * xx[2 * r + 1];
           }
         }
-        as_left(left[k], x[2 * k], x[2 * k + 1]);
       }
-      // w' = R' + R' (T - I)': the unit diagonal takes R as it is, in fp32
+      // w' block by block: its own inverse, then its share of the later blocks
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int k = 0; k < 4; ++k) {
+        uint32_t b[4];
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
+        ld_b(b, Ts, 16 * k, 16 * k, lane);
+        mma(x[2 * k], left[k], b[0], b[1]);
+        mma(x[2 * k + 1], left[k], b[2], b[3]);
+        as_left(left[k], x[2 * k], x[2 * k + 1]);
+        stsm4(frag_at(Wd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
 #pragma unroll
-        for (int k = 0; k <= i; ++k) {
-          uint32_t b[4];
+        for (int i = k + 1; i < 4; ++i) {
           ld_b(b, Ts, 16 * i, 16 * k, lane);
           mma(x[2 * i], left[k], b[0], b[1]);
           mma(x[2 * i + 1], left[k], b[2], b[3]);
         }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        as_left(left[k], x[2 * k], x[2 * k + 1]);
-        stsm4(frag_at(Wd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
       }
       if (f.S) fence_async_smem();  // the tiles also leave through TMA
       __syncwarp();
@@ -216,7 +239,7 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float2 o = *reinterpret_cast<const float2*>(e + kC + 16 * k + 8 * j);
+          const float2 o = *reinterpret_cast<const float2*>(e + kGateOB * kC + 16 * k + 8 * j);
           float(&xx)[4] = x[2 * k + j];
           xx[0] *= o.x;
           xx[1] *= o.y;
@@ -225,22 +248,59 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
         }
         as_left(left[k], x[2 * k], x[2 * k + 1]);
       }
-      const float last = e[kC - 1 - 2 * t];
+    };
+    auto update = [&](int i, uint32_t Ks, float last) {
 #pragma unroll
-      for (int i = 0; i < N / 8; ++i)
+      for (int j = 0; j < 4; ++j) {
+        S[2 * i][j] *= last;
+        S[2 * i + 1][j] *= last;
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] = last == 0.f ? 0.f : S[i][j] * last;
+      for (int k = 0; k < 4; ++k) {
+        uint32_t b[4];
+        ld_bt(b, Ks, 16 * i, 16 * k, lane);
+        mma(S[2 * i], left[k], b[0], b[1]);
+        mma(S[2 * i + 1], left[k], b[2], b[3]);
+      }
+    };
+    for (int c = 0; c + 1 < p.nc; ++c) {
+      const int st = c & 1, ns = cs == 2 ? 0 : cs + 1;
+      const uint32_t Ks = sm + L::oChain + cs * L::chain;
+      const uint32_t Kn = sm + L::oChain + ns * L::chain, Sn = sm + L::oS + (2 * w + (st ^ 1)) * N * 32;
+      solve(c);
+      const float last = reinterpret_cast<const float*>(raw + L::oE + cs * kGateBytes)[kC - 1];
+      mbar_wait_flag(c_full + ns, ns ? cph : cph ^ 1, ok);
+      if (c >= 1) mbar_wait_flag(h_free + 2 * w + (st ^ 1), ((c - 1) >> 1) & 1, ok);
+      // S' = e_last S' + (o beta w)' K, each pair of tiles followed by the
+      // next chunk's product with the pair before
+      zero(x);
+      update(0, Ks, last);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int i = 1; i < N / 16; ++i) {
+        update(i, Ks, last);
+        state_product(i - 1, Kn, Sn);
+      }
+      state_product(N / 16 - 1, Kn, Sn);
+      if (*reinterpret_cast<const float*>(raw + L::oE + ns * kGateBytes) == 0.f) {
+        // the next chunk starts a sequence: it does not read the state, whatever that holds
+        zero(x);
 #pragma unroll
-        for (int i = 0; i < N / 8; i += 2) {
-          uint32_t b[4];
-          ld_bt(b, Ks, 8 * i, 16 * k, lane);
-          mma(S[i], left[k], b[0], b[1]);
-          mma(S[i + 1], left[k], b[2], b[3]);
-        }
+        for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < N / 16; ++ks) stsm4(frag_at(Sn, 16 * ks, lane), 0u, 0u, 0u, 0u);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(c_free + st);
+      if (lane == 0) mbar_arrive(c_free + cs);
+      cs = ns;
+      if (ns == 0) cph ^= 1;
+    }
+    solve(p.nc - 1);
+    if (f.fin) {
+      const float last = reinterpret_cast<const float*>(raw + L::oE + cs * kGateBytes)[kC - 1];
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) update(i, sm + L::oChain + cs * L::chain, last);
     }
     if (f.fin) store_state<N>(S, f.fin, state0, lane, p.st_bf16);
   } else {
@@ -250,7 +310,7 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
       const uint32_t Qs = sm + L::oOut + st * L::out, As = Qs + L::kK;
       const uint32_t Sd = sm + L::oS + (2 * cw + st) * N * 32, Wd = sm + L::oW + (2 * cw + st) * 2048;
       const uint32_t Yd = sm + L::oY + (2 * cw + st) * 2048;
-      const float* e = reinterpret_cast<const float*>(raw + L::oE + (2 + st) * kGateBytes) + 2 * t;
+      const float* e = reinterpret_cast<const float*>(raw + L::oE + (3 + st) * kGateBytes) + 2 * t;
       mbar_wait_flag(o_full + st, (c >> 1) & 1, ok);
       mbar_wait_flag(h_full + 2 * cw + st, (c >> 1) & 1, ok);
       if (f.S && lane == 0) {
@@ -276,8 +336,8 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
         const float2 ej = *reinterpret_cast<const float2*>(e + 8 * j);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          y[j][2 * r] = ej.x != 0.f ? p.scale * ej.x * y[j][2 * r] : 0.f;
-          y[j][2 * r + 1] = ej.y != 0.f ? p.scale * ej.y * y[j][2 * r + 1] : 0.f;
+          y[j][2 * r] *= p.scale * ej.x;
+          y[j][2 * r + 1] *= p.scale * ej.y;
         }
       }
 #pragma unroll
@@ -317,10 +377,10 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
 template <int N, int NW>
 struct RevSmem {
   static constexpr int kK = kC * N * 2, kV = kC * NW * 32;
-  // a ring two deep of K, Q, T, A, dY, gates; D' and r by warp, two each
+  // a ring three deep of K, Q, T, A, dY, gates; D' and r by warp
   static constexpr int stage = 2 * kK + 2 * (int)kTile + kV;
-  static constexpr int oSt = 0, oD = oSt + 2 * stage, oR = oD + NW * 2 * N * 32, oE = oR + NW * 2 * 2048,
-                       oBar = oE + 2 * kGateBytes, bytes = oBar + 4 * 8 + 1024;
+  static constexpr int oSt = 0, oD = oSt + 3 * stage, oR = oD + NW * 2 * N * 32, oE = oR + NW * 2048,
+                       oBar = oE + 3 * kGateBytes, bytes = oBar + 6 * 8 + 1024;
 };
 
 template <int N, int NW>
@@ -331,14 +391,14 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
   unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
   const uint32_t sm = smem_u32(raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(raw + L::oBar);
-  uint64_t* empty = full + 2;
+  uint64_t* empty = full + 3;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
   const int ptiles = p.P / (16 * NW);
   const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
   const int h = (int)((blockIdx.x / ptiles) % p.H), bi = (int)(blockIdx.x / ((long long)ptiles * p.H));
   const int grp = h / p.hpg, bh = bi * p.H + h;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, NW);
     }
@@ -349,9 +409,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
   if (w == NW) {
     if (lane == 0) {
       const float* e = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+      int st = 0, ph = 0;
       for (int k = 0; k < p.nc; ++k) {
-        const int c = p.nc - 1 - k, st = k & 1;
-        if (k >= 2) mbar_wait_flag(empty + st, ((k >> 1) - 1) & 1, ok);
+        const int c = p.nc - 1 - k;
+        if (k >= 3) mbar_wait_flag(empty + st, ph ^ 1, ok);
         unsigned char* d = raw + L::oSt + st * L::stage;
         mbar_expect_tx(full + st, L::stage + kGateBytes);
         for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, full + st, 64 * j, grp, c * kC, bi);
@@ -361,31 +422,33 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
         tma_load_4d(d + kTile, &m.A, full + st, 0, 0, c, bh);
         tma_load_4d(d + 2 * kTile, &m.v, full + st, p0, h, c * kC, bi);
         bulk_load(raw + L::oE + st * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, full + st);
+        if (++st == 3) st = 0, ph ^= 1;
       }
     }
   } else {
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
-    float D[N / 8][4];
+    float D[N / 8][4], x[8][4];
     load_state<N>(D, f.dfin, state0, lane, p.st_bf16);
-    for (int k0 = 0; k0 < p.nc; ++k0) {
-      const int c = p.nc - 1 - k0, st = k0 & 1;
-      const uint32_t Ks = sm + L::oSt + st * L::stage, Qs = Ks + L::kK, Ts = Qs + L::kK, As = Ts + kTile, Ys = As + kTile;
-      const uint32_t Dd = sm + L::oD + (2 * w + st) * N * 32, Rd = sm + L::oR + (2 * w + st) * 2048;
-      const float* e = reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) + 2 * t;
-      mbar_wait_flag(full + st, (k0 >> 1) & 1, ok);
-      float x[8][4] = {};
+    // one 16-row step of D' K', and the step's bf16 copy for the gradient kernel
+    auto state_product = [&](int ks, uint32_t Ks, uint32_t Dd) {
+      uint32_t a[4], b[4];
+      as_left(a, D[2 * ks], D[2 * ks + 1]);
+      stsm4(frag_at(Dd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int ks = 0; ks < N / 16; ++ks) {
-        uint32_t a[4], b[4];
-        as_left(a, D[2 * ks], D[2 * ks + 1]);
-        stsm4(frag_at(Dd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          ld_b(b, Ks, 8 * j, 16 * ks, lane);
-          mma(x[j], a, b[0], b[1]);
-          mma(x[j + 1], a, b[2], b[3]);
-        }
+      for (int j = 0; j < 8; j += 2) {
+        ld_b(b, Ks, 8 * j, 16 * ks, lane);
+        mma(x[j], a, b[0], b[1]);
+        mma(x[j + 1], a, b[2], b[3]);
       }
+    };
+    auto zero = [](float(&v)[8][4]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
+    };
+    // the tile of D' leaves through TMA
+    auto put_state = [&](int c, uint32_t Dd) {
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -393,23 +456,36 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
           tma_store_4d(&m.S, raw + (Dd - sm) + j * 2048, 64 * j, p0 + 16 * w, c, bh);
         bulk_commit();
       }
+    };
+    int st = 0, ph = 0;
+    mbar_wait_flag(full, 0, ok);
+    zero(x);
+#pragma unroll
+    for (int ks = 0; ks < N / 16; ++ks) state_product(ks, sm + L::oSt, sm + L::oD + 2 * w * N * 32);
+    put_state(p.nc - 1, sm + L::oD + 2 * w * N * 32);
+    // from x = D' K' of chunk c its r', stored, its gradient's part of D', and (-e r)' as left operands
+    uint32_t left[4][4];
+    auto solve = [&](int c) {
+      const uint32_t Qs = sm + L::oSt + st * L::stage + L::kK, Ts = Qs + L::kK, As = Ts + kTile, Ys = As + kTile;
+      const uint32_t Rd = sm + L::oR + w * 2048;
+      const float* e = reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) + 2 * t;
+      const float last = e[kC - 1 - 2 * t];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 o = *reinterpret_cast<const float2*>(e + kC + 8 * j);
+        const float2 o = *reinterpret_cast<const float2*>(e + kGateOB * kC + 8 * j);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          x[j][2 * r] = o.x != 0.f ? o.x * x[j][2 * r] : 0.f;
-          x[j][2 * r + 1] = o.y != 0.f ? o.y * x[j][2 * r + 1] : 0.f;
+          x[j][2 * r] *= o.x;
+          x[j][2 * r + 1] *= o.y;
         }
       }
-      const float last = e[kC - 1 - 2 * t];
 #pragma unroll
       for (int i = 0; i < N / 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) D[i][j] = last == 0.f ? 0.f : D[i][j] * last;
+        for (int j = 0; j < 4; ++j) D[i][j] *= last;
       // R' += dY' A, and the part of D' that does not wait for r: (scale e dY)' Q
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 3; i >= 0; --i) {
         uint32_t y[4], b[4];
         if (NW == 4)
           load_at<8>(y, Ys, 16 * w, 16 * i, lane);
@@ -437,22 +513,24 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
           mma(D[n + 1], y, b[2], b[3]);
         }
       }
-      uint32_t left[4][4];
+      // r' block by block from the last
+      if (lane == 0) bulk_wait_read<1>();  // the last chunk's r has been read (its D' was stored after)
+      __syncwarp();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) as_left(left[k], x[2 * k], x[2 * k + 1]);
+      for (int i = 3; i >= 0; --i) {
+        uint32_t b[4];
+        as_left(left[i], x[2 * i], x[2 * i + 1]);
+        load_bt<8>(b, Ts, 16 * i, 16 * i, lane);
+        mma(x[2 * i], left[i], b[0], b[1]);
+        mma(x[2 * i + 1], left[i], b[2], b[3]);
+        as_left(left[i], x[2 * i], x[2 * i + 1]);
+        stsm4t(token_at(Rd, 16 * i, lane), left[i][0], left[i][1], left[i][2], left[i][3]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i; ++j) {
-          uint32_t b[4];
+        for (int j = i - 1; j >= 0; --j) {
           load_bt<8>(b, Ts, 16 * j, 16 * i, lane);
           mma(x[2 * j], left[i], b[0], b[1]);
           mma(x[2 * j + 1], left[i], b[2], b[3]);
         }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        as_left(left[k], x[2 * k], x[2 * k + 1]);
-        stsm4t(token_at(Rd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
       }
       fence_async_smem();
       __syncwarp();
@@ -473,18 +551,57 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
         }
         as_left(left[k], x[2 * k], x[2 * k + 1]);
       }
+    };
+    auto update = [&](int i, uint32_t Ks) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 4; ++k) {
+        uint32_t b[4];
+        ld_bt(b, Ks, 16 * i, 16 * k, lane);
+        mma(D[2 * i], left[k], b[0], b[1]);
+        mma(D[2 * i + 1], left[k], b[2], b[3]);
+      }
+    };
+    // a chunk whose first token starts a sequence has no gradient to pass on, whatever its values
+    auto starts = [&]() { return *reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) == 0.f; };
+    auto zero_state = [&]() {
 #pragma unroll
-        for (int n = 0; n < N / 8; n += 2) {
-          uint32_t b[4];
-          ld_bt(b, Ks, 8 * n, 16 * k, lane);
-          mma(D[n], left[k], b[0], b[1]);
-          mma(D[n + 1], left[k], b[2], b[3]);
-        }
-      if (lane == 0) bulk_wait_read<2>();  // the last chunk's two tiles have been read
+      for (int i = 0; i < N / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) D[i][j] = 0.f;
+    };
+    for (int k0 = 0; k0 + 1 < p.nc; ++k0) {
+      const int c = p.nc - 1 - k0, ns = st == 2 ? 0 : st + 1;
+      const uint32_t Ks = sm + L::oSt + st * L::stage, Kn = sm + L::oSt + ns * L::stage;
+      const uint32_t Dn = sm + L::oD + (2 * w + ((k0 + 1) & 1)) * N * 32;
+      solve(c);
+      mbar_wait_flag(full + ns, ns ? ph : ph ^ 1, ok);
+      if (lane == 0) bulk_wait_read<2>();  // the tile's last D' has been read: two stores were made since
       __syncwarp();
+      // D' += (-e r)' K, each pair of tiles followed by the next chunk's product with the pair before
+      zero(x);
+      update(0, Ks);
+#pragma unroll
+      for (int i = 1; i < N / 16; ++i) {
+        update(i, Ks);
+        state_product(i - 1, Kn, Dn);
+      }
+      state_product(N / 16 - 1, Kn, Dn);
+      if (starts()) {
+        zero(x);
+        zero_state();
+#pragma unroll
+        for (int ks = 0; ks < N / 16; ++ks) stsm4(frag_at(Dn, 16 * ks, lane), 0u, 0u, 0u, 0u);
+      }
+      put_state(c - 1, Dn);
       if (lane == 0) mbar_arrive(empty + st);
+      st = ns;
+      if (ns == 0) ph ^= 1;
+    }
+    solve(0);
+    if (f.dinit) {
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) update(i, sm + L::oSt + st * L::stage);
+      if (starts()) zero_state();
     }
     if (f.dinit) store_state<N>(D, f.dinit, state0, lane, p.st_bf16);
     if (lane == 0) bulk_wait_all();

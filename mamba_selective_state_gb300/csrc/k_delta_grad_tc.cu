@@ -38,6 +38,7 @@ constexpr int kThreads = kEpi + 128;          // and the control warp with three
 // the epilogue spills, and the ring leaves the L1 cache too small for it.
 // named barriers: the epilogue's own; a head's sums are written (by parity), and have been used
 constexpr int kBarSums = 2, kBarFree = 4;
+constexpr int kSums = kEpi + 64;  // the epilogue, the warp of <S0, D1> and the one that uses the sums
 constexpr int kRegsEpi = 112, kRegsCtl = 32;
 constexpr uint32_t kTile = 8192;              // [64][64] bf16, 128-byte swizzle
 constexpr int kGate = kGateRows * kC * 4;
@@ -57,10 +58,16 @@ struct GradSmem {
                        oCol = oGate + 4 * kGate,       // [2][4][64] column sums by lane quarter
                        oRow = oCol + 2 * 4 * kC * 4,   // [2][4][128] row sums by column quarter
                        oOut = oRow + 2 * 4 * 128 * 4,  // [2][4][64] k.(D1 w)
-                       oDiag = oOut + 2 * 4 * kC * 4, oRed = oDiag + 2 * kC * 4, oBar = oRed + 2 * kWarps * 4,
+                       oDiag = oOut + 2 * 4 * kC * 4, oRed = oDiag + 2 * kC * 4, oBar = oRed + 16,
                        bytes = oBar + 256 + 1024;
   static_assert(kStages * stage >= 4 * (int)kTile, "the pairs' operand reuses the ring");
 };
+
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 // Sum over the warp's lanes of v[0..15]: lane l returns the total of v[l >> 1].
 __device__ __forceinline__ float sum16(float (&v)[16], int lane) {
@@ -103,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_free + i, kWarps + 1);
+      mbar_init(s_free + i, 2);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(g_full + i, 1);
@@ -207,18 +214,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hh = w - kWarps - 1; hh < p.hpg; hh += 2) {
         const int buf = hh & 1;
         const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
-        const int* sg = reinterpret_cast<const int*>(ga + 5 * kC);
+        const int* sg = reinterpret_cast<const int*>(ga + kGateSeg * kC);
         const float* colp = reinterpret_cast<const float*>(raw + L::oCol) + buf * 4 * kC;
         const float* rowp = reinterpret_cast<const float*>(raw + L::oRow) + buf * 4 * 128;
         const float* outp = reinterpret_cast<const float*>(raw + L::oOut) + buf * 4 * kC;
         const float* diag = reinterpret_cast<const float*>(raw + L::oDiag) + buf * kC;
-        const float* red = reinterpret_cast<const float*>(raw + L::oRed) + buf * kWarps;
         mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
-        bar_sync(kBarSums + buf, kEpi + 32);
+        bar_sync(kBarSums + buf, kSums);
         // this head's dbeta, and dg as the reverse cumulative sum of dgam
-        float d[2], all = 0.f, sdot = 0.f;
-#pragma unroll
-        for (int x2 = 0; x2 < kWarps; ++x2) sdot += red[x2];
+        float d[2], all = 0.f;
+        const float sdot = reinterpret_cast<const float*>(raw + L::oRed)[buf];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int a = 2 * lane + j;
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float r = 0.f;
 #pragma unroll
           for (int x2 = 0; x2 < 4; ++x2) r += rowp[x2 * 128 + a] + rowp[x2 * 128 + 64 + a];
-          const float b2 = ga[3 * kC + a];
+          const float b2 = ga[kGateBeta * kC + a];
           d[j] = r - b2 * (cj + o);
           all += b2 * o;
           if (a < n)
@@ -252,7 +257,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(g_free + (hh & 3));
-        if (hh + 2 < p.hpg) bar_arrive(kBarFree + buf, kEpi + 32);
+        if (hh + 2 < p.hpg) bar_arrive(kBarFree + buf, kSums);
+      }
+    } else if (w == kWarps + 3) {
+      // <S0, D1> of every head: the diagonal of 16 x 8 products
+      const int g = lane >> 2, t = lane & 3;
+      for (int hh = 0; hh < p.hpg; ++hh) {
+        float sd = 0.f;
+        for (int pc = 0; pc < npc; ++pc) {
+          const int s = hh * npc + pc, st = s % L::kStages;
+          mbar_wait_flag(s_full + st, (s / L::kStages) & 1, ok);
+          const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 1) * kTile;
+          for (int r = 0; r < 64; r += 16) {
+            float x0[4] = {}, x1[4] = {};
+#pragma unroll
+            for (int k = 0; k < N; k += 16) {
+              uint32_t a[4], b[4];
+              load_a<8>(a, S0 + (k >> 6) * kTile, r, k & 63, lane);
+              load_b<8>(b, D1 + (k >> 6) * kTile, r, k & 63, lane);
+              mm::mma(x0, a, b[0], b[1]);
+              mm::mma(x1, a, b[2], b[3]);
+            }
+            if (t == (g >> 1)) sd += (g & 1) ? x0[1] + x1[3] : x0[0] + x1[2];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + st);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+        if (hh >= 2) bar_sync(kBarFree + (hh & 1), kSums);
+        if (lane == 0) reinterpret_cast<float*>(raw + L::oRed)[hh & 1] = sd;
+        __syncwarp();
+        bar_arrive(kBarSums + (hh & 1), kSums);
       }
     }
   } else {
@@ -264,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float acc[NC], pair[16], qk[16];
     // acc[j0 ..] += fac x over 16 columns of a product; returns the dot product with this row of q or k
     const uint32_t own = sm + L::oQK + ((cq * NC) >> 6) * 2 * kTile + (lower ? 0 : kTile);
-    auto add16 = [&](float (&a)[NC], int j0, uint32_t col, float fac, bool on) {
+    auto add16 = [&](float (&a)[NC], int j0, uint32_t col, float fac) {
       float x[16], dot = 0.f;
       tmem_ld16(col, x);
 #pragma unroll
@@ -274,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 y = unpack2(v[j]);
-          const float x0 = on ? x[8 * u + 2 * j] : 0.f, x1 = on ? x[8 * u + 2 * j + 1] : 0.f;
+          const float x0 = x[8 * u + 2 * j], x1 = x[8 * u + 2 * j + 1];
           a[j0 + 8 * u + 2 * j] += fac * x0;
           a[j0 + 8 * u + 2 * j + 1] += fac * x1;
           dot += y.x * x0 + y.y * x1;
@@ -282,12 +318,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return dot;
     };
+    // the pairs (i, 16 cq + j): all of them, none, or those around the diagonal
+    const bool none = !(quarter & 1) && cq >= 2, all = (quarter & 1) && cq < 2;
+    const float sign = lower ? p.scale : -1.f;
+    float qk_own = 0.f, pair_own = 0.f;
     {
       mbar_wait_flag(qk_full, 0, ok);
       mbar_wait_flag(qk_done, 0, ok);
       tc_fence_after();
       tmem_ld16(tlane + cq * 16, qk);
       tc_fence_before();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        qk[j] *= sign;
+        qk_own = 16 * cq + j == i ? qk[j] : qk_own;
+      }
+      for (int x = tid; x < 2 * 4 * kC; x += kEpi) reinterpret_cast<float*>(raw + L::oCol)[x] = 0.f;
       // every warp has read q k^T before the first head's product takes its place
       bar_sync(1, kEpi);
       if (tid == 0) mbar_arrive(z_done);
@@ -299,44 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int hh = 0; hh < p.hpg; ++hh) {
       const int buf = hh & 1;
       const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
-      const int* sg = reinterpret_cast<const int*>(ga + 5 * kC);
+      const int* sg = reinterpret_cast<const int*>(ga + kGateSeg * kC);
       float* colp = reinterpret_cast<float*>(raw + L::oCol) + buf * 4 * kC;
       float* rowp = reinterpret_cast<float*>(raw + L::oRow) + buf * 4 * 128;
       float* outp = reinterpret_cast<float*>(raw + L::oOut) + buf * 4 * kC;
       float* diag = reinterpret_cast<float*>(raw + L::oDiag) + buf * kC;
-      float* red = reinterpret_cast<float*>(raw + L::oRed) + buf * kWarps;
-      if (hh >= 2) bar_sync(kBarFree + buf, kEpi + 32);  // head hh - 2's sums have been used
+      if (hh >= 2) bar_sync(kBarFree + buf, kSums);  // head hh - 2's sums have been used
       mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
-      // <S0, D1>, a few elements a thread
-      float sd = 0.f;
-      for (int pc = 0; pc < npc; ++pc) {
-        const int s = hh * npc + pc, st = s % L::kStages;
-        mbar_wait_flag(s_full + st, (s / L::kStages) & 1, ok);
-        const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 1) * kTile;
-#pragma unroll
-        for (int u = 0; u < NB; ++u) {
-          const uint4 a = lds128(S0 + (tid + u * kEpi) * 16), b = lds128(D1 + (tid + u * kEpi) * 16);
-          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 y = unpack2(av[x]), z = unpack2(bv[x]);
-            sd += y.x * z.x + y.y * z.y;
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free + st);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-      if (lane == 0) red[w] = sd;
-      const float ei = ga[i], be = ga[3 * kC + i], oi = ga[4 * kC + i], gi = ga[2 * kC + i];
-      const int si = sg[i];
+      const float ei = ga[i], be = ga[kGateBeta * kC + i], oi = ga[kGateO * kC + i];
       mbar_wait_flag(x_full + buf, (hh >> 1) & 1, ok);
       tc_fence_after();
       if (!lower) {  // w D1: dk_i += o_i beta_i D1 w_i
         float dot = 0.f;
 #pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 16) dot += add16(acc, j0, tlane + kX3 + cq * NC + j0, oi * be, oi != 0.f);
+        for (int j0 = 0; j0 < NC; j0 += 16) dot += add16(acc, j0, tlane + kX3 + cq * NC + j0, oi * be);
         outp[cq * kC + i] = oi * dot;
       }
       tc_fence_before();
@@ -346,46 +368,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float fac = lower ? p.scale * ei : -ei;
       float rsum = 0.f;
 #pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += 16) rsum += add16(acc, j0, tlane + buf * kX + cq * NC + j0, fac, ei != 0.f);
+      for (int j0 = 0; j0 < NC; j0 += 16) rsum += add16(acc, j0, tlane + buf * kX + cq * NC + j0, fac);
       rsum *= fac;
-      // the pairs (i, 16 cq + j)
       float x[16];
-      tmem_ld16(tlane + buf * kX + N + cq * 16, x);
+      if (!none) tmem_ld16(tlane + buf * kX + N + cq * 16, x);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(x_free + buf);
-      const float sign = lower ? p.scale : -1.f;
-      const int most = lower ? i : i - 1;
-      float own_pair = 0.f;
-      // (no branches: each pair's chain of loads and exponential has its latency, and sixteen overlap)
+      if (all) {
+        // below the diagonal the decay is that from token 32 times that to it
+        const float ri = ga[kGateHalf * kC + i];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j0 = 16 * cq + 4 * u;
-        const float4 g4 = *reinterpret_cast<const float4*>(ga + 2 * kC + j0);
-        const float4 b4 = *reinterpret_cast<const float4*>(ga + 3 * kC + j0);
-        const int4 s4 = *reinterpret_cast<const int4*>(sg + j0);
-        const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
-        const int sj[4] = {s4.x, s4.y, s4.z, s4.w};
+        for (int u = 0; u < 4; ++u) {
+          const int j0 = 16 * cq + 4 * u;
+          const float4 c4 = *reinterpret_cast<const float4*>(ga + kGateHalf * kC + j0);
+          const float4 b4 = *reinterpret_cast<const float4*>(ga + kGateBeta * kC + j0);
+          const float cj[4] = {c4.x, c4.y, c4.z, c4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int j = 4 * u + v;
-          const bool in = (j0 + v <= most) & (sj[v] == si);
-          const float Ez = sign * __expf(gi - gj[v]) * x[j];
-          const float z = in ? Ez : 0.f;
-          const float both = z * qk[j];
-          pair[j] += bj[v] * z;
-          own_pair = j0 + v == i ? both : own_pair;
-          x[j] = j0 + v == i ? 0.f : both;
-          rsum += bj[v] * x[j];
+          for (int v = 0; v < 4; ++v) {
+            const int j = 4 * u + v;
+            const float z = x[j] * ri * cj[v];
+            pair[j] += bj[v] * z;
+            x[j] = z * qk[j];
+            rsum += bj[v] * x[j];
+          }
+        }
+      } else if (!none) {
+        const float gi = ga[kGateGam * kC + i];
+        const int si = sg[i];
+        if (lower) {  // a token's own pair: it does not depend on the decays
+          float own_x = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) own_x = 16 * cq + j == i ? x[j] : own_x;
+          pair_own += be * own_x;
+          if ((i >> 4) == cq) diag[i] = own_x * qk_own;
+        }
+        // (no branches: each pair's chain of loads and exponential has its latency, and sixteen overlap)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j0 = 16 * cq + 4 * u;
+          const float4 g4 = *reinterpret_cast<const float4*>(ga + kGateGam * kC + j0);
+          const float4 b4 = *reinterpret_cast<const float4*>(ga + kGateBeta * kC + j0);
+          const int4 s4 = *reinterpret_cast<const int4*>(sg + j0);
+          const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
+          const int sj[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int j = 4 * u + v;
+            const float Ex = exp2_fast(gi - gj[v]) * x[j];
+            const float z = (j0 + v < i) & (sj[v] == si) ? Ex : 0.f;
+            pair[j] += bj[v] * z;
+            x[j] = z * qk[j];
+            rsum += bj[v] * x[j];
+          }
         }
       }
-      if (lower && (i >> 4) == cq) diag[i] = own_pair;  // a token's own pair does not depend on the decays
       rowp[cq * 128 + row] = rsum;
-      const float cs = sum16(x, lane);
-      if ((lane & 1) == 0) colp[quarter * kC + 16 * cq + (lane >> 1)] = cs;
+      if (!none) {
+        const float cs = sum16(x, lane);
+        if ((lane & 1) == 0) colp[quarter * kC + 16 * cq + (lane >> 1)] = cs;
+      }
       __syncwarp();
-      bar_arrive(kBarSums + buf, kEpi + 32);
+      bar_arrive(kBarSums + buf, kSums);
     }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) pair[j] = sign * (lower && 16 * cq + j == i ? pair_own : pair[j]);
     // The pairs' part for all heads: rows of [0 | Z ; Z^T | M + M^T] against
     // [q ; k], Z (i, j) and M (i, j) summed over the heads.  All of the ring's
     // products are done: the last head's x_full followed them.
