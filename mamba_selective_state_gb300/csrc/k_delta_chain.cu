@@ -106,10 +106,17 @@ struct FwdSmem {
                        oBar = oE + 5 * kGateBytes, bytes = oBar + (10 + 4 * NW) * 8 + 1024;
 };
 
+// Column, output and copying warps.  Nine warps would leave each 168 registers
+// (three on one sub-partition), which the chain's loads need more than:
+// registers are handed over by groups of four warps, so three idle ones join
+// the copying warp (launched with 168 each: 240 + 208 + 40 <= 3 x 168).
+constexpr int fwd_threads(int nw) { return nw == 4 ? 384 : (2 * nw + 1) * 32; }
+
 template <int N, int NW>
-__global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
+__global__ void __launch_bounds__(fwd_threads(NW), 1)
     delta_chain_fwd_kernel(DeltaPlan p, DeltaBufs f, const __grid_constant__ ChainMaps m) {
   using L = FwdSmem<N, NW>;
+  constexpr bool kHandOver = NW == 4;
   extern __shared__ unsigned char raw_[];
   unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
   const uint32_t sm = smem_u32(raw);
@@ -138,8 +145,9 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
   }
   __syncthreads();
   bool ok = true;
-  if (w == 2 * NW) {
-    if (lane == 0) {
+  if (w >= 2 * NW) {
+    if (kHandOver) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (w == 2 * NW && lane == 0) {
       const float* e = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
       int cs = 0, cph = 0;  // the chain's ring position and phase
       for (int c = 0; c < p.nc; ++c) {
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
         if (c >= 3) mbar_wait_flag(c_free + cs, cph ^ 1, ok);
         unsigned char* d = raw + L::oChain + cs * L::chain;
         mbar_expect_tx(c_full + cs, L::chain + kGateBytes);
-        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, c_full + cs, 64 * j, grp, c * kC, bi);
+        tma_load_4d(d, &m.k, c_full + cs, 0, c * kC, grp * (N / 64), bi);
         tma_load_4d(d + L::kK, &m.T, c_full + cs, 0, 0, c, bh);
         tma_load_4d(d + L::kK + kTile, &m.v, c_full + cs, p0, h, c * kC, bi);
         bulk_load(raw + L::oE + cs * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, c_full + cs);
@@ -155,28 +163,35 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
         if (c >= 2) mbar_wait_flag(o_free + st, ((c >> 1) - 1) & 1, ok);
         d = raw + L::oOut + st * L::out;
         mbar_expect_tx(o_full + st, L::out + kGateBytes);
-        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.q, o_full + st, 64 * j, grp, c * kC, bi);
+        tma_load_4d(d, &m.q, o_full + st, 0, c * kC, grp * (N / 64), bi);
         tma_load_4d(d + L::kK, &m.A, o_full + st, 0, 0, c, bh);
         bulk_load(raw + L::oE + (3 + st) * kGateBytes, e + (long long)c * kGateRows * kC, kGateBytes, o_full + st);
       }
     }
   } else if (w < NW) {
+    if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
     float S[N / 8][4], x[8][4];
     load_state<N>(S, f.init, state0, lane, p.st_bf16);
     int cs = 0, cph = 0;
-    // S' K' of the chunk at ring position `pos` for one 16-row step of K, and
-    // the step's bf16 copy for the output warps
-    auto state_product = [&](int ks, uint32_t Ks, uint32_t Sd) {
-      uint32_t a[4], b[4];
-      as_left(a, S[2 * ks], S[2 * ks + 1]);
-      stsm4(frag_at(Sd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
+    // S' K' for one 16-row step of K; the step's bf16 copy stays in `half` until
+    // the products are under way (a store to shared memory would hold back
+    // the loads of the next step's operands)
+    uint32_t half[N / 16][4];
+    auto state_product = [&](int ks, uint32_t Ks) {
+      uint32_t b[4];
+      as_left(half[ks], S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         ld_b(b, Ks, 8 * j, 16 * ks, lane);
-        mma(x[j], a, b[0], b[1]);
-        mma(x[j + 1], a, b[2], b[3]);
+        mma(x[j], half[ks], b[0], b[1]);
+        mma(x[j + 1], half[ks], b[2], b[3]);
       }
+    };
+    auto put_state = [&](uint32_t Sd) {
+#pragma unroll
+      for (int ks = 0; ks < N / 16; ++ks)
+        stsm4(frag_at(Sd, 16 * ks, lane), half[ks][0], half[ks][1], half[ks][2], half[ks][3]);
     };
     auto zero = [](float(&v)[8][4]) {
 #pragma unroll
@@ -187,7 +202,8 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
     mbar_wait_flag(c_full, 0, ok);
     zero(x);
 #pragma unroll
-    for (int ks = 0; ks < N / 16; ++ks) state_product(ks, sm + L::oChain, sm + L::oS + 2 * w * N * 32);
+    for (int ks = 0; ks < N / 16; ++ks) state_product(ks, sm + L::oChain);
+    put_state(sm + L::oS + 2 * w * N * 32);
     // from x = S' K' of a chunk its w', handed to the output warp, and (o beta w)' as left operands
     uint32_t left[4][4];
     auto solve = [&](int c) {
@@ -195,43 +211,50 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
       const uint32_t Ts = sm + L::oChain + cs * L::chain + L::kK, Vs = Ts + kTile;
       const uint32_t Wd = sm + L::oW + (2 * w + st) * 2048;
       const float* e = reinterpret_cast<const float*>(raw + L::oE + cs * kGateBytes) + 2 * t;
+      // all the operands before the first product that waits for another
+      uint32_t v[4][4], tb[10][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (NW == 4)
+          load_at<8>(v[k], Vs, 16 * w, 16 * k, lane);
+        else
+          load_at<4>(v[k], Vs, 16 * w, 16 * k, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k <= i; ++k) ld_b(tb[i * (i + 1) / 2 + k], Ts, 16 * i, 16 * k, lane);
       // R' = V' - e (S' K')
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t v[4];
-        if (NW == 4)
-          load_at<8>(v, Vs, 16 * w, 16 * k, lane);
-        else
-          load_at<4>(v, Vs, 16 * w, 16 * k, lane);
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float2 ej = *reinterpret_cast<const float2*>(e + 16 * k + 8 * j);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float2 vv = unpack2(v[2 * j + r]);
+            const float2 vv = unpack2(v[k][2 * j + r]);
             float(&xx)[4] = x[2 * k + j];
             xx[2 * r] = vv.x - ej.x * xx[2 * r];
             xx[2 * r + 1] = vv.y - ej.y * xx[2 * r + 1];
           }
         }
-      }
       // w' block by block: its own inverse, then its share of the later blocks
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t b[4];
+        const uint32_t(&d)[4] = tb[k * (k + 1) / 2 + k];
         as_left(left[k], x[2 * k], x[2 * k + 1]);
-        ld_b(b, Ts, 16 * k, 16 * k, lane);
-        mma(x[2 * k], left[k], b[0], b[1]);
-        mma(x[2 * k + 1], left[k], b[2], b[3]);
+        mma(x[2 * k], left[k], d[0], d[1]);
+        mma(x[2 * k + 1], left[k], d[2], d[3]);
         as_left(left[k], x[2 * k], x[2 * k + 1]);
-        stsm4(frag_at(Wd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
 #pragma unroll
         for (int i = k + 1; i < 4; ++i) {
-          ld_b(b, Ts, 16 * i, 16 * k, lane);
+          const uint32_t(&b)[4] = tb[i * (i + 1) / 2 + k];
           mma(x[2 * i], left[k], b[0], b[1]);
           mma(x[2 * i + 1], left[k], b[2], b[3]);
         }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        stsm4(frag_at(Wd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
       if (f.S) fence_async_smem();  // the tiles also leave through TMA
       __syncwarp();
       if (lane == 0) mbar_arrive(h_full + 2 * w + st);
@@ -278,9 +301,9 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
 #pragma unroll
       for (int i = 1; i < N / 16; ++i) {
         update(i, Ks, last);
-        state_product(i - 1, Kn, Sn);
+        state_product(i - 1, Kn);
       }
-      state_product(N / 16 - 1, Kn, Sn);
+      state_product(N / 16 - 1, Kn);
       if (*reinterpret_cast<const float*>(raw + L::oE + ns * kGateBytes) == 0.f) {
         // the next chunk starts a sequence: it does not read the state, whatever that holds
         zero(x);
@@ -289,8 +312,9 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < N / 16; ++ks) stsm4(frag_at(Sn, 16 * ks, lane), 0u, 0u, 0u, 0u);
+        for (int ks = 0; ks < N / 16; ++ks) half[ks][0] = half[ks][1] = half[ks][2] = half[ks][3] = 0u;
       }
+      put_state(Sn);
       __syncwarp();
       if (lane == 0) mbar_arrive(c_free + cs);
       cs = ns;
@@ -304,6 +328,7 @@ __global__ void __launch_bounds__((2 * NW + 1) * 32, 1)
     }
     if (f.fin) store_state<N>(S, f.fin, state0, lane, p.st_bf16);
   } else {
+    if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int cw = w - NW;
     for (int c = 0; c < p.nc; ++c) {
       const int st = c & 1;
@@ -379,7 +404,7 @@ struct RevSmem {
   static constexpr int kK = kC * N * 2, kV = kC * NW * 32;
   // a ring three deep of K, Q, T, A, dY, gates; D' and r by warp
   static constexpr int stage = 2 * kK + 2 * (int)kTile + kV;
-  static constexpr int oSt = 0, oD = oSt + 3 * stage, oR = oD + NW * 2 * N * 32, oE = oR + NW * 2048,
+  static constexpr int oSt = 0, oD = oSt + 3 * stage, oR = oD + NW * N * 32, oE = oR + NW * 2048,
                        oBar = oE + 3 * kGateBytes, bytes = oBar + 6 * 8 + 1024;
 };
 
@@ -415,8 +440,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
         if (k >= 3) mbar_wait_flag(empty + st, ph ^ 1, ok);
         unsigned char* d = raw + L::oSt + st * L::stage;
         mbar_expect_tx(full + st, L::stage + kGateBytes);
-        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + j * kTile, &m.k, full + st, 64 * j, grp, c * kC, bi);
-        for (int j = 0; j < N / 64; ++j) tma_load_4d(d + L::kK + j * kTile, &m.q, full + st, 64 * j, grp, c * kC, bi);
+        tma_load_4d(d, &m.k, full + st, 0, c * kC, grp * (N / 64), bi);
+        tma_load_4d(d + L::kK, &m.q, full + st, 0, c * kC, grp * (N / 64), bi);
         d += 2 * L::kK;
         tma_load_4d(d, &m.T, full + st, 0, 0, c, bh);
         tma_load_4d(d + kTile, &m.A, full + st, 0, 0, c, bh);
@@ -429,16 +454,16 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
     float D[N / 8][4], x[8][4];
     load_state<N>(D, f.dfin, state0, lane, p.st_bf16);
-    // one 16-row step of D' K', and the step's bf16 copy for the gradient kernel
-    auto state_product = [&](int ks, uint32_t Ks, uint32_t Dd) {
-      uint32_t a[4], b[4];
-      as_left(a, D[2 * ks], D[2 * ks + 1]);
-      stsm4(frag_at(Dd, 16 * ks, lane), a[0], a[1], a[2], a[3]);
+    // one 16-row step of D' K'; the step's bf16 copy for the gradient kernel stays in `half`
+    uint32_t half[N / 16][4];
+    auto state_product = [&](int ks, uint32_t Ks) {
+      uint32_t b[4];
+      as_left(half[ks], D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         ld_b(b, Ks, 8 * j, 16 * ks, lane);
-        mma(x[j], a, b[0], b[1]);
-        mma(x[j + 1], a, b[2], b[3]);
+        mma(x[j], half[ks], b[0], b[1]);
+        mma(x[j + 1], half[ks], b[2], b[3]);
       }
     };
     auto zero = [](float(&v)[8][4]) {
@@ -447,13 +472,28 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
     };
-    // the tile of D' leaves through TMA
-    auto put_state = [&](int c, uint32_t Dd) {
+    // r' of chunk c (but for the first call) and D' after chunk c - 1 leave through TMA
+    const uint32_t Dd = sm + L::oD + w * N * 32, Rd = sm + L::oR + w * 2048;
+    uint32_t rk[4][4];
+    auto put_r = [&]() {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) stsm4t(token_at(Rd, 16 * k, lane), rk[k][0], rk[k][1], rk[k][2], rk[k][3]);
+    };
+    auto put = [&](int c, bool with_r, bool with_d) {
+      if (lane == 0) bulk_wait_read<0>();  // the tiles' last contents have been read
+      __syncwarp();
+      if (with_r) put_r();
+      if (with_d)
+#pragma unroll
+        for (int ks = 0; ks < N / 16; ++ks)
+          stsm4(frag_at(Dd, 16 * ks, lane), half[ks][0], half[ks][1], half[ks][2], half[ks][3]);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        for (int j = 0; j < N / 64; ++j)
-          tma_store_4d(&m.S, raw + (Dd - sm) + j * 2048, 64 * j, p0 + 16 * w, c, bh);
+        if (with_r) tma_store_4d(&m.y, raw + (Rd - sm), p0 + 16 * w, h, c * kC, bi);
+        if (with_d)
+          for (int j = 0; j < N / 64; ++j)
+            tma_store_4d(&m.S, raw + (Dd - sm) + j * 2048, 64 * j, p0 + 16 * w, c - 1, bh);
         bulk_commit();
       }
     };
@@ -461,13 +501,12 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
     mbar_wait_flag(full, 0, ok);
     zero(x);
 #pragma unroll
-    for (int ks = 0; ks < N / 16; ++ks) state_product(ks, sm + L::oSt, sm + L::oD + 2 * w * N * 32);
-    put_state(p.nc - 1, sm + L::oD + 2 * w * N * 32);
-    // from x = D' K' of chunk c its r', stored, its gradient's part of D', and (-e r)' as left operands
+    for (int ks = 0; ks < N / 16; ++ks) state_product(ks, sm + L::oSt);
+    put(p.nc, false, true);
+    // from x = D' K' of a chunk its r' (rk), its gradient's part of D', and (-e r)' as left operands
     uint32_t left[4][4];
-    auto solve = [&](int c) {
+    auto solve = [&]() {
       const uint32_t Qs = sm + L::oSt + st * L::stage + L::kK, Ts = Qs + L::kK, As = Ts + kTile, Ys = As + kTile;
-      const uint32_t Rd = sm + L::oR + w * 2048;
       const float* e = reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes) + 2 * t;
       const float last = e[kC - 1 - 2 * t];
 #pragma unroll
@@ -514,29 +553,24 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
         }
       }
       // r' block by block from the last
-      if (lane == 0) bulk_wait_read<1>();  // the last chunk's r has been read (its D' was stored after)
-      __syncwarp();
+      uint32_t tb[10][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) load_bt<8>(tb[i * (i + 1) / 2 + j], Ts, 16 * j, 16 * i, lane);
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
-        uint32_t b[4];
-        as_left(left[i], x[2 * i], x[2 * i + 1]);
-        load_bt<8>(b, Ts, 16 * i, 16 * i, lane);
-        mma(x[2 * i], left[i], b[0], b[1]);
-        mma(x[2 * i + 1], left[i], b[2], b[3]);
-        as_left(left[i], x[2 * i], x[2 * i + 1]);
-        stsm4t(token_at(Rd, 16 * i, lane), left[i][0], left[i][1], left[i][2], left[i][3]);
+        const uint32_t(&d)[4] = tb[i * (i + 1) / 2 + i];
+        as_left(rk[i], x[2 * i], x[2 * i + 1]);
+        mma(x[2 * i], rk[i], d[0], d[1]);
+        mma(x[2 * i + 1], rk[i], d[2], d[3]);
+        as_left(rk[i], x[2 * i], x[2 * i + 1]);
 #pragma unroll
         for (int j = i - 1; j >= 0; --j) {
-          load_bt<8>(b, Ts, 16 * j, 16 * i, lane);
-          mma(x[2 * j], left[i], b[0], b[1]);
-          mma(x[2 * j + 1], left[i], b[2], b[3]);
+          const uint32_t(&b)[4] = tb[i * (i + 1) / 2 + j];
+          mma(x[2 * j], rk[i], b[0], b[1]);
+          mma(x[2 * j + 1], rk[i], b[2], b[3]);
         }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_4d(&m.y, raw + (Rd - sm), p0 + 16 * w, h, c * kC, bi);
-        bulk_commit();
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -572,32 +606,30 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
     for (int k0 = 0; k0 + 1 < p.nc; ++k0) {
       const int c = p.nc - 1 - k0, ns = st == 2 ? 0 : st + 1;
       const uint32_t Ks = sm + L::oSt + st * L::stage, Kn = sm + L::oSt + ns * L::stage;
-      const uint32_t Dn = sm + L::oD + (2 * w + ((k0 + 1) & 1)) * N * 32;
-      solve(c);
+      solve();
       mbar_wait_flag(full + ns, ns ? ph : ph ^ 1, ok);
-      if (lane == 0) bulk_wait_read<2>();  // the tile's last D' has been read: two stores were made since
-      __syncwarp();
       // D' += (-e r)' K, each pair of tiles followed by the next chunk's product with the pair before
       zero(x);
       update(0, Ks);
 #pragma unroll
       for (int i = 1; i < N / 16; ++i) {
         update(i, Ks);
-        state_product(i - 1, Kn, Dn);
+        state_product(i - 1, Kn);
       }
-      state_product(N / 16 - 1, Kn, Dn);
+      state_product(N / 16 - 1, Kn);
       if (starts()) {
         zero(x);
         zero_state();
 #pragma unroll
-        for (int ks = 0; ks < N / 16; ++ks) stsm4(frag_at(Dn, 16 * ks, lane), 0u, 0u, 0u, 0u);
+        for (int ks = 0; ks < N / 16; ++ks) half[ks][0] = half[ks][1] = half[ks][2] = half[ks][3] = 0u;
       }
-      put_state(c - 1, Dn);
+      put(c, true, true);
       if (lane == 0) mbar_arrive(empty + st);
       st = ns;
       if (ns == 0) ph ^= 1;
     }
-    solve(0);
+    solve();
+    put(0, true, false);
     if (f.dinit) {
 #pragma unroll
       for (int i = 0; i < N / 16; ++i) update(i, sm + L::oSt + st * L::stage);
@@ -626,7 +658,13 @@ bool chain_maps(const DeltaPlan& p, const DeltaBufs& f, bool reverse, int nw, Ch
     return encode_tmap_bf16_4d(t, base, d, s, box, 128);
   };
   const uint32_t cols = 16 * nw;
-  bool good = tokens(&m->q, f.q, N, G, p.qs, 64, 128) && tokens(&m->k, f.k, N, G, p.ks, 64, 128) &&
+  // q and k: all dstate columns of a group in one copy, 64-column blocks of [token][64] one after the other
+  auto groups = [&](CUtensorMap* t, const void* base, uint64_t stride) {
+    const uint64_t d[4] = {64, Ln, G * N / 64, b}, s[3] = {stride * e, 128, Ln * stride * e};
+    const uint32_t box[4] = {64, (uint32_t)kC, (uint32_t)N / 64, 1};
+    return encode_tmap_bf16_4d(t, base, d, s, box, 128);
+  };
+  bool good = groups(&m->q, f.q, p.qs) && groups(&m->k, f.k, p.ks) &&
               tokens(&m->v, reverse ? f.dy : f.v, P, H, reverse ? H * P : p.vs, cols, (int)cols * 2) &&
               tokens(&m->y, reverse ? f.dv : f.y, P, H, H * P, 16, 0) && chunks(&m->T, f.T, 64, 64, 64) &&
               chunks(&m->A, f.A, 64, 64, 64);
@@ -653,7 +691,7 @@ cudaError_t launch_chain_t(const DeltaPlan& p, const DeltaBufs& f, bool reverse,
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     set_kernel_name("delta_chain_fwd");
-    kern<<<grid, (2 * NW + 1) * 32, smem, s>>>(p, f, m);
+    kern<<<grid, fwd_threads(NW), smem, s>>>(p, f, m);
   }
   return cudaGetLastError();
 }
