@@ -8,7 +8,7 @@
 // so a thread group of eight lanes keeps one column's dstate values in fp32
 // registers and walks the tokens.  Both dot products are taken of the old
 // state in one pass (S.q = a S_old.q + (q.k) beta w), so that a token costs
-// one round of three shuffles.  A single token is bound by the state's bytes
+// one round of three shuffles; the next tokens are on their way meanwhile.  A single token is bound by the state's bytes
 // (each read and written once, 16-byte accesses, whole 128-byte lines per
 // group); a long sequence by the latency of one token's chain.
 #include "delta_internal.cuh"
@@ -19,7 +19,6 @@ namespace {
 constexpr int kLanes = 8;                    // lanes per state column
 constexpr int kThreads = 128;
 constexpr int kCols = kThreads / kLanes;     // columns per CTA
-constexpr int kTok = 16;                     // tokens staged at a time
 
 __device__ __forceinline__ float group_sum(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
@@ -63,65 +62,81 @@ __device__ __forceinline__ void store_col(const float (&S)[NR], void* base, long
   }
 }
 
-template <int NR>
+// TOK tokens in shared memory, as fp32
+template <int NR, int TOK>
 struct Stage {
-  float q[kTok][NR * kLanes];
-  float k[kTok][NR * kLanes];
-  float v[kTok][kCols];   // v of this CTA's columns (the reverse pass: dy)
-  float a[kTok], beta[kTok], qk[kTok];
-  int reset[kTok];
+  float q[TOK][NR * kLanes];
+  float k[TOK][NR * kLanes];
+  float v[TOK][kCols];   // v of this CTA's columns (the reverse pass: dy)
+  float a[TOK], beta[TOK];
+  int reset[TOK];
 };
 
-// One chunk of tokens [t0, t0 + n) into shared memory, as fp32.
-template <typename T, int NR>
-__device__ __forceinline__ void stage_tokens(Stage<NR>& sm, const DeltaPlan& p, const DeltaBufs& f, const void* vals,
-                                             long long vstride, int bi, int h, int p0, int t0, int n) {
-  const int grp = h / p.hpg;
-  const long long tok0 = (long long)bi * p.L + t0;
-  const T* q = static_cast<const T*>(f.q);
-  const T* k = static_cast<const T*>(f.k);
-  for (int i = threadIdx.x; i < n * NR * kLanes; i += kThreads) {
-    const int t = i / (NR * kLanes), e = i % (NR * kLanes);
-    float qv = 0.f, kv = 0.f;
-    if (e < p.N) {
-      qv = to_f(q[(tok0 + t) * p.qs + (long long)grp * p.N + e]);
-      kv = to_f(k[(tok0 + t) * p.ks + (long long)grp * p.N + e]);
-    }
-    sm.q[t][e] = qv;
-    sm.k[t][e] = kv;
-  }
-  for (int i = threadIdx.x; i < n * kCols; i += kThreads) {
-    const int t = i / kCols, c = i % kCols;
-    sm.v[t][c] = p0 + c < p.P ? to_f(static_cast<const T*>(vals)[(tok0 + t) * vstride + (long long)h * p.P + p0 + c])
-                              : 0.f;
-  }
-  if (threadIdx.x < n) {
-    const int t = threadIdx.x;
-    const long long i = (tok0 + t) * p.H + h;
-    sm.a[t] = expf(to_f(static_cast<const T*>(f.g)[i]));
-    sm.beta[t] = to_f(static_cast<const T*>(f.beta)[i]);
-    sm.reset[t] = f.seq != nullptr && t0 + t > 0 && f.seq[tok0 + t] != f.seq[tok0 + t - 1];
-  }
-}
-
-// q.k of every staged token, one warp at a time over the tokens.
-template <int NR>
-__device__ __forceinline__ void token_dots(Stage<NR>& sm, int n) {
-  const int lane = threadIdx.x & 31;
-  for (int t = threadIdx.x >> 5; t < n; t += kThreads / 32) {
-    float d = 0.f;
-    for (int e = lane; e < NR * kLanes; e += 32) d += sm.q[t][e] * sm.k[t][e];
+// A thread's part of TOK tokens on their way to shared memory: loaded ahead,
+// written when the stage is free.
+template <typename T, int NR, int TOK>
+struct Ahead {
+  static constexpr int E = (TOK * NR * kLanes + kThreads - 1) / kThreads;  // q and k values
+  static constexpr int EV = (TOK * kCols + kThreads - 1) / kThreads;
+  T q[E], k[E], v[EV];
+  T g, beta;
+  int reset;
+  __device__ __forceinline__ void load(const DeltaPlan& p, const DeltaBufs& f, const void* vals, long long vstride,
+                                       int bi, int h, int p0, int t0, int n) {
+    const int grp = h / p.hpg;
+    const long long tok0 = (long long)bi * p.L + t0;
+    const T zero = from_f<T>(0.f);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) sm.qk[t] = d;
+    for (int i = 0; i < E; ++i) {
+      const int x = threadIdx.x + i * kThreads, t = x / (NR * kLanes), e = x % (NR * kLanes);
+      q[i] = k[i] = zero;
+      if (t < n && e < p.N) {
+        q[i] = static_cast<const T*>(f.q)[(tok0 + t) * p.qs + (long long)grp * p.N + e];
+        k[i] = static_cast<const T*>(f.k)[(tok0 + t) * p.ks + (long long)grp * p.N + e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EV; ++i) {
+      const int x = threadIdx.x + i * kThreads, t = x / kCols, c = x % kCols;
+      v[i] = zero;
+      if (t < n && p0 + c < p.P)
+        v[i] = static_cast<const T*>(vals)[(tok0 + t) * vstride + (long long)h * p.P + p0 + c];
+    }
+    g = beta = zero;
+    reset = 0;
+    if (threadIdx.x < n) {
+      const long long i = (tok0 + threadIdx.x) * p.H + h;
+      g = static_cast<const T*>(f.g)[i];
+      beta = static_cast<const T*>(f.beta)[i];
+      reset = f.seq != nullptr && t0 + threadIdx.x > 0 && f.seq[tok0 + threadIdx.x] != f.seq[tok0 + threadIdx.x - 1];
+    }
   }
-}
+  __device__ __forceinline__ void put(Stage<NR, TOK>& sm) const {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int x = threadIdx.x + i * kThreads;
+      if (x >= TOK * NR * kLanes) break;
+      (&sm.q[0][0])[x] = to_f(q[i]);
+      (&sm.k[0][0])[x] = to_f(k[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < EV; ++i) {
+      const int x = threadIdx.x + i * kThreads;
+      if (x < TOK * kCols) (&sm.v[0][0])[x] = to_f(v[i]);
+    }
+    if (threadIdx.x < TOK) {
+      sm.a[threadIdx.x] = expf(to_f(g));
+      sm.beta[threadIdx.x] = to_f(beta);
+      sm.reset[threadIdx.x] = reset;
+    }
+  }
+};
 
 // Forward: kStep takes its states from a pool, else from init; f.S and f.w,
 // when given, get the states entering each chunk of p.C tokens and every w.
-template <typename T, int NR, bool kStep>
-__global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaPlan p, DeltaBufs f, DeltaStep st) {
-  __shared__ Stage<NR> sm;
+template <typename T, int NR, int TOK, bool kStep>
+__global__ void __launch_bounds__(kThreads, kStep && TOK == 1 && NR <= 16 ? 8 : 1) delta_recurrent_kernel(DeltaPlan p, DeltaBufs f, DeltaStep st) {
+  __shared__ Stage<NR, TOK> sm;
   const int ptiles = (p.P + kCols - 1) / kCols;
   const int p0 = (int)(blockIdx.x % ptiles) * kCols;
   const int h = (int)((blockIdx.x / ptiles) % p.H);
@@ -133,6 +148,8 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaPlan p, 
   float S[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) S[i] = 0.f;
+  Ahead<T, NR, TOK> ahead;
+  ahead.load(p, f, f.v, p.vs, bi, h, p0, 0, min(TOK, p.L));
   int keep = p.L;  // the state after this many tokens is the one that is kept
   long long slot = bi;
   bool pad = false;
@@ -149,21 +166,29 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaPlan p, 
     store_col<NR>(S, st.out, out_row, lane, p.N, 0);
   // without y the tokens past the last kept one are not needed
   const int last = kStep && !f.y ? keep : p.L;
-  for (int t0 = 0; t0 < last; t0 += kTok) {
-    const int n = min(kTok, last - t0);
+  for (int t0 = 0; t0 < last; t0 += TOK) {
+    const int n = min(TOK, last - t0);
     if (t0) __syncthreads();
-    stage_tokens<T, NR>(sm, p, f, f.v, p.vs, bi, h, p0, t0, n);
-    __syncthreads();
-    token_dots<NR>(sm, n);
-    __syncthreads();
-    for (int t = 0; t < n; ++t) {
-      if (sm.reset[t]) {
+    ahead.put(sm);
+    // (no token of this stage starts a sequence: the usual case has no branch)
+    const bool resets = __syncthreads_or(ahead.reset);
+    if (t0 + TOK < last) ahead.load(p, f, f.v, p.vs, bi, h, p0, t0 + TOK, min(TOK, last - t0 - TOK));
+    // (the stages divide the chunks, so that only their first tokens begin one)
+    if (!kStep && f.S && t0 % p.C == 0) {
+      if (sm.reset[0]) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) S[i] = 0.f;
       }
-      if (!kStep && f.S && (t0 + t) % p.C == 0 && live)
-        store_col<NR>(S, f.S, ((((long long)bi * p.H + h) * p.nc + (t0 + t) / p.C) * p.P + col) * p.N, lane, p.N, 0);
-      float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f}, kk[NR];
+      if (live)
+        store_col<NR>(S, f.S, ((((long long)bi * p.H + h) * p.nc + t0 / p.C) * p.P + col) * p.N, lane, p.N, 0);
+    }
+    long long o = (((long long)bi * p.L + t0) * p.H + h) * p.P + col;
+    auto token = [&](int t, bool checked) {
+      if (checked && sm.reset[t]) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) S[i] = 0.f;
+      }
+      float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f}, kk[NR];
 #pragma unroll
       for (int i = 0; i < NR; i += 4) {
         const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[t][elem_n(lane, i)]);
@@ -171,23 +196,33 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaPlan p, 
         kk[i] = k4.x; kk[i + 1] = k4.y; kk[i + 2] = k4.z; kk[i + 3] = k4.w;
         sk[0] += k4.x * S[i]; sk[1] += k4.y * S[i + 1]; sk[2] += k4.z * S[i + 2]; sk[3] += k4.w * S[i + 3];
         sq[0] += q4.x * S[i]; sq[1] += q4.y * S[i + 1]; sq[2] += q4.z * S[i + 2]; sq[3] += q4.w * S[i + 3];
+        d[0] += k4.x * q4.x; d[1] += k4.y * q4.y; d[2] += k4.z * q4.z; d[3] += k4.w * q4.w;
       }
       const float a = sm.a[t];
       const float dk = group_sum((sk[0] + sk[1]) + (sk[2] + sk[3]));
       const float dq = group_sum((sq[0] + sq[1]) + (sq[2] + sq[3]));
+      const float qk = group_sum((d[0] + d[1]) + (d[2] + d[3]));
       const float w = sm.v[t][c] - a * dk;
       const float u = sm.beta[t] * w;
 #pragma unroll
       for (int i = 0; i < NR; ++i) S[i] = a * S[i] + kk[i] * u;
       if (live && lane == 0) {
-        const long long o = (((long long)bi * p.L + t0 + t) * p.H + h) * p.P + col;
         if (f.y) {
-          const float y = pad ? 0.f : p.scale * (a * dq + sm.qk[t] * u);
+          const float y = pad ? 0.f : p.scale * (a * dq + qk * u);
           static_cast<T*>(f.y)[o] = from_f<T>(y);
         }
         if (!kStep && f.w) static_cast<float*>(f.w)[o] = w;
       }
+      o += (long long)p.H * p.P;
       if (kStep && t0 + t + 1 == keep && st.out && live && !pad) store_col<NR>(S, st.out, out_row, lane, p.N, 0);
+    };
+    if (resets) {
+      for (int t = 0; t < n; ++t) token(t, true);
+    } else if (n == TOK) {
+#pragma unroll(TOK > 4 ? 4 : TOK)
+      for (int t = 0; t < TOK; ++t) token(t, false);
+    } else {
+      for (int t = 0; t < n; ++t) token(t, false);
     }
   }
   if (!kStep && f.fin && live)
@@ -197,9 +232,9 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(DeltaPlan p, 
 // Reverse: D, the gradient of the state, in the same layout; per token, last
 // first, D += scale dy_p q; r = beta k.D; D = a (D - r k).  Writes r (as dv,
 // and in fp32 for the gradient kernel) and D after each chunk of p.C tokens.
-template <typename T, int NR>
+template <typename T, int NR, int TOK>
 __global__ void __launch_bounds__(kThreads) delta_reverse_kernel(DeltaPlan p, DeltaBufs f) {
-  __shared__ Stage<NR> sm;
+  __shared__ Stage<NR, TOK> sm;
   const int ptiles = (p.P + kCols - 1) / kCols;
   const int p0 = (int)(blockIdx.x % ptiles) * kCols;
   const int h = (int)((blockIdx.x / ptiles) % p.H);
@@ -212,20 +247,24 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_kernel(DeltaPlan p, De
   float D[NR];
 #pragma unroll
   for (int i = 0; i < NR; ++i) D[i] = 0.f;
+  const int first = (p.L - 1) / TOK * TOK;
+  const long long dys = (long long)p.H * p.P;
+  Ahead<T, NR, TOK> ahead;
+  ahead.load(p, f, f.dy, dys, bi, h, p0, first, p.L - first);
   if (f.dfin && live) load_col<NR>(D, f.dfin, state_row, lane, p.N, p.st_bf16);
-  for (int t0 = (p.L - 1) / kTok * kTok; t0 >= 0; t0 -= kTok) {
-    const int n = min(kTok, p.L - t0);
+  for (int t0 = first; t0 >= 0; t0 -= TOK) {
+    const int n = min(TOK, p.L - t0);
     __syncthreads();
-    stage_tokens<T, NR>(sm, p, f, f.dy, (long long)p.H * p.P, bi, h, p0, t0, n);
-    __syncthreads();
-    token_dots<NR>(sm, n);
-    __syncthreads();
-    for (int t = n - 1; t >= 0; --t) {
-      const int tt = t0 + t;
-      if (((tt + 1) % p.C == 0 || tt + 1 == p.L) && live)
-        store_col<NR>(D, f.D, ((((long long)bi * p.H + h) * p.nc + tt / p.C) * p.P + col) * p.N, lane, p.N, 0);
+    ahead.put(sm);
+    const bool resets = __syncthreads_or(ahead.reset);
+    if (t0 > 0) ahead.load(p, f, f.dy, dys, bi, h, p0, t0 - TOK, TOK);
+    // the stages divide the chunks, so that only their last tokens end one
+    if (((t0 + n) % p.C == 0 || t0 + n == p.L) && live)
+      store_col<NR>(D, f.D, ((((long long)bi * p.H + h) * p.nc + (t0 + n - 1) / p.C) * p.P + col) * p.N, lane, p.N, 0);
+    long long o = (((long long)bi * p.L + t0 + n - 1) * p.H + h) * p.P + col;
+    auto token = [&](int t, bool checked) {
       const float dy = p.scale * sm.v[t][c];
-      float dk[4] = {0.f, 0.f, 0.f, 0.f}, kk[NR], qq[NR];
+      float dk[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f}, kk[NR], qq[NR];
 #pragma unroll
       for (int i = 0; i < NR; i += 4) {
         const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[t][elem_n(lane, i)]);
@@ -233,12 +272,16 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_kernel(DeltaPlan p, De
         kk[i] = k4.x; kk[i + 1] = k4.y; kk[i + 2] = k4.z; kk[i + 3] = k4.w;
         qq[i] = q4.x; qq[i + 1] = q4.y; qq[i + 2] = q4.z; qq[i + 3] = q4.w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dk[j] += kk[i + j] * D[i + j];
+        for (int j = 0; j < 4; ++j) {
+          dk[j] += kk[i + j] * D[i + j];
+          d[j] += kk[i + j] * qq[i + j];
+        }
       }
       const float kd = group_sum((dk[0] + dk[1]) + (dk[2] + dk[3]));
-      const float r = sm.beta[t] * (kd + sm.qk[t] * dy);
-      const float a = sm.reset[t] ? 0.f : sm.a[t];
-      if (sm.reset[t]) {
+      const float qk = group_sum((d[0] + d[1]) + (d[2] + d[3]));
+      const float r = sm.beta[t] * (kd + qk * dy);
+      const float a = sm.a[t];
+      if (checked && sm.reset[t]) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) D[i] = 0.f;
       } else {
@@ -246,10 +289,18 @@ __global__ void __launch_bounds__(kThreads) delta_reverse_kernel(DeltaPlan p, De
         for (int i = 0; i < NR; ++i) D[i] = a * (D[i] + qq[i] * dy - kk[i] * r);
       }
       if (live && lane == 0) {
-        const long long o = (((long long)bi * p.L + tt) * p.H + h) * p.P + col;
         static_cast<T*>(f.dv)[o] = from_f<T>(r);
         static_cast<float*>(f.r)[o] = r;
       }
+      o -= dys;
+    };
+    if (resets) {
+      for (int t = n - 1; t >= 0; --t) token(t, true);
+    } else if (n == TOK) {
+#pragma unroll 4
+      for (int t = TOK - 1; t >= 0; --t) token(t, false);
+    } else {
+      for (int t = n - 1; t >= 0; --t) token(t, false);
     }
   }
   if (f.dinit && live) store_col<NR>(D, f.dinit, state_row, lane, p.N, p.st_bf16);
@@ -259,15 +310,19 @@ template <typename T, int NR>
 cudaError_t launch_t(const DeltaPlan& p, const DeltaBufs& f, const DeltaStep* st, bool reverse, cudaStream_t s) {
   const long long grid = (long long)((p.P + kCols - 1) / kCols) * p.H * p.b;
   const DeltaStep none = {nullptr, nullptr, nullptr, nullptr, 0};
+  constexpr int kTok = NR > 16 ? 8 : 16;  // tokens staged at a time; they divide a chunk of 32
   if (reverse) {
     set_kernel_name("delta_reverse");
-    delta_reverse_kernel<T, NR><<<(unsigned)grid, kThreads, 0, s>>>(p, f);
+    delta_reverse_kernel<T, NR, kTok><<<(unsigned)grid, kThreads, 0, s>>>(p, f);
   } else if (st) {
     set_kernel_name("delta_step");
-    delta_recurrent_kernel<T, NR, true><<<(unsigned)grid, kThreads, 0, s>>>(p, f, *st);
+    if (p.L == 1)  // no shared memory for tokens that are not there
+      delta_recurrent_kernel<T, NR, 1, true><<<(unsigned)grid, kThreads, 0, s>>>(p, f, *st);
+    else
+      delta_recurrent_kernel<T, NR, 4, true><<<(unsigned)grid, kThreads, 0, s>>>(p, f, *st);
   } else {
     set_kernel_name("delta_recurrent");
-    delta_recurrent_kernel<T, NR, false><<<(unsigned)grid, kThreads, 0, s>>>(p, f, none);
+    delta_recurrent_kernel<T, NR, kTok, false><<<(unsigned)grid, kThreads, 0, s>>>(p, f, none);
   }
   return cudaGetLastError();
 }

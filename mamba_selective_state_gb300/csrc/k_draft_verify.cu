@@ -21,7 +21,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
 constexpr int kMaxCluster = 8;
 
 struct VerifyArgs {
@@ -34,15 +33,13 @@ struct VerifyArgs {
   int K;
 };
 
-// Larger ratio first, then lower index.  Ratios that are not above zero (or
-// are NaN) never enter; key 0 means none.
-__device__ __forceinline__ unsigned long long race_key(float w, float noise, unsigned v) {
-  const float s = w / noise;
-  return w > 0.f && s > 0.f ? ((unsigned long long)__float_as_uint(s) << 32) | (0xffffffffu - v) : 0ull;
+// Larger ratio first, then lower index; key 0 means none.
+__device__ __forceinline__ unsigned long long race_key(float s, unsigned v) {
+  return s > 0.f ? ((unsigned long long)__float_as_uint(s) << 32) | (0xffffffffu - v) : 0ull;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_draft_kernel(VerifyArgs a) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draft_kernel(VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   const unsigned ncta = cluster.num_blocks(), rank = cluster.block_rank();
   const long long b = blockIdx.x / ncta;
@@ -85,17 +82,38 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(VerifyArgs a) {
   // round 0: the residual weights; round 1, only where none was positive: p
   unsigned long long best = 0;
   for (int round = 0; round < 2; ++round) {
-    unsigned long long key = 0;
-#pragma unroll 4
-    for (long long v = lo + threadIdx.x; v < hi; v += kThreads) {
-      float w = to_f(p[v]);
-      if (round == 0) {
-        if (q) w -= to_f(q[v]);
-        if (v == one) w -= 1.f;
+    // A thread meets its words in ascending order, so the first of equal ratios
+    // stays.  A ratio is divided out only where an estimate of it (off by a few
+    // units of 2^-23) says that it may be the largest yet; ratios that are not
+    // above zero, or are NaN, never are.
+    float top = 0.f, bar = 0.f;
+    unsigned at = 0;
+    constexpr int kAhead = 8;
+    for (long long v0 = lo + threadIdx.x; v0 < hi; v0 += kAhead * kThreads) {
+      float w[kAhead], r[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const long long v = v0 + i * kThreads;
+        const bool in = v < hi;
+        w[i] = in ? to_f(p[v]) : 0.f;
+        r[i] = in ? noise[v] : 1.f;
+        if (round == 0 && q) w[i] -= in ? to_f(q[v]) : 0.f;
       }
-      const unsigned long long k = race_key(w, noise[v], (unsigned)v);
-      key = k > key ? k : key;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const long long v = v0 + i * kThreads;
+        if (round == 0 && v == one) w[i] -= 1.f;
+        if (w[i] > 0.f && !(__fdividef(w[i], r[i]) < bar)) {
+          const float s = w[i] / r[i];
+          if (s > top) {
+            top = s;
+            at = (unsigned)v;
+            bar = s * 0.999f;
+          }
+        }
+      }
     }
+    unsigned long long key = race_key(top, at);
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
@@ -126,11 +144,8 @@ __global__ void __launch_bounds__(kThreads) verify_draft_kernel(VerifyArgs a) {
   }
 }
 
-template <typename T>
-cudaError_t launch_verify(const VerifyArgs& a, int64_t batch, cudaStream_t s) {
-  // CTAs per sequence: one for each 2048 words of the vocabulary, in powers of two up to the portable cluster size
-  int ncta = 1;
-  while (ncta < kMaxCluster && (long long)ncta * 2048 < a.V) ncta *= 2;
+template <typename T, int kThreads>
+cudaError_t launch_verify_t(const VerifyArgs& a, int64_t batch, int ncta, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(batch * ncta));
   cfg.blockDim = dim3(kThreads);
@@ -143,7 +158,17 @@ cudaError_t launch_verify(const VerifyArgs& a, int64_t batch, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   set_kernel_name("verify_draft");
-  return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, verify_draft_kernel<T, kThreads>, a);
+}
+
+template <typename T>
+cudaError_t launch_verify(const VerifyArgs& a, int64_t batch, cudaStream_t s) {
+  // CTAs per sequence: one for each 2048 words of the vocabulary, in powers of two up to the portable cluster size;
+  // wide ones while every CTA has an SM of its own, else four narrow ones to an SM
+  int ncta = 1;
+  while (ncta < kMaxCluster && (long long)ncta * 2048 < a.V) ncta *= 2;
+  return batch * ncta <= device_sm_count() ? launch_verify_t<T, 512>(a, batch, ncta, s)
+                                           : launch_verify_t<T, 256>(a, batch, ncta, s);
 }
 
 bool misaligned16(const void* ptr) { return ptr && (reinterpret_cast<uintptr_t>(ptr) & 15u); }

@@ -1,9 +1,11 @@
 // k_state_cache.cu -- recurrent states put away in 8 bits and read back.
 //
-// One row of dstate values has one scale.  A warp takes a row: its values
-// stay in registers between the maximum and the rounding, so the states are
-// read once; both directions are bound by HBM (5 bytes per value, 4 of them
-// the fp32 state).
+// One row of dstate values has one scale.  Its values stay in registers
+// between the maximum and the rounding, so the states are read once; both
+// directions are bound by HBM (5 bytes per value, 4 of them the fp32 state).
+// Rows of a multiple of four values take four to a lane, in 16-byte accesses,
+// as few lanes to a row as hold it, and four rows to a lane at a time; other
+// rows take a warp and single values.
 #include <cuda_fp8.h>
 
 #include "ssd_internal.cuh"
@@ -94,6 +96,138 @@ __global__ void __launch_bounds__(kThreads) cache_load_kernel(CacheArgs a) {
   }
 }
 
+constexpr int kRows = 4;  // rows of a lane in flight
+
+template <bool kFp8>
+__device__ __forceinline__ uint32_t encode4(float4 v, float inv) {
+  return (uint32_t)encode<kFp8>(v.x * inv) | (uint32_t)encode<kFp8>(v.y * inv) << 8 |
+         (uint32_t)encode<kFp8>(v.z * inv) << 16 | (uint32_t)encode<kFp8>(v.w * inv) << 24;
+}
+
+// LR lanes to a row (a power of two), V vectors of four values to a lane.
+template <bool kFp8, int LR, int V>
+__global__ void __launch_bounds__(kThreads) cache_store4_kernel(CacheArgs a) {
+  const int lane = threadIdx.x % LR;
+  const long long row0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / LR;
+  const long long step = (long long)gridDim.x * kThreads / LR;
+  const int n4 = a.N / 4;
+  float4 v[kRows][V];
+  long long to[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const long long row = row0 + r * step;
+    to[r] = -1;
+    if (row < a.rows) {
+      const long long bi = row / a.hp, slot = a.slots ? a.slots[bi] : bi;
+      if (slot >= 0 && slot < a.nslots) to[r] = slot * a.hp + (row - bi * a.hp);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int n = i * LR + lane;
+      v[r][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (to[r] >= 0 && n < n4) v[r][i] = __ldcs(reinterpret_cast<const float4*>(a.in) + row * n4 + n);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    float big = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float m = fmaxf(fmaxf(fabsf(v[r][i].x), fabsf(v[r][i].y)), fmaxf(fabsf(v[r][i].z), fabsf(v[r][i].w)));
+      big = fmaxf(big, m);
+      // infinities show in the maximum, a NaN in the sum
+      bad |= !(m <= 3.402823466e38f) || (v[r][i].x - v[r][i].x) + (v[r][i].y - v[r][i].y) +
+                                                (v[r][i].z - v[r][i].z) + (v[r][i].w - v[r][i].w) != 0.f;
+    }
+    unsigned any = bad;
+#pragma unroll
+    for (int o = LR / 2; o; o >>= 1) {
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      any |= __shfl_xor_sync(0xffffffffu, any, o);
+    }
+    if (to[r] < 0) continue;
+    const float top = kFp8 ? 448.f : 127.f;
+    const bool empty = any || !(big >= kTiny);
+    const float inv = empty ? 0.f : top / big;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int n = i * LR + lane;
+      if (n < n4) reinterpret_cast<uint32_t*>(a.vals)[to[r] * n4 + n] = empty ? 0u : encode4<kFp8>(v[r][i], inv);
+    }
+    if (lane == 0) a.scales[to[r]] = any ? __int_as_float(0x7fc00000) : empty ? 0.f : big / top;
+  }
+}
+
+template <bool kFp8, int LR, int V>
+__global__ void __launch_bounds__(kThreads) cache_load4_kernel(CacheArgs a) {
+  const int lane = threadIdx.x % LR;
+  const long long row0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / LR;
+  const long long step = (long long)gridDim.x * kThreads / LR;
+  const int n4 = a.N / 4;
+  uint32_t v[kRows][V];
+  float sc[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const long long row = row0 + r * step;
+    sc[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[r][i] = 0u;
+    if (row < a.rows) {
+      const long long bi = row / a.hp, slot = a.slots ? a.slots[bi] : bi;
+      if (slot >= 0 && slot < a.nslots) {
+        const long long from = slot * a.hp + (row - bi * a.hp);
+        sc[r] = a.scales[from];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i * LR + lane < n4) v[r][i] = reinterpret_cast<const uint32_t*>(a.vals)[from * n4 + i * LR + lane];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const long long row = row0 + r * step;
+    if (row >= a.rows) break;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int n = i * LR + lane;
+      const uint32_t x = v[r][i];
+      if (n < n4)
+        __stcs(reinterpret_cast<float4*>(a.out) + row * n4 + n,
+               make_float4(decode<kFp8>(x & 255) * sc[r], decode<kFp8>((x >> 8) & 255) * sc[r],
+                           decode<kFp8>((x >> 16) & 255) * sc[r], decode<kFp8>(x >> 24) * sc[r]));
+    }
+  }
+}
+
+template <bool kFp8, int LR, int V>
+void launch4(const CacheArgs& a, bool store, cudaStream_t s) {
+  const long long per = kThreads / LR * kRows;
+  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+  if (store)
+    cache_store4_kernel<kFp8, LR, V><<<grid, kThreads, 0, s>>>(a);
+  else
+    cache_load4_kernel<kFp8, LR, V><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <bool kFp8>
+void launch_cache(const CacheArgs& a, bool store, cudaStream_t s) {
+  if (a.N % 4 == 0) {
+    const int n4 = a.N / 4;
+    if (n4 <= 4) launch4<kFp8, 4, 1>(a, store, s);
+    else if (n4 <= 8) launch4<kFp8, 8, 1>(a, store, s);
+    else if (n4 <= 16) launch4<kFp8, 16, 1>(a, store, s);
+    else if (n4 <= 32) launch4<kFp8, 32, 1>(a, store, s);
+    else launch4<kFp8, 32, 2>(a, store, s);
+    return;
+  }
+  const unsigned grid = (unsigned)((a.rows + kThreads / 32 - 1) / (kThreads / 32));
+  if (store)
+    cache_store_kernel<kFp8><<<grid, kThreads, 0, s>>>(a);
+  else
+    cache_load_kernel<kFp8><<<grid, kThreads, 0, s>>>(a);
+}
+
 bool misaligned16(const void* ptr) { return ptr && (reinterpret_cast<uintptr_t>(ptr) & 15u); }
 
 int run_cache(const ssd_cache_problem* pr, const float* in, float* out, const void* vals, const float* scales,
@@ -124,17 +258,12 @@ int run_cache(const ssd_cache_problem* pr, const float* in, float* out, const vo
                  (int)(pr->nheads * pr->headdim),
                  (int)pr->dstate};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)((a.rows + kThreads / 32 - 1) / (kThreads / 32));
-  const bool fp8 = pr->format == SSD_CACHE_E4M3;
   prof_before(s);
   set_kernel_name(store ? "state_cache_store" : "state_cache_load");
-  if (store) {
-    if (fp8) cache_store_kernel<true><<<grid, kThreads, 0, s>>>(a);
-    else cache_store_kernel<false><<<grid, kThreads, 0, s>>>(a);
-  } else {
-    if (fp8) cache_load_kernel<true><<<grid, kThreads, 0, s>>>(a);
-    else cache_load_kernel<false><<<grid, kThreads, 0, s>>>(a);
-  }
+  if (pr->format == SSD_CACHE_E4M3)
+    launch_cache<true>(a, store, s);
+  else
+    launch_cache<false>(a, store, s);
   const cudaError_t e = cudaGetLastError();
   prof_after(s);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;

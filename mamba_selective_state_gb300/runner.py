@@ -3,6 +3,8 @@ C ABI.  Allocation and argument marshalling only; the layer runs in libssd.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -125,42 +127,64 @@ class NormDevice:
         return {k: v.detach().to("cpu", torch.float64) for k, v in out.items()}
 
 
-def _token_stride(t, inner, what):
+def _token_stride(shape, strides, inner, what):
     """Elements between the tokens of a (b, L, heads, d) tensor whose last two
     axes are dense and whose rows are L tokens long (a column block of a
     wider projection is one)."""
-    b, L, heads, d = t.shape
-    stride = t.stride(1) if L > 1 else t.stride(0) if b > 1 else inner
-    if ((d > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != d)
-            or (b > 1 and t.stride(0) != L * stride) or stride < inner):
+    b, L, heads, d = shape
+    stride = strides[1] if L > 1 else strides[0] if b > 1 else inner
+    if ((d > 1 and strides[3] != 1) or (heads > 1 and strides[2] != d)
+            or (b > 1 and strides[0] != L * stride) or stride < inner):
         raise ValueError(f"{what}: its heads must be dense and its tokens evenly spaced")
     return stride
 
 
 def _dense(t, shape, dtype, what, device=None):
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or \
-            (device is not None and t.device != device):
+    if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                          or (device is not None and t.device != device)):
         raise ValueError(f"{what}: expected a dense {tuple(shape)} {dtype} tensor on {device}")
 
 
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
-def _delta_shape(q, k, v, g, beta):
-    if v.dim() != 4 or q.dim() != 4 or v.dtype not in _FLOATS:
+# the problem structs of repeated shapes (the library only reads them)
+_verify_problem = functools.lru_cache(maxsize=256)(_lib.make_verify_problem)
+_cache_problem = functools.lru_cache(maxsize=256)(_lib.make_cache_problem)
+
+
+@functools.lru_cache(maxsize=256)
+def _delta_layout(meta):
+    """(b, L, H, P, N, G) and the token strides of q, k, v from the tensors'
+    shapes, strides, types and devices; raises where they do not fit."""
+    (q, k, v, g, beta) = meta
+    if len(v[0]) != 4 or len(q[0]) != 4 or v[2] not in _FLOATS:
         raise ValueError("v must be (b, L, H, P) and q (b, L, G, N), both fp32 or bf16")
-    b, L, H, P = v.shape
-    G, N = q.shape[2:]
+    b, L, H, P = v[0]
+    G, N = q[0][2:]
     for t, what in ((q, "q"), (k, "k")):
-        if tuple(t.shape) != (b, L, G, N) or t.dtype != v.dtype or t.device != v.device:
-            raise ValueError(f"{what}: expected a {(b, L, G, N)} {v.dtype} tensor on {v.device}")
-    _dense(g, (b, L, H), v.dtype, "g", v.device)
-    _dense(beta, (b, L, H), v.dtype, "beta", v.device)
-    strides = dict(q_stride=_token_stride(q, G * N, "q"), k_stride=_token_stride(k, G * N, "k"),
-                   v_stride=_token_stride(v, H * P, "v"))
+        if tuple(t[0]) != (b, L, G, N) or t[2:] != v[2:]:
+            raise ValueError(f"{what}: expected a {(b, L, G, N)} {v[2]} tensor on {v[3]}")
+    for t, what in ((g, "g"), (beta, "beta")):
+        dense = (L * H, H, 1)
+        if tuple(t[0]) != (b, L, H) or t[2:] != v[2:] or any(
+                n > 1 and s != d for n, s, d in zip(t[0], t[1], dense)):
+            raise ValueError(f"{what}: expected a dense {(b, L, H)} {v[2]} tensor on {v[3]}")
+    strides = (_token_stride(q[0], q[1], G * N, "q"), _token_stride(k[0], k[1], G * N, "k"),
+               _token_stride(v[0], v[1], H * P, "v"))
     return (b, L, H, P, N, G), strides
+
+
+def _delta_shape(q, k, v, g, beta):
+    return _delta_layout(tuple((t.shape, t.stride(), t.dtype, t.device)
+                               for t in (q, k, v, g, beta)))
+
+
+@functools.lru_cache(maxsize=256)
+def _step_problem(shape, scale, dtype, strides):
+    b, T, H, P, N, G = shape
+    return _lib.make_delta_problem(b, T, H, P, N, G, scale, dtype, q_stride=strides[0],
+                                   k_stride=strides[1], v_stride=strides[2])
 
 
 class DeltaDevice:
@@ -193,7 +217,7 @@ class DeltaDevice:
             bflags |= _lib.SSD_WANT_DINIT
         scale = N ** -0.5 if scale is None else scale
         make = lambda f: _lib.make_delta_problem(  # noqa: E731
-            b, L, H, P, N, G, scale, dt, state_dtype, f, **strides)
+            b, L, H, P, N, G, scale, dt, state_dtype, f, *strides)
         self.fwd_prob, self.bwd_prob = make(flags), make(bflags)
         self.y = torch.empty((b, L, H, P), dtype=dt, device=dev)
         self.final = torch.empty((b, H, P, N), dtype=state_dtype, device=dev)
@@ -257,14 +281,15 @@ class DeltaStepDevice:
         in order, from each sequence's slot; returns y (b, T, H, P), or None
         without ``outputs``.  The states written are those after the first
         ``lengths[b]`` tokens (default: all); ``update=False`` writes none."""
-        (b, T, H, P, N, G), strides = _delta_shape(q, k, v, g, beta)
+        shape, strides = _delta_shape(q, k, v, g, beta)
+        b, T, H, P, N, G = shape
         nslots = self.states.shape[0]
-        if tuple(self.states.shape[1:]) != (H, P, N) or v.device != self.states.device:
+        if self.states.shape[1:] != (H, P, N) or v.device != self.states.device:
             raise ValueError("the tokens' heads do not fit the states")
         _dense(slots, (b,), torch.int32, "slots", v.device)
         _dense(lengths, (b,), torch.int32, "lengths", v.device)
         scale = N ** -0.5 if scale is None else scale
-        prob = _lib.make_delta_problem(b, T, H, P, N, G, scale, v.dtype, **strides)
+        prob = _step_problem(shape, scale, v.dtype, strides)
         y = torch.empty((b, T, H, P), dtype=v.dtype, device=v.device) if outputs else None
         _lib.ssd_delta_step(prob, q, k, v, g, beta, nslots, self.states,
                             self.states_out if update else None, slots, lengths, y,
@@ -290,7 +315,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniform, noise, length
     _dense(lengths, (b,), torch.int32, "lengths", dev)
     tokens = torch.empty((b, K1), dtype=torch.int32, device=dev)
     accepted = torch.empty(b, dtype=torch.int32, device=dev)
-    prob = _lib.make_verify_problem(b, K1 - 1, V, target_probs.dtype)
+    prob = _verify_problem(b, K1 - 1, V, target_probs.dtype)
     _lib.ssd_verify_draft(prob, target_probs, draft_probs, draft_tokens, lengths, uniform, noise,
                           tokens, accepted, stream=stream, check=check)
     return tokens, accepted
@@ -313,7 +338,7 @@ class StateCache:
         b = states.shape[0]
         _dense(states, (b,) + self.shape[1:], torch.float32, "states", self.values.device)
         _dense(slots, (b,), torch.int32, "slots", self.values.device)
-        return _lib.make_cache_problem(b, *self.shape[1:], self.shape[0], self.FORMATS[self.form])
+        return _cache_problem(b, *self.shape[1:], self.shape[0], self.FORMATS[self.form])
 
     def store(self, states, slots=None, stream=None, check=True):
         """Quantise states (b, H, P, N) into their slots (default: 0 .. b-1)."""
