@@ -50,9 +50,9 @@ struct DeltaBufs {
   void* fin;
   const void *dy, *dfin;
   void *dq, *dk, *dv, *dg, *dbeta, *dinit;
-  // recurrent kernels (fp32): S (b,H,nc,P,N) states entering each chunk,
-  // w (b,L,H,P), D (b,H,nc,P,N) gradients of the state after each chunk,
-  // r (b,L,H,P).  Tensor-core kernels: bf16 S, D (b,H,nc,P,N), w transposed
+  // fp32 kernels: S (b,H,nc,P,N) states entering each chunk, w (b,L,H,P),
+  // D (b,H,nc,P,N) gradients of the state after each chunk, r (b,L,H,P),
+  // T = (I + M)^-1 and A (b,H,nc,C,C), e (b,H,nc,2,C).  Tensor-core kernels: bf16 S, D (b,H,nc,P,N), w transposed
   // (b,H,nc,P,C), T and A (b,H,nc,C,C), and fp32 gate records e
   // (b,H,nc,kGateRows,C); r is dv.
   void *S, *w, *T, *A, *e, *D, *r;
@@ -89,9 +89,12 @@ constexpr int kDeltaChunk = 64;  // tokens per chunk of the tensor-core kernels
 // the number of sequence starts up to the token (an int).
 enum { kGateE, kGateOB, kGateGam, kGateBeta, kGateO, kGateHalf, kGateSeg, kGateRows };
 
-cudaError_t launch_delta_recurrent(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+constexpr int kDeltaChunkF32 = 32;  // and of the fp32 kernels
+
 cudaError_t launch_delta_step(const DeltaPlan& p, const DeltaBufs& f, const DeltaStep& st, cudaStream_t s);
-cudaError_t launch_delta_reverse(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+// the fp32 kernels
+cudaError_t launch_delta_prep_simt(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
+cudaError_t launch_delta_chain_simt(const DeltaPlan& p, const DeltaBufs& f, bool reverse, cudaStream_t s);
 cudaError_t launch_delta_grad(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s);
 
 // the tensor-core kernels

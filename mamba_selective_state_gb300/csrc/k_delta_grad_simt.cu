@@ -18,7 +18,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kC = 32;        // tokens per chunk
+constexpr int kC = kDeltaChunkF32;
 constexpr int kTp = 16;       // headdim columns staged at a time
 constexpr int kThreads = 256; // 16 pairs of rows x 16 columns
 

@@ -55,7 +55,7 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
   p->bf16 = pr->dtype == SSD_BF16;
   p->st_bf16 = pr->state_dtype == SSD_BF16;
   p->tc = p->bf16 && p->P % 64 == 0 && (p->N == 64 || p->N == 128) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0;
-  p->C = p->tc ? kDeltaChunk : 32;
+  p->C = p->tc ? kDeltaChunk : kDeltaChunkF32;
   p->nc = (p->L + p->C - 1) / p->C;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -82,10 +82,18 @@ int make_delta_plan(const ssd_delta_problem* pr, DeltaPlan* p) {
     p->bwd_bytes = off;
     return SSD_OK;
   }
+  const size_t units = bh * p->nc, cc = (size_t)p->C * p->C * 4;
   p->sv_S = take(states * 4);
   p->sv_w = take(rows * 4);
+  p->sv_T = take(units * cc);
+  p->sv_A = take(units * cc);
+  p->sv_e = take(units * 2 * p->C * 4);
   p->saved_bytes = off;
-  p->fwd_bytes = kStatusBytes;
+  off = kStatusBytes;
+  p->wf_T = take(units * cc);
+  p->wf_A = take(units * cc);
+  p->wf_e = take(units * 2 * p->C * 4);
+  p->fwd_bytes = off;
   off = kStatusBytes;
   p->wb_D = take(states * 4);
   p->wb_r = take(rows * 4);
@@ -149,15 +157,16 @@ int ssd_delta_fwd(const ssd_delta_problem* prob, const void* q, const void* k, c
   char* ws = static_cast<char*>(workspace);
   f.status = reinterpret_cast<int*>(ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  f.T = sv ? sv + p.sv_T : ws + p.wf_T;
+  f.A = sv ? sv + p.sv_A : ws + p.wf_A;
+  f.e = sv ? sv + p.sv_e : ws + p.wf_e;
   if (p.tc) {
-    f.T = sv ? sv + p.sv_T : ws + p.wf_T;
-    f.A = sv ? sv + p.sv_A : ws + p.wf_A;
-    f.e = sv ? sv + p.sv_e : ws + p.wf_e;
     DELTA_LAUNCH(launch_delta_prep(p, f, s));
     DELTA_LAUNCH(launch_delta_chain_fwd(p, f, s));
-    return SSD_OK;
+  } else {
+    DELTA_LAUNCH(launch_delta_prep_simt(p, f, s));
+    DELTA_LAUNCH(launch_delta_chain_simt(p, f, false, s));
   }
-  DELTA_LAUNCH(launch_delta_recurrent(p, f, s));
   return SSD_OK;
 }
 
@@ -192,18 +201,18 @@ int ssd_delta_bwd(const ssd_delta_problem* prob, const void* q, const void* k, c
   f.D = ws + p.wb_D;
   f.r = ws + p.wb_r;
   f.status = reinterpret_cast<int*>(ws);
+  f.T = sv + p.sv_T;
+  f.A = sv + p.sv_A;
+  f.e = sv + p.sv_e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p.tc) {
-    f.T = sv + p.sv_T;
-    f.A = sv + p.sv_A;
-    f.e = sv + p.sv_e;
     if (cudaMemsetAsync(f.status, 0, sizeof(int), s) != cudaSuccess) return SSD_ERR_CUDA;
     DELTA_LAUNCH(launch_delta_chain_bwd(p, f, s));
     DELTA_LAUNCH(launch_delta_grad_tc(p, f, s));
-    return SSD_OK;
+  } else {
+    DELTA_LAUNCH(launch_delta_chain_simt(p, f, true, s));
+    DELTA_LAUNCH(launch_delta_grad(p, f, s));
   }
-  DELTA_LAUNCH(launch_delta_reverse(p, f, s));
-  DELTA_LAUNCH(launch_delta_grad(p, f, s));
   return SSD_OK;
 }
 
