@@ -6,14 +6,14 @@
 // tokens of dY and of r as the 128 rows of one left operand,
 //
 //   [dY ; r] [S0 | w']  ->  dY S0, r S0 (64 x dstate) and dY w', r w' (64 x 64)
-//   [.. ; w]  D1        ->  w D1
+//   [w ; w]  D1         ->  w D1, twice: each half of the warps takes half its columns
 //
 // come from tcgen05 products into tensor memory (S0, D1 and w' are stored with
 // headdim as rows, as the chains write them, and enter as MN-major operands).
 // Sixteen warps read them back: a thread owns one token's row -- of dY and dq
-// in the lower 64 lanes, of r, w and dk in the upper -- and a quarter of the
+// in the lower 64 lanes, of r and dk in the upper -- and a quarter of the
 // columns, so the dot products with q and k and the sums over heads stay in
-// its registers.  q k^T and k k^T do not depend on the head, and the pairs'
+// its registers (as pairs, for the two-value fp32 multiply-add).  q k^T and k k^T do not depend on the head, and the pairs'
 // part of dq and dk is summed over the heads before its products with k and
 // q: both are one more product of 128 rows per group.  The pairs'
 // contributions to dgam are formed once in fp32 and summed by rows and by
@@ -34,12 +34,10 @@ constexpr int kEpi = kWarps * 32;
 constexpr int kThreads = kEpi + 128;          // and the control warp with three idle ones: registers
                                               // are handed over by groups of four warps
 // Registers a thread: 640 threads are launched with 96; the control warps keep
-// 32 and the epilogue warps take 112 (4 x 112 + 32 = 5 x 96).  Without that
-// the epilogue spills, and the ring leaves the L1 cache too small for it.
-// named barriers: the epilogue's own; a head's sums are written (by parity), and have been used
-constexpr int kBarSums = 2, kBarFree = 4;
-constexpr int kSums = kEpi + 64;  // the epilogue, the warp of <S0, D1> and the one that uses the sums
-constexpr int kRegsEpi = 112, kRegsCtl = 32;
+// 64 and the epilogue warps take 104 (4 x 104 + 64 = 5 x 96).  Where the
+// epilogue spills, it waits: the ring leaves the L1 cache too small for that.
+constexpr int kRegsEpi = 104, kRegsCtl = 64;
+constexpr int kPairThreads = 12 * 32;         // of the warps that have pairs at all
 constexpr uint32_t kTile = 8192;              // [64][64] bf16, 128-byte swizzle
 constexpr int kGate = kGateRows * kC * 4;
 
@@ -50,18 +48,45 @@ struct GradMaps {
 template <int N>
 struct GradSmem {
   static constexpr int NB = N / 64;
-  // per head and 64 columns of headdim: dY, r, S0, w, D1
-  static constexpr int stage = (2 + 2 * NB + 1) * (int)kTile;
-  static constexpr int kStages = N == 128 ? 3 : 4;
+  // per head and 64 columns of headdim: dY, r, S0, w, w, D1
+  static constexpr int stage = (2 + 2 * NB + 2) * (int)kTile;
+  static constexpr int kStages = N == 128 ? 2 : 3;
   // q and k: for each 64 columns of dstate the tile of q above that of k
   static constexpr int oQK = 0, oSt = NB * 2 * (int)kTile, oGate = oSt + kStages * stage,  // four gate records
                        oCol = oGate + 4 * kGate,       // [2][4][64] column sums by lane quarter
                        oRow = oCol + 2 * 4 * kC * 4,   // [2][4][128] row sums by column quarter
-                       oOut = oRow + 2 * 4 * 128 * 4,  // [2][4][64] k.(D1 w)
-                       oDiag = oOut + 2 * 4 * kC * 4, oRed = oDiag + 2 * kC * 4, oBar = oRed + 16,
+                       oOut = oRow + 2 * 4 * 128 * 4,  // [2][8][64] k.(D1 w) by columns
+                       oDiag = oOut + 2 * 8 * kC * 4, oRed = oDiag + 2 * kC * 4,
+                       oPair = oRed + 16,                    // q k^T or k k^T by pair of columns and thread
+                       oHalf = oPair + 8 * kPairThreads * 8, // the lower lanes' half of w D1, likewise
+                       oBar = oHalf + N / 16 * (kEpi / 2) * 8,
                        bytes = oBar + 256 + 1024;
   static_assert(kStages * stage >= 4 * (int)kTile, "the pairs' operand reuses the ring");
 };
+
+// Two fp32 values in one register pair
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 sub2(f2 a, f2 b) { return fma2(b, pair2(-1.f, -1.f), a); }
 
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
@@ -97,8 +122,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sm = smem_u32(raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(raw + L::oBar);
   uint64_t *s_full = bars, *s_free = bars + 4, *g_full = bars + 8, *g_free = bars + 12, *x_full = bars + 16,
-           *x_free = bars + 18, *x3_free = bars + 20, *qk_full = bars + 21, *qk_done = bars + 22, *z_done = bars + 23;
-  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bars + 24);
+           *x_free = bars + 18, *x3_free = bars + 20, *qk_full = bars + 21, *qk_done = bars + 22, *z_done = bars + 23,
+           *sums = bars + 24, *used = bars + 26;  // a head's sums are written, and have been used
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bars + 28);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int c = (int)(blockIdx.x % p.nc);
   const int grp = (int)((blockIdx.x / p.nc) % p.G);
@@ -119,6 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(x_full + i, 1);
       mbar_init(x_free + i, kWarps);
+      mbar_init(sums + i, kWarps + 1);
+      mbar_init(used + i, 1);
     }
     mbar_init(x3_free, kWarps);
     mbar_init(qk_full, 1);
@@ -154,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(d, &m.dy, s_full + st, 64 * pc, h, t0, bi);
         tma_load_4d(d + kTile, &m.dv, s_full + st, 64 * pc, h, t0, bi);
         for (int j = 0; j < NB; ++j) tma_load_4d(d + (2 + j) * kTile, &m.S, s_full + st, 64 * j, 64 * pc, c, bh);
-        tma_load_4d(d + (2 + NB) * kTile, &m.w, s_full + st, 0, 64 * pc, c, bh);
-        for (int j = 0; j < NB; ++j) tma_load_4d(d + (3 + NB + j) * kTile, &m.D, s_full + st, 64 * j, 64 * pc, c, bh);
+        for (int j = 0; j < 2; ++j) tma_load_4d(d + (2 + NB + j) * kTile, &m.w, s_full + st, 0, 64 * pc, c, bh);
+        for (int j = 0; j < NB; ++j) tma_load_4d(d + (4 + NB + j) * kTile, &m.D, s_full + st, 64 * j, 64 * pc, c, bh);
       };
       mbar_expect_tx(qk_full, NB * 2 * kTile);
       for (int j = 0; j < NB; ++j) {
@@ -163,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(raw + L::oQK + (2 * j + 1) * kTile, &m.k, qk_full, 64 * j, grp, t0, bi);
       }
       int loaded = 0;
-      for (; loaded < L::kStages - 1 && loaded < steps; ++loaded) load(loaded);
+      for (; loaded < L::kStages && loaded < steps; ++loaded) load(loaded);
       // [q ; k] k^T into the first columns
       mbar_wait_flag(qk_full, 0, ok);
       tc_fence_after();
@@ -175,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(qk_done);
       for (int s = 0; s < steps; ++s) {
         const int hh = s / npc, pc = s % npc, st = s % L::kStages, use = s / L::kStages, buf = hh & 1;
-        if (loaded < steps) load(loaded++);
+        // the stage of the step before: its products and <S0, D1> were taken during the last head's epilogue
+        if (s >= 1 && loaded < steps) load(loaded++);
         mbar_wait_flag(s_full + st, use & 1, ok);
         if (pc == 0) {
           // the buffer's last head has been read (the first head's: q k^T)
@@ -183,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (hh == 0) mbar_wait_flag(z_done, 0, ok);
         }
         tc_fence_after();
-        const uint32_t base = sm + L::oSt + st * L::stage, S0 = base + 2 * kTile, D1 = base + (3 + NB) * kTile;
+        const uint32_t base = sm + L::oSt + st * L::stage, S0 = base + 2 * kTile, D1 = base + (4 + NB) * kTile;
         for (int ks = 0; ks < 4; ++ks)
           mma_bf16(tm + buf * kX, smem_desc(base + ks * 32, 16, 1024, kSwz128),
                    smem_desc(S0 + ks * 2048, kTile, 1024, kSwz128), idesc_bf16(128, N + 64, 0, 1), pc > 0 || ks > 0);
@@ -191,9 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_flag(x3_free, (hh - 1) & 1, ok);
           tc_fence_after();
         }
-        // rows 64.. are w: the tile before it only fills the product's 128 rows
         for (int ks = 0; ks < 4; ++ks)
-          mma_bf16(tm + kX3, smem_desc(S0 + (NB - 1) * kTile + ks * 2048, kTile, 1024, kSwz128),
+          mma_bf16(tm + kX3, smem_desc(S0 + NB * kTile + ks * 2048, kTile, 1024, kSwz128),
                    smem_desc(D1 + ks * 2048, kTile, 1024, kSwz128), idesc_bf16(128, N, 1, 1), pc > 0 || ks > 0);
         mma_commit(s_free + st);
         if (pc == npc - 1) mma_commit(x_full + buf);
@@ -217,17 +245,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int* sg = reinterpret_cast<const int*>(ga + kGateSeg * kC);
         const float* colp = reinterpret_cast<const float*>(raw + L::oCol) + buf * 4 * kC;
         const float* rowp = reinterpret_cast<const float*>(raw + L::oRow) + buf * 4 * 128;
-        const float* outp = reinterpret_cast<const float*>(raw + L::oOut) + buf * 4 * kC;
+        const float* outp = reinterpret_cast<const float*>(raw + L::oOut) + buf * 8 * kC;
         const float* diag = reinterpret_cast<const float*>(raw + L::oDiag) + buf * kC;
         mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
-        bar_sync(kBarSums + buf, kSums);
+        mbar_wait_flag(sums + buf, (hh >> 1) & 1, ok);
         // this head's dbeta, and dg as the reverse cumulative sum of dgam
         float d[2], all = 0.f;
         const float sdot = reinterpret_cast<const float*>(raw + L::oRed)[buf];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int a = 2 * lane + j;
-          const float o = (outp[a] + outp[kC + a]) + (outp[2 * kC + a] + outp[3 * kC + a]);
+          float o = 0.f;
+#pragma unroll
+          for (int x2 = 0; x2 < 8; ++x2) o += outp[x2 * kC + a];
           const float cj = (colp[a] + colp[kC + a]) + (colp[2 * kC + a] + colp[3 * kC + a]);
           float r = 0.f;
 #pragma unroll
@@ -256,8 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a < n) static_cast<__nv_bfloat16*>(f.dg)[(tok0 + a) * p.H + h0 + hh] = __float2bfloat16_rn(v);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(g_free + (hh & 3));
-        if (hh + 2 < p.hpg) bar_arrive(kBarFree + buf, kSums);
+        if (lane == 0) {
+          mbar_arrive(g_free + (hh & 3));
+          mbar_arrive(used + buf);
+        }
       }
     } else if (w == kWarps + 3) {
       // <S0, D1> of every head: the diagonal of 16 x 8 products
@@ -267,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int pc = 0; pc < npc; ++pc) {
           const int s = hh * npc + pc, st = s % L::kStages;
           mbar_wait_flag(s_full + st, (s / L::kStages) & 1, ok);
-          const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 1) * kTile;
+          const uint32_t S0 = sm + L::oSt + st * L::stage + 2 * kTile, D1 = S0 + (NB + 2) * kTile;
           for (int r = 0; r < 64; r += 16) {
             float x0[4] = {}, x1[4] = {};
 #pragma unroll
@@ -285,10 +317,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
-        if (hh >= 2) bar_sync(kBarFree + (hh & 1), kSums);
-        if (lane == 0) reinterpret_cast<float*>(raw + L::oRed)[hh & 1] = sd;
+        if (hh >= 2) mbar_wait_flag(used + (hh & 1), ((hh >> 1) - 1) & 1, ok);
+        if (lane == 0) {
+          reinterpret_cast<float*>(raw + L::oRed)[hh & 1] = sd;
+          mbar_arrive(sums + (hh & 1));
+        }
         __syncwarp();
-        bar_arrive(kBarSums + (hh & 1), kSums);
       }
     }
   } else {
@@ -297,27 +331,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 32 * quarter + lane, i = row & 63;
     const bool lower = quarter < 2;                  // dY, dq, q k^T; else r, w, dk, k k^T
     const uint32_t tlane = tmem_addr(tm, 32 * quarter, 0);
-    float acc[NC], pair[16], qk[16];
-    // acc[j0 ..] += fac x over 16 columns of a product; returns the dot product with this row of q or k
-    const uint32_t own = sm + L::oQK + ((cq * NC) >> 6) * 2 * kTile + (lower ? 0 : kTile);
-    auto add16 = [&](float (&a)[NC], int j0, uint32_t col, float fac) {
-      float x[16], dot = 0.f;
-      tmem_ld16(col, x);
+    // sums over heads: this row of dq or dk, the pairs, and in shared memory (registers are short) the lower lanes'
+    // half of w D1
+    f2 acc[NC / 2], pair[8];
+    f2* acc3 = reinterpret_cast<f2*>(raw + L::oHalf) + (cq * 64 + row);  // [NC / 4][256], the lower lanes' only
+    // this thread's 16 products of q or k and k, scaled
+    f2* qk = reinterpret_cast<f2*>(raw + L::oPair) + ((cq < 2 ? w : 8 + 2 * (cq - 2) + (quarter >> 1)) * 32 + lane);
+    // Column pairs c0.. of a product: a[] += fac x; returns the dot product with the row of q or k at `own`
+    const uint32_t own_k = sm + L::oQK + ((cq * NC) >> 6) * 2 * kTile + kTile, own = lower ? own_k - kTile : own_k;
+    auto add8 = [&](f2* a, const float* x, uint32_t row_at, int col, f2 fac, f2 dot) {
+      const uint4 v4 = lds128(row_at + tile_off<8>(i, (((cq * NC) & 63) + col) / 8));
+      const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4 v4 = lds128(own + tile_off<8>(i, (((cq * NC) & 63) + j0) / 8 + u));
-        const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 y = unpack2(v[j]);
-          const float x0 = x[8 * u + 2 * j], x1 = x[8 * u + 2 * j + 1];
-          a[j0 + 8 * u + 2 * j] += fac * x0;
-          a[j0 + 8 * u + 2 * j + 1] += fac * x1;
-          dot += y.x * x0 + y.y * x1;
-        }
+      for (int j = 0; j < 4; ++j) {
+        const f2 x2 = pair2(x[2 * j], x[2 * j + 1]);
+        a[j] = fma2(fac, x2, a[j]);
+        dot = fma2(pair2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xffff0000u)), x2, dot);
       }
       return dot;
     };
+    const f2 zero2 = pair2(0.f, 0.f);
     // the pairs (i, 16 cq + j): all of them, none, or those around the diagonal
     const bool none = !(quarter & 1) && cq >= 2, all = (quarter & 1) && cq < 2;
     const float sign = lower ? p.scale : -1.f;
@@ -326,50 +359,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_flag(qk_full, 0, ok);
       mbar_wait_flag(qk_done, 0, ok);
       tc_fence_after();
-      tmem_ld16(tlane + cq * 16, qk);
+      float q16[16];
+      tmem_ld16(tlane + cq * 16, q16);
       tc_fence_before();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        qk[j] *= sign;
-        qk_own = 16 * cq + j == i ? qk[j] : qk_own;
+        q16[j] *= sign;
+        qk_own = 16 * cq + j == i ? q16[j] : qk_own;
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!none) qk[j * kPairThreads] = pair2(q16[2 * j], q16[2 * j + 1]);
       for (int x = tid; x < 2 * 4 * kC; x += kEpi) reinterpret_cast<float*>(raw + L::oCol)[x] = 0.f;
       // every warp has read q k^T before the first head's product takes its place
       bar_sync(1, kEpi);
       if (tid == 0) mbar_arrive(z_done);
     }
 #pragma unroll
-    for (int j = 0; j < NC; ++j) acc[j] = 0.f;
+    for (int j = 0; j < NC / 2; ++j) acc[j] = zero2;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) pair[j] = 0.f;
+    for (int j = 0; j < NC / 4; ++j)
+      if (lower) acc3[j * (kEpi / 2)] = zero2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pair[j] = zero2;
     for (int hh = 0; hh < p.hpg; ++hh) {
       const int buf = hh & 1;
       const float* ga = reinterpret_cast<const float*>(raw + L::oGate + (hh & 3) * kGate);
       const int* sg = reinterpret_cast<const int*>(ga + kGateSeg * kC);
       float* colp = reinterpret_cast<float*>(raw + L::oCol) + buf * 4 * kC;
       float* rowp = reinterpret_cast<float*>(raw + L::oRow) + buf * 4 * 128;
-      float* outp = reinterpret_cast<float*>(raw + L::oOut) + buf * 4 * kC;
+      float* outp = reinterpret_cast<float*>(raw + L::oOut) + buf * 8 * kC;
       float* diag = reinterpret_cast<float*>(raw + L::oDiag) + buf * kC;
-      if (hh >= 2) bar_sync(kBarFree + buf, kSums);  // head hh - 2's sums have been used
+      if (hh >= 2) mbar_wait_flag(used + buf, ((hh >> 1) - 1) & 1, ok);  // head hh - 2's sums
       mbar_wait_flag(g_full + (hh & 3), (hh >> 2) & 1, ok);
       const float ei = ga[i], be = ga[kGateBeta * kC + i], oi = ga[kGateO * kC + i];
       mbar_wait_flag(x_full + buf, (hh >> 1) & 1, ok);
       tc_fence_after();
-      if (!lower) {  // w D1: dk_i += o_i beta_i D1 w_i
-        float dot = 0.f;
+      {  // w D1: dk_i += o_i beta_i D1 w_i, the lower lanes the first half of this quarter's columns
+        constexpr int H3 = NC / 2;
+        float x3[16];
+        tmem_ld16(tlane + kX3 + cq * NC + (NC == 32 && !lower ? 16 : 0), x3);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x3_free);
+        const f2 fac = pair2(oi * be, oi * be);
+        f2 dot = zero2;
 #pragma unroll
-        for (int j0 = 0; j0 < NC; j0 += 16) dot += add16(acc, j0, tlane + kX3 + cq * NC + j0, oi * be);
-        outp[cq * kC + i] = oi * dot;
+        for (int u = 0; u < H3 / 8; ++u) {
+          if (lower) {
+            f2 t[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[j] = acc3[(4 * u + j) * (kEpi / 2)];
+            dot = add8(t, x3 + 8 * u, own_k, 8 * u, fac, dot);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc3[(4 * u + j) * (kEpi / 2)] = t[j];
+          } else
+            dot = add8(acc + H3 / 2 + 4 * u, x3 + (NC == 32 ? 0 : H3) + 8 * u, own_k, H3 + 8 * u, fac, dot);
+        }
+        const float2 d = both2(dot);
+        outp[((lower ? 0 : 4) + cq) * kC + i] = oi * (d.x + d.y);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x3_free);
       // dY S0 or r S0: dq_i += scale e_i ..., dk_i -= e_i ...
-      const float fac = lower ? p.scale * ei : -ei;
-      float rsum = 0.f;
+      const float fac1 = lower ? p.scale * ei : -ei;
+      f2 rsum2 = zero2;
 #pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += 16) rsum += add16(acc, j0, tlane + buf * kX + cq * NC + j0, fac);
-      rsum *= fac;
+      for (int j0 = 0; j0 < NC; j0 += 16) {
+        float x[16];
+        tmem_ld16(tlane + buf * kX + cq * NC + j0, x);
+        const f2 fac = pair2(fac1, fac1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) rsum2 = add8(acc + j0 / 2 + 4 * u, x + 8 * u, own, j0 + 8 * u, fac, rsum2);
+      }
+      rsum2 = mul2(rsum2, pair2(fac1, fac1));
       float x[16];
       if (!none) tmem_ld16(tlane + buf * kX + N + cq * 16, x);
       tc_fence_before();
@@ -378,24 +439,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (all) {
         // below the diagonal the decay is that from token 32 times that to it
         const float ri = ga[kGateHalf * kC + i];
+        const f2 ri2 = pair2(ri, ri);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int j0 = 16 * cq + 4 * u;
-          const float4 c4 = *reinterpret_cast<const float4*>(ga + kGateHalf * kC + j0);
-          const float4 b4 = *reinterpret_cast<const float4*>(ga + kGateBeta * kC + j0);
-          const float cj[4] = {c4.x, c4.y, c4.z, c4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
+          const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(ga + kGateHalf * kC + 16 * cq + 4 * u);
+          const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(ga + kGateBeta * kC + 16 * cq + 4 * u);
+          const f2 cj[2] = {c4.x, c4.y}, bj[2] = {b4.x, b4.y};
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int j = 4 * u + v;
-            const float z = x[j] * ri * cj[v];
-            pair[j] += bj[v] * z;
-            x[j] = z * qk[j];
-            rsum += bj[v] * x[j];
+          for (int v = 0; v < 2; ++v) {
+            const int j = 2 * u + v;
+            const f2 z = mul2(pair2(x[2 * j], x[2 * j + 1]), mul2(ri2, cj[v]));
+            pair[j] = fma2(bj[v], z, pair[j]);
+            const f2 both = mul2(z, qk[j * kPairThreads]);
+            rsum2 = fma2(bj[v], both, rsum2);
+            const float2 bb = both2(both);
+            x[2 * j] = bb.x;
+            x[2 * j + 1] = bb.y;
           }
         }
       } else if (!none) {
         const float gi = ga[kGateGam * kC + i];
         const int si = sg[i];
+        const f2 gi2 = pair2(gi, gi);
         if (lower) {  // a token's own pair: it does not depend on the decays
           float own_x = 0.f;
 #pragma unroll
@@ -407,32 +472,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int j0 = 16 * cq + 4 * u;
-          const float4 g4 = *reinterpret_cast<const float4*>(ga + kGateGam * kC + j0);
-          const float4 b4 = *reinterpret_cast<const float4*>(ga + kGateBeta * kC + j0);
+          const ulonglong2 g4 = *reinterpret_cast<const ulonglong2*>(ga + kGateGam * kC + j0);
+          const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(ga + kGateBeta * kC + j0);
           const int4 s4 = *reinterpret_cast<const int4*>(sg + j0);
-          const float gj[4] = {g4.x, g4.y, g4.z, g4.w}, bj[4] = {b4.x, b4.y, b4.z, b4.w};
+          const f2 gj[2] = {g4.x, g4.y}, bj[2] = {b4.x, b4.y};
           const int sj[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int j = 4 * u + v;
-            const float Ex = exp2_fast(gi - gj[v]) * x[j];
-            const float z = (j0 + v < i) & (sj[v] == si) ? Ex : 0.f;
-            pair[j] += bj[v] * z;
-            x[j] = z * qk[j];
-            rsum += bj[v] * x[j];
+          for (int v = 0; v < 2; ++v) {
+            const int j = 2 * u + v, jj = j0 + 2 * v;
+            const float2 a = both2(sub2(gi2, gj[v]));
+            const float z0 = exp2_fast(a.x) * x[2 * j], z1 = exp2_fast(a.y) * x[2 * j + 1];
+            const f2 z = pair2((jj < i) & (sj[2 * v] == si) ? z0 : 0.f, (jj + 1 < i) & (sj[2 * v + 1] == si) ? z1 : 0.f);
+            pair[j] = fma2(bj[v], z, pair[j]);
+            const f2 both = mul2(z, qk[j * kPairThreads]);
+            rsum2 = fma2(bj[v], both, rsum2);
+            const float2 bb = both2(both);
+            x[2 * j] = bb.x;
+            x[2 * j + 1] = bb.y;
           }
         }
       }
-      rowp[cq * 128 + row] = rsum;
+      const float2 rs = both2(rsum2);
+      rowp[cq * 128 + row] = rs.x + rs.y;
       if (!none) {
         const float cs = sum16(x, lane);
         if ((lane & 1) == 0) colp[quarter * kC + 16 * cq + (lane >> 1)] = cs;
       }
       __syncwarp();
-      bar_arrive(kBarSums + buf, kSums);
+      if (lane == 0) mbar_arrive(sums + buf);
     }
+    float z16[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) pair[j] = sign * (lower && 16 * cq + j == i ? pair_own : pair[j]);
+    for (int j = 0; j < 8; ++j) {
+      const float2 v = both2(pair[j]);
+      z16[2 * j] = sign * (lower && 16 * cq + 2 * j == i ? pair_own : v.x);
+      z16[2 * j + 1] = sign * (lower && 16 * cq + 2 * j + 1 == i ? pair_own : v.y);
+    }
     // The pairs' part for all heads: rows of [0 | Z ; Z^T | M + M^T] against
     // [q ; k], Z (i, j) and M (i, j) summed over the heads.  All of the ring's
     // products are done: the last head's x_full followed them.
@@ -447,14 +522,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(Zb + 2 * kTile + tile_off<8>(i, 2 * cq + u)),
-                     "r"(pack2(pair[8 * u], pair[8 * u + 1])), "r"(pack2(pair[8 * u + 2], pair[8 * u + 3])),
-                     "r"(pack2(pair[8 * u + 4], pair[8 * u + 5])), "r"(pack2(pair[8 * u + 6], pair[8 * u + 7]))
+                     "r"(pack2(z16[8 * u], z16[8 * u + 1])), "r"(pack2(z16[8 * u + 2], z16[8 * u + 3])),
+                     "r"(pack2(z16[8 * u + 4], z16[8 * u + 5])), "r"(pack2(z16[8 * u + 6], z16[8 * u + 7]))
                      : "memory");
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const int jj = 16 * cq + j;
-      const __nv_bfloat16 v = __float2bfloat16_rn(pair[j]);
+      const __nv_bfloat16 v = __float2bfloat16_rn(z16[j]);
       const uint16_t b = *reinterpret_cast<const uint16_t*>(&v);
       if (lower) {  // Z^T below the zeros
         asm volatile("st.shared.b16 [%0], %1;" ::"r"(Zb + elem_off<8>(64 + jj, i)), "h"(b) : "memory");
@@ -475,7 +550,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld16(tlane + cq * NC + j0, x);
       uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = pack2(acc[j0 + 2 * j] + x[2 * j], acc[j0 + 2 * j + 1] + x[2 * j + 1]);
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = both2(acc[j0 / 2 + j]);
+        const int col = j0 + 2 * j;
+        // (the lower lanes' half of w D1 belongs to the same token's row of dk)
+        const float2 more = !lower && col < NC / 2 ? both2(acc3[col / 2 * (kEpi / 2) - 64]) : make_float2(0.f, 0.f);
+        o[j] = pack2(v.x + x[2 * j] + more.x, v.y + x[2 * j + 1] + more.y);
+      }
       if (i < n) {
         reinterpret_cast<uint4*>(dst + j0)[0] = make_uint4(o[0], o[1], o[2], o[3]);
         reinterpret_cast<uint4*>(dst + j0)[1] = make_uint4(o[4], o[5], o[6], o[7]);
