@@ -52,9 +52,9 @@ struct DeltaBufs {
   void *dq, *dk, *dv, *dg, *dbeta, *dinit;
   // fp32 kernels: S (b,H,nc,P,N) states entering each chunk, w (b,L,H,P),
   // D (b,H,nc,P,N) gradients of the state after each chunk, r (b,L,H,P),
-  // T = (I + M)^-1 and A (b,H,nc,C,C), e (b,H,nc,2,C).  Tensor-core kernels: bf16 S, D (b,H,nc,P,N), w transposed
-  // (b,H,nc,P,C), T and A (b,H,nc,C,C), and fp32 gate records e
-  // (b,H,nc,kGateRows,C); r is dv.
+  // T = (I + M)^-1 and A (b,H,nc,C,C), e (b,H,nc,2,C).  Tensor-core kernels:
+  // bf16 S, D (b,H,nc,P,N), w transposed (b,H,nc,P,C), T and A (b,H,nc,C,C; see
+  // k_delta_prep.cu), and fp32 gate records e (b,H,nc,kGateRows,C); r is dv.
   void *S, *w, *T, *A, *e, *D, *r;
   int* status;  // device status word, at the start of the workspace
 };

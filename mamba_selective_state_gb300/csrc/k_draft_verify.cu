@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draf
   for (int round = 0; round < 2; ++round) {
     // A thread meets its words in ascending order, so the first of equal ratios
     // stays.  A ratio is divided out only where an estimate of it (off by a few
-    // units of 2^-23) says that it may be the largest yet; ratios that are not
-    // above zero, or are NaN, never are.
+    // units of 2^-23, where divisor and ratio are neither huge nor tiny) says
+    // that it may be the largest yet; ratios that are not above zero, or are
+    // NaN, never are.
     float top = 0.f, bar = 0.f;
     unsigned at = 0;
     constexpr int kAhead = 8;
@@ -103,12 +104,12 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draf
       for (int i = 0; i < kAhead; ++i) {
         const long long v = v0 + i * kThreads;
         if (round == 0 && v == one) w[i] -= 1.f;
-        if (w[i] > 0.f && !(__fdividef(w[i], r[i]) < bar)) {
+        if (w[i] > 0.f && (!(__fdividef(w[i], r[i]) < bar) || r[i] > 8e37f)) {
           const float s = w[i] / r[i];
           if (s > top) {
             top = s;
             at = (unsigned)v;
-            bar = s * 0.999f;
+            bar = s > 1e-37f ? s * 0.999f : 0.f;
           }
         }
       }

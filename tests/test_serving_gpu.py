@@ -77,6 +77,19 @@ def test_verification_at_its_limits():
     assert kept[0] == 0 and kept[6] == 0 and tokens[6, 0] == 0 and tokens[11, 0] == 17
 
 
+@pytest.mark.parametrize("noise,weight", [(1e38, 1.0), (3e38, 1.0), (1e-30, 1.0), (1.0, 1e-38),
+                                          (1e-3, 1e-44)])
+def test_verification_at_extreme_ratios(noise, weight):
+    """Divisors and ratios at the ends of the fp32 range: still the largest
+    quotient, in the words' order."""
+    rng = np.random.default_rng(9)
+    b, V = 2, 3000
+    t = lambda x: torch.from_numpy(x.astype(np.float32))  # noqa: E731
+    verify(dict(target=t(weight * rng.uniform(0.1, 1, (b, 1, V))), draft=torch.zeros(b, 0, V),
+                tokens=torch.zeros(b, 0, dtype=torch.int32), uniform=torch.zeros(b, 0),
+                noise=t(noise * rng.uniform(0.5, 1, (b, V))), lengths=None))
+
+
 def test_verification_ties_take_the_lowest_index():
     b, V = 3, 20000
     c = dict(target=torch.full((b, 1, V), 1.0 / V), draft=torch.zeros(b, 0, V),
