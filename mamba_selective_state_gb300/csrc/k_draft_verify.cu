@@ -75,10 +75,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draf
   const bool refused = kept < len_s;
   const T* p = static_cast<const T*>(a.p) + (b * (a.K + 1) + kept) * a.V;
   const T* q = refused && a.q ? static_cast<const T*>(a.q) + (b * a.K + kept) * a.V : nullptr;
-  const long long one = refused && !a.q ? a.tok[b * a.K + kept] : -1;
+  const int one = refused && !a.q ? a.tok[b * a.K + kept] : -1;
   const float* noise = a.noise + b * a.V;
-  const long long per = (a.V + ncta - 1) / ncta;
-  const long long lo = rank * per, hi = lo + per < a.V ? lo + per : a.V;
+  // (a row's words are counted in 32 bits)
+  const unsigned V = (unsigned)a.V, per = (V + ncta - 1) / ncta;
+  const unsigned lo = min(rank * per, V), hi = min(lo + per, V);
   // round 0: the residual weights; round 1, only where none was positive: p
   unsigned long long best = 0;
   for (int round = 0; round < 2; ++round) {
@@ -90,25 +91,39 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draf
     float top = 0.f, bar = 0.f;
     unsigned at = 0;
     constexpr int kAhead = 8;
-    for (long long v0 = lo + threadIdx.x; v0 < hi; v0 += kAhead * kThreads) {
+    for (unsigned v0 = lo + threadIdx.x; v0 < hi; v0 += kAhead * kThreads) {
+      // (unconditional loads, past the end of the last word: all are in flight before the first is used)
       float w[kAhead], r[kAhead];
+      T pv[kAhead], qv[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const long long v = v0 + i * kThreads;
-        const bool in = v < hi;
-        w[i] = in ? to_f(p[v]) : 0.f;
-        r[i] = in ? noise[v] : 1.f;
-        if (round == 0 && q) w[i] -= in ? to_f(q[v]) : 0.f;
+        const unsigned v = min(v0 + i * kThreads, hi - 1);
+        pv[i] = p[v];
+        r[i] = noise[v];
+      }
+      if (round == 0 && q) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) qv[i] = q[min(v0 + i * kThreads, hi - 1)];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) w[i] = to_f(pv[i]) - to_f(qv[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) w[i] = to_f(pv[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) w[i] = v0 + i * kThreads < hi ? w[i] : 0.f;
+      if (round == 0 && one >= 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) w[i] -= v0 + i * kThreads == one ? 1.f : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const long long v = v0 + i * kThreads;
-        if (round == 0 && v == one) w[i] -= 1.f;
+        const unsigned v = v0 + i * kThreads;
         if (w[i] > 0.f && (!(__fdividef(w[i], r[i]) < bar) || r[i] > 8e37f)) {
           const float s = w[i] / r[i];
           if (s > top) {
             top = s;
-            at = (unsigned)v;
+            at = v;
             bar = s > 1e-37f ? s * 0.999f : 0.f;
           }
         }

@@ -29,6 +29,13 @@ struct CacheArgs {
   int hp, N;               // rows per state, values per row
 };
 
+// The factor and the scale of a row whose largest value is `big`: products
+// with the reciprocals 1 / big and 1 / top, each rounded by itself.
+template <bool kFp8>
+__device__ __forceinline__ float factor_of(float big) { return __frcp_rn(big) * (kFp8 ? 448.f : 127.f); }
+template <bool kFp8>
+__device__ __forceinline__ float scale_of(float big) { return big * (kFp8 ? 1.f / 448.f : 1.f / 127.f); }
+
 // Below this largest value top / amax is not finite: the row is zeros.
 constexpr float kTiny = 3.009265538105056e-36f;  // 2^-118
 
@@ -67,16 +74,15 @@ __global__ void __launch_bounds__(kThreads) cache_store_kernel(CacheArgs a) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
   bad = __any_sync(0xffffffffu, bad);
-  const float top = kFp8 ? 448.f : 127.f;
   const bool empty = bad || !(big >= kTiny);
-  const float inv = empty ? 0.f : top / big;
+  const float inv = empty ? 0.f : factor_of<kFp8>(big);
   const long long to = slot * a.hp + row % a.hp;
 #pragma unroll
   for (int i = 0; i < kMaxVals; ++i) {
     const int n = i * 32 + lane;
     if (n < a.N) a.vals[to * a.N + n] = empty ? 0 : encode<kFp8>(v[i] * inv);
   }
-  if (lane == 0) a.scales[to] = bad ? __int_as_float(0x7fc00000) : empty ? 0.f : big / top;
+  if (lane == 0) a.scales[to] = bad ? __int_as_float(0x7fc00000) : empty ? 0.f : scale_of<kFp8>(big);
 }
 
 template <bool kFp8>
@@ -100,8 +106,29 @@ constexpr int kRows = 4;  // rows of a lane in flight
 
 template <bool kFp8>
 __device__ __forceinline__ uint32_t encode4(float4 v, float inv) {
-  return (uint32_t)encode<kFp8>(v.x * inv) | (uint32_t)encode<kFp8>(v.y * inv) << 8 |
-         (uint32_t)encode<kFp8>(v.z * inv) << 16 | (uint32_t)encode<kFp8>(v.w * inv) << 24;
+  if (kFp8)
+    return (uint32_t)encode<true>(v.x * inv) | (uint32_t)encode<true>(v.y * inv) << 8 |
+           (uint32_t)encode<true>(v.z * inv) << 16 | (uint32_t)encode<true>(v.w * inv) << 24;
+  // |v inv| <= 127 (1 + 2^-22): the sum with 1.5 * 2^23 rounds it to an integer, ties to even, in its low byte
+  // (float-to-integer conversions run at a quarter of the rate)
+  const float magic = 12582912.f;
+  const uint32_t x = __float_as_uint(__fadd_rn(__fmul_rn(v.x, inv), magic)),
+                 y = __float_as_uint(__fadd_rn(__fmul_rn(v.y, inv), magic)),
+                 z = __float_as_uint(__fadd_rn(__fmul_rn(v.z, inv), magic)),
+                 w = __float_as_uint(__fadd_rn(__fmul_rn(v.w, inv), magic));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+}
+
+// The largest of the row's lanes (values that are not negative order as integers)
+template <int LR>
+__device__ __forceinline__ float row_max(float v) {
+  if constexpr (LR == 32) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+  } else {
+#pragma unroll
+    for (int o = LR / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 
 // LR lanes to a row (a power of two), V vectors of four values to a lane.
@@ -131,31 +158,24 @@ __global__ void __launch_bounds__(kThreads) cache_store4_kernel(CacheArgs a) {
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     float big = 0.f;
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float m = fmaxf(fmaxf(fabsf(v[r][i].x), fabsf(v[r][i].y)), fmaxf(fabsf(v[r][i].z), fabsf(v[r][i].w)));
-      big = fmaxf(big, m);
-      // infinities show in the maximum, a NaN in the sum
-      bad |= !(m <= 3.402823466e38f) || (v[r][i].x - v[r][i].x) + (v[r][i].y - v[r][i].y) +
-                                                (v[r][i].z - v[r][i].z) + (v[r][i].w - v[r][i].w) != 0.f;
+      const float4 x = v[r][i];
+      // infinities show in the maximum, a NaN in the differences, which are zero for every other value
+      const float nan = (x.x - x.x) + (x.y - x.y) + (x.z - x.z) + (x.w - x.w);
+      big = fmaxf(fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+      big = nan == 0.f ? big : __int_as_float(0x7f800000);
     }
-    unsigned any = bad;
-#pragma unroll
-    for (int o = LR / 2; o; o >>= 1) {
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-      any |= __shfl_xor_sync(0xffffffffu, any, o);
-    }
+    big = row_max<LR>(big);
     if (to[r] < 0) continue;
-    const float top = kFp8 ? 448.f : 127.f;
-    const bool empty = any || !(big >= kTiny);
-    const float inv = empty ? 0.f : top / big;
+    const bool any = big == __int_as_float(0x7f800000), empty = any || !(big >= kTiny);
+    const float inv = empty ? 0.f : factor_of<kFp8>(big);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int n = i * LR + lane;
       if (n < n4) reinterpret_cast<uint32_t*>(a.vals)[to[r] * n4 + n] = empty ? 0u : encode4<kFp8>(v[r][i], inv);
     }
-    if (lane == 0) a.scales[to[r]] = any ? __int_as_float(0x7fc00000) : empty ? 0.f : big / top;
+    if (lane == 0) a.scales[to[r]] = any ? __int_as_float(0x7fc00000) : empty ? 0.f : scale_of<kFp8>(big);
   }
 }
 

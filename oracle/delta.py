@@ -126,8 +126,8 @@ def cache_roundtrip(states, form):
         big = np.abs(x).max(-1, keepdims=True)
         bad = ~np.isfinite(x).all(-1, keepdims=True)
         empty = ~(big >= f(2.0 ** -118))
-        y = (x * np.where(empty, f(0), top / big)).astype(f)
-        scale = np.where(bad, f(np.nan), np.where(empty, f(0), big / top)).astype(f)
+        y = (x * np.where(empty, f(0), (f(1) / big) * top)).astype(f)
+        scale = np.where(bad, f(np.nan), np.where(empty, f(0), big * (f(1) / top))).astype(f)
     y = np.where(bad, f(0), y)
     if form == "int8":
         y = np.clip(np.rint(y), -127, 127)
