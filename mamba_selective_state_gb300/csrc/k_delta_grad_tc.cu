@@ -13,11 +13,20 @@
 // Sixteen warps read them back: a thread owns one token's row -- of dY and dq
 // in the lower 64 lanes, of r and dk in the upper -- and a quarter of the
 // columns, so the dot products with q and k and the sums over heads stay in
-// its registers (as pairs, for the two-value fp32 multiply-add).  q k^T and k k^T do not depend on the head, and the pairs'
-// part of dq and dk is summed over the heads before its products with k and
-// q: both are one more product of 128 rows per group.  The pairs'
-// contributions to dgam are formed once in fp32 and summed by rows and by
-// columns, so that what cancels in their running difference cancels exactly.
+// its registers (as pairs, for the two-value fp32 multiply-add).  q k^T and
+// k k^T do not depend on the head, and the pairs' part of dq and dk is summed
+// over the heads before its products with k and q: both are one more product
+// of 128 rows per group.  The pairs' contributions to dgam are formed once in
+// fp32 and summed by rows and by columns, so that what cancels in their running
+// difference cancels exactly.
+//
+// Measured: 356 us at batch 2, L = 8192, 64 heads in 8 groups, headdim 64 and
+// dstate 128, where it reads 0.95 GB (2.7 TB/s).  The sixteen warps' epilogue
+// bounds it: of 60,000 cycles for eight heads it takes 40,000, the first loads
+// 7,500, and waiting for products 9,200.  A third stage of the ring, prefetches
+// into L2 and a kernel that also accumulates dq and dk in tensor memory (from
+// left operands that are scaled and written back) did not shorten it: 359 to
+// 394 us.
 #include "delta_internal.cuh"
 #include "mma_common.cuh"
 #include "tma_host.h"
@@ -31,9 +40,9 @@ using namespace tc;
 constexpr int kC = kDeltaChunk;
 constexpr int kWarps = 16;                    // epilogue warps
 constexpr int kEpi = kWarps * 32;
-constexpr int kThreads = kEpi + 128;          // and the control warp with three idle ones: registers
-                                              // are handed over by groups of four warps
-// Registers a thread: 640 threads are launched with 96; the control warps keep
+constexpr int kThreads = kEpi + 128;          // and a warp of copies and products, two of sums, one of
+                                              // <S0, D1>; registers are handed over by groups of four warps
+// Registers a thread: 640 threads are launched with 96; the other warps keep
 // 64 and the epilogue warps take 104 (4 x 104 + 64 = 5 x 96).  Where the
 // epilogue spills, it waits: the ring leaves the L1 cache too small for that.
 constexpr int kRegsEpi = 104, kRegsCtl = 64;
@@ -509,8 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       z16[2 * j + 1] = sign * (lower && 16 * cq + 2 * j + 1 == i ? pair_own : v.y);
     }
     // The pairs' part for all heads: rows of [0 | Z ; Z^T | M + M^T] against
-    // [q ; k], Z (i, j) and M (i, j) summed over the heads.  All of the ring's
-    // products are done: the last head's x_full followed them.
+    // [q ; k], Z (i, j) and M (i, j) summed over the heads.  Their operand takes
+    // the ring's place once the products and the warp of <S0, D1> have left it.
+    const int steps = p.hpg * npc;
+    for (int s = steps > L::kStages ? steps - L::kStages : 0; s < steps; ++s)
+      mbar_wait_flag(s_free + s % L::kStages, (s / L::kStages) & 1, ok);
     bar_sync(1, kEpi);
     const uint32_t Zb = sm + L::oSt;  // 128 rows x 64 columns of q's tokens, then of k's
     if (lower) {
