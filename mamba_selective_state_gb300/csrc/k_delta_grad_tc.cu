@@ -26,7 +26,9 @@
 // 7,500, and waiting for products 9,200.  A third stage of the ring, prefetches
 // into L2 and a kernel that also accumulates dq and dk in tensor memory (from
 // left operands that are scaled and written back) did not shorten it: 359 to
-// 394 us.
+// 394 us.  Nor did evening out the warps' work, with w D1 only for those of the
+// earlier tokens, which have few pairs (399 us): a warp's own chain of reads
+// counts, not the number of instructions.
 #include "delta_internal.cuh"
 #include "mma_common.cuh"
 #include "tma_host.h"
