@@ -20,7 +20,7 @@
 // fp32 and summed by rows and by columns, so that what cancels in their running
 // difference cancels exactly.
 //
-// Measured: 356 us at batch 2, L = 8192, 64 heads in 8 groups, headdim 64 and
+// Measured: 363 us at batch 2, L = 8192, 64 heads in 8 groups, headdim 64 and
 // dstate 128, where it reads 0.95 GB (2.7 TB/s).  The sixteen warps' epilogue
 // bounds it: of 60,000 cycles for eight heads it takes 40,000, the first loads
 // 7,500, and waiting for products 9,200.  A third stage of the ring, prefetches

@@ -132,6 +132,24 @@ def test_forward_and_gradient(b, L, H, P, N, G, dtype, nseq, init, dfinal):
     check(draw(b, L, H, P, N, G, dtype, seed=L, nseq=nseq, init=init, dfinal=dfinal))
 
 
+@pytest.mark.parametrize("L,H,P,N,starts", [
+    (700, 2, 64, 64, []),                             # packed in name only
+    (700, 2, 64, 128, [1]),
+    (700, 2, 64, 64, [64, 128, 320, 448, 576]),       # sequences of whole chunks
+    (1301, 2, 64, 128, [63, 65, 640, 641, 1299]),     # starts at both ends of a chunk
+    (1301, 1, 128, 64, [650, 655, 660, 700, 1024]),   # several in a chunk
+    (1301, 2, 64, 64, [1281]),                        # in the last chunk alone
+    (1301, 2, 64, 64, list(range(1, 1301))),          # sequences of one token
+    (513, 40, 64, 64, [255, 256, 257, 512]),          # 64 columns a CTA
+])
+def test_packed_chains_in_pieces(L, H, P, N, starts):
+    d = draw(1, L, H, P, N, 1, B, seed=L + len(starts), init=True, dfinal=True)
+    cuts = np.zeros((1, L), np.int32)
+    cuts[0, starts] = 1
+    d["seq_idx"] = torch.from_numpy(np.cumsum(cuts, 1).astype(np.int32))
+    check(d)
+
+
 @pytest.mark.parametrize("dtype,N", [(F, 48), (B, 128)])
 def test_forward_alone_matches(dtype, N):
     d = draw(2, 140, 4, 64, N, 2, dtype, init=True)
