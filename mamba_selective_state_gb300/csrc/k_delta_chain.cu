@@ -260,10 +260,7 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
       uint32_t v[4][4], tb[10][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (NW == 4)
-          load_at<8>(v[k], Vs, 16 * w, 16 * k, lane);
-        else
-          load_at<4>(v[k], Vs, 16 * w, 16 * k, lane);
+        load_at<2 * NW>(v[k], Vs, 16 * w, 16 * k, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -584,10 +581,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         uint32_t y[4], b[4];
-        if (NW == 4)
-          load_at<8>(y, Ys, 16 * w, 16 * i, lane);
-        else
-          load_at<4>(y, Ys, 16 * w, 16 * i, lane);
+        load_at<2 * NW>(y, Ys, 16 * w, 16 * i, lane);
 #pragma unroll
         for (int j = 0; j <= i; ++j) {
           load_bt<8>(b, As, 16 * j, 16 * i, lane);
@@ -699,21 +693,24 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
   if (!ok) atomicOr(f.status, kDevTimeout);
 }
 
-// 64 columns a CTA, or 32 where 64 would leave half the SMs idle.  Packed rows
-// have their chains in as many pieces as there are SMs for, and 64 columns
-// rather than one piece of 32 (one row of 20,011 tokens in 16 sequences, 64
-// heads of 64 x 64: forward 226 us instead of 286, reverse 209 instead of 330;
-// where a single sequence leaves one piece, 406 and 387).
+// Columns a CTA: 64, or 32 or 16 while every CTA still has an SM of its own --
+// fewer warps share an SM's shared memory, but each CTA copies the chunks'
+// operands for itself (one row of 4001 tokens, 32 heads of 64 x 128, forward:
+// 78 us by 32 columns, 75 by 16; 8192 tokens: reverse 197 and 186).  Packed rows have their chains in as many
+// pieces as there are SMs for, and rather twice the columns than one piece (one
+// row of 20,011 tokens in 16 sequences, 64 heads of 64 x 64: forward 226 us
+// instead of 286, reverse 209 instead of 330; where a single sequence leaves one
+// piece, 406 and 387).
 struct ChainShape {
-  bool narrow;
-  int pieces;
+  int warps, pieces;  // of 16 columns
 };
 ChainShape chain_shape(const DeltaPlan& p, const DeltaBufs& f) {
   const long long sms = device_sm_count(), wide = (long long)p.b * p.H * (p.P / 64);
-  ChainShape c = {wide * 2 <= sms, 1};
+  auto warps = [&](int pieces) { return wide * 4 * pieces <= sms ? 1 : wide * 2 * pieces <= sms ? 2 : 4; };
+  ChainShape c = {warps(1), 1};
   if (f.seq && wide * 2 <= sms && p.nc >= 8) {
-    c.narrow = wide * 4 <= sms;
-    const long long fit = sms / (c.narrow ? 2 * wide : wide);
+    c.warps = warps(2);
+    const long long fit = sms / (wide * (4 / c.warps));
     c.pieces = (int)(fit < p.nc / 4 ? fit : p.nc / 4);
   }
   return c;
@@ -775,11 +772,13 @@ cudaError_t launch_chain(const DeltaPlan& p, const DeltaBufs& f, bool reverse, c
   const ChainShape c = chain_shape(p, f);
   auto go = [&](auto cut) {
     constexpr bool kPieces = decltype(cut)::value;
-    if (c.narrow)
-      return p.N == 128 ? launch_chain_t<128, 2, kPieces>(p, f, c.pieces, reverse, s)
-                        : launch_chain_t<64, 2, kPieces>(p, f, c.pieces, reverse, s);
-    return p.N == 128 ? launch_chain_t<128, 4, kPieces>(p, f, c.pieces, reverse, s)
-                      : launch_chain_t<64, 4, kPieces>(p, f, c.pieces, reverse, s);
+    auto shaped = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      return c.warps == 4   ? launch_chain_t<N, 4, kPieces>(p, f, c.pieces, reverse, s)
+             : c.warps == 2 ? launch_chain_t<N, 2, kPieces>(p, f, c.pieces, reverse, s)
+                            : launch_chain_t<N, 1, kPieces>(p, f, c.pieces, reverse, s);
+    };
+    return p.N == 128 ? shaped(std::integral_constant<int, 128>()) : shaped(std::integral_constant<int, 64>());
   };
   return c.pieces > 1 ? go(std::true_type()) : go(std::false_type());
 }

@@ -25,7 +25,7 @@ using tc::smem_u32;
 
 template <int U>
 __device__ __forceinline__ uint32_t tile_off(int row, int unit) {
-  const int x = U >= 8 ? (row & 7) : ((row >> 1) & 3);
+  const int x = U >= 8 ? (row & 7) : U == 4 ? ((row >> 1) & 3) : ((row >> 2) & 1);
   return (uint32_t)(row * U + (unit ^ x)) * 16u;
 }
 // byte offset of element (row, col) of a bf16 tile
