@@ -9,9 +9,14 @@
 // the inverse of the triangular system among it) runs for all chunks at once;
 // a chain's CTA keeps 16 columns of its head's state in shared memory and does
 // four products a chunk, four columns and one token (or state row) a thread,
-// with the next chunk's operands on their way to registers.  Bound by the
-// latency of those products: one warp a sub-partition with eight independent
-// sums takes 0.4 of the time of two warps with four.
+// with the next chunk's operands on their way to registers.  Measured: 96 us
+// forward and 112 reverse for 32 chunks of 12 heads of 40 x 56 (36 CTAs), 5,900
+// cycles and 1,970 instructions a warp for a chunk.  Bound by shared memory's
+// pipe (2.9 passes for each of 250 loads a warp) and the latency of the products
+// it feeds: four more warps that take the loads, the outputs and Q S off the
+// chain did not help (100 and 107 us, and 690 instead of 478 us where the SMs
+// are full), nor did longer unrolled loops; two warps a sub-partition with half
+// the columns each took 2.5 times as long.
 #include "delta_internal.cuh"
 
 namespace ssd {

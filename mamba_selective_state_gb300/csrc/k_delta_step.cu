@@ -14,6 +14,8 @@
 // (Taking four tokens against one state, with the products that they owe each
 // other from tables, costs more for up to eight tokens than it saves: 11.9 us
 // against 9.8 at 4 sequences of 5 tokens, 48 heads of 64 x 16.)
+// Measured with 64 sequences of one token, 64 heads of 64 x 128: 46 us for 269 MB
+// of states, in and out (5.8 TB/s).
 #include "delta_internal.cuh"
 
 namespace ssd {

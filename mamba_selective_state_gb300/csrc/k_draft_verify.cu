@@ -11,13 +11,15 @@
 //
 // Bound by the dependent reads before the row (the drafted tokens, their
 // probabilities) and the first touch of rows that lie megabytes apart: 4 us to
-// the first words and 10 to the fourth 16 KB of each CTA, after which they come
-// at 7 TB/s.  batch 4 of 32,000 words: 11 us; batch 128 of 100,003 (102 MB):
-// 38 us, 2.7 TB/s.  A ring of bulk copies instead of the loads into registers
-// took 35 us there and 29 instead of 28 at batch 64 of 128,000 fp32 words.
+// the first words and 10 to the fourth 16 KB of each CTA.  batch 4 of 32,000 fp32
+// words: 10 us; batch 128 of 100,003 bf16 words (102 MB): 30 us, 3.4 TB/s.  Words
+// whose bounds were checked one by one, with a best ratio of each thread's own,
+// took 48 instructions each and 38 us there.
 #include <cooperative_groups.h>
 
 #include "ssd_internal.cuh"
+
+#include <type_traits>
 
 namespace ssd {
 
@@ -43,6 +45,39 @@ struct VerifyArgs {
 __device__ __forceinline__ unsigned long long race_key(float s, unsigned v) {
   return s > 0.f ? ((unsigned long long)__float_as_uint(s) << 32) | (0xffffffffu - v) : 0ull;
 }
+
+// What one thread has met of the race, in ascending order of the words, so
+// that the first of equal ratios stays.  A ratio is divided out only where an
+// estimate of it (off by a few units of 2^-23, where divisor and ratio are
+// neither huge nor tiny) says that it may be the largest that the warp has met
+// yet; ratios that are not above zero, or are NaN, never are.
+struct Race {
+  float top = 0.f, bar = 0.f;
+  unsigned at = 0;
+  __device__ __forceinline__ bool may_win(float w, float r) const {
+    return w > 0.f && (!(__fdividef(w, r) < bar) || r > 8e37f);
+  }
+  // K words, a step apart; the warp's lanes come together
+  template <int K>
+  __device__ __forceinline__ void meet(const float (&w)[K], const float (&r)[K], unsigned v, unsigned step) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < K; ++i) any |= may_win(w[i], r[i]);
+    if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if (may_win(w[i], r[i])) {
+          const float s = w[i] / r[i];
+          if (s > top) {
+            top = s;
+            at = v + i * step;
+          }
+        }
+      const float s = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      bar = s > 1e-37f ? s * 0.999f : 0.f;
+    }
+  }
+};
 
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draft_kernel(VerifyArgs a) {
@@ -91,53 +126,49 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draf
   // round 0: the residual weights; round 1, only where none was positive: p
   unsigned long long best = 0;
   for (int round = 0; round < 2; ++round) {
-    // A thread meets its words in ascending order, so the first of equal ratios
-    // stays.  A ratio is divided out only where an estimate of it (off by a few
-    // units of 2^-23, where divisor and ratio are neither huge nor tiny) says
-    // that it may be the largest yet; ratios that are not above zero, or are
-    // NaN, never are.
-    float top = 0.f, bar = 0.f;
-    unsigned at = 0;
+    Race race;
+    // A CTA's words in tiles of eight to a thread: unconditional loads, all in
+    // flight before the first is used; whole tiles need no bounds, in the last
+    // one what lies past the end is read from the last word and weighs nothing
     constexpr int kAhead = 8;
-    for (unsigned v0 = lo + threadIdx.x; v0 < hi; v0 += kAhead * kThreads) {
-      // (unconditional loads, past the end of the last word: all are in flight before the first is used)
+    const bool minus = round == 0 && q;
+    const int gone = round == 0 ? one : -1;
+    auto tile = [&](unsigned u0, auto whole) {
+      const unsigned v0 = u0 + threadIdx.x;
+      const T *pt = p + v0, *qt = q + v0;
+      const float* rt = noise + v0;
       float w[kAhead], r[kAhead];
       T pv[kAhead], qv[kAhead];
+      auto at = [&](int i) { return decltype(whole)::value ? i * kThreads : (int)(min(v0 + i * kThreads, hi - 1) - v0); };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const unsigned v = min(v0 + i * kThreads, hi - 1);
-        pv[i] = p[v];
-        r[i] = noise[v];
+        pv[i] = pt[at(i)];
+        r[i] = rt[at(i)];
       }
-      if (round == 0 && q) {
+      if (minus) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) qv[i] = q[min(v0 + i * kThreads, hi - 1)];
+        for (int i = 0; i < kAhead; ++i) qv[i] = qt[at(i)];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) w[i] = to_f(pv[i]) - to_f(qv[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) w[i] = to_f(pv[i]);
       }
+      if (gone >= 0) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) w[i] = v0 + i * kThreads < hi ? w[i] : 0.f;
-      if (round == 0 && one >= 0) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) w[i] -= v0 + i * kThreads == one ? 1.f : 0.f;
+        for (int i = 0; i < kAhead; ++i) w[i] -= v0 + i * kThreads == gone ? 1.f : 0.f;
       }
+      if (!decltype(whole)::value) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const unsigned v = v0 + i * kThreads;
-        if (w[i] > 0.f && (!(__fdividef(w[i], r[i]) < bar) || r[i] > 8e37f)) {
-          const float s = w[i] / r[i];
-          if (s > top) {
-            top = s;
-            at = v;
-            bar = s > 1e-37f ? s * 0.999f : 0.f;
-          }
-        }
+        for (int i = 0; i < kAhead; ++i) w[i] = v0 + i * kThreads < hi ? w[i] : 0.f;
       }
-    }
-    unsigned long long key = race_key(top, at);
+      race.meet(w, r, v0, kThreads);
+    };
+    constexpr unsigned kTile = kAhead * kThreads;
+    unsigned u0 = lo;
+    for (; u0 < hi && hi - u0 >= kTile; u0 += kTile) tile(u0, std::true_type());
+    if (u0 < hi) tile(u0, std::false_type());
+    unsigned long long key = race_key(race.top, race.at);
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       const unsigned long long k = __shfl_xor_sync(0xffffffffu, key, o);
@@ -189,8 +220,8 @@ template <typename T>
 cudaError_t launch_verify(const VerifyArgs& a, int64_t batch, cudaStream_t s) {
   // CTAs per sequence: one for each 2048 words of the vocabulary, in powers of two up to the portable cluster size,
   // but no more than are resident at once, four narrow ones to an SM: every wave has the dependent reads before its
-  // row anew (batch 128, 100,003 words: 38 us in one wave, 41 in two).  Wide CTAs while each has an SM of its own
-  // (batch 4, 32,000 words: 11 us, with narrow ones 12; batch 128 of 5,000: 19 and 12).
+  // row anew (batch 128, 100,003 words, before other savings: 38 us in one wave, 41 in two).  Wide CTAs while each has
+  // an SM of its own (batch 4, 32,000 words: 11 us, with narrow ones 12; batch 128 of 5,000: 19 and 12).
   const int sms = device_sm_count();
   int ncta = 1;
   while (ncta < kMaxCluster && (long long)ncta * 2048 < a.V && batch * ncta * 2 <= 4 * sms) ncta *= 2;
