@@ -5,6 +5,7 @@ Submodules:
   inputs     seeded synthetic inputs of the layer workloads (no arithmetic)
   build_ext  builds libssd.so in-tree with nvcc for sm_103a
   _lib       ctypes binding of the C ABI (raises if libssd.so is missing)
-  runner     device buffers of one problem and the calls through the C ABI
+  runner     device buffers of one problem and the calls through the C ABI: the SSD layer,
+             the gated delta rule (DeltaDevice, DeltaStepDevice), verify_draft, StateCache
 """
 __all__ = ["inputs", "build_ext"]

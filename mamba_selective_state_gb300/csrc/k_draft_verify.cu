@@ -12,7 +12,7 @@
 // Bound by the dependent reads before the row (the drafted tokens, their
 // probabilities) and the first touch of rows that lie megabytes apart: 4 us to
 // the first words and 10 to the fourth 16 KB of each CTA.  batch 4 of 32,000 fp32
-// words: 10 us; batch 128 of 100,003 bf16 words (102 MB): 30 us, 3.4 TB/s.  Words
+// words: 10 us; batch 128 of 100,003 bf16 words (102 MB): 28 to 30 us, 3.5 TB/s.  Words
 // whose bounds were checked one by one, with a best ratio of each thread's own,
 // took 48 instructions each and 38 us there.
 #include <cooperative_groups.h>
