@@ -82,6 +82,10 @@ struct Race {
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draft_kernel(VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
+  // Another CTA's shared memory may be written only once that CTA is known to
+  // have started: each says so here, and the wait comes before the first such
+  // write, long after the others have arrived.
+  cluster.barrier_arrive();
   const unsigned ncta = cluster.num_blocks(), rank = cluster.block_rank();
   const long long b = blockIdx.x / ncta;
   __shared__ int kept_s, len_s;
@@ -176,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) verify_draf
     }
     if (lane == 0) warp_best[threadIdx.x >> 5] = key;
     __syncthreads();
+    if (round == 0) cluster.barrier_wait();
     if (threadIdx.x < 32) {
       key = lane < kThreads / 32 ? warp_best[lane] : 0;
 #pragma unroll
