@@ -145,6 +145,13 @@ def _dense(t, shape, dtype, what, device=None):
         raise ValueError(f"{what}: expected a dense {tuple(shape)} {dtype} tensor on {device}")
 
 
+def _on_gpu(device, what):
+    """The library gets bare pointers and launches on the current device: a
+    tensor anywhere else would be read there at an address that is not its own."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: expected tensors on the current CUDA device, not on {device}")
+
+
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
@@ -199,6 +206,7 @@ class DeltaDevice:
     def __init__(self, q, k, v, g, beta, scale=None, initial_states=None, seq_idx=None, dy=None,
                  dfinal_states=None, state_dtype=torch.float32):
         (b, L, H, P, N, G), strides = _delta_shape(q, k, v, g, beta)
+        _on_gpu(v.device, "DeltaDevice")
         if state_dtype not in _FLOATS:
             raise ValueError("state_dtype must be fp32 or bf16")
         if dfinal_states is not None and dy is None:
@@ -237,6 +245,7 @@ class DeltaDevice:
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
 
     def fwd(self, stream=None, check=True):
+        _on_gpu(self.v.device, "DeltaDevice")
         return _lib.ssd_delta_fwd(self.fwd_prob, self.q, self.k, self.v, self.g, self.beta,
                                   self.init, self.seq_idx, self.y, self.final, self.saved,
                                   self.workspace, stream=stream, check=check)
@@ -244,6 +253,7 @@ class DeltaDevice:
     def bwd(self, stream=None, check=True):
         if self.saved is None:
             raise ValueError("built without dy: there is no backward")
+        _on_gpu(self.v.device, "DeltaDevice")
         return _lib.ssd_delta_bwd(self.bwd_prob, self.q, self.k, self.v, self.g, self.beta,
                                   self.seq_idx, self.dy, self.dfinal, self.dq, self.dk, self.dv,
                                   self.dg, self.dbeta, self.dinit, self.saved, self.workspace,
@@ -270,6 +280,7 @@ class DeltaStepDevice:
     def __init__(self, states, states_out=None):
         if states.dim() != 4:
             raise ValueError("states must be (nslots, H, P, N)")
+        _on_gpu(states.device, "states")
         _dense(states, states.shape, torch.float32, "states")
         self.states = states
         self.states_out = states if states_out is None else states_out
@@ -286,6 +297,7 @@ class DeltaStepDevice:
         nslots = self.states.shape[0]
         if self.states.shape[1:] != (H, P, N) or v.device != self.states.device:
             raise ValueError("the tokens' heads do not fit the states")
+        _on_gpu(v.device, "DeltaStepDevice")
         _dense(slots, (b,), torch.int32, "slots", v.device)
         _dense(lengths, (b,), torch.int32, "lengths", v.device)
         scale = N ** -0.5 if scale is None else scale
@@ -307,6 +319,7 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniform, noise, length
         raise ValueError("target_probs must be (b, K + 1, V), fp32 or bf16")
     b, K1, V = target_probs.shape
     dev = target_probs.device
+    _on_gpu(dev, "verify_draft")
     _dense(target_probs, (b, K1, V), target_probs.dtype, "target_probs", dev)
     _dense(draft_probs, (b, K1 - 1, V), target_probs.dtype, "draft_probs", dev)
     _dense(draft_tokens, (b, K1 - 1), torch.int32, "draft_tokens", dev)
@@ -330,12 +343,15 @@ class StateCache:
     def __init__(self, nslots, nheads, headdim, dstate, form="int8", device="cuda"):
         if form not in self.FORMATS:
             raise ValueError(f"form must be one of {sorted(self.FORMATS)}")
+        if torch.device(device).type != "cuda":
+            raise ValueError(f"the cache lives on a CUDA device, not on {device}")
         self.shape, self.form = (nslots, nheads, headdim, dstate), form
         self.values = torch.empty(self.shape, dtype=torch.uint8, device=device)
         self.scales = torch.zeros(self.shape[:3], dtype=torch.float32, device=device)
 
     def _prob(self, states, slots):
         b = states.shape[0]
+        _on_gpu(self.values.device, "StateCache")
         _dense(states, (b,) + self.shape[1:], torch.float32, "states", self.values.device)
         _dense(slots, (b,), torch.int32, "slots", self.values.device)
         return _cache_problem(b, *self.shape[1:], self.shape[0], self.FORMATS[self.form])
