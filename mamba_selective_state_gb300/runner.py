@@ -3,6 +3,7 @@ C ABI.  Allocation and argument marshalling only; the layer runs in libssd.
 """
 from __future__ import annotations
 
+import contextlib
 import functools
 
 import torch
@@ -152,6 +153,17 @@ def _on_gpu(device, what):
         raise ValueError(f"{what}: expected tensors on the current CUDA device, not on {device}")
 
 
+def _allocating_on(stream):
+    """Memory of a call's own outputs comes from the stream that fills them:
+    the allocator hands out a block of another stream's as soon as that stream's
+    later work may have it, which says nothing about this one's."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 _FLOATS = (torch.float32, torch.bfloat16)
 
 
@@ -290,7 +302,8 @@ class DeltaStepDevice:
              outputs=True, stream=None, check=True):
         """All tokens of q, k (b, T, G, N), v (b, T, H, P), g, beta (b, T, H)
         in order, from each sequence's slot; returns y (b, T, H, P), or None
-        without ``outputs``.  The states written are those after the first
+        without ``outputs`` (y is ``stream``'s: another stream waits for it before
+        it reads it).  The states written are those after the first
         ``lengths[b]`` tokens (default: all); ``update=False`` writes none."""
         shape, strides = _delta_shape(q, k, v, g, beta)
         b, T, H, P, N, G = shape
@@ -302,7 +315,10 @@ class DeltaStepDevice:
         _dense(lengths, (b,), torch.int32, "lengths", v.device)
         scale = N ** -0.5 if scale is None else scale
         prob = _step_problem(shape, scale, v.dtype, strides)
-        y = torch.empty((b, T, H, P), dtype=v.dtype, device=v.device) if outputs else None
+        y = None
+        if outputs:
+            with _allocating_on(stream):
+                y = torch.empty((b, T, H, P), dtype=v.dtype, device=v.device)
         _lib.ssd_delta_step(prob, q, k, v, g, beta, nslots, self.states,
                             self.states_out if update else None, slots, lengths, y,
                             stream=stream, check=check)
@@ -314,7 +330,8 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniform, noise, length
     """Keep the drafted tokens that the target accepts and draw the next one:
     (tokens (b, K + 1) int32, kept (b) int32) of target_probs (b, K + 1, V),
     draft_probs (b, K, V) or None, draft_tokens (b, K), uniform (b, K) and
-    noise (b, V), standard exponentials."""
+    noise (b, V), standard exponentials.  The results are ``stream``'s: another
+    stream waits for it before it reads them."""
     if target_probs.dim() != 3 or target_probs.dtype not in _FLOATS:
         raise ValueError("target_probs must be (b, K + 1, V), fp32 or bf16")
     b, K1, V = target_probs.shape
@@ -326,8 +343,9 @@ def verify_draft(target_probs, draft_probs, draft_tokens, uniform, noise, length
     _dense(uniform, (b, K1 - 1), torch.float32, "uniform", dev)
     _dense(noise, (b, V), torch.float32, "noise", dev)
     _dense(lengths, (b,), torch.int32, "lengths", dev)
-    tokens = torch.empty((b, K1), dtype=torch.int32, device=dev)
-    accepted = torch.empty(b, dtype=torch.int32, device=dev)
+    with _allocating_on(stream):
+        tokens = torch.empty((b, K1), dtype=torch.int32, device=dev)
+        accepted = torch.empty(b, dtype=torch.int32, device=dev)
     prob = _verify_problem(b, K1 - 1, V, target_probs.dtype)
     _lib.ssd_verify_draft(prob, target_probs, draft_probs, draft_tokens, lengths, uniform, noise,
                           tokens, accepted, stream=stream, check=check)
