@@ -265,15 +265,17 @@ __device__ __forceinline__ void read_state(ChunkSmem<NP>& sm, const DeltaPlan& p
     sm.S[n][col] = src && n < p.N && p0 + col < p.P ? ld_state(src, base + (long long)col * p.N + n, p.st_bf16) : 0.f;
   }
 }
-// (four values of a column to a thread: two threads fill a 32-byte sector)
+// (four values of a column to a thread: two threads fill a 32-byte sector; zeros
+// for a state that nobody sees)
 template <int NP>
 __device__ __forceinline__ void write_state(const ChunkSmem<NP>& sm, const DeltaPlan& p, void* dst, long long base,
-                                            int p0, int bf16) {
+                                            int p0, int bf16, bool seen = true) {
   const int col = threadIdx.x % kCols;
   if (p0 + col >= p.P) return;
   const long long row = base + (long long)col * p.N;
   for (int n = threadIdx.x / kCols * 4; n < p.N; n += kThreads / kCols * 4) {
-    const float4 v = make_float4(sm.S[n][col], sm.S[n + 1][col], sm.S[n + 2][col], sm.S[n + 3][col]);
+    const float4 v = seen ? make_float4(sm.S[n][col], sm.S[n + 1][col], sm.S[n + 2][col], sm.S[n + 3][col])
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
     if (!bf16 && (p.N & 3) == 0) {
       *reinterpret_cast<float4*>(static_cast<float*>(dst) + row + n) = v;
     } else {
@@ -296,6 +298,89 @@ __device__ __forceinline__ void put_row(const DeltaPlan& p, void* dst, long long
     if (col + j < p.P) d[j] = from_f<O>(part(v, j));
 }
 
+__device__ __forceinline__ bool finite4(float4 v) {
+  return (v.x - v.x) + (v.y - v.y) + (v.z - v.z) + (v.w - v.w) == 0.f;
+}
+
+// A chunk token by token, by the definition alone.  The chunk's products
+// multiply what a token must not see by zero, which does not hide an infinity or
+// a NaN from it: a chunk whose solve gives one is done again here, so that such
+// a value reaches what it reaches by definition -- not the tokens before it, nor
+// the next sequence of a packed row.  Eight threads walk a column; columns do
+// not meet.
+constexpr int kWalkers = kThreads / kCols;
+__device__ __forceinline__ float walk_sum(float v) {
+#pragma unroll
+  for (int o = kWalkers / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+struct WalkGate {
+  float a, beta;
+  bool starts;  // the token does not see the state before it
+};
+template <typename T>
+__device__ __forceinline__ WalkGate walk_gate(const DeltaPlan& p, const DeltaBufs& f, int bi, int h, int t) {
+  const long long tok = (long long)bi * p.L + t;
+  const float g = to_f(static_cast<const T*>(f.g)[tok * p.H + h]);
+  const bool cut = f.seq != nullptr && t > 0 && f.seq[tok] != f.seq[tok - 1];
+  return {expf(g), to_f(static_cast<const T*>(f.beta)[tok * p.H + h]), cut || g < kForget};
+}
+
+// Forward: S from the state before chunk c to the one after it; y and w
+template <typename T, int NP>
+__device__ __noinline__ void walk_fwd(ChunkSmem<NP>& sm, const DeltaPlan& p, const DeltaBufs& f, int bi, int h, int p0,
+                                      int c) {
+  const int col = threadIdx.x / kWalkers, l = threadIdx.x % kWalkers;
+  for (int i = 0; i < kC && c * kC + i < p.L; ++i) {
+    const int t = c * kC + i;
+    const WalkGate x = walk_gate<T>(p, f, bi, h, t);
+    float d = 0.f, y = 0.f;
+    for (int n = l; n < p.N; n += kWalkers) {
+      const float s = x.starts ? 0.f : x.a * sm.S[n][col];
+      sm.S[n][col] = s;
+      d += s * sm.k[i][n];
+    }
+    const float w = sm.v[i][col] - walk_sum(d), u = x.beta * w;
+    for (int n = l; n < p.N; n += kWalkers) {
+      const float s = sm.S[n][col] + u * sm.k[i][n];
+      sm.S[n][col] = s;
+      y += s * sm.q[i][n];
+    }
+    y = walk_sum(y);
+    if (l == 0 && p0 + col < p.P) {
+      const long long o = (((long long)bi * p.L + t) * p.H + h) * p.P + p0 + col;
+      static_cast<T*>(f.y)[o] = from_f<T>(p.scale * y);
+      if (f.w) static_cast<float*>(f.w)[o] = w;
+    }
+  }
+}
+// Reverse: S holds the gradient of the state after chunk c, then of the one before it; r
+template <typename T, int NP>
+__device__ __noinline__ void walk_bwd(ChunkSmem<NP>& sm, const DeltaPlan& p, const DeltaBufs& f, int bi, int h, int p0,
+                                      int c) {
+  const int col = threadIdx.x / kWalkers, l = threadIdx.x % kWalkers;
+  for (int i = min(kC, p.L - c * kC) - 1; i >= 0; --i) {
+    const int t = c * kC + i;
+    const WalkGate x = walk_gate<T>(p, f, bi, h, t);
+    const long long o = (((long long)bi * p.L + t) * p.H + h) * p.P + p0 + col;
+    const bool live = p0 + col < p.P;
+    const float dy = live ? p.scale * to_f(static_cast<const T*>(f.dy)[o]) : 0.f;
+    float d = 0.f;
+    for (int n = l; n < p.N; n += kWalkers) {
+      const float s = sm.S[n][col] + dy * sm.q[i][n];
+      sm.S[n][col] = s;
+      d += s * sm.k[i][n];
+    }
+    const float r = x.beta * walk_sum(d);
+    for (int n = l; n < p.N; n += kWalkers)
+      sm.S[n][col] = x.starts ? 0.f : x.a * (sm.S[n][col] - r * sm.k[i][n]);
+    if (l == 0 && live) {
+      static_cast<T*>(f.dv)[o] = from_f<T>(r);
+      static_cast<float*>(f.r)[o] = r;
+    }
+  }
+}
+
 template <typename T, int NP>
 __global__ void __launch_bounds__(kThreads) delta_chain_simt_fwd_kernel(DeltaPlan p, DeltaBufs f) {
   extern __shared__ __align__(16) unsigned char raw[];
@@ -316,7 +401,7 @@ __global__ void __launch_bounds__(kThreads) delta_chain_simt_fwd_kernel(DeltaPla
     put_chunk<T, NP, false>(sm, ahead);
     __syncthreads();
     if (kPrefetch && c + 1 < p.nc) ahead.load(p, f, f.v, p.vs, bi, h, p0, c + 1);
-    if (f.S) write_state(sm, p, f.S, ((bh * p.nc + c) * p.P + p0) * p.N, p0, 0);
+    if (f.S) write_state(sm, p, f.S, ((bh * p.nc + c) * p.P + p0) * p.N, p0, 0, sm.e[0] != 0.f);
     // K S and Q S
     float4 x = zero, y = zero;
 #pragma unroll 4
@@ -339,7 +424,10 @@ __global__ void __launch_bounds__(kThreads) delta_chain_simt_fwd_kernel(DeltaPla
     float4 w = zero;
     tri(w, sm.T[i], sm.R, 0, w_rows, pp);
     sts4(&sm.w[i][pp], w);
-    __syncthreads();
+    if (__syncthreads_or(!finite4(w))) {
+      walk_fwd<T, NP>(sm, p, f, bi, h, p0, c);
+      continue;
+    }
     sts4(&sm.R[i][pp], mul4(sm.e[kC + i], w));
     tri(y, sm.A[i], sm.w, 0, w_rows, pp);
     const int t = c * kC + i;
@@ -418,7 +506,10 @@ __global__ void __launch_bounds__(kThreads) delta_chain_simt_bwd_kernel(DeltaPla
       put_row<T>(p, f.dv, o, p0 + pp, r);
       put_row<float>(p, f.r, o, p0 + pp, r);
     }
-    __syncthreads();
+    if (__syncthreads_or(!finite4(r))) {
+      walk_bwd<T, NP>(sm, p, f, bi, h, p0, c);  // writes the chunk's r anew
+      continue;
+    }
     // D = e_last D + Q^T (scale e dY) - K^T (e r); none passes a sequence's first token
     float4 s[NP / 32];
 #pragma unroll
