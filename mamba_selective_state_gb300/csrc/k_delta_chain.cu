@@ -98,6 +98,144 @@ __device__ __forceinline__ void store_state(const float (&S)[N / 8][4], void* ds
     }
 }
 
+// A chunk token by token, by the definition alone.  The chunk's products
+// multiply what a token must not see by zero, which does not hide an infinity or
+// a NaN from it.  In a chunk without a sequence's start that stays in the
+// sequence and in the chunk; where one starts (no state passes through), and the
+// result is not finite, the chunk is done again here, one warp's 16 columns as
+// in the products' accumulators, from the operands in global memory.
+template <int M>
+__device__ __forceinline__ bool all_finite(const float (&v)[M][4]) {
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fine &= fabsf(v[i][j]) <= 3.402823466e38f;
+  return __all_sync(0xffffffffu, fine);
+}
+// the same of a [64][16] bf16 tile
+__device__ __forceinline__ bool all_finite_tile(uint32_t tile, int lane) {
+  bool fine = true;
+  for (int i = lane; i < kC * 2; i += 32) {
+    const uint4 v = lds128(tile + i * 16);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) fine &= (u[j] & 0x7f80u) != 0x7f80u && (u[j] & 0x7f800000u) != 0x7f800000u;
+  }
+  return __all_sync(0xffffffffu, fine);
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+__device__ __forceinline__ void sts16(uint32_t addr, float v) {
+  const __nv_bfloat16 b = __float2bfloat16_rn(v);
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const uint16_t*>(&b)) : "memory");
+}
+// Since such a chunk is rare, and the tests for it would cost every chain a
+// tenth of its time, they are left to a second pass over the chain's chunks, made
+// where the first one gave a value that is not finite and met a sequence's start.
+enum { kNotFinite = 1, kExpired = 2 };
+// 0 x + sum: NaN from the first value on that is not finite
+__device__ __forceinline__ __nv_bfloat162 times_zero(uint32_t x, __nv_bfloat162 sum) {
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.f, 0.f), sum);
+}
+struct Walk {
+  const DeltaPlan& p;
+  const DeltaBufs& f;
+  int bi, h, c, col, lane;  // col: the warp's first column of headdim
+  struct Gate {
+    float a, beta;
+    bool starts;  // the token does not see the state before it
+  };
+  __device__ __forceinline__ long long token(int i) const { return (long long)bi * p.L + c * kC + i; }
+  __device__ __forceinline__ int tokens() const { return min(kC, p.L - c * kC); }
+  __device__ __forceinline__ Gate gate(int i) const {
+    const long long tok = token(i), o = tok * p.H + h;
+    const float g = to_f(static_cast<const __nv_bfloat16*>(f.g)[o]);
+    const bool cut = f.seq != nullptr && c * kC + i > 0 && f.seq[tok] != f.seq[tok - 1];
+    return {expf(g), to_f(static_cast<const __nv_bfloat16*>(f.beta)[o]), cut || g < kForget};
+  }
+  // this lane's values of a row of q or k, eight columns apart
+  __device__ __forceinline__ const uint32_t* row(const void* x, long long stride, int N, int i) const {
+    return reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(x) + token(i) * stride +
+                                             (long long)(h / p.hpg) * N) + (lane & 3);
+  }
+  // and of v or dy: columns lane / 4 and eight further
+  __device__ __forceinline__ float2 column(const void* x, long long stride, int i) const {
+    const __nv_bfloat16* v =
+        static_cast<const __nv_bfloat16*>(x) + token(i) * stride + (long long)h * p.P + col + (lane >> 2);
+    return make_float2(to_f(v[0]), to_f(v[8]));
+  }
+  template <int N>
+  __device__ __forceinline__ void state_from(float (&S)[N / 8][4], uint32_t tile) const {
+#pragma unroll
+    for (int ks = 0; ks < N / 16; ++ks) {
+      uint32_t a[4];
+      ldsm4(a, frag_at(tile, 16 * ks, lane));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack2(a[j]);
+        S[2 * ks + (j >> 1)][2 * (j & 1)] = v.x;
+        S[2 * ks + (j >> 1)][2 * (j & 1) + 1] = v.y;
+      }
+    }
+  }
+  // S'x for the two columns: the row's products over dstate
+  template <int N>
+  __device__ __forceinline__ float2 dot(const float (&S)[N / 8][4], const uint32_t* x) const {
+    float2 d = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j) {
+      const float2 v = unpack2(x[4 * j]);
+      d.x += S[j][0] * v.x + S[j][1] * v.y;
+      d.y += S[j][2] * v.x + S[j][3] * v.y;
+    }
+    return make_float2(quad_sum(d.x), quad_sum(d.y));
+  }
+  template <int N>
+  __device__ __forceinline__ void add(float (&S)[N / 8][4], float2 u, const uint32_t* x) const {
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j) {
+      const float2 v = unpack2(x[4 * j]);
+      S[j][0] += u.x * v.x;
+      S[j][1] += u.x * v.y;
+      S[j][2] += u.y * v.x;
+      S[j][3] += u.y * v.y;
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void decay(float (&S)[N / 8][4], const Gate& x) const {
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) S[j][m] = x.starts ? 0.f : x.a * S[j][m];
+  }
+  // Forward from the state in `tile`: the state S after the chunk and, with kOut,
+  // y into a [64][16] tile
+  template <int N, bool kOut>
+  __device__ __forceinline__ void forward(float (&S)[N / 8][4], uint32_t tile, uint32_t out) const {
+    state_from<N>(S, tile);
+    const int n = tokens();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const Gate x = gate(i);
+      const uint32_t* k = row(f.k, p.ks, N, i);
+      const float2 v = column(f.v, p.vs, i);
+      decay<N>(S, x);
+      const float2 d = dot<N>(S, k);
+      add<N>(S, make_float2(x.beta * (v.x - d.x), x.beta * (v.y - d.y)), k);
+      if (kOut) {
+        const float2 y = dot<N>(S, row(f.q, p.qs, N, i));
+        if ((lane & 3) == 0) {
+          sts16(out + i * 32 + (lane >> 2) * 2, p.scale * y.x);
+          sts16(out + i * 32 + (lane >> 2) * 2 + 16, p.scale * y.y);
+        }
+      }
+    }
+  }
+};
+
 struct ChainMaps {
   CUtensorMap q, k, v, T, A, y, S, w;  // reverse: v is dy, y is dv, S is D
 };
@@ -144,7 +282,7 @@ struct FwdSmem {
   static constexpr int chain = kK + (int)kTile + kV, out = kK + (int)kTile;
   static constexpr int oChain = 0, oOut = oChain + 3 * chain, oS = oOut + 2 * out,  // S' by warp, two each
                        oW = oS + NW * 2 * N * 32, oY = oW + NW * 2 * 2048, oE = oY + NW * 2 * 2048,
-                       oBar = oE + 5 * kGateBytes, bytes = oBar + (10 + 4 * NW) * 8 + 1024;
+                       oBar = oE + 5 * kGateBytes, oPlace = oBar + (10 + 4 * NW) * 8, bytes = oPlace + 64 + 1024;
 };
 
 // Column, output and copying warps.  Nine warps would leave each 168 registers
@@ -153,74 +291,33 @@ struct FwdSmem {
 // the copying warp (launched with 168 each: 240 + 208 + 40 <= 3 x 168).
 constexpr int fwd_threads(int nw) { return nw == 4 ? 384 : (2 * nw + 1) * 32; }
 
-template <int N, int NW, bool kPieces>
-__global__ void __launch_bounds__(fwd_threads(NW), 1)
-    delta_chain_fwd_kernel(DeltaPlan p, DeltaBufs f, int pieces, const __grid_constant__ ChainMaps m) {
+// A forward chain's CTA: its columns and its chunks
+struct FwdPlace {
+  int bi, h, p0, z, first, nch;
+  bool last_of_row;
+};
+template <int N, int NW>
+struct FwdChain {
   using L = FwdSmem<N, NW>;
-  constexpr bool kHandOver = NW == 4;
-  extern __shared__ unsigned char raw_[];
-  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
-  const uint32_t sm = smem_u32(raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + L::oBar);
-  uint64_t *c_full = bars, *c_free = bars + 3, *o_full = bars + 6, *o_free = bars + 8;
-  uint64_t *h_full = bars + 10, *h_free = h_full + 2 * NW;  // [warp][2]
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-  const int ptiles = p.P / (16 * NW);
-  const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
-  const int h = (int)((blockIdx.x / ptiles) % p.H), row = (int)(blockIdx.x / ((long long)ptiles * p.H));
-  const int bi = kPieces ? row % p.b : row, z = kPieces ? row / p.b : 0;  // the batch row and its piece
-  const int grp = h / p.hpg, bh = bi * p.H + h;
-  const float* gates = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
-  __shared__ Piece piece_s;
-  if (kPieces && w == 0) {
-    const Piece found = find_piece(gates, z, pieces, p.nc, lane);
-    if (lane == 0) piece_s = found;
-  }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(c_full + i, 1);
-      mbar_init(c_free + i, NW);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(o_full + i, 1);
-      mbar_init(o_free + i, NW);
-    }
-    for (int i = 0; i < 2 * NW; ++i) {
-      mbar_init(h_full + i, 1);
-      mbar_init(h_free + i, 1);
-    }
-    mbar_fence_init();
-  }
-  __syncthreads();
-  const Piece piece = kPieces ? piece_s : Piece{0, p.nc};
-  if (z && piece.first >= piece.next) return;  // no cut of its own
-  // its chunks; a later piece gives no outputs for its first one
-  const int first = piece.first, nch = min(piece.next + 1, p.nc) - first;
-  bool ok = true;
-  if (w >= 2 * NW) {
-    if (kHandOver) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (w == 2 * NW && lane == 0) {
-      int cs = 0, cph = 0;  // the chain's ring position and phase
-      for (int k = 0; k < nch; ++k) {
-        const int st = k & 1, c = first + k;
-        if (k >= 3) mbar_wait_flag(c_free + cs, cph ^ 1, ok);
-        unsigned char* d = raw + L::oChain + cs * L::chain;
-        mbar_expect_tx(c_full + cs, L::chain + kGateBytes);
-        tma_load_4d(d, &m.k, c_full + cs, 0, c * kC, grp * (N / 64), bi);
-        tma_load_4d(d + L::kK, &m.T, c_full + cs, 0, 0, c, bh);
-        tma_load_4d(d + L::kK + kTile, &m.v, c_full + cs, p0, h, c * kC, bi);
-        bulk_load(raw + L::oE + cs * kGateBytes, gates + (long long)c * kGateRows * kC, kGateBytes, c_full + cs);
-        if (++cs == 3) cs = 0, cph ^= 1;
-        if (k >= 2) mbar_wait_flag(o_free + st, ((k >> 1) - 1) & 1, ok);
-        d = raw + L::oOut + st * L::out;
-        mbar_expect_tx(o_full + st, L::out + kGateBytes);
-        tma_load_4d(d, &m.q, o_full + st, 0, c * kC, grp * (N / 64), bi);
-        tma_load_4d(d + L::kK, &m.A, o_full + st, 0, 0, c, bh);
-        bulk_load(raw + L::oE + (3 + st) * kGateBytes, gates + (long long)c * kGateRows * kC, kGateBytes, o_full + st);
-      }
-    }
-  } else if (w < NW) {
-    if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+  const DeltaPlan& p;
+  const DeltaBufs& f;
+  unsigned char* raw;
+  uint32_t sm;
+  uint64_t* bars;
+  int w, lane;
+  bool ok;
+  int bi, h, p0, z, first, nch, bh;
+  bool last_of_row;
+  __device__ __forceinline__ FwdChain(const DeltaPlan& p, const DeltaBufs& f, unsigned char* raw, const FwdPlace& at)
+      : p(p), f(f), raw(raw), sm(smem_u32(raw)), bars(reinterpret_cast<uint64_t*>(raw + L::oBar)),
+        w(threadIdx.x >> 5), lane(threadIdx.x & 31), ok(true), bi(at.bi), h(at.h), p0(at.p0), z(at.z), first(at.first),
+        nch(at.nch), bh(at.bi * p.H + at.h), last_of_row(at.last_of_row) {}
+
+  // The column warps' part; kGuard: the second pass
+  template <bool kGuard>
+  __device__ __forceinline__ void columns() {
+    uint64_t *c_full = bars, *c_free = bars + 3, *h_full = bars + 10, *h_free = h_full + 2 * NW;
+    const int t = lane & 3;
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
     float S[N / 8][4], x[8][4];
     load_state<N>(S, z ? nullptr : f.init, state0, lane, p.st_bf16);
@@ -334,6 +431,11 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
         mma(S[2 * i + 1], left[k], b[2], b[3]);
       }
     };
+    // chunk c again token by token, from the state that the output warp also has
+    auto walk = [&](int c) {
+      Walk{p, f, bi, h, first + c, p0 + 16 * w, lane}.template forward<N, false>(
+          S, sm + L::oS + (2 * w + (c & 1)) * N * 32, 0);
+    };
     for (int c = 0; c + 1 < nch; ++c) {
       const int st = c & 1, ns = cs == 2 ? 0 : cs + 1;
       const uint32_t Ks = sm + L::oChain + cs * L::chain;
@@ -361,6 +463,11 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
           for (int j = 0; j < 4; ++j) S[i][j] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < N / 16; ++ks) half[ks][0] = half[ks][1] = half[ks][2] = half[ks][3] = 0u;
+      } else if (kGuard && last == 0.f && !all_finite(S)) {
+        walk(c);
+        zero(x);
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) state_product(i, Kn);
       }
       put_state(Sn);
       __syncwarp();
@@ -369,16 +476,24 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
       if (ns == 0) cph ^= 1;
     }
     solve(nch - 1);
-    const bool last_piece = piece.next == p.nc;
+    const bool last_piece = last_of_row;
     if (f.fin && last_piece) {
       const float last = reinterpret_cast<const float*>(raw + L::oE + cs * kGateBytes)[kC - 1];
 #pragma unroll
       for (int i = 0; i < N / 16; ++i) update(i, sm + L::oChain + cs * L::chain, last);
+      if (kGuard && last == 0.f && !all_finite(S)) walk(nch - 1);
     }
     if (f.fin && last_piece) store_state<N>(S, f.fin, state0, lane, p.st_bf16);
-  } else {
-    if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int cw = w - NW;
+  }
+
+  // The output warps' part (warp cw's columns); true where an output was not
+  // finite and a sequence begins
+  template <bool kGuard>
+  __device__ __forceinline__ bool outputs(const ChainMaps& m, int cw) {
+    uint64_t *o_full = bars + 6, *o_free = bars + 8, *h_full = bars + 10, *h_free = h_full + 2 * NW;
+    const int t = lane & 3;
+    bool cut = false;
+    __nv_bfloat162 seen = __floats2bfloat162_rn(0.f, 0.f);  // NaN once an output was not finite
     for (int k = 0; k < nch; ++k) {
       const int st = k & 1, c = first + k;
       const bool write = k > 0 || z == 0;
@@ -426,13 +541,25 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
           mma(y[2 * i + 1], a, b[2], b[3]);
         }
       }
+      const bool cut_here = e[kC - 1 - 2 * t] == 0.f;
+      cut |= cut_here;
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free + st);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t a[4];
         as_left(a, y[2 * k], y[2 * k + 1]);
+        if (!kGuard)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) seen = times_zero(a[j], seen);
         stsm4t(token_at(Yd, 16 * k, lane), a[0], a[1], a[2], a[3]);
+      }
+      if (kGuard && cut_here) {
+        __syncwarp();
+        if (!all_finite_tile(Yd, lane)) {
+          float S[N / 8][4];
+          Walk{p, f, bi, h, c, p0 + 16 * cw, lane}.template forward<N, true>(S, Sd, Yd);
+        }
       }
       fence_async_smem();
       __syncwarp();
@@ -445,6 +572,137 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
       __syncwarp();
     }
     if (lane == 0) bulk_wait_all();
+    const float2 nan = __bfloat1622float2(seen);
+    return cut && !(nan.x + nan.y == 0.f);
+  }
+};
+// The second pass, as calls that need nothing but the CTA's place in shared
+// memory (batch 2, L = 8192, 64 heads: 219 us for the first pass so, 213 without
+// a second one, 222 with more operands to keep for it, 229 inlined, and 239 to 265
+// with the tests and walks in one pass for all).
+__device__ __forceinline__ unsigned char* chain_smem() {
+  extern __shared__ unsigned char raw_[];
+  return raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
+}
+template <int N, int NW>
+__device__ __noinline__ bool columns_again(const DeltaPlan& p, const DeltaBufs& f) {
+  unsigned char* raw = chain_smem();
+  FwdChain<N, NW> x(p, f, raw, *reinterpret_cast<const FwdPlace*>(raw + FwdSmem<N, NW>::oPlace));
+  x.template columns<true>();
+  return x.ok;
+}
+template <int N, int NW>
+__device__ __noinline__ bool outputs_again(const DeltaPlan& p, const DeltaBufs& f, const ChainMaps& m) {
+  unsigned char* raw = chain_smem();
+  FwdChain<N, NW> x(p, f, raw, *reinterpret_cast<const FwdPlace*>(raw + FwdSmem<N, NW>::oPlace));
+  x.template outputs<true>(m, x.w - NW);
+  return x.ok;
+}
+
+template <int N, int NW, bool kPieces>
+__global__ void __launch_bounds__(fwd_threads(NW), 1)
+    delta_chain_fwd_kernel(const __grid_constant__ DeltaPlan p, const __grid_constant__ DeltaBufs f, int pieces,
+                           const __grid_constant__ ChainMaps m) {
+  using L = FwdSmem<N, NW>;
+  constexpr bool kHandOver = NW == 4;
+  extern __shared__ unsigned char raw_[];
+  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
+  const uint32_t sm = smem_u32(raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + L::oBar);
+  uint64_t *c_full = bars, *c_free = bars + 3, *o_full = bars + 6, *o_free = bars + 8;
+  uint64_t *h_full = bars + 10, *h_free = h_full + 2 * NW;  // [warp][2]
+  constexpr int kThreads = fwd_threads(NW), kBars = 10 + 4 * NW;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ptiles = p.P / (16 * NW);
+  const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
+  const int h = (int)((blockIdx.x / ptiles) % p.H), row = (int)(blockIdx.x / ((long long)ptiles * p.H));
+  const int bi = kPieces ? row % p.b : row, z = kPieces ? row / p.b : 0;  // the batch row and its piece
+  const int grp = h / p.hpg, bh = bi * p.H + h;
+  const float* gates = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+  __shared__ Piece piece_s;
+  if (kPieces && w == 0) {
+    const Piece found = find_piece(gates, z, pieces, p.nc, lane);
+    if (lane == 0) piece_s = found;
+  }
+  __shared__ int redo_s;
+  auto init_bars = [&]() {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(c_full + i, 1);
+      mbar_init(c_free + i, NW);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(o_full + i, 1);
+      mbar_init(o_free + i, NW);
+    }
+    for (int i = 0; i < 2 * NW; ++i) {
+      mbar_init(h_full + i, 1);
+      mbar_init(h_free + i, 1);
+    }
+    mbar_fence_init();
+  };
+  if (threadIdx.x == 0) {
+    init_bars();
+    redo_s = 0;
+  }
+  __syncthreads();
+  const Piece piece = kPieces ? piece_s : Piece{0, p.nc};
+  if (z && piece.first >= piece.next) return;  // no cut of its own
+  // its chunks; a later piece gives no outputs for its first one
+  const int first = piece.first, nch = min(piece.next + 1, p.nc) - first;
+  const FwdPlace here = {bi, h, p0, z, first, nch, piece.next == p.nc};
+  if (threadIdx.x == 0) *reinterpret_cast<FwdPlace*>(raw + L::oPlace) = here;
+  FwdChain<N, NW> x(p, f, raw, here);
+  bool& ok = x.ok;
+  // Every warp has ended its first pass: whether there is to be a second one
+  auto again = [&]() {
+    if (!ok) atomicOr(&redo_s, kExpired);
+    bar_sync(0, kThreads);
+    const bool redo = redo_s == kNotFinite;
+    if (redo) {
+      if (threadIdx.x == kThreads - 1) {
+        for (int i = 0; i < kBars; ++i) mbar_inval(bars + i);
+        init_bars();
+      }
+      bar_sync(0, kThreads);
+    }
+    return redo;
+  };
+  if (w >= 2 * NW) {
+    if (kHandOver) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    auto copies = [&]() {
+      int cs = 0, cph = 0;  // the chain's ring position and phase
+      for (int k = 0; k < nch; ++k) {
+        const int st = k & 1, c = first + k;
+        if (k >= 3) mbar_wait_flag(c_free + cs, cph ^ 1, ok);
+        unsigned char* d = raw + L::oChain + cs * L::chain;
+        mbar_expect_tx(c_full + cs, L::chain + kGateBytes);
+        tma_load_4d(d, &m.k, c_full + cs, 0, c * kC, grp * (N / 64), bi);
+        tma_load_4d(d + L::kK, &m.T, c_full + cs, 0, 0, c, bh);
+        tma_load_4d(d + L::kK + kTile, &m.v, c_full + cs, p0, h, c * kC, bi);
+        bulk_load(raw + L::oE + cs * kGateBytes, gates + (long long)c * kGateRows * kC, kGateBytes, c_full + cs);
+        if (++cs == 3) cs = 0, cph ^= 1;
+        if (k >= 2) mbar_wait_flag(o_free + st, ((k >> 1) - 1) & 1, ok);
+        d = raw + L::oOut + st * L::out;
+        mbar_expect_tx(o_full + st, L::out + kGateBytes);
+        tma_load_4d(d, &m.q, o_full + st, 0, c * kC, grp * (N / 64), bi);
+        tma_load_4d(d + L::kK, &m.A, o_full + st, 0, 0, c, bh);
+        bulk_load(raw + L::oE + (3 + st) * kGateBytes, gates + (long long)c * kGateRows * kC, kGateBytes, o_full + st);
+      }
+    };
+    const bool copies_here = w == 2 * NW && lane == 0;
+    if (copies_here) copies();
+    __syncwarp();
+    if (again() && copies_here) copies();
+  } else if (w < NW) {
+    if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    x.template columns<false>();
+    if (again()) ok = columns_again<N, NW>(p, f);
+  } else {
+    if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int cw = w - NW;
+    if (x.template outputs<false>(m, cw)) atomicOr(&redo_s, kNotFinite);
+    __syncwarp();
+    if (again()) ok = outputs_again<N, NW>(p, f, m);
   }
   if (!ok) atomicOr(f.status, kDevTimeout);
 }
