@@ -345,10 +345,11 @@ int ssd_gated_rmsnorm_bwd(const ssd_norm_problem* prob, const void* y, const voi
  * states, sums and decays in fp32; where the tensor cores form the products
  * (headdim a multiple of 64, dstate 64 or 128, strides multiples of 8) their
  * operands -- the carried state among them -- are rounded to bf16, and a value
- * that is not finite may reach the y of tokens before it, of its own sequence and
- * its own chunk of 64 tokens.  It never reaches another sequence's y or state.
- * In the gradient of any problem it may reach every token of its 64-token chunk,
- * also across a sequence start.
+ * that is not finite may reach the y of tokens before it (dv: after it), within
+ * its own sequence and its own chunk of 64 tokens.  In no problem does it reach y,
+ * dv, the final state or the initial state's gradient through a sequence's start
+ * or a decay that forgets.  dq, dk, dg and dbeta may take it up in every token of
+ * the chunks (64 tokens; fp32 kernels: 32) in which its sequence has one.
  *
  * Limits: headdim, dstate <= 256; nheads % ngroups == 0; ownership, errors
  * and stream semantics as above; device-side waits are bounded, and one that

@@ -31,9 +31,9 @@
 // Bound by a warp's own sequence of products (148 of 16 x 8 x 16 a chunk on one
 // sub-partition's tensor pipe, 8 cycles each, between the solve's waits) and, with
 // four column warps, by shared-memory reads of the right operands (about 70 KB
-// per 16 columns and chunk).  Measured at dstate 128: 1.66 us a chunk for 64
-// columns (batch 2, L = 8192, 64 heads: 213 us forward, 231 with what the backward
-// needs, 214 reverse), 1.24 for 32 and 1.18 for 16.
+// per 16 columns and chunk).  Measured at dstate 128: 1.69 us a chunk for 64
+// columns (batch 2, L = 8192, 64 heads: 217 us forward, 238 with what the backward
+// needs, 224 reverse), 1.24 for 32 and 1.18 for 16.
 #include "delta_internal.cuh"
 #include "mma_common.cuh"
 #include "tma_host.h"
@@ -136,9 +136,17 @@ __device__ __forceinline__ void sts16(uint32_t addr, float v) {
 // tenth of its time, they are left to a second pass over the chain's chunks, made
 // where the first one gave a value that is not finite and met a sequence's start.
 enum { kNotFinite = 1, kExpired = 2 };
-// 0 x + sum: NaN from the first value on that is not finite
-__device__ __forceinline__ __nv_bfloat162 times_zero(uint32_t x, __nv_bfloat162 sum) {
-  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(0.f, 0.f), sum);
+// seen += x 0, a product like the others: NaN from the first x on that is not finite
+__device__ __forceinline__ void watch(float (&seen)[4], const uint32_t (&x)[4]) { mma(seen, x, 0u, 0u); }
+__device__ __forceinline__ bool met_not_finite(const float (&seen)[4]) {
+  return __any_sync(0xffffffffu, !(seen[0] + seen[1] + seen[2] + seen[3] == 0.f));
+}
+// Whether a sequence begins in one of n chunks, or the state is forgotten there (e: the first one's gate record)
+__device__ __forceinline__ bool any_start(const float* e, int n, int lane) {
+  bool cut = false;
+  for (int c = lane; c < n; c += 32)
+    cut |= reinterpret_cast<const int*>(e + ((long long)c * kGateRows + kGateSeg) * kC)[kC - 1] != 0;
+  return __any_sync(0xffffffffu, cut);
 }
 struct Walk {
   const DeltaPlan& p;
@@ -234,6 +242,30 @@ struct Walk {
       }
     }
   }
+  // Reverse from the gradient of the state after the chunk (in `tile`, or zeros):
+  // the gradient D of the one before it, and r into a [64][16] tile
+  template <int N>
+  __device__ __forceinline__ void reverse(float (&D)[N / 8][4], uint32_t tile, bool zeros, uint32_t out) const {
+    state_from<N>(D, tile);
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) D[j][m] = zeros ? 0.f : D[j][m];
+#pragma unroll 1
+    for (int i = tokens() - 1; i >= 0; --i) {
+      const Gate x = gate(i);
+      const uint32_t* k = row(f.k, p.ks, N, i);
+      const float2 y = column(f.dy, (long long)p.H * p.P, i);
+      add<N>(D, make_float2(p.scale * y.x, p.scale * y.y), row(f.q, p.qs, N, i));
+      const float2 d = dot<N>(D, k), r = make_float2(x.beta * d.x, x.beta * d.y);
+      add<N>(D, make_float2(-r.x, -r.y), k);
+      decay<N>(D, x);
+      if ((lane & 3) == 0) {
+        sts16(out + i * 32 + (lane >> 2) * 2, r.x);
+        sts16(out + i * 32 + (lane >> 2) * 2 + 16, r.y);
+      }
+    }
+  }
 };
 
 struct ChainMaps {
@@ -312,6 +344,9 @@ struct FwdChain {
       : p(p), f(f), raw(raw), sm(smem_u32(raw)), bars(reinterpret_cast<uint64_t*>(raw + L::oBar)),
         w(threadIdx.x >> 5), lane(threadIdx.x & 31), ok(true), bi(at.bi), h(at.h), p0(at.p0), z(at.z), first(at.first),
         nch(at.nch), bh(at.bi * p.H + at.h), last_of_row(at.last_of_row) {}
+  __device__ __forceinline__ const float* gates() const {
+    return static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+  }
 
   // The column warps' part; kGuard: the second pass
   template <bool kGuard>
@@ -492,8 +527,7 @@ struct FwdChain {
   __device__ __forceinline__ bool outputs(const ChainMaps& m, int cw) {
     uint64_t *o_full = bars + 6, *o_free = bars + 8, *h_full = bars + 10, *h_free = h_full + 2 * NW;
     const int t = lane & 3;
-    bool cut = false;
-    __nv_bfloat162 seen = __floats2bfloat162_rn(0.f, 0.f);  // NaN once an output was not finite
+    float seen[4] = {};  // NaN once an output was not finite
     for (int k = 0; k < nch; ++k) {
       const int st = k & 1, c = first + k;
       const bool write = k > 0 || z == 0;
@@ -541,20 +575,17 @@ struct FwdChain {
           mma(y[2 * i + 1], a, b[2], b[3]);
         }
       }
-      const bool cut_here = e[kC - 1 - 2 * t] == 0.f;
-      cut |= cut_here;
+      const bool cut = kGuard && e[kC - 1 - 2 * t] == 0.f;
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free + st);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t a[4];
         as_left(a, y[2 * k], y[2 * k + 1]);
-        if (!kGuard)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) seen = times_zero(a[j], seen);
+        if (!kGuard) watch(seen, a);
         stsm4t(token_at(Yd, 16 * k, lane), a[0], a[1], a[2], a[3]);
       }
-      if (kGuard && cut_here) {
+      if (cut) {
         __syncwarp();
         if (!all_finite_tile(Yd, lane)) {
           float S[N / 8][4];
@@ -572,14 +603,13 @@ struct FwdChain {
       __syncwarp();
     }
     if (lane == 0) bulk_wait_all();
-    const float2 nan = __bfloat1622float2(seen);
-    return cut && !(nan.x + nan.y == 0.f);
+    return !kGuard && met_not_finite(seen) && any_start(gates() + (long long)first * kGateRows * kC, nch, lane);
   }
 };
 // The second pass, as calls that need nothing but the CTA's place in shared
-// memory (batch 2, L = 8192, 64 heads: 219 us for the first pass so, 213 without
-// a second one, 222 with more operands to keep for it, 229 inlined, and 239 to 265
-// with the tests and walks in one pass for all).
+// memory (batch 2, L = 8192, 64 heads: 217 us for the first pass so, 213 without
+// a second one, 229 inlined, and 239 to 265 with the tests and walks in one pass
+// for all).
 __device__ __forceinline__ unsigned char* chain_smem() {
   extern __shared__ unsigned char raw_[];
   return raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
@@ -597,6 +627,23 @@ __device__ __noinline__ bool outputs_again(const DeltaPlan& p, const DeltaBufs& 
   FwdChain<N, NW> x(p, f, raw, *reinterpret_cast<const FwdPlace*>(raw + FwdSmem<N, NW>::oPlace));
   x.template outputs<true>(m, x.w - NW);
   return x.ok;
+}
+
+// By every warp of a CTA at its first pass's end (redo: what they found): whether
+// there is a second one, with the barriers as at the start
+template <typename Init>
+__device__ __forceinline__ bool chain_again(int& redo, bool ok, uint64_t* bars, int nbars, int threads, Init init) {
+  if (!ok) atomicOr(&redo, kExpired);
+  bar_sync(0, threads);
+  const bool again = redo == kNotFinite;
+  if (again) {
+    if (threadIdx.x == threads - 1) {
+      for (int i = 0; i < nbars; ++i) mbar_inval(bars + i);
+      init();
+    }
+    bar_sync(0, threads);
+  }
+  return again;
 }
 
 template <int N, int NW, bool kPieces>
@@ -654,19 +701,7 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
   FwdChain<N, NW> x(p, f, raw, here);
   bool& ok = x.ok;
   // Every warp has ended its first pass: whether there is to be a second one
-  auto again = [&]() {
-    if (!ok) atomicOr(&redo_s, kExpired);
-    bar_sync(0, kThreads);
-    const bool redo = redo_s == kNotFinite;
-    if (redo) {
-      if (threadIdx.x == kThreads - 1) {
-        for (int i = 0; i < kBars; ++i) mbar_inval(bars + i);
-        init_bars();
-      }
-      bar_sync(0, kThreads);
-    }
-    return redo;
-  };
+  auto again = [&]() { return chain_again(redo_s, ok, bars, kBars, kThreads, init_bars); };
   if (w >= 2 * NW) {
     if (kHandOver) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     auto copies = [&]() {
@@ -713,63 +748,40 @@ struct RevSmem {
   // a ring three deep of K, Q, T, A, dY, gates; D' and r by warp
   static constexpr int stage = 2 * kK + 2 * (int)kTile + kV;
   static constexpr int oSt = 0, oD = oSt + 3 * stage, oR = oD + NW * N * 32, oE = oR + NW * 2048,
-                       oBar = oE + 3 * kGateBytes, bytes = oBar + 6 * 8 + 1024;
+                       oBar = oE + 3 * kGateBytes, oPlace = oBar + 6 * 8, bytes = oPlace + 64 + 1024;
 };
 
-template <int N, int NW, bool kPieces>
-__global__ void __launch_bounds__((NW + 1) * 32, 1)
-    delta_chain_bwd_kernel(DeltaPlan p, DeltaBufs f, int pieces, const __grid_constant__ ChainMaps m) {
+
+// A reverse chain's CTA: its columns and its chunks, `right` the first of them
+struct RevPlace {
+  int bi, h, p0, z, right, nch;
+  bool inner;
+};
+template <int N, int NW>
+struct RevChain {
   using L = RevSmem<N, NW>;
-  extern __shared__ unsigned char raw_[];
-  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
-  const uint32_t sm = smem_u32(raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(raw + L::oBar);
-  uint64_t* empty = full + 3;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
-  const int ptiles = p.P / (16 * NW);
-  const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
-  const int h = (int)((blockIdx.x / ptiles) % p.H), row = (int)(blockIdx.x / ((long long)ptiles * p.H));
-  const int bi = kPieces ? row % p.b : row, z = kPieces ? row / p.b : 0;  // the batch row and its piece
-  const int grp = h / p.hpg, bh = bi * p.H + h;
-  const float* gates = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
-  __shared__ Piece piece_s;
-  if (kPieces && w == 0) {
-    const Piece found = find_piece(gates, z, pieces, p.nc, lane);
-    if (lane == 0) piece_s = found;
+  const DeltaPlan& p;
+  const DeltaBufs& f;
+  unsigned char* raw;
+  uint32_t sm;
+  int w, lane;
+  bool ok;
+  int bi, h, p0, z, right, nch, bh;
+  bool inner;
+  __device__ __forceinline__ RevChain(const DeltaPlan& p, const DeltaBufs& f, unsigned char* raw, const RevPlace& at)
+      : p(p), f(f), raw(raw), sm(smem_u32(raw)), w(threadIdx.x >> 5), lane(threadIdx.x & 31), ok(true), bi(at.bi),
+        h(at.h), p0(at.p0), z(at.z), right(at.right), nch(at.nch), bh(at.bi * p.H + at.h), inner(at.inner) {}
+  __device__ __forceinline__ const float* gates() const {
+    return static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, NW);
-    }
-    mbar_fence_init();
-  }
-  __syncthreads();
-  const Piece piece = kPieces ? piece_s : Piece{0, p.nc};
-  if (z && piece.first >= piece.next) return;  // no cut of its own
-  // its chunks, from the right; an earlier piece gives no outputs for its first one (which is the next piece's too)
-  const bool inner = piece.next < p.nc;
-  const int right = inner ? piece.next : p.nc - 1, nch = right + 1 - piece.first;
-  bool ok = true;
-  if (w == NW) {
-    if (lane == 0) {
-      int st = 0, ph = 0;
-      for (int k = 0; k < nch; ++k) {
-        const int c = right - k;
-        if (k >= 3) mbar_wait_flag(empty + st, ph ^ 1, ok);
-        unsigned char* d = raw + L::oSt + st * L::stage;
-        mbar_expect_tx(full + st, L::stage + kGateBytes);
-        tma_load_4d(d, &m.k, full + st, 0, c * kC, grp * (N / 64), bi);
-        tma_load_4d(d + L::kK, &m.q, full + st, 0, c * kC, grp * (N / 64), bi);
-        d += 2 * L::kK;
-        tma_load_4d(d, &m.T, full + st, 0, 0, c, bh);
-        tma_load_4d(d + kTile, &m.A, full + st, 0, 0, c, bh);
-        tma_load_4d(d + 2 * kTile, &m.v, full + st, p0, h, c * kC, bi);
-        bulk_load(raw + L::oE + st * kGateBytes, gates + (long long)c * kGateRows * kC, kGateBytes, full + st);
-        if (++st == 3) st = 0, ph ^= 1;
-      }
-    }
-  } else {
+
+  // The column warps' part (kGuard: the second pass); true where an r was not
+  // finite and a sequence begins
+  template <bool kGuard>
+  __device__ __forceinline__ bool columns(const ChainMaps& m) {
+    uint64_t *full = reinterpret_cast<uint64_t*>(raw + L::oBar), *empty = full + 3;
+    const int t = lane & 3;
+    float seen[4] = {};  // NaN once an r was not finite
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
     float D[N / 8][4], x[8][4];
     load_state<N>(D, inner ? nullptr : f.dfin, state0, lane, p.st_bf16);
@@ -798,10 +810,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) stsm4t(token_at(Rd, 16 * k, lane), rk[k][0], rk[k][1], rk[k][2], rk[k][3]);
     };
-    auto put = [&](int c, bool with_r, bool with_d) {
+    auto put = [&](int c, bool with_r, bool with_d, bool walked = false) {
       if (lane == 0) bulk_wait_read<0>();  // the tiles' last contents have been read
       __syncwarp();
-      if (with_r) put_r();
+      if (with_r && !walked) put_r();
       if (with_d)
 #pragma unroll
         for (int ks = 0; ks < N / 16; ++ks)
@@ -888,6 +900,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
           mma(x[2 * j + 1], rk[i], b[2], b[3]);
         }
       }
+      if (!kGuard)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) watch(seen, rk[k]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -919,40 +934,140 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) D[i][j] = 0.f;
     };
+    // whether step k0's chunk was walked: r is in its tile and D is the gradient before the chunk
+    auto walked_at = [&](int k0) {
+      if (!kGuard || reinterpret_cast<const float*>(raw + L::oE + st * kGateBytes)[kC - 1] != 0.f ||
+          (all_finite(x) && all_finite(D)))
+        return false;
+      if (lane == 0) bulk_wait_read<0>();  // the last r has been read
+      __syncwarp();
+      Walk{p, f, bi, h, right - k0, p0 + 16 * w, lane}.template reverse<N>(D, Dd, inner && k0 == 0, Rd);
+      return true;
+    };
     for (int k0 = 0; k0 + 1 < nch; ++k0) {
       const int c = right - k0, ns = st == 2 ? 0 : st + 1;
       const uint32_t Ks = sm + L::oSt + st * L::stage, Kn = sm + L::oSt + ns * L::stage;
       solve();
+      const bool walked = walked_at(k0);
       mbar_wait_flag(full + ns, ns ? ph : ph ^ 1, ok);
       // D' += (-e r)' K, each pair of tiles followed by the next chunk's product with the pair before
       zero(x);
-      update(0, Ks);
+      if (walked) {
 #pragma unroll
-      for (int i = 1; i < N / 16; ++i) {
-        update(i, Ks);
-        state_product(i - 1, Kn);
+        for (int i = 0; i < N / 16; ++i) state_product(i, Kn);
+      } else {
+        update(0, Ks);
+#pragma unroll
+        for (int i = 1; i < N / 16; ++i) {
+          update(i, Ks);
+          state_product(i - 1, Kn);
+        }
+        state_product(N / 16 - 1, Kn);
       }
-      state_product(N / 16 - 1, Kn);
       if (starts()) {
         zero(x);
         zero_state();
 #pragma unroll
         for (int ks = 0; ks < N / 16; ++ks) half[ks][0] = half[ks][1] = half[ks][2] = half[ks][3] = 0u;
       }
-      put(c, k0 > 0 || !inner, true);
+      put(c, k0 > 0 || !inner, true, walked);
       if (lane == 0) mbar_arrive(empty + st);
       st = ns;
       if (ns == 0) ph ^= 1;
     }
     solve();
-    if (nch > 1 || !inner) put(piece.first, true, false);
+    const bool walked = walked_at(nch - 1);
+    if (nch > 1 || !inner) put(right + 1 - nch, true, false, walked);
     if (f.dinit && z == 0) {
+      if (!walked)
 #pragma unroll
-      for (int i = 0; i < N / 16; ++i) update(i, sm + L::oSt + st * L::stage);
+        for (int i = 0; i < N / 16; ++i) update(i, sm + L::oSt + st * L::stage);
       if (starts()) zero_state();
     }
     if (f.dinit && z == 0) store_state<N>(D, f.dinit, state0, lane, p.st_bf16);
     if (lane == 0) bulk_wait_all();
+    const float* e = gates() + (long long)(right + 1 - nch) * kGateRows * kC;
+    return !kGuard && met_not_finite(seen) && any_start(e, nch, lane);
+  }
+};
+template <int N, int NW>
+__device__ __noinline__ bool reverse_again(const DeltaPlan& p, const DeltaBufs& f, const ChainMaps& m) {
+  unsigned char* raw = chain_smem();
+  RevChain<N, NW> x(p, f, raw, *reinterpret_cast<const RevPlace*>(raw + RevSmem<N, NW>::oPlace));
+  x.template columns<true>(m);
+  return x.ok;
+}
+
+template <int N, int NW, bool kPieces>
+__global__ void __launch_bounds__((NW + 1) * 32, 1)
+    delta_chain_bwd_kernel(const __grid_constant__ DeltaPlan p, const __grid_constant__ DeltaBufs f, int pieces,
+                           const __grid_constant__ ChainMaps m) {
+  using L = RevSmem<N, NW>;
+  extern __shared__ unsigned char raw_[];
+  unsigned char* raw = raw_ + ((1024 - (smem_u32(raw_) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + L::oBar);
+  uint64_t* empty = full + 3;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ptiles = p.P / (16 * NW);
+  const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
+  const int h = (int)((blockIdx.x / ptiles) % p.H), row = (int)(blockIdx.x / ((long long)ptiles * p.H));
+  const int bi = kPieces ? row % p.b : row, z = kPieces ? row / p.b : 0;  // the batch row and its piece
+  const int grp = h / p.hpg, bh = bi * p.H + h;
+  const float* gates = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
+  __shared__ Piece piece_s;
+  if (kPieces && w == 0) {
+    const Piece found = find_piece(gates, z, pieces, p.nc, lane);
+    if (lane == 0) piece_s = found;
+  }
+  __shared__ int redo_s;
+  auto init_bars = [&]() {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, NW);
+    }
+    mbar_fence_init();
+  };
+  if (threadIdx.x == 0) {
+    init_bars();
+    redo_s = 0;
+  }
+  __syncthreads();
+  const Piece piece = kPieces ? piece_s : Piece{0, p.nc};
+  if (z && piece.first >= piece.next) return;  // no cut of its own
+  // its chunks, from the right; an earlier piece gives no outputs for its first one (which is the next piece's too)
+  const bool inner = piece.next < p.nc;
+  const int right = inner ? piece.next : p.nc - 1, nch = right + 1 - piece.first;
+  const RevPlace here = {bi, h, p0, z, right, nch, inner};
+  if (threadIdx.x == 0) *reinterpret_cast<RevPlace*>(raw + L::oPlace) = here;
+  RevChain<N, NW> x(p, f, raw, here);
+  bool& ok = x.ok;
+  // Every warp has ended its first pass: whether there is to be a second one
+  auto again = [&]() { return chain_again(redo_s, ok, full, 6, (NW + 1) * 32, init_bars); };
+  if (w == NW) {
+    auto copies = [&]() {
+      int st = 0, ph = 0;
+      for (int k = 0; k < nch; ++k) {
+        const int c = right - k;
+        if (k >= 3) mbar_wait_flag(empty + st, ph ^ 1, ok);
+        unsigned char* d = raw + L::oSt + st * L::stage;
+        mbar_expect_tx(full + st, L::stage + kGateBytes);
+        tma_load_4d(d, &m.k, full + st, 0, c * kC, grp * (N / 64), bi);
+        tma_load_4d(d + L::kK, &m.q, full + st, 0, c * kC, grp * (N / 64), bi);
+        d += 2 * L::kK;
+        tma_load_4d(d, &m.T, full + st, 0, 0, c, bh);
+        tma_load_4d(d + kTile, &m.A, full + st, 0, 0, c, bh);
+        tma_load_4d(d + 2 * kTile, &m.v, full + st, p0, h, c * kC, bi);
+        bulk_load(raw + L::oE + st * kGateBytes, gates + (long long)c * kGateRows * kC, kGateBytes, full + st);
+        if (++st == 3) st = 0, ph ^= 1;
+      }
+    };
+    if (lane == 0) copies();
+    __syncwarp();
+    if (again() && lane == 0) copies();
+  } else {
+    if (x.template columns<false>(m)) atomicOr(&redo_s, kNotFinite);
+    __syncwarp();
+    if (again()) ok = reverse_again<N, NW>(p, f, m);
   }
   if (!ok) atomicOr(f.status, kDevTimeout);
 }
