@@ -82,6 +82,28 @@ __device__ __forceinline__ void st_state(void* p, long long i, int bf16, float v
 // and sums that held such a term would lose the digits of the others.
 constexpr float kForget = -100.0f;
 
+// The decays' running sum over a chunk of the fp32 kernels, a token a lane, in
+// two parts: differences of it are taken before it is rounded.  (31 decays may sum
+// to -3000, which fp32 holds to 2e-4, while the pairs behind them differ by 1e-2.)
+// starts becomes the number of sequence starts up to the lane.
+struct GateSum {
+  float hi, lo;
+};
+__device__ __forceinline__ GateSum gate_sum(float g, int& starts, int lane) {
+  double sum = g;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double ug = __shfl_up_sync(0xffffffffu, sum, o);
+    const int us = __shfl_up_sync(0xffffffffu, starts, o);
+    if (lane >= o) {
+      sum += ug;
+      starts += us;
+    }
+  }
+  const float hi = (float)sum;
+  return {hi, (float)(sum - hi)};
+}
+
 constexpr int kDeltaChunk = 64;  // tokens per chunk of the tensor-core kernels
 // Rows of a chunk's gate record (fp32): e_i; o_j beta_j; gam_i log2(e); beta;
 // o_j; the decay between token 32 and the token (of the second half's rows

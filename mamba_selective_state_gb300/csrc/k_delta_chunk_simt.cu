@@ -9,8 +9,8 @@
 // the inverse of the triangular system among it) runs for all chunks at once;
 // a chain's CTA keeps 16 columns of its head's state in shared memory and does
 // four products a chunk, four columns and one token (or state row) a thread,
-// with the next chunk's operands on their way to registers.  Measured: 96 us
-// forward and 112 reverse for 32 chunks of 12 heads of 40 x 56 (36 CTAs), 5,900
+// with the next chunk's operands on their way to registers.  Measured: 102 us
+// forward and 105 reverse for 32 chunks of 12 heads of 40 x 56 (36 CTAs), 5,900
 // cycles and 1,970 instructions a warp for a chunk.  Bound by shared memory's
 // pipe (2.9 passes for each of 250 loads a warp) and the latency of the products
 // it feeds: four more warps that take the loads, the outputs and Q S off the
@@ -55,8 +55,8 @@ __global__ void __launch_bounds__(kPrep) delta_prep_simt_kernel(DeltaPlan p, Del
   float* qk_s = k_s + kC * ks;            // [kC][kTs]
   float* kk_s = qk_s + kC * kTs;
   float* M_s = kk_s + kC * kTs;           // [8][kC][kTs] by warp
-  float* g_s = M_s + 8 * kC * kTs;        // [8][2][kC]: gam, beta
-  int* s_s = reinterpret_cast<int*>(g_s + 8 * 2 * kC);  // [8][kC]
+  float* g_s = M_s + 8 * kC * kTs;        // [8][3][kC]: gam in two parts, beta
+  int* s_s = reinterpret_cast<int*>(g_s + 8 * 3 * kC);  // [8][kC]
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const int nsplit = (p.hpg + heads_per_cta - 1) / heads_per_cta;
   long long idx = blockIdx.x;
@@ -100,8 +100,9 @@ __global__ void __launch_bounds__(kPrep) delta_prep_simt_kernel(DeltaPlan p, Del
   __syncthreads();
   const int h0 = grp * p.hpg + sp * heads_per_cta, h1 = min(h0 + heads_per_cta, (grp + 1) * p.hpg);
   float* M = M_s + w * kC * kTs;
-  float* gam = g_s + w * 2 * kC;
-  float* bet = gam + kC;
+  float* gam = g_s + w * 3 * kC;
+  float* gam_lo = gam + kC;
+  float* bet = gam_lo + kC;
   int* seg = s_s + w * kC;
   for (int h = h0 + w; h < h1; h += kPrep / 32) {
     const long long unit = ((long long)bi * p.H + h) * p.nc + c;
@@ -114,29 +115,23 @@ __global__ void __launch_bounds__(kPrep) delta_prep_simt_kernel(DeltaPlan p, Del
       rs = (f.seq != nullptr && t0 + lane > 0 && f.seq[tok0 + lane] != f.seq[tok0 + lane - 1]) || g < kForget;
       if (rs) g = 0.f;
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float ug = __shfl_up_sync(0xffffffffu, g, o);
-      const int ur = __shfl_up_sync(0xffffffffu, rs, o);
-      if (lane >= o) {
-        g += ug;
-        rs += ur;
-      }
-    }
-    const float last = __shfl_sync(0xffffffffu, g, 31);
+    const GateSum sum = gate_sum(g, rs, lane);
+    const float hi = sum.hi, lo = sum.lo, hi_last = __shfl_sync(0xffffffffu, hi, 31),
+                lo_last = __shfl_sync(0xffffffffu, lo, 31);
     const int slast = __shfl_sync(0xffffffffu, rs, 31);
     __syncwarp();
-    gam[lane] = g;
+    gam[lane] = hi;
+    gam_lo[lane] = lo;
     bet[lane] = be;
     seg[lane] = rs;
     float* rec = static_cast<float*>(f.e) + unit * kRec;
-    rec[lane] = rs == 0 ? expf(g) : 0.f;
-    rec[kC + lane] = rs == slast ? expf(last - g) * be : 0.f;
+    rec[lane] = rs == 0 ? expf(hi) : 0.f;
+    rec[kC + lane] = rs == slast ? expf((hi_last - hi) + (lo_last - lo)) * be : 0.f;
     __syncwarp();
     // column `lane` of M and A
     float* A = static_cast<float*>(f.A) + unit * kC * kC;
     for (int i = 0; i < kC; ++i) {
-      const float E = (lane <= i) & (seg[i] == rs) ? expf(gam[i] - g) * be : 0.f;
+      const float E = (lane <= i) & (seg[i] == rs) ? expf((gam[i] - hi) + (gam_lo[i] - lo)) * be : 0.f;
       M[i * kTs + lane] = lane < i ? E * kk_s[i * kTs + lane] : 0.f;
       A[i * kC + lane] = p.scale * E * qk_s[i * kTs + lane];
     }
@@ -535,7 +530,7 @@ __global__ void __launch_bounds__(kThreads) delta_chain_simt_bwd_kernel(DeltaPla
 template <typename T>
 cudaError_t launch_prep_t(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
   const int np = (p.N + 3) & ~3;
-  const size_t smem = sizeof(float) * (2 * kC * (np + 4) + 10 * kC * kTs + 8 * 3 * kC);
+  const size_t smem = sizeof(float) * (2 * kC * (np + 4) + 10 * kC * kTs + 8 * 4 * kC);
   auto kern = delta_prep_simt_kernel<T>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

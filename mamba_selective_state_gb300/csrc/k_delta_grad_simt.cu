@@ -44,7 +44,8 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaPlan p, Delta
   float* Z_s = kk_s + kC * (kC + 1);
   float* M_s = Z_s + kC * (kC + 1);
   float* gam = M_s + kC * (kC + 1);      // [kC] each
-  float* bet = gam + kC;
+  float* gam_lo = gam + kC;              // the cumulative decay in two parts
+  float* bet = gam_lo + kC;
   float* drow = bet + kC;                // what row i's decay gains
   float* dout = drow + kC;               // beta_j o_j k_j.(D1 w_j)
   float* dbo = dout + kC;                // the same without beta_j
@@ -102,17 +103,9 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaPlan p, Delta
         rs = f.seq != nullptr && t0 + t > 0 && f.seq[tok0 + t] != f.seq[tok0 + t - 1];
         if (g < kForget) { rs = 1; }
       }
-      float sum = rs ? 0.f : g;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float up = __shfl_up_sync(0xffffffffu, sum, o);
-        const int ur = __shfl_up_sync(0xffffffffu, rs, o);
-        if (t >= o) {
-          sum += up;
-          rs += ur;
-        }
-      }
-      gam[t] = sum;
+      const GateSum sum = gate_sum(rs ? 0.f : g, rs, t);
+      gam[t] = sum.hi;
+      gam_lo[t] = sum.lo;
       bet[t] = be;
       seg[t] = rs;
     }
@@ -171,13 +164,13 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaPlan p, Delta
 #pragma unroll
     for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sd;
-    const float glast = gam[kC - 1];
+    const float glast = gam[kC - 1], glast_lo = gam_lo[kC - 1];
     const int slast = seg[kC - 1];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       const int i = i0 + a;
       const float e = seg[i] == 0 ? expf(gam[i]) : 0.f;
-      const float o = seg[i] == slast ? expf(glast - gam[i]) : 0.f;
+      const float o = seg[i] == slast ? expf((glast - gam[i]) + (glast_lo - gam_lo[i])) : 0.f;
       float row = 0.f, out = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -191,7 +184,8 @@ __global__ void __launch_bounds__(kThreads) delta_grad_kernel(DeltaPlan p, Delta
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int jj = j * 16 + tx;
-        const float E = jj <= i && seg[i] == seg[jj] ? expf(gam[i] - gam[jj]) : 0.f;
+        const float E =
+            jj <= i && seg[i] == seg[jj] ? expf((gam[i] - gam[jj]) + (gam_lo[i] - gam_lo[jj])) : 0.f;
         Z_s[i * (kC + 1) + jj] = p.scale * E * m1[a][j];
         M_s[i * (kC + 1) + jj] = jj < i ? -E * m2[a][j] : 0.f;
       }
@@ -269,7 +263,7 @@ template <typename T, int NJ>
 cudaError_t launch_t(const DeltaPlan& p, const DeltaBufs& f, cudaStream_t s) {
   constexpr int NP = NJ * 16;
   const size_t smem = sizeof(float) * (2 * kC * (NP + 1) + 2 * kTp * NP + 3 * kC * (kTp + 1) + 4 * kC * (kC + 1) +
-                                       6 * kC + 8);
+                                       7 * kC + 8);
   auto kern = delta_grad_kernel<T, NJ>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;

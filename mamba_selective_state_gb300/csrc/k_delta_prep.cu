@@ -67,7 +67,9 @@ __global__ void __launch_bounds__(kThreads, 3) delta_prep_kernel(DeltaPlan p, De
   const int h1 = min(h0 + heads_per_cta, (grp + 1) * p.hpg);
 
   // gam, beta and sequence starts of head h into its slot, its record to
-  // global, by one warp with two tokens a lane
+  // global, by one warp with two tokens a lane.  (gam is one fp32 sum of at most 64
+  // decays of -100: it rounds a pair's decay by up to 2e-4 of it, a tenth of the
+  // bf16 rounding of the products that take it.)
   auto gates = [&](int h) {
     float* gam = reinterpret_cast<float*>(raw + L::oGate) + (h - h0) * 2 * kC;
     int* seg = reinterpret_cast<int*>(raw + L::oSeg) + (h - h0) * kC;
