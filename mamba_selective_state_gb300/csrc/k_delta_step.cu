@@ -110,7 +110,7 @@ struct Ahead {
     }
     if (threadIdx.x < TOK * kCols) (&sm.v[0][0])[threadIdx.x] = to_f(v);
     if (threadIdx.x < TOK) {
-      sm.a[threadIdx.x] = expf(to_f(g));
+      sm.a[threadIdx.x] = to_f(g) < kForget ? 0.f : expf(to_f(g));  // 0: the state is forgotten
       sm.beta[threadIdx.x] = to_f(beta);
     }
   }
@@ -153,6 +153,11 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 && NR <= 16 ? 8 : 1)
 #pragma unroll
     for (int t = 0; t < TOK; ++t) {
       if (t >= n) break;
+      const float a = sm.a[t];
+      if (a == 0.f) {  // whatever it holds
+#pragma unroll
+        for (int i = 0; i < NR; ++i) S[i] = 0.f;
+      }
       float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f}, kk[NR];
 #pragma unroll
       for (int i = 0; i < NR; i += 4) {
@@ -163,7 +168,6 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 && NR <= 16 ? 8 : 1)
         sq[0] += q4.x * S[i]; sq[1] += q4.y * S[i + 1]; sq[2] += q4.z * S[i + 2]; sq[3] += q4.w * S[i + 3];
         d[0] += k4.x * q4.x; d[1] += k4.y * q4.y; d[2] += k4.z * q4.z; d[3] += k4.w * q4.w;
       }
-      const float a = sm.a[t];
       const float dk = group_sum((sk[0] + sk[1]) + (sk[2] + sk[3]));
       const float dq = group_sum((sq[0] + sq[1]) + (sq[2] + sq[3]));
       const float qk = group_sum((d[0] + d[1]) + (d[2] + d[3]));
