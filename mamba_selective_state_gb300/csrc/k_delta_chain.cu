@@ -278,31 +278,56 @@ struct ChainMaps {
 // piece z begins at the cut nearest to z / pieces of the chunks, from zeros, and
 // goes through the next piece's first chunk; what that chunk's columns give is
 // written by the one of the two pieces that enters it with its neighbour's state
-// (or gradient).  A row without cuts is left to piece 0.
+// (or gradient).
+//
+// The host cannot see the cuts.  A CTA that takes a piece has twice the columns
+// that it would have of a whole chain (see chain_shape), and where a row's cuts
+// leave one piece nearly the whole chain, that is a loss: then the row's first two
+// CTAs take the whole chain, half of the column warps each, and the others end.
 struct Piece {
   int first, next;  // its first chunk, and the next piece's (or nc)
+  int z;            // its number; 0 where it begins with the row
+  int warp0, warps; // the column warps at work
+  __device__ __forceinline__ bool has(int w) const { return w >= warp0 && w < warp0 + warps; }
 };
-// The cut nearest to chunk `mid`, or nc; e: the gate records
+// The cut nearest to chunk `mid`, or nc; e: the gate records.  (128 chunks to
+// either side at a time: a row without cuts is searched to its ends.)
 __device__ __forceinline__ int near_cut(const float* e, int mid, int nc, int lane) {
   // (the segment of a chunk's last token, counted from the chunk's start)
   auto cut = [&](int c) {
-    return c >= 0 && c < nc && reinterpret_cast<const int*>(e + ((long long)c * kGateRows + kGateSeg) * kC)[kC - 1] != 0;
+    const bool in = c >= 0 && c < nc;
+    return in && reinterpret_cast<const int*>(e + ((long long)c * kGateRows + kGateSeg) * kC)[kC - 1] != 0;
   };
-  for (int d0 = 0; d0 < nc; d0 += 32) {
-    const unsigned below = __ballot_sync(0xffffffffu, cut(mid - d0 - lane));
-    const unsigned above = __ballot_sync(0xffffffffu, cut(mid + d0 + lane));
-    if (below | above) {
-      const int l = __ffs(below | above) - 1;
-      return below >> l & 1 ? mid - d0 - l : mid + d0 + l;
+  for (int d0 = 0; d0 < nc; d0 += 128) {
+    bool below[4], above[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      below[u] = cut(mid - d0 - 32 * u - lane);
+      above[u] = cut(mid + d0 + 32 * u + lane);
+    }
+    for (int u = 0; u < 4; ++u) {
+      const unsigned lo = __ballot_sync(0xffffffffu, below[u]), hi = __ballot_sync(0xffffffffu, above[u]);
+      if (lo | hi) {
+        const int l = __ffs(lo | hi) - 1, d = d0 + 32 * u + l;
+        return lo >> l & 1 ? mid - d : mid + d;
+      }
     }
   }
   return nc;
 }
+template <int NW>
 __device__ __forceinline__ Piece find_piece(const float* e, int z, int pieces, int nc, int lane) {
-  Piece r;
-  r.first = z ? near_cut(e, (int)((long long)z * nc / pieces), nc, lane) : 0;
-  r.next = z + 1 < pieces ? near_cut(e, (int)((long long)(z + 1) * nc / pieces), nc, lane) : nc;
-  return r;
+  auto cut = [&](int i) {
+    return i <= 0 ? 0 : i < pieces ? near_cut(e, (int)((long long)i * nc / pieces), nc, lane) : nc;
+  };
+  if (NW > 1) {  // two or three pieces
+    const int c1 = cut(1), c2 = cut(2);
+    const int largest = max(max(min(c1 + 1, nc), min(c2 + 1, nc) - c1), nc - c2);
+    // (a chunk of 64 columns takes 1.37 times as long as one of 32, one of 32 1.05 times as long as one of 16)
+    if (NW == 4 ? largest * 4 > nc * 3 : largest * 16 > nc * 15) return {0, nc, 0, z * (NW / 2), z < 2 ? NW / 2 : 0};
+    return {z == 0 ? 0 : z == 1 ? c1 : c2, z == 0 ? c1 : z == 1 ? c2 : nc, z, 0, NW};
+  }
+  return {cut(z), cut(z + 1), z, 0, NW};
 }
 
 // NW column warps: 16 NW columns a CTA
@@ -322,6 +347,9 @@ struct FwdSmem {
 // registers are handed over by groups of four warps, so three idle ones join
 // the copying warp (launched with 168 each: 240 + 208 + 40 <= 3 x 168).
 constexpr int fwd_threads(int nw) { return nw == 4 ? 384 : (2 * nw + 1) * 32; }
+// The column warp whose outputs warp w forms: not one of its own sub-partition, so
+// that half of the column warps and their output warps have all four.
+__device__ __forceinline__ int output_columns(int w, int nw) { return (w - nw) ^ (nw / 2); }
 
 // A forward chain's CTA: its columns and its chunks
 struct FwdPlace {
@@ -625,7 +653,7 @@ template <int N, int NW>
 __device__ __noinline__ bool outputs_again(const DeltaPlan& p, const DeltaBufs& f, const ChainMaps& m) {
   unsigned char* raw = chain_smem();
   FwdChain<N, NW> x(p, f, raw, *reinterpret_cast<const FwdPlace*>(raw + FwdSmem<N, NW>::oPlace));
-  x.template outputs<true>(m, x.w - NW);
+  x.template outputs<true>(m, output_columns(x.w, NW));
   return x.ok;
 }
 
@@ -663,23 +691,23 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
   const int ptiles = p.P / (16 * NW);
   const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
   const int h = (int)((blockIdx.x / ptiles) % p.H), row = (int)(blockIdx.x / ((long long)ptiles * p.H));
-  const int bi = kPieces ? row % p.b : row, z = kPieces ? row / p.b : 0;  // the batch row and its piece
+  const int bi = kPieces ? row % p.b : row;
   const int grp = h / p.hpg, bh = bi * p.H + h;
   const float* gates = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
   __shared__ Piece piece_s;
   if (kPieces && w == 0) {
-    const Piece found = find_piece(gates, z, pieces, p.nc, lane);
+    const Piece found = find_piece<NW>(gates, row / p.b, pieces, p.nc, lane);
     if (lane == 0) piece_s = found;
   }
   __shared__ int redo_s;
   auto init_bars = [&]() {
     for (int i = 0; i < 3; ++i) {
       mbar_init(c_full + i, 1);
-      mbar_init(c_free + i, NW);
+      mbar_init(c_free + i, kPieces ? max(piece_s.warps, 1) : NW);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(o_full + i, 1);
-      mbar_init(o_free + i, NW);
+      mbar_init(o_free + i, kPieces ? max(piece_s.warps, 1) : NW);
     }
     for (int i = 0; i < 2 * NW; ++i) {
       mbar_init(h_full + i, 1);
@@ -692,8 +720,9 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
     redo_s = 0;
   }
   __syncthreads();
-  const Piece piece = kPieces ? piece_s : Piece{0, p.nc};
-  if (z && piece.first >= piece.next) return;  // no cut of its own
+  const Piece piece = kPieces ? piece_s : Piece{0, p.nc, 0, 0, NW};
+  const int z = piece.z;
+  if ((z && piece.first >= piece.next) || piece.warps == 0) return;  // no cut of its own, or nothing left
   // its chunks; a later piece gives no outputs for its first one
   const int first = piece.first, nch = min(piece.next + 1, p.nc) - first;
   const FwdPlace here = {bi, h, p0, z, first, nch, piece.next == p.nc};
@@ -730,14 +759,16 @@ __global__ void __launch_bounds__(fwd_threads(NW), 1)
     if (again() && copies_here) copies();
   } else if (w < NW) {
     if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
-    x.template columns<false>();
-    if (again()) ok = columns_again<N, NW>(p, f);
+    const bool live = !kPieces || piece.has(w);
+    if (live) x.template columns<false>();
+    if (again() && live) ok = columns_again<N, NW>(p, f);
   } else {
     if (kHandOver) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int cw = w - NW;
-    if (x.template outputs<false>(m, cw)) atomicOr(&redo_s, kNotFinite);
+    const int cw = output_columns(w, NW);
+    const bool live = !kPieces || piece.has(cw);
+    if (live && x.template outputs<false>(m, cw)) atomicOr(&redo_s, kNotFinite);
     __syncwarp();
-    if (again()) ok = outputs_again<N, NW>(p, f, m);
+    if (again() && live) ok = outputs_again<N, NW>(p, f, m);
   }
   if (!ok) atomicOr(f.status, kDevTimeout);
 }
@@ -1011,19 +1042,19 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
   const int ptiles = p.P / (16 * NW);
   const int p0 = (int)(blockIdx.x % ptiles) * 16 * NW;
   const int h = (int)((blockIdx.x / ptiles) % p.H), row = (int)(blockIdx.x / ((long long)ptiles * p.H));
-  const int bi = kPieces ? row % p.b : row, z = kPieces ? row / p.b : 0;  // the batch row and its piece
+  const int bi = kPieces ? row % p.b : row;
   const int grp = h / p.hpg, bh = bi * p.H + h;
   const float* gates = static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
   __shared__ Piece piece_s;
   if (kPieces && w == 0) {
-    const Piece found = find_piece(gates, z, pieces, p.nc, lane);
+    const Piece found = find_piece<NW>(gates, row / p.b, pieces, p.nc, lane);
     if (lane == 0) piece_s = found;
   }
   __shared__ int redo_s;
   auto init_bars = [&]() {
     for (int i = 0; i < 3; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, NW);
+      mbar_init(empty + i, kPieces ? max(piece_s.warps, 1) : NW);
     }
     mbar_fence_init();
   };
@@ -1032,8 +1063,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
     redo_s = 0;
   }
   __syncthreads();
-  const Piece piece = kPieces ? piece_s : Piece{0, p.nc};
-  if (z && piece.first >= piece.next) return;  // no cut of its own
+  const Piece piece = kPieces ? piece_s : Piece{0, p.nc, 0, 0, NW};
+  const int z = piece.z;
+  if ((z && piece.first >= piece.next) || piece.warps == 0) return;  // no cut of its own, or nothing left
   // its chunks, from the right; an earlier piece gives no outputs for its first one (which is the next piece's too)
   const bool inner = piece.next < p.nc;
   const int right = inner ? piece.next : p.nc - 1, nch = right + 1 - piece.first;
@@ -1065,9 +1097,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
     __syncwarp();
     if (again() && lane == 0) copies();
   } else {
-    if (x.template columns<false>(m)) atomicOr(&redo_s, kNotFinite);
+    const bool live = !kPieces || piece.has(w);
+    if (live && x.template columns<false>(m)) atomicOr(&redo_s, kNotFinite);
     __syncwarp();
-    if (again()) ok = reverse_again<N, NW>(p, f, m);
+    if (again() && live) ok = reverse_again<N, NW>(p, f, m);
   }
   if (!ok) atomicOr(f.status, kDevTimeout);
 }
