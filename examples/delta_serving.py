@@ -62,10 +62,13 @@ def generate(layer, prompt, batch, new, draft, seed=1):
     dev = prompt.device
     gen = torch.Generator(device=dev).manual_seed(seed)
     # the prompt's state, but for its last token: that is the first one fed to the loop
-    pre = runner.DeltaDevice(*layer.inputs(prompt[None, :-1]))
-    pre.fwd()
     cache = runner.StateCache(1, layer.H, layer.P, layer.N, "int8", device=dev)
-    cache.store(pre.final)
+    if len(prompt) > 1:
+        pre = runner.DeltaDevice(*layer.inputs(prompt[None, :-1]))
+        pre.fwd()
+        cache.store(pre.final)
+    else:
+        cache.store(torch.zeros(1, layer.H, layer.P, layer.N, device=dev))
     states = torch.empty(batch, layer.H, layer.P, layer.N, device=dev)
     cache.load(torch.zeros(batch, dtype=torch.int32, device=dev), states)  # one slot, many sequences
     pool = runner.DeltaStepDevice(states)
@@ -86,7 +89,8 @@ def generate(layer, prompt, batch, new, draft, seed=1):
         p = layer.probs(pool.step(*ins, update=False))
         uniform = torch.rand(batch, draft, generator=gen, device=dev)
         noise = torch.empty(batch, p.shape[-1], device=dev).exponential_(generator=gen)
-        chosen, n = runner.verify_draft(p, torch.stack(q, 1), tokens[:, 1:].contiguous(), uniform, noise)
+        chosen, n = runner.verify_draft(p, torch.stack(q, 1) if q else None, tokens[:, 1:].contiguous(),
+                                        uniform, noise)
         # move on by the token that was fed and the drafted ones that were kept
         pool.step(*ins, lengths=n + 1, outputs=False)
         last = chosen.gather(1, n[:, None].long())[:, 0]
