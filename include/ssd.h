@@ -443,8 +443,9 @@ int ssd_verify_draft(const ssd_verify_problem* prob, const void* target_probs,
  * values has one fp32 scale: with a = max |x| of the row and t = 127 (int8)
  * or 448 (e4m3), scale = a * (1 / t) and each value is x * ((1 / a) * t)
  * rounded to nearest, ties to even (fp32, every operation rounded).  A row
- * whose a is below 2^-118 (t / a is not finite for it) is stored as zeros with
- * scale 0; a row that holds an infinity or a NaN reads back as NaN throughout.
+ * whose a is below 2^-118 is stored as zeros with scale 0 (a bound chosen for
+ * both formats: (1 / a) * t is finite from about 2^-119.2 on for e4m3 and 2^-121
+ * for int8); a row that holds an infinity or a NaN reads back as NaN throughout.
  * cache (nslots, H, P, N) bytes, scales (nslots, H, P)
  * fp32.  slots (b) int32 or NULL as for ssd_delta_step; the store passes over
  * slots outside the pool (and must not get one twice), the load gives zeros
