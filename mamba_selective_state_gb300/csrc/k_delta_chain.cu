@@ -381,6 +381,7 @@ struct FwdChain {
   __device__ __forceinline__ void columns() {
     uint64_t *c_full = bars, *c_free = bars + 3, *h_full = bars + 10, *h_free = h_full + 2 * NW;
     const int t = lane & 3;
+    const bool saves = f.S != nullptr;
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
     float S[N / 8][4], x[8][4];
     load_state<N>(S, z ? nullptr : f.init, state0, lane, p.st_bf16);
@@ -463,7 +464,7 @@ struct FwdChain {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         stsm4(frag_at(Wd, 16 * k, lane), left[k][0], left[k][1], left[k][2], left[k][3]);
-      if (f.S) fence_async_smem();  // the tiles also leave through TMA
+      if (saves) fence_async_smem();  // the tiles also leave through TMA
       __syncwarp();
       if (lane == 0) mbar_arrive(h_full + 2 * w + st);
 #pragma unroll
@@ -555,6 +556,8 @@ struct FwdChain {
   __device__ __forceinline__ bool outputs(const ChainMaps& m, int cw) {
     uint64_t *o_full = bars + 6, *o_free = bars + 8, *h_full = bars + 10, *h_free = h_full + 2 * NW;
     const int t = lane & 3;
+    const bool saves = f.S != nullptr;
+    const float scale = p.scale;
     float seen[4] = {};  // NaN once an output was not finite
     for (int k = 0; k < nch; ++k) {
       const int st = k & 1, c = first + k;
@@ -565,7 +568,7 @@ struct FwdChain {
       const float* e = reinterpret_cast<const float*>(raw + L::oE + (3 + st) * kGateBytes) + 2 * t;
       mbar_wait_flag(o_full + st, (k >> 1) & 1, ok);
       mbar_wait_flag(h_full + 2 * cw + st, (k >> 1) & 1, ok);
-      if (f.S && write && lane == 0) {
+      if (saves && write && lane == 0) {
         for (int j = 0; j < N / 64; ++j)
           tma_store_4d(&m.S, raw + (Sd - sm) + j * 2048, 64 * j, p0 + 16 * cw, c, bh);
         tma_store_4d(&m.w, raw + (Wd - sm), 0, p0 + 16 * cw, c, bh);
@@ -588,8 +591,8 @@ struct FwdChain {
         const float2 ej = *reinterpret_cast<const float2*>(e + 8 * j);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          y[j][2 * r] *= p.scale * ej.x;
-          y[j][2 * r + 1] *= p.scale * ej.y;
+          y[j][2 * r] *= scale * ej.x;
+          y[j][2 * r + 1] *= scale * ej.y;
         }
       }
 #pragma unroll
@@ -806,13 +809,16 @@ struct RevChain {
     return static_cast<const float*>(f.e) + (long long)bh * p.nc * kGateRows * kC;
   }
 
-  // The column warps' part (kGuard: the second pass); true where an r was not
+  // The column warps' part (kGuard: the second pass); true where a value was not
   // finite and a sequence begins
   template <bool kGuard>
   __device__ __forceinline__ bool columns(const ChainMaps& m) {
     uint64_t *full = reinterpret_cast<uint64_t*>(raw + L::oBar), *empty = full + 3;
     const int t = lane & 3;
-    float seen[4] = {};  // NaN once an r was not finite
+    const float scale = p.scale;
+    // Whether a value was not finite: an r that is not leaves no column of D finite,
+    // and D stays so up to a chunk whose first token starts a sequence, or to the end
+    bool bad = false;
     const long long state0 = ((long long)bh * p.P + p0 + 16 * w) * N;
     float D[N / 8][4], x[8][4];
     load_state<N>(D, inner ? nullptr : f.dfin, state0, lane, p.st_bf16);
@@ -901,7 +907,7 @@ struct RevChain {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float2 v = unpack2(y[2 * j + r]);
-            y[2 * j + r] = pack2(p.scale * ej.x * v.x, p.scale * ej.y * v.y);
+            y[2 * j + r] = pack2(scale * ej.x * v.x, scale * ej.y * v.y);
           }
         }
 #pragma unroll
@@ -931,9 +937,6 @@ struct RevChain {
           mma(x[2 * j + 1], rk[i], b[2], b[3]);
         }
       }
-      if (!kGuard)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) watch(seen, rk[k]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
 #pragma unroll
@@ -996,6 +999,7 @@ struct RevChain {
         state_product(N / 16 - 1, Kn);
       }
       if (starts()) {
+        if (!kGuard) bad |= !all_finite(D);
         zero(x);
         zero_state();
 #pragma unroll
@@ -1007,6 +1011,7 @@ struct RevChain {
       if (ns == 0) ph ^= 1;
     }
     solve();
+    if (!kGuard) bad |= !all_finite(x) || !all_finite(D);
     const bool walked = walked_at(nch - 1);
     if (nch > 1 || !inner) put(right + 1 - nch, true, false, walked);
     if (f.dinit && z == 0) {
@@ -1018,7 +1023,7 @@ struct RevChain {
     if (f.dinit && z == 0) store_state<N>(D, f.dinit, state0, lane, p.st_bf16);
     if (lane == 0) bulk_wait_all();
     const float* e = gates() + (long long)(right + 1 - nch) * kGateRows * kC;
-    return !kGuard && met_not_finite(seen) && any_start(e, nch, lane);
+    return bad && any_start(e, nch, lane);
   }
 };
 template <int N, int NW>
