@@ -28,12 +28,19 @@
 // the backward.  One more warp issues the TMA copies of the next chunks.  (Output
 // warps that take 32 columns of every other chunk read Q and A half as often, and
 // were not faster: 232 us instead of 231 below, 236 instead of 227 packed.)
+// Every operand of a product is rounded to bf16 on its way into it -- T and A, S',
+// w', (o beta w)', D', r', (scale e dY)' -- because the tensor cores take no more:
+// both halves of an operand would be three products for one, and twice the shared
+// memory, on chains bound by both.  The accumulators, S and D among them, are fp32
+// from the first chunk to the last, so the roundings do not add up along a row: y is
+// 3.5e-3 off float64 in the 2-norm, where rounding y itself is 1.7e-3.
 // Bound by a warp's own sequence of products (148 of 16 x 8 x 16 a chunk on one
 // sub-partition's tensor pipe, 8 cycles each, between the solve's waits) and, with
 // four column warps, by shared-memory reads of the right operands (about 70 KB
-// per 16 columns and chunk).  Measured at dstate 128: 1.69 us a chunk for 64
-// columns (batch 2, L = 8192, 64 heads: 217 us forward, 238 with what the backward
-// needs, 224 reverse), 1.24 for 32 and 1.18 for 16.
+// per 16 columns and chunk; that pipe is busy for 73 % of the forward's cycles and
+// 67 % of the reverse's, the tensor pipe for 62 and 65 %).  Measured at dstate 128:
+// 1.69 us a chunk for 64 columns (batch 2, L = 8192, 64 heads: 217 us forward, 233
+// with what the backward needs, 219 reverse), 1.24 for 32 and 1.18 for 16.
 #include "delta_internal.cuh"
 #include "mma_common.cuh"
 #include "tma_host.h"
@@ -1113,11 +1120,11 @@ __global__ void __launch_bounds__((NW + 1) * 32, 1)
 // Columns a CTA: 64, or 32 or 16 while every CTA still has an SM of its own --
 // fewer warps share an SM's shared memory, but each CTA copies the chunks'
 // operands for itself (one row of 4001 tokens, 32 heads of 64 x 128, forward:
-// 78 us by 32 columns, 75 by 16; 8192 tokens: reverse 197 and 186).  Packed rows have their chains in as many
-// pieces as there are SMs for, and rather twice the columns than one piece (one
-// row of 20,011 tokens in 16 sequences, 64 heads of 64 x 64: forward 226 us
-// instead of 286, reverse 209 instead of 330; where a single sequence leaves one
-// piece, 406 and 387).
+// 78 us by 32 columns, 75 by 16; 8192 tokens: reverse 197 and 186).  Packed rows
+// have their chains in as many pieces as there are SMs for, and rather twice the
+// columns than one piece (one row of 20,011 tokens in 16 sequences, 64 heads of 64 x
+// 64: forward 229 us instead of 292, reverse 216 instead of 338; where one sequence
+// leaves one piece, and two CTAs share its columns, 289 and 362).
 struct ChainShape {
   int warps, pieces;  // of 16 columns
 };

@@ -1,6 +1,8 @@
 // k_delta_grad_tc.cu -- dq, dk, dg and dbeta of the gated delta rule on the
 // tensor cores, chunk by chunk: the formulas at the head of
-// k_delta_grad_simt.cu, with bf16 S0, D1, w and r = dv from the chains.
+// k_delta_grad_simt.cu, with bf16 S0, D1, w and r = dv from the chains (operands of
+// bf16 products, and half the bytes of what is saved; so is the pairs' part summed
+// over the heads, Z and M, before its product with k and q).
 //
 // One CTA takes a chunk of a group and walks its heads.  Per head, with the
 // tokens of dY and of r as the 128 rows of one left operand,

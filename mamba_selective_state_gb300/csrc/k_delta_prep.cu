@@ -14,6 +14,8 @@
 // One CTA takes a chunk of up to eight heads of a group: k k^T and q k^T do
 // not depend on the head and stay in registers, four warps with 16 rows of
 // k k^T (T) and four with q k^T (A).  A warp's rows depend on no other warp's.
+// M, the inverses and A are formed in fp32 and rounded to bf16 once, as operands of
+// the chains' products (see k_delta_chain.cu).
 // Bound by the instructions of the pairs' decays and of the substitution: 110 us
 // at batch 2, L = 8192, 64 heads in 8 groups, where it writes 0.30 GB.
 #include "delta_internal.cuh"

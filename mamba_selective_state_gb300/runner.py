@@ -213,7 +213,9 @@ class DeltaDevice:
     one projection's output; g (log decay), beta (b, L, H).  States
     (b, H, P, N) are ``state_dtype``.  ``fwd`` fills y and final; ``bwd``,
     after a ``fwd`` on the same inputs, dq, dk, dv, dg, dbeta and (with
-    initial states) dinit.  The tensors may be refilled between calls."""
+    initial states) dinit.  The tensors may be refilled between calls.  All are on
+    the current CUDA device; the buffers belong to the stream that is current here,
+    and calls on another one come after its work."""
 
     def __init__(self, q, k, v, g, beta, scale=None, initial_states=None, seq_idx=None, dy=None,
                  dfinal_states=None, state_dtype=torch.float32):
