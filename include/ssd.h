@@ -313,6 +313,61 @@ int ssd_gated_rmsnorm_bwd(const ssd_norm_problem* prob, const void* y, const voi
                           ssd_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The norm that takes in the residual, as it stands before a layer's input
+ * projection, with its output in the type or in 8 bits:
+ *
+ *   h[r,j]   = x[r,j] + residual[r,j]      rounded to residual_dtype (h = x without a residual)
+ *   rstd[r]  = 1 / sqrt(mean_j h[r,j]^2 + eps)
+ *   out[r,j] = h[r,j] * rstd[r] * weight[j]
+ *
+ * 8-bit output by the state cache's rule (below), a row of out to a scale:
+ * out stands for code * scales[r]; a row that holds an infinity or a NaN gets
+ * the scale NaN, one of values below 2^-118 zeros.  The squares are summed in
+ * fp32: |h| beyond about 1e18 overflows them, and out is then 0.
+ *
+ * The backward, for the upstream gradients dout of out (of the values that the
+ * codes stand for, if they are 8 bits: their rounding passes it through) and,
+ * if non-NULL, dh of h, writes
+ *   dx = dresidual = dh + the norm's own,  dweight[j] = sum_r dout h rstd
+ * with dresidual NULL where dx is enough (the same type).  It recomputes rstd
+ * from h.  dweight is summed in a fixed order: bitwise reproducible run to run
+ * on one device.
+ *
+ * Layouts (device memory, 16-byte aligned, dense but for x):
+ *   x                (rows, dim)  dtype, x_stride elements from row to row (0: dense)
+ *   dout, dx         (rows, dim)  dtype;  out: dtype, or one byte a value
+ *   residual, h, dh, dresidual   (rows, dim)  residual_dtype
+ *   weight, dweight  (dim) fp32;  scales (rows) fp32, iff out_format is not SSD_OUT_PLAIN
+ * residual_dtype is dtype, or SSD_F32 for bf16 layers on an fp32 stream.  h may
+ * be NULL (not wanted) or the residual itself (updated in place).  dim <=
+ * 16384; eps > 0.  Ownership, errors and stream semantics as above; no
+ * device-side waits. */
+enum { SSD_NORM_HAS_RESIDUAL = 2 /* residual is given */ };
+typedef enum { SSD_OUT_PLAIN = 0, SSD_OUT_INT8 = 1, SSD_OUT_E4M3 = 2 } ssd_out_format;
+
+typedef struct {
+  int64_t rows, dim, x_stride;
+  float eps;
+  int32_t dtype;          /* ssd_dtype of x, out (SSD_OUT_PLAIN), dout, dx */
+  int32_t residual_dtype; /* ssd_dtype of residual, h, dh, dresidual */
+  int32_t out_format;     /* ssd_out_format; the backward does not read it */
+  int32_t flags;          /* SSD_NORM_HAS_RESIDUAL */
+} ssd_add_norm_problem;
+
+int ssd_add_rmsnorm_fwd(const ssd_add_norm_problem* prob, const void* x, const void* residual,
+                        const float* weight, void* h, void* out, float* scales,
+                        ssd_stream_t stream);
+
+/* Bytes of device workspace ssd_add_rmsnorm_bwd needs (partial dweights; a
+ * pure function of the problem, 0 if it is invalid). */
+size_t ssd_add_rmsnorm_bwd_workspace_bytes(const ssd_add_norm_problem* prob);
+
+int ssd_add_rmsnorm_bwd(const ssd_add_norm_problem* prob, const void* h, const float* weight,
+                        const void* dout, const void* dh, void* dx, void* dresidual,
+                        float* dweight, void* workspace, size_t workspace_bytes,
+                        ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * The gated delta rule: the recurrence of a layer whose state is corrected
  * by what it already holds, instead of only added to.  Per batch row and
  * head, with a state S (headdim x dstate), a log decay g and a strength beta:
@@ -462,6 +517,87 @@ int ssd_state_cache_store(const ssd_cache_problem* prob, const float* states, co
                           void* cache, float* scales, ssd_stream_t stream);
 int ssd_state_cache_load(const ssd_cache_problem* prob, const void* cache, const float* scales,
                          const int32_t* slots, float* states, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The product of 8-bit codes, as the norm above writes them, with weights of
+ * the same form:
+ *
+ *   out[m,n] = a_scales[m] * w_scales[n] * sum_k a[m,k] * w[n,k]  + bias[n]
+ *
+ * a (m, k), w (n, k): int8 (all 256 values) or e4m3, dense; a_scales (m),
+ * w_scales (n), bias (n; or NULL) fp32; out (m, n) out_dtype, dense.  Device
+ * memory, 16-byte aligned.  The sums are fp32: those of int8 codes are exact
+ * while their partial sums stay below 2^24 (always for k <= 1024).  A NaN or an
+ * infinity in a token's scale or codes stays in its row of out, one in a
+ * channel's in its column.  m, n, k <= 2^22.  Ownership, errors and stream
+ * semantics as above; device-side waits are bounded, and one that expired is
+ * recorded in the status word at the start of the workspace
+ * (ssd_read_device_status).  Results are bitwise reproducible run to run. */
+typedef struct {
+  int64_t m, n, k;
+  int32_t format;    /* ssd_cache_format of a and w */
+  int32_t out_dtype; /* ssd_dtype of out */
+  int32_t flags;     /* 0 */
+} ssd_matmul_problem;
+
+/* Bytes of device workspace ssd_scaled_matmul needs (a pure function of the
+ * problem, at least 256; 0 if it is invalid). */
+size_t ssd_scaled_matmul_workspace_bytes(const ssd_matmul_problem* prob);
+
+int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float* a_scales,
+                      const void* w, const float* w_scales, const float* bias, void* out,
+                      void* workspace, size_t workspace_bytes, ssd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens, the entropy and the top alternatives of
+ * their distributions, and the gradient to the logits.  Per row, with
+ * z = scale * logits:
+ *
+ *   lse = log sum_v exp z_v      logprob = z[token] - lse
+ *   entropy = -sum_v p_v log p_v,  p = exp(z - lse)
+ *
+ * and the ntop words of the largest logits in descending order, ties to the
+ * lower index, with their log probabilities.
+ *
+ * logits (rows, vocab) dtype, logit_stride elements from row to row (0:
+ * dense); tokens (rows) int32; logprobs, entropy, lse (rows) fp32; top_tokens
+ * int32 and top_logprobs fp32 (rows, ntop).  A token outside [0, vocab) is
+ * padding: its logprob is 0 and has no gradient.  A logit of -inf excludes its
+ * word: its log probability is -inf, its gradient 0, and it is no alternative;
+ * places for which no word is left hold -1 and -inf.  A row that excludes every
+ * word has lse -inf, logprob -inf, entropy 0 and no gradient.  A NaN or +inf in
+ * a row makes its lse, logprobs, entropy and gradient NaN; the alternatives are
+ * then those of the values that are not NaN.  Of logprobs (given with tokens),
+ * entropy, lse and the alternatives each may be NULL, but not all.
+ *
+ * The backward takes lse and, for dentropy, entropy from the forward, and the
+ * upstream gradients dlogprobs (given with tokens) and dentropy (rows) fp32 --
+ * either may be NULL -- and writes dlogits (rows, vocab) dtype, grad_stride
+ * elements from row to row (0: dense):
+ *   dlogits_v = scale * (dlogprob * (1[v = token] - p_v)
+ *                        - dentropy * p_v * (log p_v + entropy))
+ * dlogits may be logits itself (then with the same stride).
+ *
+ * Device memory, 16-byte aligned (strides are free).  scale > 0; ntop <= 32;
+ * 1 <= vocab < 2^31.  All sums are fp32.  Ownership, errors and stream
+ * semantics as above; no workspace.  Results are bitwise reproducible run to
+ * run. */
+typedef struct {
+  int64_t rows, vocab;
+  int64_t logit_stride, grad_stride; /* elements from row to row; 0 = dense */
+  float scale;
+  int32_t ntop;
+  int32_t dtype; /* ssd_dtype of logits and dlogits */
+  int32_t flags; /* 0 */
+} ssd_logprob_problem;
+
+int ssd_token_logprobs(const ssd_logprob_problem* prob, const void* logits, const int32_t* tokens,
+                       float* logprobs, float* entropy, float* lse, int32_t* top_tokens,
+                       float* top_logprobs, ssd_stream_t stream);
+int ssd_token_logprobs_bwd(const ssd_logprob_problem* prob, const void* logits,
+                           const int32_t* tokens, const float* lse, const float* entropy,
+                           const float* dlogprobs, const float* dentropy, void* dlogits,
+                           ssd_stream_t stream);
 
 /* Library build/version string, e.g. "libssd 0.1 sm_103a". */
 const char* ssd_version(void);

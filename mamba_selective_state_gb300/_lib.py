@@ -33,6 +33,10 @@ SSD_PATH_SINGLE_PASS = 1 << 18
 SSD_TEST_FEW_CTAS = 1 << 19
 SSD_SCAN_WARP_SHUFFLE = 1 << 20
 SSD_NORM_HAS_Z = 1
+SSD_NORM_HAS_RESIDUAL = 2
+SSD_OUT_PLAIN = 0
+SSD_OUT_INT8 = 1
+SSD_OUT_E4M3 = 2
 SSD_CACHE_INT8 = 0
 SSD_CACHE_E4M3 = 1
 
@@ -45,7 +49,9 @@ EXPORTS = ["ssd_fwd_workspace_bytes", "ssd_bwd_workspace_bytes", "ssd_fwd", "ssd
            "ssd_gated_rmsnorm_bwd", "ssd_delta_fwd_workspace_bytes",
            "ssd_delta_bwd_workspace_bytes", "ssd_delta_saved_bytes", "ssd_delta_fwd",
            "ssd_delta_bwd", "ssd_delta_step", "ssd_verify_draft", "ssd_state_cache_store",
-           "ssd_state_cache_load"]
+           "ssd_state_cache_load", "ssd_add_rmsnorm_fwd", "ssd_add_rmsnorm_bwd_workspace_bytes",
+           "ssd_add_rmsnorm_bwd", "ssd_scaled_matmul_workspace_bytes", "ssd_scaled_matmul",
+           "ssd_token_logprobs", "ssd_token_logprobs_bwd"]
 SSD_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -82,6 +88,26 @@ class ssd_cache_problem(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("nslots", ctypes.c_int64), ("format", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
+class ssd_add_norm_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32), ("out_format", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class ssd_matmul_problem(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
+
+
+class ssd_logprob_problem(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("logit_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("ntop", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -149,6 +175,23 @@ def _load():
     lib.ssd_state_cache_store.restype = i32
     lib.ssd_state_cache_load.argtypes = [cpp] + [vp] * 4 + [vp]
     lib.ssd_state_cache_load.restype = i32
+    app = ctypes.POINTER(ssd_add_norm_problem)
+    lib.ssd_add_rmsnorm_fwd.argtypes = [app] + [vp] * 6 + [vp]
+    lib.ssd_add_rmsnorm_fwd.restype = i32
+    lib.ssd_add_rmsnorm_bwd_workspace_bytes.argtypes = [app]
+    lib.ssd_add_rmsnorm_bwd_workspace_bytes.restype = sz
+    lib.ssd_add_rmsnorm_bwd.argtypes = [app] + [vp] * 8 + [sz, vp]
+    lib.ssd_add_rmsnorm_bwd.restype = i32
+    mpp = ctypes.POINTER(ssd_matmul_problem)
+    lib.ssd_scaled_matmul_workspace_bytes.argtypes = [mpp]
+    lib.ssd_scaled_matmul_workspace_bytes.restype = sz
+    lib.ssd_scaled_matmul.argtypes = [mpp] + [vp] * 7 + [sz, vp]
+    lib.ssd_scaled_matmul.restype = i32
+    lpp = ctypes.POINTER(ssd_logprob_problem)
+    lib.ssd_token_logprobs.argtypes = [lpp] + [vp] * 7 + [vp]
+    lib.ssd_token_logprobs.restype = i32
+    lib.ssd_token_logprobs_bwd.argtypes = [lpp] + [vp] * 7 + [vp]
+    lib.ssd_token_logprobs_bwd.restype = i32
     return lib
 
 
@@ -429,4 +472,86 @@ def ssd_state_cache_load(prob, cache, scales, slots, states, stream=None, check=
                                   _p(states), _stream(stream))
     if check and rc != SSD_OK:
         raise SSDError(rc, "ssd_state_cache_load")
+    return rc
+
+
+def make_add_norm_problem(rows, dim, eps, dtype, residual_dtype=None, out_format=SSD_OUT_PLAIN,
+                          residual=True, x_stride=0) -> ssd_add_norm_problem:
+    return ssd_add_norm_problem(rows, dim, x_stride, eps, _dtype_code(dtype),
+                                _dtype_code(dtype if residual_dtype is None else residual_dtype),
+                                out_format, SSD_NORM_HAS_RESIDUAL if residual else 0)
+
+
+def ssd_add_rmsnorm_fwd(prob, x, residual, weight, h, out, scales=None, stream=None,
+                        check=True) -> int:
+    """Enqueue the residual's addition and the norm on ``stream`` (default:
+    torch's current stream)."""
+    rc = LIB.ssd_add_rmsnorm_fwd(ctypes.byref(prob), _p(x), _p(residual), _p(weight), _p(h),
+                                 _p(out), _p(scales), _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_add_rmsnorm_fwd")
+    return rc
+
+
+def ssd_add_rmsnorm_bwd_workspace_bytes(prob: ssd_add_norm_problem) -> int:
+    return int(LIB.ssd_add_rmsnorm_bwd_workspace_bytes(ctypes.byref(prob)))
+
+
+def ssd_add_rmsnorm_bwd(prob, h, weight, dout, dh, dx, dresidual, dweight, workspace,
+                        workspace_bytes=None, stream=None, check=True) -> int:
+    """Enqueue the norm's backward on ``stream``."""
+    rc = LIB.ssd_add_rmsnorm_bwd(ctypes.byref(prob), _p(h), _p(weight), _p(dout), _p(dh), _p(dx),
+                                 _p(dresidual), _p(dweight), _p(workspace),
+                                 _nbytes(workspace) if workspace_bytes is None else workspace_bytes,
+                                 _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_add_rmsnorm_bwd")
+    return rc
+
+
+def make_matmul_problem(m, n, k, fmt, out_dtype) -> ssd_matmul_problem:
+    return ssd_matmul_problem(m, n, k, fmt, _dtype_code(out_dtype), 0)
+
+
+def ssd_scaled_matmul_workspace_bytes(prob: ssd_matmul_problem) -> int:
+    return int(LIB.ssd_scaled_matmul_workspace_bytes(ctypes.byref(prob)))
+
+
+def ssd_scaled_matmul(prob, a, a_scales, w, w_scales, bias, out, workspace, workspace_bytes=None,
+                      stream=None, check=True) -> int:
+    """Enqueue the product of 8-bit codes on ``stream``."""
+    rc = LIB.ssd_scaled_matmul(ctypes.byref(prob), _p(a), _p(a_scales), _p(w), _p(w_scales),
+                               _p(bias), _p(out), _p(workspace),
+                               _nbytes(workspace) if workspace_bytes is None else workspace_bytes,
+                               _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_scaled_matmul")
+    return rc
+
+
+def make_logprob_problem(rows, vocab, scale, ntop, dtype, logit_stride=0,
+                         grad_stride=0) -> ssd_logprob_problem:
+    return ssd_logprob_problem(rows, vocab, logit_stride, grad_stride, scale, ntop,
+                               _dtype_code(dtype), 0)
+
+
+def ssd_token_logprobs(prob, logits, tokens, logprobs, entropy, lse, top_tokens=None,
+                       top_logprobs=None, stream=None, check=True) -> int:
+    """Enqueue the tokens' log probabilities on ``stream``."""
+    rc = LIB.ssd_token_logprobs(ctypes.byref(prob), _p(logits), _p(tokens), _p(logprobs),
+                                _p(entropy), _p(lse), _p(top_tokens), _p(top_logprobs),
+                                _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_token_logprobs")
+    return rc
+
+
+def ssd_token_logprobs_bwd(prob, logits, tokens, lse, entropy, dlogprobs, dentropy, dlogits,
+                           stream=None, check=True) -> int:
+    """Enqueue the gradient to the logits on ``stream``."""
+    rc = LIB.ssd_token_logprobs_bwd(ctypes.byref(prob), _p(logits), _p(tokens), _p(lse),
+                                    _p(entropy), _p(dlogprobs), _p(dentropy), _p(dlogits),
+                                    _stream(stream))
+    if check and rc != SSD_OK:
+        raise SSDError(rc, "ssd_token_logprobs_bwd")
     return rc

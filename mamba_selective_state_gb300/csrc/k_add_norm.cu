@@ -1,0 +1,467 @@
+// k_add_norm.cu -- the norm that takes in the residual, forward (output in the
+// type, or in 8 bits with a scale for each row) and backward, and its C ABI.
+//
+//   h = x + residual, in the residual's type          v = h in fp32
+//   r = 1 / sqrt(mean v^2 + eps)                      out = v r weight
+//   backward, with g = dout weight and n = v r:
+//   dx = dresidual = dh + r (g - n mean(g n))         dweight = sum over rows of dout n
+//
+// The norm reads h as it is stored: the backward, which has only h, then sees
+// the forward's own values.  Everything but the stored tensors is fp32.
+//
+// Bound by HBM; each tensor is read and written once.  A CTA takes a row, a
+// thread 8 neighbouring columns at a time (one 16-byte access in bf16), which
+// stay in registers from the sum to the store; in the backward they stay the
+// thread's own from row to row, so that it also holds their dweight.  The CTAs'
+// dweights are joined by a second kernel in a fixed order.
+#include <string.h>
+
+#include "codes.cuh"
+#include "ssd_internal.cuh"
+
+namespace ssd {
+
+int device_check();
+
+namespace {
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxDim = kMaxThreads * 8 * 4;
+constexpr int kMaxSlices = 1216;  // CTAs of the backward, each with a row of partial dweights
+
+struct AddNormArgs {
+  const void *x, *res;
+  const float* w;
+  void *h, *out;
+  float* scales;
+  const void *dout, *dh;
+  void *dx, *dres;
+  float* part;
+  long long rows, xs;  // xs: elements from row to row of x
+  int dim, codes;      // codes: 0 none, 1 int8, 2 e4m3
+  float inv_dim, eps;
+};
+
+// Eight values of a row: neighbours (piece p) where rows are whole 16-byte
+// vectors, else columns a CTA's width apart.
+template <typename T, bool kVec>
+struct Cols {
+  static __device__ __forceinline__ int col(int i, int j) {
+    return kVec ? (i * (int)blockDim.x + (int)threadIdx.x) * 8 + j : (i * 8 + j) * (int)blockDim.x + (int)threadIdx.x;
+  }
+  static __device__ __forceinline__ void load(const T* row, int i, int dim, float (&v)[8]) {
+    if constexpr (kVec) {
+      const int c = col(i, 0);
+      if (c < dim) {
+        if constexpr (sizeof(T) == 2) {
+          const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + c));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+          }
+        } else {
+          const float4 a = __ldcs(reinterpret_cast<const float4*>(row + c)),
+                       b = __ldcs(reinterpret_cast<const float4*>(row + c) + 1);
+          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = col(i, j) < dim ? to_f(row[col(i, j)]) : 0.f;
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int i, int dim, const float (&v)[8]) {
+    if constexpr (kVec) {
+      const int c = col(i, 0);
+      if (c < dim) {
+        if constexpr (sizeof(T) == 2) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+          __stcs(reinterpret_cast<float4*>(row + c), make_float4(v[0], v[1], v[2], v[3]));
+          __stcs(reinterpret_cast<float4*>(row + c) + 1, make_float4(v[4], v[5], v[6], v[7]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col(i, j) < dim) row[col(i, j)] = from_f<T>(v[j]);
+    }
+  }
+};
+
+// The weight's values stay in the caches: every row reads them.
+template <bool kVec>
+__device__ __forceinline__ void load_weight(const float* w, int i, int dim, float (&v)[8]) {
+  using C = Cols<float, kVec>;
+  if constexpr (kVec) {
+    const int c = C::col(i, 0);
+    if (c < dim) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = C::col(i, j) < dim ? __ldg(w + C::col(i, j)) : 0.f;
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Sum over the CTA, the same for every thread, in a fixed order.  red: a value
+// for each warp, not in use by an earlier call that some warp may still be in.
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+  v = warp_sum(v);
+  if (blockDim.x == 32) return v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += red[i];
+  return v;
+}
+
+template <bool kFp8, bool kVec>
+__device__ __forceinline__ void store_codes(uint8_t* row, int i, int dim, const float (&v)[8], float inv, bool zero) {
+  using C = Cols<float, kVec>;
+  if constexpr (kVec) {
+    const int c = C::col(i, 0);
+    if (c < dim) {
+      uint2 u = make_uint2(0, 0);
+      if (!zero)
+        u = make_uint2(encode4<kFp8>(make_float4(v[0], v[1], v[2], v[3]), inv),
+                       encode4<kFp8>(make_float4(v[4], v[5], v[6], v[7]), inv));
+      *reinterpret_cast<uint2*>(row + c) = u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (C::col(i, j) < dim) row[C::col(i, j)] = zero ? 0 : encode<kFp8>(v[j] * inv);
+  }
+}
+
+// NP: pieces of 8 columns to a thread
+template <typename T, typename R, int NP, bool kVec>
+__global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a) {
+  __shared__ float red[2][kMaxThreads / 32], big_s[2][kMaxThreads / 32];
+  int par = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
+    float v[NP][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) Cols<T, kVec>::load(static_cast<const T*>(a.x) + row * a.xs, i, a.dim, v[i]);
+    if (a.res) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        float u[8];
+        Cols<R, kVec>::load(static_cast<const R*>(a.res) + row * a.dim, i, a.dim, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = to_f(from_f<R>(v[i][j] + u[j]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (a.h) Cols<R, kVec>::store(static_cast<R*>(a.h) + row * a.dim, i, a.dim, v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    const float r = rsqrtf(cta_sum(ss, red[par]) * a.inv_dim + a.eps);
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float w[8];
+      load_weight<kVec>(a.w, i, a.dim, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = v[i][j] * r * w[j];
+        // what is not finite makes the row's largest an infinity
+        big = fmaxf(big, fabsf(v[i][j]) <= 3.402823466e38f ? fabsf(v[i][j]) : __int_as_float(0x7f800000));
+      }
+    }
+    if (a.codes == 0) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) Cols<T, kVec>::store(static_cast<T*>(a.out) + row * a.dim, i, a.dim, v[i]);
+      continue;
+    }
+    // (values that are not negative order as integers)
+    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+    if (blockDim.x > 32) {
+      if ((threadIdx.x & 31) == 0) big_s[par][threadIdx.x >> 5] = big;
+      __syncthreads();
+      for (int i = 0; i < (int)(blockDim.x >> 5); ++i) big = fmaxf(big, big_s[par][i]);
+    }
+    const bool bad = big == __int_as_float(0x7f800000), zero = bad || !(big >= kTiny);
+    const bool fp8 = a.codes == 2;
+    const float inv = zero ? 0.f : fp8 ? factor_of<true>(big) : factor_of<false>(big);
+    uint8_t* to = static_cast<uint8_t*>(a.out) + row * a.dim;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (fp8) store_codes<true, kVec>(to, i, a.dim, v[i], inv, zero);
+      else store_codes<false, kVec>(to, i, a.dim, v[i], inv, zero);
+    }
+    if (threadIdx.x == 0)
+      a.scales[row] = bad ? __int_as_float(0x7fc00000) : zero ? 0.f : fp8 ? scale_of<true>(big) : scale_of<false>(big);
+  }
+}
+
+template <typename T, typename R, int NP, bool kVec>
+__global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a) {
+  __shared__ float red[2][2][kMaxThreads / 32];
+  float dw[NP][8];
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  int par = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
+    float v[NP][8], d[NP][8];
+    float ss = 0.f, sg = 0.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      Cols<R, kVec>::load(static_cast<const R*>(a.h) + row * a.dim, i, a.dim, v[i]);
+      Cols<T, kVec>::load(static_cast<const T*>(a.dout) + row * a.dim, i, a.dim, d[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float w[8];
+      load_weight<kVec>(a.w, i, a.dim, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ss = fmaf(v[i][j], v[i][j], ss);
+        sg = fmaf(d[i][j] * w[j], v[i][j], sg);
+      }
+    }
+    ss = warp_sum(ss);
+    sg = warp_sum(sg);
+    if (blockDim.x > 32) {
+      if ((threadIdx.x & 31) == 0) {
+        red[par][0][threadIdx.x >> 5] = ss;
+        red[par][1][threadIdx.x >> 5] = sg;
+      }
+      __syncthreads();
+      ss = sg = 0.f;
+      for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
+        ss += red[par][0][i];
+        sg += red[par][1][i];
+      }
+    }
+    const float r = rsqrtf(ss * a.inv_dim + a.eps);
+    const float proj = sg * r * a.inv_dim;  // mean(g n)
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      float w[8], u[8];
+      load_weight<kVec>(a.w, i, a.dim, w);
+      if (a.dh) {
+        Cols<R, kVec>::load(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = v[i][j] * r;
+        dw[i][j] = fmaf(d[i][j], n, dw[i][j]);
+        u[j] += r * (d[i][j] * w[j] - n * proj);
+      }
+      Cols<T, kVec>::store(static_cast<T*>(a.dx) + row * a.dim, i, a.dim, u);
+      if (a.dres) Cols<R, kVec>::store(static_cast<R*>(a.dres) + row * a.dim, i, a.dim, u);
+    }
+  }
+  float* part = a.part + (long long)blockIdx.x * a.dim;
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (Cols<T, kVec>::col(i, j) < a.dim) part[Cols<T, kVec>::col(i, j)] = dw[i][j];
+}
+
+// dweight[c] = sum of the slices' partials: 32 columns to a CTA, each warp a
+// run of slices, then the warps in order.
+constexpr int kFoldWarps = 16;
+__global__ void __launch_bounds__(kFoldWarps * 32) add_norm_fold_kernel(const float* part, float* dweight, int slices,
+                                                                        int dim) {
+  __shared__ float sums[kFoldWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const int per = (slices + kFoldWarps - 1) / kFoldWarps;
+  float s = 0.f;
+  if (c < dim) {
+    const int hi = min((warp + 1) * per, slices);
+#pragma unroll 8
+    for (int i = warp * per; i < hi; ++i) s += part[(long long)i * dim + c];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < dim) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kFoldWarps; ++i) s += sums[i][lane];
+    dweight[c] = s;
+  }
+}
+
+// Threads to a row and pieces to a thread.  Few rows: as many threads as there
+// are pieces, for the shortest way through one row.  Many rows: two pieces to a
+// thread, four where 512 threads of two would not hold the row.
+struct Shape {
+  int threads, np;
+};
+Shape shape_of(int dim, long long rows, int sms) {
+  const int pieces = (dim + 7) / 8;
+  int np = rows > 2 * sms && pieces >= 64 ? 2 : 1;
+  while (pieces > np * kMaxThreads) np *= 2;
+  const int t = ((pieces + np - 1) / np + 31) / 32 * 32;
+  return {t, np};
+}
+
+template <typename T, typename R, int NP, bool kVec>
+cudaError_t launch_np(const AddNormArgs& a, int threads, unsigned grid, bool bwd, cudaStream_t s) {
+  if (bwd) {
+    set_kernel_name("add_norm_bwd");
+    add_norm_bwd_kernel<T, R, NP, kVec><<<grid, threads, 0, s>>>(a);
+  } else {
+    set_kernel_name("add_norm_fwd");
+    add_norm_fwd_kernel<T, R, NP, kVec><<<grid, threads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+template <typename T, typename R>
+cudaError_t launch_t(const AddNormArgs& a, const Shape& sh, bool vec, unsigned grid, bool bwd, cudaStream_t s) {
+  if (vec) {
+    if (sh.np == 1) return launch_np<T, R, 1, true>(a, sh.threads, grid, bwd, s);
+    if (sh.np == 2) return launch_np<T, R, 2, true>(a, sh.threads, grid, bwd, s);
+    return launch_np<T, R, 4, true>(a, sh.threads, grid, bwd, s);
+  }
+  if (sh.np == 1) return launch_np<T, R, 1, false>(a, sh.threads, grid, bwd, s);
+  if (sh.np == 2) return launch_np<T, R, 2, false>(a, sh.threads, grid, bwd, s);
+  return launch_np<T, R, 4, false>(a, sh.threads, grid, bwd, s);
+}
+cudaError_t launch(const ssd_add_norm_problem& pr, const AddNormArgs& a, const Shape& sh, unsigned grid, bool bwd,
+                   cudaStream_t s) {
+  const bool vec = a.dim % 8 == 0 && (bwd || a.xs % 8 == 0);
+  if (pr.dtype == SSD_F32) return launch_t<float, float>(a, sh, vec, grid, bwd, s);
+  if (pr.residual_dtype == SSD_F32) return launch_t<__nv_bfloat16, float>(a, sh, vec, grid, bwd, s);
+  return launch_t<__nv_bfloat16, __nv_bfloat16>(a, sh, vec, grid, bwd, s);
+}
+
+int check(const ssd_add_norm_problem* pr) {
+  if (!pr || pr->rows < 1 || pr->dim < 1 || pr->x_stride < 0 || (pr->x_stride && pr->x_stride < pr->dim))
+    return SSD_ERR_INVALID_ARGUMENT;
+  if (!(pr->eps > 0.f && pr->eps <= 3.402823466e38f)) return SSD_ERR_INVALID_ARGUMENT;
+  if ((pr->dtype != SSD_F32 && pr->dtype != SSD_BF16) || (pr->residual_dtype != SSD_F32 && pr->residual_dtype != SSD_BF16))
+    return SSD_ERR_INVALID_ARGUMENT;
+  if (pr->out_format < SSD_OUT_PLAIN || pr->out_format > SSD_OUT_E4M3) return SSD_ERR_INVALID_ARGUMENT;
+  if (pr->flags & ~SSD_NORM_HAS_RESIDUAL) return SSD_ERR_INVALID_ARGUMENT;
+  // without a residual there is nothing of another type to add to
+  if (!(pr->flags & SSD_NORM_HAS_RESIDUAL) && pr->residual_dtype != pr->dtype) return SSD_ERR_INVALID_ARGUMENT;
+  if (pr->dtype == SSD_F32 && pr->residual_dtype == SSD_BF16) return SSD_ERR_UNSUPPORTED;
+  const int64_t xs = pr->x_stride ? pr->x_stride : pr->dim;
+  if (pr->dim > kMaxDim || xs > (1LL << 30) || pr->rows > (1LL << 40) || (double)pr->rows * (double)xs >= (double)(1LL << 40))
+    return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+bool misaligned16(const void* ptr) { return ptr && (reinterpret_cast<uintptr_t>(ptr) & 15u); }
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+int ssd_add_rmsnorm_fwd(const ssd_add_norm_problem* pr, const void* x, const void* residual, const float* weight,
+                        void* h, void* out, float* scales, ssd_stream_t stream) {
+  int rc = check(pr);
+  if (rc != SSD_OK) return rc;
+  if (!x || !weight || !out) return SSD_ERR_INVALID_ARGUMENT;
+  if (((pr->flags & SSD_NORM_HAS_RESIDUAL) != 0) != (residual != nullptr)) return SSD_ERR_INVALID_ARGUMENT;
+  if ((pr->out_format != SSD_OUT_PLAIN) != (scales != nullptr)) return SSD_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {x, residual, weight, h, out, scales};
+  for (const void* q : ptrs)
+    if (misaligned16(q)) return SSD_ERR_INVALID_ARGUMENT;
+  rc = device_check();
+  if (rc != SSD_OK) return rc;
+  AddNormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.res = residual; a.w = weight; a.h = h; a.out = out; a.scales = scales;
+  a.rows = pr->rows;
+  a.xs = pr->x_stride ? pr->x_stride : pr->dim;
+  a.dim = (int)pr->dim;
+  a.codes = pr->out_format;
+  a.inv_dim = 1.f / (float)pr->dim;
+  a.eps = pr->eps;
+  const int sms = device_sm_count();
+  const Shape sh = shape_of(a.dim, a.rows, sms);
+  // as many CTAs as are resident with 64 registers to a thread
+  long long grid = (long long)sms * (1024 / sh.threads);
+  if (grid > a.rows) grid = a.rows;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  prof_before(s);
+  const cudaError_t e = launch(*pr, a, sh, (unsigned)grid, false, s);
+  prof_after(s);
+  return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+size_t ssd_add_rmsnorm_bwd_workspace_bytes(const ssd_add_norm_problem* pr) {
+  if (check(pr) != SSD_OK) return 0;
+  const int64_t slices = pr->rows < kMaxSlices ? pr->rows : kMaxSlices;
+  return ((size_t)slices * (size_t)pr->dim * sizeof(float) + 255) & ~(size_t)255;
+}
+
+int ssd_add_rmsnorm_bwd(const ssd_add_norm_problem* pr, const void* h, const float* weight, const void* dout,
+                        const void* dh, void* dx, void* dresidual, float* dweight, void* workspace,
+                        size_t workspace_bytes, ssd_stream_t stream) {
+  int rc = check(pr);
+  if (rc != SSD_OK) return rc;
+  if (!h || !weight || !dout || !dx || !dweight || !workspace) return SSD_ERR_INVALID_ARGUMENT;
+  if (dresidual && !(pr->flags & SSD_NORM_HAS_RESIDUAL)) return SSD_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {h, weight, dout, dh, dx, dresidual, dweight, workspace};
+  for (const void* q : ptrs)
+    if (misaligned16(q)) return SSD_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < ssd_add_rmsnorm_bwd_workspace_bytes(pr)) return SSD_ERR_WORKSPACE_TOO_SMALL;
+  rc = device_check();
+  if (rc != SSD_OK) return rc;
+  AddNormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.h = const_cast<void*>(h);
+  a.w = weight; a.dout = dout; a.dh = dh; a.dx = dx; a.dres = dresidual;
+  a.part = static_cast<float*>(workspace);
+  a.rows = pr->rows;
+  a.dim = (int)pr->dim;
+  a.inv_dim = 1.f / (float)pr->dim;
+  a.eps = pr->eps;
+  const int sms = device_sm_count();
+  const Shape sh = shape_of(a.dim, a.rows, sms);
+  long long grid = (long long)sms * (768 / sh.threads < 8 ? (768 / sh.threads > 0 ? 768 / sh.threads : 1) : 8);
+  if (grid > a.rows) grid = a.rows;
+  if (grid > kMaxSlices) grid = kMaxSlices;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  prof_before(s);
+  cudaError_t e = launch(*pr, a, sh, (unsigned)grid, true, s);
+  prof_after(s);
+  if (e != cudaSuccess) return SSD_ERR_CUDA;
+  prof_before(s);
+  set_kernel_name("add_norm_fold");
+  add_norm_fold_kernel<<<(a.dim + 31) / 32, kFoldWarps * 32, 0, s>>>(a.part, dweight, (int)grid, a.dim);
+  e = cudaGetLastError();
+  prof_after(s);
+  return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // extern "C"

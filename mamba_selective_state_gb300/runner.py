@@ -386,3 +386,209 @@ class StateCache:
         slot may be read many times, one outside the cache gives zeros."""
         return _lib.ssd_state_cache_load(self._prob(out, slots), self.values, self.scales, slots,
                                          out, stream=stream, check=check)
+
+
+# torch's types of the 8-bit codes
+CODE_TYPES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
+class AddNormDevice:
+    """The norm that takes in the residual: the caller's device tensors, the
+    outputs and the calls through the C ABI.
+
+    x (rows, dim), rows evenly spaced; residual (rows, dim), x's type or fp32,
+    or None.  ``fwd`` fills h (residual's type; x itself without a residual) and
+    out, or with ``form`` ("int8", "e4m3") codes and scales; ``h_out`` (the
+    residual itself, for instance) takes h instead of a buffer of its own.
+    With ``dout`` (x's type) and optionally ``dh`` (h's), ``bwd`` after a ``fwd``
+    fills dx, dresidual (dx itself where the types are the same) and dweight.
+    The tensors may be refilled between calls.  All are on the current CUDA
+    device; the buffers belong to the stream that is current here, and calls on
+    another one come after its work."""
+
+    FORMATS = {None: _lib.SSD_OUT_PLAIN, "int8": _lib.SSD_OUT_INT8, "e4m3": _lib.SSD_OUT_E4M3}
+
+    def __init__(self, x, weight, residual=None, eps=1e-5, form=None, h_out=None, dout=None,
+                 dh=None):
+        if x.dim() != 2 or x.dtype not in _FLOATS:
+            raise ValueError("x must be (rows, dim), fp32 or bf16")
+        if form not in self.FORMATS:
+            raise ValueError("form must be None, 'int8' or 'e4m3'")
+        rows, dim = x.shape
+        dev = x.device
+        stride = x.stride(0) if rows > 1 else dim
+        if (dim > 1 and x.stride(1) != 1) or stride < dim:
+            raise ValueError("x: its rows must be dense and evenly spaced")
+        rt = x.dtype if residual is None else residual.dtype
+        if rt is not x.dtype and rt is not torch.float32:
+            raise ValueError("residual must be of x's type or fp32")
+        _on_gpu(dev, "AddNormDevice")
+        _dense(weight, (dim,), torch.float32, "weight", dev)
+        _dense(residual, (rows, dim), rt, "residual", dev)
+        _dense(h_out, (rows, dim), rt, "h_out", dev)
+        _dense(dout, (rows, dim), x.dtype, "dout", dev)
+        _dense(dh, (rows, dim), rt, "dh", dev)
+        if dh is not None and dout is None:
+            raise ValueError("dh needs dout")
+        if residual is None and dout is not None and not x.is_contiguous():
+            raise ValueError("the backward reads x as h: it must be dense")
+        self.x, self.weight, self.residual, self.dout, self.dh = x, weight, residual, dout, dh
+        self.prob = _lib.make_add_norm_problem(rows, dim, eps, x.dtype, rt, self.FORMATS[form],
+                                               residual is not None, stride)
+        ws = _lib.ssd_add_rmsnorm_bwd_workspace_bytes(self.prob)
+        if ws == 0:
+            raise _lib.SSDError(_lib.SSD_ERR_INVALID_ARGUMENT, "add_norm problem")
+        new = lambda dt: torch.empty((rows, dim), dtype=dt, device=dev)  # noqa: E731
+        self.out = self.codes = self.scales = None
+        if form is None:
+            self.out = new(x.dtype)
+        else:
+            self.codes = new(CODE_TYPES[form])
+            self.scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        self._h = h_out if h_out is not None else None if residual is None else new(rt)
+        self.h = x if self._h is None else self._h
+        if dout is not None:
+            self.dx = new(x.dtype)
+            self.dresidual = None if residual is None else self.dx if rt is x.dtype else new(rt)
+            self.dweight = torch.empty(dim, dtype=torch.float32, device=dev)
+            self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+
+    def fwd(self, stream=None, check=True):
+        _on_gpu(self.x.device, "AddNormDevice")
+        return _lib.ssd_add_rmsnorm_fwd(self.prob, self.x, self.residual, self.weight, self._h,
+                                        self.codes if self.out is None else self.out, self.scales,
+                                        stream=stream, check=check)
+
+    def bwd(self, stream=None, check=True):
+        if self.dout is None:
+            raise ValueError("built without dout: there is no backward")
+        _on_gpu(self.x.device, "AddNormDevice")
+        own = None if self.dresidual is self.dx else self.dresidual
+        return _lib.ssd_add_rmsnorm_bwd(self.prob, self.h, self.weight, self.dout, self.dh,
+                                        self.dx, own, self.dweight, self.workspace, stream=stream,
+                                        check=check)
+
+
+_matmul_problem = functools.lru_cache(maxsize=256)(_lib.make_matmul_problem)
+
+
+class Linear8:
+    """A linear map whose weights are 8-bit codes (n, k), int8 or e4m3, with a
+    scale for each output channel; it takes tokens in the same codes with a
+    scale for each, as AddNormDevice writes them."""
+
+    def __init__(self, codes, scales, bias=None, out_dtype=torch.bfloat16):
+        if codes.dim() != 2 or codes.dtype not in CODE_TYPES.values():
+            raise ValueError("codes must be (n, k), int8 or float8_e4m3fn")
+        if out_dtype not in _FLOATS:
+            raise ValueError("out_dtype must be fp32 or bf16")
+        n = codes.shape[0]
+        _on_gpu(codes.device, "Linear8")
+        _dense(codes, codes.shape, codes.dtype, "codes", codes.device)
+        _dense(scales, (n,), torch.float32, "scales", codes.device)
+        _dense(bias, (n,), torch.float32, "bias", codes.device)
+        self.codes, self.scales, self.bias, self.out_dtype = codes, scales, bias, out_dtype
+        self.format = StateCache.FORMATS["int8" if codes.dtype is torch.int8 else "e4m3"]
+
+    @classmethod
+    def from_weight(cls, weight, form="int8", bias=None, out_dtype=torch.bfloat16):
+        """Weights (n, k) rounded to 8 bits, a scale for each row of k: by the
+        state cache's rule, once."""
+        if form not in CODE_TYPES:
+            raise ValueError(f"form must be one of {sorted(CODE_TYPES)}")
+        w = weight.detach().float()
+        top = 127.0 if form == "int8" else 448.0
+        big = w.abs().amax(1, keepdim=True)
+        bad = ~torch.isfinite(w).all(1, keepdim=True)
+        empty = ~(big >= 2.0 ** -118)
+        y = torch.where(bad | empty, 0.0, w * torch.where(empty, 0.0, (1.0 / big) * top))
+        y = torch.round(y).clamp_(-127, 127) if form == "int8" else y.clamp_(-448, 448)
+        scales = torch.where(bad, float("nan"), torch.where(empty, 0.0, big * (1.0 / top)))
+        return cls(y.to(CODE_TYPES[form]), scales[:, 0].contiguous(), bias, out_dtype)
+
+    def __call__(self, codes, scales, out=None, stream=None, check=True):
+        """out (m, n) of the tokens' codes (m, k) and scales (m); a new tensor
+        unless given (``stream``'s: another stream waits for it before it reads
+        it)."""
+        n, k = self.codes.shape
+        if codes.dim() != 2 or codes.shape[1] != k:
+            raise ValueError(f"codes: expected (m, {k})")
+        m, dev = codes.shape[0], self.codes.device
+        _on_gpu(dev, "Linear8")
+        _dense(codes, (m, k), self.codes.dtype, "codes", dev)
+        _dense(scales, (m,), torch.float32, "scales", dev)
+        _dense(out, (m, n), self.out_dtype, "out", dev)
+        prob = _matmul_problem(m, n, k, self.format, self.out_dtype)
+        ws = _lib.ssd_scaled_matmul_workspace_bytes(prob)
+        if ws == 0:
+            raise _lib.SSDError(_lib.SSD_ERR_INVALID_ARGUMENT, "matmul problem")
+        with _allocating_on(stream):
+            if out is None:
+                out = torch.empty((m, n), dtype=self.out_dtype, device=dev)
+            self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        _lib.ssd_scaled_matmul(prob, codes, scales, self.codes, self.scales, self.bias, out,
+                               self.workspace, ws, stream=stream, check=check)
+        return out
+
+    def device_status(self, stream=None):
+        """Synchronises; the status word of the last call."""
+        return _lib.ssd_read_device_status(self.workspace, stream)
+
+
+class LogProbsDevice:
+    """Log probabilities of given tokens: the caller's device tensors, the
+    outputs and the calls through the C ABI.
+
+    logits (rows, vocab), fp32 or bf16, rows evenly spaced; tokens (rows) int32
+    (outside the vocabulary: padding).  ``fwd`` fills logprobs, entropy, lse
+    (rows) and, with ``ntop``, top_tokens and top_logprobs (rows, ntop).  With
+    ``dlogprobs`` and/or ``dentropy`` (rows), ``bwd`` after a ``fwd`` fills
+    dlogits, laid out as logits; ``dlogits=logits`` overwrites them.  The tensors
+    may be refilled between calls.  All are on the current CUDA device; the
+    buffers belong to the stream that is current here, and calls on another one
+    come after its work."""
+
+    def __init__(self, logits, tokens, scale=1.0, ntop=0, dlogprobs=None, dentropy=None,
+                 dlogits=None):
+        if logits.dim() != 2 or logits.dtype not in _FLOATS:
+            raise ValueError("logits must be (rows, vocab), fp32 or bf16")
+        rows, vocab = logits.shape
+        dev = logits.device
+        spaced = lambda t: t.stride(0) if rows > 1 else vocab  # noqa: E731
+        for t, what in ((logits, "logits"), (dlogits, "dlogits")):
+            if t is not None and (t.shape != logits.shape or t.dtype is not logits.dtype or t.device != dev
+                                  or (vocab > 1 and t.stride(1) != 1) or spaced(t) < vocab):
+                raise ValueError(f"{what}: expected (rows, vocab) with dense, evenly spaced rows")
+        _on_gpu(dev, "LogProbsDevice")
+        _dense(tokens, (rows,), torch.int32, "tokens", dev)
+        _dense(dlogprobs, (rows,), torch.float32, "dlogprobs", dev)
+        _dense(dentropy, (rows,), torch.float32, "dentropy", dev)
+        self.back = dlogprobs is not None or dentropy is not None
+        if dlogits is not None and not self.back:
+            raise ValueError("dlogits needs dlogprobs or dentropy")
+        self.logits, self.tokens, self.dlogprobs, self.dentropy = logits, tokens, dlogprobs, dentropy
+        self.dlogits = dlogits
+        if self.back and dlogits is None:
+            self.dlogits = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
+        self.prob = _lib.make_logprob_problem(rows, vocab, scale, ntop, logits.dtype, spaced(logits),
+                                              spaced(self.dlogits) if self.back else 0)
+        new = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+        self.logprobs, self.entropy, self.lse = new(rows), new(rows), new(rows)
+        self.top_tokens = new(rows, ntop, dt=torch.int32) if ntop else None
+        self.top_logprobs = new(rows, ntop) if ntop else None
+
+    def fwd(self, stream=None, check=True):
+        _on_gpu(self.logits.device, "LogProbsDevice")
+        return _lib.ssd_token_logprobs(self.prob, self.logits, self.tokens, self.logprobs,
+                                       self.entropy, self.lse, self.top_tokens, self.top_logprobs,
+                                       stream=stream, check=check)
+
+    def bwd(self, stream=None, check=True):
+        if not self.back:
+            raise ValueError("built without dlogprobs and dentropy: there is no backward")
+        _on_gpu(self.logits.device, "LogProbsDevice")
+        return _lib.ssd_token_logprobs_bwd(self.prob, self.logits,
+                                           None if self.dlogprobs is None else self.tokens, self.lse,
+                                           None if self.dentropy is None else self.entropy,
+                                           self.dlogprobs, self.dentropy, self.dlogits,
+                                           stream=stream, check=check)
