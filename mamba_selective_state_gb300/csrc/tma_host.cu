@@ -40,4 +40,17 @@ bool encode_tmap_bf16_4d(CUtensorMap* out, const void* base, const uint64_t dims
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_rows(CUtensorMap* out, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t stride_bytes,
+                      uint32_t box_rows) {
+  std::call_once(g_once, resolve);
+  if (!g_encode) return false;
+  cuuint64_t d[2] = {row_bytes, rows};
+  cuuint64_t st[1] = {stride_bytes};
+  cuuint32_t bx[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), d, st, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace ssd
