@@ -529,7 +529,7 @@ int ssd_state_cache_load(const ssd_cache_problem* prob, const void* cache, const
  * memory, 16-byte aligned.  The sums are fp32: those of int8 codes are exact
  * while their partial sums stay below 2^24 (always for k <= 1024).  A NaN or an
  * infinity in a token's scale or codes stays in its row of out, one in a
- * channel's in its column.  m, n, k <= 2^22.  Ownership, errors and stream
+ * channel's in its column.  m, n <= 2^22, k <= 2^20.  Ownership, errors and stream
  * semantics as above; device-side waits are bounded, and one that expired is
  * recorded in the status word at the start of the workspace
  * (ssd_read_device_status).  Results are bitwise reproducible run to run. */

@@ -11,9 +11,11 @@
 //
 // Bound by HBM; each tensor is read and written once.  A CTA takes a row, a
 // thread 8 neighbouring columns at a time (one 16-byte access in bf16), which
-// stay in registers from the sum to the store; in the backward they stay the
-// thread's own from row to row, so that it also holds their dweight.  The CTAs'
-// dweights are joined by a second kernel in a fixed order.
+// stay in registers from the sum to the store, with the CTA's next row on its way;
+// in the backward they stay the thread's own from row to row, so that it also
+// holds their dweight.  The CTAs' dweights are joined by a second kernel in a
+// fixed order.  16,384 rows of 4096 bf16: with a bf16 stream to e4m3 77 us (6.1
+// TB/s); on an fp32 stream to bf16 132 us (6.1), its backward 179 us (6.0).
 #include <string.h>
 
 #include "codes.cuh"
@@ -42,38 +44,55 @@ struct AddNormArgs {
   float inv_dim, eps;
 };
 
-// Eight values of a row: neighbours (piece p) where rows are whole 16-byte
-// vectors, else columns a CTA's width apart.
+// Eight values of a row: neighbours where rows are whole 16-byte vectors, else
+// columns a CTA's width apart.  They are fetched as they lie and turned into
+// fp32 when they are wanted, so that a row ahead costs few registers.
 template <typename T, bool kVec>
 struct Cols {
+  struct Raw {
+    uint4 u[sizeof(T) / 2];
+  };
   static __device__ __forceinline__ int col(int i, int j) {
     return kVec ? (i * (int)blockDim.x + (int)threadIdx.x) * 8 + j : (i * 8 + j) * (int)blockDim.x + (int)threadIdx.x;
   }
-  static __device__ __forceinline__ void load(const T* row, int i, int dim, float (&v)[8]) {
+  static __device__ __forceinline__ void fetch(const T* row, int i, int dim, Raw& r) {
     if constexpr (kVec) {
       const int c = col(i, 0);
-      if (c < dim) {
-        if constexpr (sizeof(T) == 2) {
-          const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + c));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-          }
-        } else {
-          const float4 a = __ldcs(reinterpret_cast<const float4*>(row + c)),
-                       b = __ldcs(reinterpret_cast<const float4*>(row + c) + 1);
-          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+        r.u[j] = c < dim ? __ldcs(reinterpret_cast<const uint4*>(row + c) + j) : make_uint4(0, 0, 0, 0);
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        w[j] = 0;
+        if (col(i, j) < dim) {
+          if constexpr (sizeof(T) == 2) w[j] = __ldcs(reinterpret_cast<const unsigned short*>(row) + col(i, j));
+          else w[j] = __ldcs(reinterpret_cast<const uint32_t*>(row) + col(i, j));
         }
+      }
+      if constexpr (sizeof(T) == 2) {
+        r.u[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
       } else {
+        r.u[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        r.u[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void values(const Raw& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
     } else {
+      const uint4 x = r.u[sizeof(T) / 2 - 1];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = col(i, j) < dim ? to_f(row[col(i, j)]) : 0.f;
+      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[j]);
+      v[4] = __uint_as_float(x.x); v[5] = __uint_as_float(x.y);
+      v[6] = __uint_as_float(x.z); v[7] = __uint_as_float(x.w);
     }
   }
   static __device__ __forceinline__ void store(T* row, int i, int dim, const float (&v)[8]) {
@@ -157,28 +176,43 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int i, int dim, const 
   }
 }
 
-// NP: pieces of 8 columns to a thread
+// NP: pieces of 8 columns to a thread.  The next row of a CTA is on its way
+// while this one is summed, rounded and written.
 template <typename T, typename R, int NP, bool kVec>
 __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a) {
+  using X = Cols<T, kVec>;
+  using H = Cols<R, kVec>;
   __shared__ float red[2][kMaxThreads / 32], big_s[2][kMaxThreads / 32];
+  typename X::Raw x[NP];
+  typename H::Raw y[NP];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      X::fetch(static_cast<const T*>(a.x) + row * a.xs, i, a.dim, x[i]);
+      if (a.res) H::fetch(static_cast<const R*>(a.res) + row * a.dim, i, a.dim, y[i]);
+    }
+  };
+  fetch(blockIdx.x);
+  float w0[8];  // the weight of a single piece stays in registers
+  if (NP == 1) load_weight<kVec>(a.w, 0, a.dim, w0);
   int par = 0;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
     float v[NP][8];
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < NP; ++i) Cols<T, kVec>::load(static_cast<const T*>(a.x) + row * a.xs, i, a.dim, v[i]);
-    if (a.res) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
+    for (int i = 0; i < NP; ++i) {
+      X::values(x[i], v[i]);
+      if (a.res) {
         float u[8];
-        Cols<R, kVec>::load(static_cast<const R*>(a.res) + row * a.dim, i, a.dim, u);
+        H::values(y[i], u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = to_f(from_f<R>(v[i][j] + u[j]));
       }
     }
+    if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      if (a.h) Cols<R, kVec>::store(static_cast<R*>(a.h) + row * a.dim, i, a.dim, v[i]);
+      if (a.h) H::store(static_cast<R*>(a.h) + row * a.dim, i, a.dim, v[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     }
@@ -187,17 +221,17 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       float w[8];
-      load_weight<kVec>(a.w, i, a.dim, w);
+      if (NP > 1) load_weight<kVec>(a.w, i, a.dim, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[i][j] = v[i][j] * r * w[j];
+        v[i][j] = v[i][j] * r * (NP == 1 ? w0[j] : w[j]);
         // what is not finite makes the row's largest an infinity
         big = fmaxf(big, fabsf(v[i][j]) <= 3.402823466e38f ? fabsf(v[i][j]) : __int_as_float(0x7f800000));
       }
     }
     if (a.codes == 0) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) Cols<T, kVec>::store(static_cast<T*>(a.out) + row * a.dim, i, a.dim, v[i]);
+      for (int i = 0; i < NP; ++i) X::store(static_cast<T*>(a.out) + row * a.dim, i, a.dim, v[i]);
       continue;
     }
     // (values that are not negative order as integers)
@@ -223,21 +257,37 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a
 
 template <typename T, typename R, int NP, bool kVec>
 __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a) {
+  using X = Cols<T, kVec>;
+  using H = Cols<R, kVec>;
   __shared__ float red[2][2][kMaxThreads / 32];
   float dw[NP][8];
 #pragma unroll
   for (int i = 0; i < NP; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  typename H::Raw h[NP], dh[NP];
+  typename X::Raw dout[NP];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      H::fetch(static_cast<const R*>(a.h) + row * a.dim, i, a.dim, h[i]);
+      X::fetch(static_cast<const T*>(a.dout) + row * a.dim, i, a.dim, dout[i]);
+    }
+  };
+  constexpr bool kNext = NP <= 2;  // (four pieces leave no registers for another row)
+  if (kNext) fetch(blockIdx.x);
   int par = 0;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
     float v[NP][8], d[NP][8];
     float ss = 0.f, sg = 0.f;
+    if (!kNext) fetch(row);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      Cols<R, kVec>::load(static_cast<const R*>(a.h) + row * a.dim, i, a.dim, v[i]);
-      Cols<T, kVec>::load(static_cast<const T*>(a.dout) + row * a.dim, i, a.dim, d[i]);
+      if (a.dh && kNext) H::fetch(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, dh[i]);
+      H::values(h[i], v[i]);
+      X::values(dout[i], d[i]);
     }
+    if (kNext && row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       float w[8];
@@ -268,11 +318,11 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
     for (int i = 0; i < NP; ++i) {
       float w[8], u[8];
       load_weight<kVec>(a.w, i, a.dim, w);
-      if (a.dh) {
-        Cols<R, kVec>::load(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, u);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = 0.f;
+      for (int j = 0; j < 8; ++j) u[j] = 0.f;
+      if (a.dh) {
+        if (!kNext) H::fetch(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, dh[i]);
+        H::values(dh[i], u);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -280,16 +330,18 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
         dw[i][j] = fmaf(d[i][j], n, dw[i][j]);
         u[j] += r * (d[i][j] * w[j] - n * proj);
       }
-      Cols<T, kVec>::store(static_cast<T*>(a.dx) + row * a.dim, i, a.dim, u);
-      if (a.dres) Cols<R, kVec>::store(static_cast<R*>(a.dres) + row * a.dim, i, a.dim, u);
+      X::store(static_cast<T*>(a.dx) + row * a.dim, i, a.dim, u);
+      if (a.dres) H::store(static_cast<R*>(a.dres) + row * a.dim, i, a.dim, u);
     }
   }
+  // (the launch that joins the partial sums comes up while the last of them are written)
+  asm volatile("griddepcontrol.launch_dependents;");
   float* part = a.part + (long long)blockIdx.x * a.dim;
 #pragma unroll
   for (int i = 0; i < NP; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (Cols<T, kVec>::col(i, j) < a.dim) part[Cols<T, kVec>::col(i, j)] = dw[i][j];
+      if (X::col(i, j) < a.dim) part[X::col(i, j)] = dw[i][j];
 }
 
 // dweight[c] = sum of the slices' partials: 32 columns to a CTA, each warp a
@@ -298,6 +350,7 @@ constexpr int kFoldWarps = 16;
 __global__ void __launch_bounds__(kFoldWarps * 32) add_norm_fold_kernel(const float* part, float* dweight, int slices,
                                                                         int dim) {
   __shared__ float sums[kFoldWarps][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   const int per = (slices + kFoldWarps - 1) / kFoldWarps;
   float s = 0.f;
@@ -317,17 +370,30 @@ __global__ void __launch_bounds__(kFoldWarps * 32) add_norm_fold_kernel(const fl
 }
 
 // Threads to a row and pieces to a thread.  Few rows: as many threads as there
-// are pieces, for the shortest way through one row.  Many rows: two pieces to a
-// thread, four where 512 threads of two would not hold the row.
+// are pieces, for the shortest way through one row (1001 rows of 1237 fp32: 4.4 us
+// with one piece, 5.9 with two).  Many rows: two pieces to a thread (16,384 rows of
+// 4096 bf16 to e4m3: 77 us, with one piece 96), four where 512 threads of two would
+// not hold the row.
 struct Shape {
   int threads, np;
 };
 Shape shape_of(int dim, long long rows, int sms) {
   const int pieces = (dim + 7) / 8;
-  int np = rows > 2 * sms && pieces >= 64 ? 2 : 1;
+  int np = rows > 8 * sms && pieces >= 64 ? 2 : 1;
   while (pieces > np * kMaxThreads) np *= 2;
   const int t = ((pieces + np - 1) / np + 31) / 32 * 32;
   return {t, np};
+}
+// CTAs: those that are resident at once, with 64 registers to a thread, and in
+// the backward 128 (16,384 x 4096 on an fp32 stream: 179 us; three CTAs to an SM
+// without the next row in registers 197).
+long long grid_of(long long rows, int threads, int sms, bool bwd) {
+  int per = (bwd ? 512 : 1024) / threads;
+  if (per > 8 && bwd) per = 8;
+  if (per < 1) per = 1;
+  long long grid = (long long)sms * per;
+  if (grid > rows) grid = rows;
+  return bwd && grid > kMaxSlices ? kMaxSlices : grid;
 }
 
 template <typename T, typename R, int NP, bool kVec>
@@ -408,9 +474,7 @@ int ssd_add_rmsnorm_fwd(const ssd_add_norm_problem* pr, const void* x, const voi
   a.eps = pr->eps;
   const int sms = device_sm_count();
   const Shape sh = shape_of(a.dim, a.rows, sms);
-  // as many CTAs as are resident with 64 registers to a thread
-  long long grid = (long long)sms * (1024 / sh.threads);
-  if (grid > a.rows) grid = a.rows;
+  const long long grid = grid_of(a.rows, sh.threads, sms, false);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_before(s);
   const cudaError_t e = launch(*pr, a, sh, (unsigned)grid, false, s);
@@ -448,9 +512,7 @@ int ssd_add_rmsnorm_bwd(const ssd_add_norm_problem* pr, const void* h, const flo
   a.eps = pr->eps;
   const int sms = device_sm_count();
   const Shape sh = shape_of(a.dim, a.rows, sms);
-  long long grid = (long long)sms * (768 / sh.threads < 8 ? (768 / sh.threads > 0 ? 768 / sh.threads : 1) : 8);
-  if (grid > a.rows) grid = a.rows;
-  if (grid > kMaxSlices) grid = kMaxSlices;
+  const long long grid = grid_of(a.rows, sh.threads, sms, true);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_before(s);
   cudaError_t e = launch(*pr, a, sh, (unsigned)grid, true, s);
@@ -458,8 +520,16 @@ int ssd_add_rmsnorm_bwd(const ssd_add_norm_problem* pr, const void* h, const flo
   if (e != cudaSuccess) return SSD_ERR_CUDA;
   prof_before(s);
   set_kernel_name("add_norm_fold");
-  add_norm_fold_kernel<<<(a.dim + 31) / 32, kFoldWarps * 32, 0, s>>>(a.part, dweight, (int)grid, a.dim);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.dim + 31) / 32));
+  cfg.blockDim = dim3(kFoldWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, add_norm_fold_kernel, static_cast<const float*>(a.part), dweight, (int)grid, a.dim);
   prof_after(s);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }

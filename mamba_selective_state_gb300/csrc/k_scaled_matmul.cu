@@ -7,14 +7,18 @@
 // codes are multiplied as fp16, which holds them and their products' factors
 // exactly; sums are fp32.  e4m3 codes go to the tensor cores as they are.
 //
-// Few tokens (m <= 64): bound by the weights' bytes.  Warps read 16 channels'
-// codes in 16-byte pieces, turn them into fp16 in registers and multiply them
-// with the tokens' by warp-level products; the order of k inside a product is
-// free, so a lane's 16 neighbouring codes serve four products as they lie.
-//
-// More tokens: tensor-memory products of 256 x 256 outputs by pairs of CTAs,
-// persistent, fed by TMA through a ring of stages, the epilogue of one tile
-// under the products of the next.  int8 codes are first written out as fp16.
+// Three kernels, by the number of tokens:
+//  * up to 16: bound by the weights' bytes.  Warps read 16 channels' codes in
+//    16-byte pieces, turn them into fp16 in registers and multiply them with
+//    the tokens' by warp-level products; the order of k inside a product is
+//    free, so a lane's 16 neighbouring codes serve four products as they lie.
+//  * up to 256: the channels are the rows of tensor-memory products with all
+//    tokens.  int8 weights stay int8 up to shared memory; warps turn them into
+//    fp16 on their way to tensor memory, from where the products take them.
+//  * more: products of 256 tokens x up to 256 channels by pairs of CTAs,
+//    persistent, the epilogue of one tile under the products of the next.
+// A launch before them writes out what they cannot read as it is: int8 tokens (and
+// with many tokens the weights) as fp16, rows that are not whole 16-byte vectors.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -29,7 +33,7 @@ int device_check();
 
 namespace {
 
-constexpr int kFewTokens = 64;
+constexpr int kFewTokens = 16, kSomeTokens = 256;
 
 struct MatmulArgs {
   const uint8_t *a, *w;
@@ -65,14 +69,18 @@ __device__ __forceinline__ void to_half(const uint4& u, uint32_t (&h)[8]) {
   }
 }
 
-// ---- rows written out with a whole number of vectors -----------------------
-// as fp16 (kHalf) or as they are, zeros behind the k-th code
+// ---- rows written out -------------------------------------------------------
+// as fp16 or as they are, with rows of whole 16-byte vectors and zeros behind
+// the k-th code
+struct PackPart {
+  const uint8_t* src;
+  uint8_t* dst;
+  long long groups, bytes;  // groups of 16 codes in all; bytes of the source
+  int per_row, half;        // groups to a row; as fp16
+};
 struct PackArgs {
-  const uint8_t *src[2];
-  uint8_t* dst[2];
-  long long groups[2];  // 16-code groups in all
-  long long bytes[2];   // of the source
-  int k, per_row;       // groups to a row
+  PackPart part[2];
+  int k;
   int* status;
 };
 
@@ -102,19 +110,19 @@ __device__ __forceinline__ uint4 load16(const uint8_t* base, long long at, int c
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <bool kHalf>
 __global__ void __launch_bounds__(256) pack_rows_kernel(PackArgs p) {
+  asm volatile("griddepcontrol.launch_dependents;");
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-  const long long total = p.groups[0] + p.groups[1];
+  const long long total = p.part[0].groups + p.part[1].groups;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    const int which = i >= p.groups[0];
-    const long long g = which ? i - p.groups[0] : i;
-    const long long row = g / p.per_row;
-    const int c = (int)(g - row * p.per_row) * 16, count = min(max(p.k - c, 0), 16);
+    const int which = i >= p.part[0].groups;
+    const PackPart& t = p.part[which];
+    const long long g = which ? i - p.part[0].groups : i, row = g / t.per_row;
+    const int c = (int)(g - row * t.per_row) * 16, count = min(max(p.k - c, 0), 16);
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (count) u = load16(p.src[which], row * p.k + c, count, p.bytes[which]);
-    uint4* to = reinterpret_cast<uint4*>(p.dst[which]);
-    if constexpr (kHalf) {
+    if (count) u = load16(t.src, row * p.k + c, count, t.bytes);
+    uint4* to = reinterpret_cast<uint4*>(t.dst);
+    if (t.half) {
       uint32_t h[8];
       to_half<false>(u, h);
       to[2 * g] = make_uint4(h[0], h[1], h[2], h[3]);
@@ -139,7 +147,7 @@ constexpr int kSkWarps = 8;
 // CT: tiles of 16 channels to a CTA; MT: groups of 8 tokens.  The warps split k,
 // 64 codes at a time; k is a multiple of 16.
 template <bool kFp8, typename O, int CT, int MT>
-__global__ void __launch_bounds__(kSkWarps * 32) skinny_kernel(MatmulArgs p) {
+__global__ void __launch_bounds__(kSkWarps * 32, MT == 1 ? 5 : 4) skinny_kernel(MatmulArgs p) {
   constexpr int kCh = CT * 16, kTok = MT * 8, kPitch = kCh + 1;
   extern __shared__ float part[];  // [warp][token][channel]
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -156,10 +164,10 @@ __global__ void __launch_bounds__(kSkWarps * 32) skinny_kernel(MatmulArgs p) {
       wrow[c][h] = p.w + r * p.k + q * 16;
     }
   float acc[CT][MT][4] = {};
-  constexpr int kAhead = CT * MT >= 8 ? 2 : 4;
+  constexpr int kAhead = 2;
   const int k = (int)p.k;
   for (int k0 = warp * 64; k0 < k; k0 += kSkWarps * 64 * kAhead) {
-    uint4 w[kAhead][CT][2];
+    uint4 w[kAhead][CT][2], tok_codes[kAhead][MT];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int kk = k0 + u * kSkWarps * 64;
@@ -169,11 +177,14 @@ __global__ void __launch_bounds__(kSkWarps * 32) skinny_kernel(MatmulArgs p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           w[u][c][h] = in ? __ldcs(reinterpret_cast<const uint4*>(wrow[c][h] + kk)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        tok_codes[u][t] = in && t * 8 + g < p.m
+                              ? __ldg(reinterpret_cast<const uint4*>(p.a + (t * 8 + g) * p.k + kk + q * 16))
+                              : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int kk = k0 + u * kSkWarps * 64;
-      const bool in = kk + q * 16 < k;
       uint32_t wh[CT][2][8];
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
@@ -182,11 +193,8 @@ __global__ void __launch_bounds__(kSkWarps * 32) skinny_kernel(MatmulArgs p) {
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        const int tok = t * 8 + g;
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (in && tok < p.m) a = __ldg(reinterpret_cast<const uint4*>(p.a + tok * p.k + kk + q * 16));
         uint32_t ah[8];
-        to_half<kFp8>(a, ah);
+        to_half<kFp8>(tok_codes[u][t], ah);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -231,28 +239,27 @@ cudaError_t launch_skinny_t(const MatmulArgs& p, cudaStream_t s) {
 template <bool kFp8, typename O>
 cudaError_t launch_skinny(const MatmulArgs& p, cudaStream_t s) {
   if (p.m <= 8) return launch_skinny_t<kFp8, O, 1, 1>(p, s);
-  if (p.m <= 16) return launch_skinny_t<kFp8, O, 1, 2>(p, s);
-  if (p.m <= 32) return launch_skinny_t<kFp8, O, 2, 4>(p, s);
-  return launch_skinny_t<kFp8, O, 2, 8>(p, s);
+  return launch_skinny_t<kFp8, O, 1, 2>(p, s);
 }
 
-// ---- many tokens: tensor-memory products by pairs of CTAs -------------------
-//
-// A pair computes 256 tokens x BN channels: each CTA holds 128 tokens' rows and
-// half of the channels' rows of every stage (128 bytes of k: 64 fp16 or 128
-// e4m3), and 128 rows of the result in its own tensor memory, twice.  The
-// leader (even rank) issues the products for both; its `full` barriers take the
-// bytes of both CTAs' copies.  Commits arrive in both CTAs.
-constexpr int kStages = 6;
-constexpr int kRowsA = 128;
-constexpr int kTcThreads = 192;  // warp 0 copies, warp 1 products, warps 2-5 epilogue
-
-template <int BN>
-struct TcSmem {
-  static constexpr int kA = kRowsA * 128, kB = BN / 2 * 128;
-  static constexpr int kStageBytes = kA + kB;
-  static constexpr int kBytes = kStages * kStageBytes + 1024 + 256;
-};
+template <bool kFp8, int kPair>
+__device__ __forceinline__ void block_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+#define SSD_MMA(group, kind)                                              \
+  asm volatile(                                                           \
+      "{\n\t.reg .pred p;\n\t"                                            \
+      "setp.ne.b32 p, %4, 0;\n\t"                                         \
+      "tcgen05.mma." group "." kind " [%0], %1, %2, %3, p;\n\t}\n" ::"r"( \
+          d),                                                             \
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)                         \
+      : "memory")
+  if constexpr (kPair && kFp8) SSD_MMA("cta_group::2", "kind::f8f6f4");
+  else if constexpr (kPair) SSD_MMA("cta_group::2", "kind::f16");
+  else if constexpr (kFp8) SSD_MMA("cta_group::1", "kind::f8f6f4");
+  else SSD_MMA("cta_group::1", "kind::f16");
+#undef SSD_MMA
+}
+// fp32 sums of fp16 (kind::f16) or e4m3 (kind::f8f6f4): both formats are number 0
+constexpr uint32_t idesc_of(int m, int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24); }
 
 __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -267,6 +274,391 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// tc::mbar_wait_flag for barriers at which another CTA's threads arrive
+__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, bool& ok) {
+  const long long c0 = clock64();
+  for (uint32_t outer = 0; outer < (ok ? 1u << 14 : 64u); ++outer) {
+    for (int i = 0; i < 64; ++i) {
+      uint32_t hit;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(hit)
+          : "r"(tc::smem_u32(bar)), "r"(parity)
+          : "memory");
+      if (hit) return;
+    }
+    if (clock64() - c0 > (1ll << 31)) break;
+  }
+  ok = false;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// ---- some tokens ------------------------------------------------------------
+// A CTA multiplies up to 128 channels (the products' rows) with up to NT tokens
+// over its share of k, 128 codes to a stage.  int8: four warps, a lane to a
+// channel, turn a stage's codes into fp16, into one of the operand's places in
+// tensor memory, four others the next stage's; shared memory then carries the
+// weights once, as int8, and the tokens as fp16.  e4m3: both
+// operands are taken from shared memory as they are.  The CTAs of a cluster
+// share k; they leave their sums in shared memory and each joins and writes some
+// of the tokens, in the order of the shares.
+constexpr int kTurners = 8;                                // warps that turn codes into fp16, and write results
+constexpr int kSomeThreads = kTurners * 32 + 64;           // and one that copies, one for the products
+
+template <bool kFp8, int NT>
+struct SomeShape {
+  static constexpr int kTok = (kFp8 ? 1 : 2) * NT * 128;   // bytes of a stage's tokens
+  static constexpr int kStageBytes = 128 * 128 + kTok;
+  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
+  static constexpr int kBytes = kStages * kStageBytes + 1024;
+  static constexpr int kPlaces = kFp8 ? 0 : 4;             // of the operand in tensor memory, 64 columns each
+  static constexpr uint32_t kCols = NT + 64 * kPlaces <= 64 ? 64 : NT + 64 * kPlaces <= 128 ? 128 : NT + 64 * kPlaces <= 256 ? 256 : 512;
+  static_assert(NT * 128 * 4 <= kStages * kStageBytes, "the sums fit into the stages");
+};
+
+struct SomeArgs {
+  MatmulArgs p;
+  int ch, kb, per;  // channels of a CTA (a multiple of 8); stages of k in all; of a CTA
+  int clear;        // no launch before this one has cleared the status word
+};
+
+// 16 codes of a lane's row at a time to 8 columns of tensor memory
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The launch before this one has ended and what it wrote is there (nothing, where
+// this one did not start early)
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// D (+)= A B^T with A in tensor memory: lane i is row i, a column two neighbouring k
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+template <bool kFp8, typename O, int NT>
+__global__ void __launch_bounds__(kSomeThreads)
+    some_tokens_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap, SomeArgs s) {
+  using S = SomeShape<kFp8, NT>;
+  constexpr int kStages = S::kStages, kPlaces = S::kPlaces ? S::kPlaces : 1;
+  extern __shared__ uint8_t raw[];
+  const MatmulArgs& p = s.p;
+  const uint32_t pad = (1024u - (tc::smem_u32(raw) & 1023u)) & 1023u, smem = tc::smem_u32(raw) + pad;
+  __shared__ uint64_t full[kStages], empty[kStages], turned[kPlaces], taken[kPlaces], done;
+  __shared__ uint32_t tmem_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cta_rank();
+  uint32_t ncta;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
+  const int quarters = (s.ch + 31) / 32;  // lane quarters that hold channels
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kPlaces; ++i) {
+      tc::mbar_init(&turned[i], quarters);
+      tc::mbar_init(&taken[i], 1);
+    }
+    tc::mbar_init(&done, 1);
+    tc::mbar_fence_init();
+    if (s.clear && blockIdx.x == 0) *p.status = 0;  // (a wait that expires does so a second later)
+  }
+  if (warp == kTurners + 1 && lane == 0) {
+    tc::prefetch_tmap(&amap);
+    tc::prefetch_tmap(&wmap);
+  }
+  if (warp == kTurners) tc::tmem_alloc(&tmem_s, S::kCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_s;
+  const long long n0 = (long long)(blockIdx.x / ncta) * s.ch;
+  const int b0 = (int)rank * s.per, nb = min(s.per, s.kb - b0);
+  bool ok = true;
+
+  if (warp == kTurners + 1) {
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      for (int b = 0; b < nb; ++b) {
+        tc::mbar_wait_flag(&empty[st], ph ^ 1, ok);
+        const uint32_t to = smem + st * S::kStageBytes;
+        tc::mbar_expect_tx(&full[st], s.ch * 128 + S::kTok);
+        box_load(to, &wmap, &full[st], (b0 + b) * 128, (int)n0);
+        if (b == 0) grid_wait();  // the tokens, written out by the launch before
+        if constexpr (kFp8) {
+          box_load(to + 128 * 128, &amap, &full[st], (b0 + b) * 128, 0);
+        } else {
+          box_load(to + 128 * 128, &amap, &full[st], (b0 + b) * 256, 0);
+          box_load(to + 128 * 128 + NT * 128, &amap, &full[st], (b0 + b) * 256 + 128, 0);
+        }
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  } else if (warp == kTurners) {
+    if (lane == 0) {
+      int st = 0, pl = 0;
+      uint32_t ph = 0, pph = 0;
+      for (int b = 0; b < nb; ++b) {
+        tc::mbar_wait_flag(&full[st], ph, ok);
+        const uint32_t w = smem + st * S::kStageBytes, a = w + 128 * 128;
+        if constexpr (kFp8) {
+          tc::tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            block_mma<true, false>(tmem, tc::smem_desc(w + j * 32, 16, 1024, tc::kSwz128),
+                                   tc::smem_desc(a + j * 32, 16, 1024, tc::kSwz128), idesc_of(128, NT), b | j);
+        } else {
+          tc::mbar_wait_flag(&turned[pl], pph, ok);
+          tc::tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            mma_from_tmem(tmem, tmem + NT + pl * 64 + j * 8,
+                          tc::smem_desc(a + (j >> 2) * NT * 128 + (j & 3) * 32, 16, 1024, tc::kSwz128),
+                          idesc_of(128, NT), b | j);
+          tc::mma_commit(&taken[pl]);
+          if (++pl == kPlaces) {
+            pl = 0;
+            pph ^= 1;
+          }
+        }
+        tc::mma_commit(&empty[st]);
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+      tc::mma_commit(&done);
+    }
+  } else if (!kFp8 && (warp & 3) < quarters) {
+    const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane;
+    uint4 u[8];
+    // a stage's codes of this lane's channel, and the stage after the next
+    int st = half % kStages;
+    uint32_t ph = 0;
+    auto read = [&]() {
+      tc::mbar_wait_flag(&full[st], ph, ok);
+      const uint32_t row = smem + st * S::kStageBytes + r * 128;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[j].x), "=r"(u[j].y), "=r"(u[j].z), "=r"(u[j].w)
+                     : "r"(row + ((j ^ (r & 7)) << 4))
+                     : "memory");
+      st += 2;
+      if (st >= kStages) {
+        st -= kStages;
+        ph ^= 1;
+      }
+    };
+    if (half < nb) read();
+    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + NT;
+    for (int b = half; b < nb; b += 2) {
+      uint32_t h[2][32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t x[8];
+        to_half<false>(u[j], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j >> 2][(j & 3) * 8 + i] = x[i];
+      }
+      tc::fence_async_smem();  // (read here, written by the next copy)
+      // (with two stages the next but one waits for this one's product)
+      if (kStages > 2 && b + 2 < nb) read();
+      const int pl = b % kPlaces;
+      tc::mbar_wait_flag(&taken[pl], (uint32_t)(b / kPlaces & 1) ^ 1u, ok);
+      tc::tc_fence_after();
+      __syncwarp();
+      tmem_store32(to + pl * 64, h[0]);
+      tmem_store32(to + pl * 64 + 32, h[1]);
+      tmem_store_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&turned[pl]);
+      if (kStages == 2 && b + 2 < nb) read();
+    }
+  }
+  __syncwarp();
+  const int share = ((int)p.m + (int)ncta - 1) / (int)ncta, lo = (int)rank * share, hi = min(lo + share, (int)p.m);
+  const int ch = lane * 4;
+  const long long n = n0 + ch;
+  const int cols = (int)min(min(p.n - n, (long long)(s.ch - ch)), 4LL);  // of this lane; may be negative
+  float ws[4], bias[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ws[i] = i < cols ? __ldg(p.ws + n + i) : 0.f;
+    bias[i] = i < cols && p.bias ? __ldg(p.bias + n + i) : 0.f;
+  }
+  // every product is done: the stages become the sums, [token][channel]
+  tc::mbar_wait_flag(&done, 0, ok);
+  tc::tc_fence_after();
+  __syncwarp();
+  float* sums = reinterpret_cast<float*>(raw + pad);
+  if (warp < kTurners && (warp & 3) < quarters) {
+    const int quarter = warp & 3, half = warp >> 2;
+#pragma unroll 2
+    for (int c = half * (NT / 2); c < (half + 1) * (NT / 2) && c < p.m; c += 16) {
+      float v[16];
+      tc::tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + quarter * 32 + lane] = v[i];
+    }
+  }
+  tc::tc_fence_before();
+  __syncwarp();
+  if (ncta > 1) cluster_sync_all();
+  else __syncthreads();
+  tc::tc_fence_after();
+  if (warp == kTurners) {
+    tc::tmem_dealloc(tmem, S::kCols);
+  } else if (warp < kTurners) {
+    for (int t = lo + warp; t < hi; t += kTurners) {
+      const float as = __ldg(p.as + t);
+      const uint32_t at = tc::smem_u32(sums + t * 128 + ch);
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (uint32_t r = 0; r < ncta; ++r) {
+        float x[4];
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                     : "r"(at_rank(at, r))
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += x[i];
+      }
+      O* out = static_cast<O*>(p.out) + t * p.n + n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = v[i] * as * ws[i];
+        if (p.bias) v[i] += bias[i];
+      }
+      if (p.n % 4 == 0 && cols >= 4) {
+        if constexpr (sizeof(O) == 2) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+          *reinterpret_cast<uint2*>(out) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        } else {
+          *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < cols) out[i] = from_f<O>(v[i]);
+      }
+    }
+  }
+  if (!ok) atomicOr(p.status, kDevTimeout);
+  __syncwarp();
+  if (ncta > 1) cluster_sync_all();  // other CTAs read this one's sums until here
+}
+
+// How the products' rows and k are shared out: k over as many CTAs of a cluster as
+// 128 channels to a CTA leave SMs free for (each with four stages at least), then
+// the channels evenly over the CTAs of as few waves as they need.
+void share_out(const MatmulArgs& p, int sms, SomeArgs* a, int* split, int* tiles) {
+  a->kb = (int)((p.k + 127) / 128);
+  const long long wide = (p.n + 127) / 128;
+  int x = (int)(sms / wide);
+  if (x > 8) x = 8;
+  if (x > a->kb / 4) x = a->kb / 4;
+  if (x < 1) x = 1;
+  a->per = (a->kb + x - 1) / x;
+  x = (a->kb + a->per - 1) / a->per;  // every share has a stage
+  const long long room = sms / x, waves = (wide + room - 1) / room;
+  a->ch = (int)((p.n + room * waves - 1) / (room * waves));
+  a->ch = (a->ch + 7) / 8 * 8;
+  *split = x;
+  *tiles = (int)((p.n + a->ch - 1) / a->ch);
+}
+
+// a, w: rows as the copies read them, of bytes in all and in memory
+struct Rows {
+  const void* at;
+  uint64_t bytes, pitch;
+};
+
+template <bool kFp8, typename O, int NT>
+cudaError_t launch_some_t(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear, bool early) {
+  using S = SomeShape<kFp8, NT>;
+  SomeArgs a;
+  a.p = p;
+  a.clear = clear;
+  int split, tiles;
+  share_out(p, device_sm_count(), &a, &split, &tiles);
+  CUtensorMap am, wm;
+  if (!encode_tmap_rows(&am, ra.at, ra.bytes, (uint64_t)p.m, ra.pitch, NT) ||
+      !encode_tmap_rows(&wm, rw.at, rw.bytes, (uint64_t)p.n, rw.pitch, (uint32_t)a.ch))
+    return cudaErrorInvalidValue;
+  auto kernel = some_tokens_kernel<kFp8, O, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kSomeThreads);
+  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  // Behind the launch that writes out the tokens this one starts early: the weights' first stages are under way by then.
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 2 : 1;
+  set_kernel_name("scaled_matmul_some");
+  return cudaLaunchKernelEx(&cfg, kernel, am, wm, a);
+}
+template <bool kFp8, typename O>
+cudaError_t launch_some(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear, bool early) {
+  if (p.m <= 32) return launch_some_t<kFp8, O, 32>(p, ra, rw, s, clear, early);
+  if (p.m <= 64) return launch_some_t<kFp8, O, 64>(p, ra, rw, s, clear, early);
+  if (p.m <= 128) return launch_some_t<kFp8, O, 128>(p, ra, rw, s, clear, early);
+  return launch_some_t<kFp8, O, 256>(p, ra, rw, s, clear, early);
+}
+
+// ---- many tokens: tensor-memory products by pairs of CTAs -------------------
+//
+// A pair computes 256 tokens x BN channels: each CTA holds 128 tokens' rows and
+// half of the channels' rows of every stage, and 128 rows of the result in its
+// own tensor memory, twice.  The leader (even rank) issues the products for
+// both; its `full` barriers take the bytes of both CTAs' copies.  Commits arrive in both CTAs.
+constexpr int kStages = 6;
+constexpr int kRowsA = 128;
+
+template <int BN>
+struct PairSmem {
+  static constexpr int kA = kRowsA * 128, kB = BN / 2 * 128;
+  static constexpr int kStageBytes = kA + kB;
+  static constexpr int kOut = 4 * 32 * 128;  // 32 rows of 128 bytes for each epilogue warp
+  static constexpr int kBytes = kStages * kStageBytes + kOut + 1024;
+};
+
 // A box into this CTA's shared memory, its bytes counted by a barrier of the pair
 __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
@@ -275,32 +667,12 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-template <bool kFp8>
-__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (kFp8)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // Arrives on the barrier at this place in both CTAs once this thread's products are done
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
-}
-__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // The tile-th pair of (token, channel) tiles: bands of 8 token tiles, channel by
@@ -314,21 +686,70 @@ __device__ __forceinline__ void tile_of(long long tile, int mt, int nt, int& tm,
   tn = in / rows;
 }
 
-struct TcArgs {
-  const float *as, *ws, *bias;
-  void* out;
-  int* status;
-  long long m, n;
-  int mt, nt, kb;  // tiles of tokens and channels; 128-byte blocks of k
+struct PairArgs {
+  MatmulArgs p;
+  int mt, nt, kb;  // tiles of tokens and channels; blocks of k
+  int clear;       // no launch before this one has cleared the status word
 };
 
+// 32 rows of 128 bytes of results from an epilogue warp, a row to a lane, through
+// shared memory, so that eight lanes write a row's 128 bytes together.
+template <typename O>
+__device__ __forceinline__ void write_rows(uint32_t buf, const uint4 (&mine)[8], O* out, long long row0, long long col0,
+                                           const MatmulArgs& p, int lane) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                 "r"(mine[j].x), "r"(mine[j].y), "r"(mine[j].z), "r"(mine[j].w)
+                 : "memory");
+  __syncwarp();
+  constexpr int n = 16 / sizeof(O);
+  if (p.n % n == 0) {
+    const int piece = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      uint4 u;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                   : "r"(buf + r * 128 + ((piece ^ (r & 7)) << 4))
+                   : "memory");
+      if (row0 + r < p.m && col0 + piece * n < p.n)
+        *reinterpret_cast<uint4*>(out + (row0 + r) * p.n + col0 + piece * n) = u;
+    }
+  } else {
+    for (int r = 0; r < 32 && row0 + r < p.m; ++r)
+#pragma unroll
+      for (int i = 0; i < 128 / (int)sizeof(O) / 32; ++i) {
+        const int c = i * 32 + lane, at = c * (int)sizeof(O);
+        const uint32_t from = buf + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15);
+        if (col0 + c < p.n) {
+          if constexpr (sizeof(O) == 2) {
+            unsigned short h;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(from) : "memory");
+            out[(row0 + r) * p.n + col0 + c] = __ushort_as_bfloat16(h);
+          } else {
+            float f;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(from) : "memory");
+            out[(row0 + r) * p.n + col0 + c] = f;
+          }
+        }
+      }
+  }
+  __syncwarp();
+}
+
+// One warp issues copies, one the products, four write results.
+constexpr int kPairThreads = 192;
 template <bool kFp8, typename O, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
-    pair_matmul_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap, TcArgs p) {
-  using S = TcSmem<BN>;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    pair_matmul_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap, PairArgs s) {
+  using S = PairSmem<BN>;
   extern __shared__ uint8_t raw[];
+  const MatmulArgs& p = s.p;
   const uint32_t smem = (tc::smem_u32(raw) + 1023u) & ~1023u;
   __shared__ uint64_t full[kStages], empty[kStages], done[2], drained[2];
+  __shared__ alignas(16) float scale_s[2][2][BN];  // the channels' scales and biases of a tile
   __shared__ uint32_t tmem_s;
   const uint32_t rank = cta_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -342,8 +763,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
       tc::mbar_init(&drained[i], 8);  // four epilogue warps of both CTAs
     }
     tc::mbar_fence_init();
+    if (s.clear && blockIdx.x == 0) *p.status = 0;  // (a wait that expires does so a second later)
   }
-  constexpr uint32_t kCols = BN * 2 < 32 ? 32 : BN * 2;
+  constexpr uint32_t kCols = BN * 2;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(&tmem_s)),
                  "r"(kCols)
@@ -355,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
   cluster_sync_all();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_s;
-  const long long tiles = (long long)p.mt * p.nt, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const long long tiles = (long long)s.mt * s.nt, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   bool ok = true;
 
   if (warp == 0) {
@@ -366,9 +788,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
       uint32_t ph = 0;
       for (long long t = pair; t < tiles; t += pairs) {
         int tm, tn;
-        tile_of(t, p.mt, p.nt, tm, tn);
+        tile_of(t, s.mt, s.nt, tm, tn);
         const int ya = tm * 256 + (int)rank * 128, yw = tn * BN + (int)rank * (BN / 2);
-        for (int b = 0; b < p.kb; ++b) {
+        for (int b = 0; b < s.kb; ++b) {
           tc::mbar_wait_flag(&empty[st], ph ^ 1, ok);
           if (rank == 0) tc::mbar_expect_tx(&full[st], 2 * S::kStageBytes);
           const uint32_t bar = at_rank(tc::smem_u32(&full[st]), 0), to = smem + st * S::kStageBytes;
@@ -383,21 +805,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      // M = 256, N = BN, fp32 sums of fp16 (kind::f16) or e4m3 (kind::f8f6f4): both formats are number 0
-      constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | (16u << 24);
       int st = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       for (long long t = pair; t < tiles; t += pairs) {
-        tc::mbar_wait_flag(&drained[acc], aph ^ 1, ok);
+        wait_cluster(&drained[acc], aph ^ 1, ok);
         tc::tc_fence_after();
-        for (int b = 0; b < p.kb; ++b) {
-          tc::mbar_wait_flag(&full[st], ph, ok);
+        for (int b = 0; b < s.kb; ++b) {
+          wait_cluster(&full[st], ph, ok);
           tc::tc_fence_after();
           const uint32_t a = smem + st * S::kStageBytes, w = a + S::kA;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            pair_mma<kFp8>(tmem + acc * BN, tc::smem_desc(a + j * 32, 16, 1024, tc::kSwz128),
-                           tc::smem_desc(w + j * 32, 16, 1024, tc::kSwz128), idesc, b | j);
+            block_mma<kFp8, true>(tmem + acc * BN, tc::smem_desc(a + j * 32, 16, 1024, tc::kSwz128),
+                                  tc::smem_desc(w + j * 32, 16, 1024, tc::kSwz128), idesc_of(256, BN), b | j);
           pair_commit(tc::smem_u32(&empty[st]));
           if (++st == kStages) {
             st = 0;
@@ -411,82 +831,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
     }
   } else {
     const int quarter = warp & 3;  // the lanes of tensor memory that this warp may read
+    const int et = (warp - 2) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const bool vec = p.n % (16 / (int)sizeof(O)) == 0;
+    const uint32_t buf = smem + kStages * S::kStageBytes + (uint32_t)quarter * 4096;
+    constexpr int CH = 128 / sizeof(O);  // columns at a time: 128 bytes of a row
     int acc = 0;
     uint32_t aph = 0;
     for (long long t = pair; t < tiles; t += pairs) {
       int tm, tn;
-      tile_of(t, p.mt, p.nt, tm, tn);
-      const long long row = (long long)tm * 256 + rank * 128 + quarter * 32 + lane, n0 = (long long)tn * BN;
-      const bool in = row < p.m;
-      const float as = in ? __ldg(p.as + row) : 0.f;
-      O* out = static_cast<O*>(p.out) + row * p.n + n0;
+      tile_of(t, s.mt, s.nt, tm, tn);
+      const long long row0 = (long long)tm * 256 + rank * 128 + quarter * 32, n0 = (long long)tn * BN;
+      const float as = row0 + lane < p.m ? __ldg(p.as + row0 + lane) : 0.f;
+      for (int i = et; i < BN; i += 128) {
+        const bool in = n0 + i < p.n;
+        scale_s[acc][0][i] = in ? __ldg(p.ws + n0 + i) : 0.f;
+        scale_s[acc][1][i] = in && p.bias ? __ldg(p.bias + n0 + i) : 0.f;
+      }
+      // (a buffer is written again two tiles on: every warp has passed this barrier of the tile between)
+      asm volatile("bar.sync 1, 128;" ::: "memory");
       tc::mbar_wait_flag(&done[acc], aph, ok);
       tc::tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < BN && n0 + c < p.n; c += 32) {
-        float v[32];
-        {
+      for (int c = 0; c < BN && n0 + c < p.n; c += CH) {
+        uint4 mine[8];
+        uint32_t* word = reinterpret_cast<uint32_t*>(mine);
+#pragma unroll
+        for (int h = 0; h < CH; h += 32) {
           float x[16], y[16];
-          tc::tmem_ld16x2(lanes + acc * BN + c, lanes + acc * BN + c + 16, x, y);
+          tc::tmem_ld16x2(lanes + acc * BN + c + h, lanes + acc * BN + c + h + 16, x, y);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i] = x[i];
-            v[16 + i] = y[i];
-          }
-        }
-        if (n0 + c + 32 <= p.n) {
-          if ((p.n & 3) == 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 s = __ldg(reinterpret_cast<const float4*>(p.ws + n0 + c + i));
-              v[i] *= as * s.x; v[i + 1] *= as * s.y; v[i + 2] *= as * s.z; v[i + 3] *= as * s.w;
-            }
+          for (int i = 0; i < 32; i += 2) {
+            float u = i < 16 ? x[i] : y[i - 16], v = i < 16 ? x[i + 1] : y[i - 15];
+            const float2 sc = *reinterpret_cast<const float2*>(&scale_s[acc][0][c + h + i]);
+            u = u * as * sc.x;
+            v = v * as * sc.y;
             if (p.bias) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 s = __ldg(reinterpret_cast<const float4*>(p.bias + n0 + c + i));
-                v[i] += s.x; v[i + 1] += s.y; v[i + 2] += s.z; v[i + 3] += s.w;
-              }
+              const float2 bi = *reinterpret_cast<const float2*>(&scale_s[acc][1][c + h + i]);
+              u += bi.x;
+              v += bi.y;
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] *= as * __ldg(p.ws + n0 + c + i);
-              if (p.bias) v[i] += __ldg(p.bias + n0 + c + i);
-            }
-          }
-          if (in && vec) {
             if constexpr (sizeof(O) == 2) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const __nv_bfloat162 b = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
-                  h[j] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                *reinterpret_cast<uint4*>(out + c + i) = make_uint4(h[0], h[1], h[2], h[3]);
-              }
+              const __nv_bfloat162 b = __floats2bfloat162_rn(u, v);
+              word[(h + i) / 2] = *reinterpret_cast<const uint32_t*>(&b);
             } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(out + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              word[i] = __float_as_uint(u);
+              word[i + 1] = __float_as_uint(v);
             }
-          } else if (in) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) out[c + i] = from_f<O>(v[i]);
           }
-        } else if (in) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n0 + c + i < p.n) {
-              v[i] *= as * __ldg(p.ws + n0 + c + i);
-              out[c + i] = from_f<O>(p.bias ? v[i] + __ldg(p.bias + n0 + c + i) : v[i]);
-            }
         }
-        __syncwarp();  // (the next load is the whole warp's)
+        write_rows<O>(buf, mine, static_cast<O*>(p.out), row0, n0 + c, p, lane);
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -505,70 +898,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads)
 }
 
 template <bool kFp8, typename O, int BN>
-cudaError_t launch_pairs_t(const MatmulArgs& p, const void* a, const void* w, uint64_t row_bytes, uint64_t stride,
-                           cudaStream_t s) {
+cudaError_t launch_pairs_t(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear) {
   CUtensorMap am, wm;
-  if (!encode_tmap_rows(&am, a, row_bytes, (uint64_t)p.m, stride, kRowsA) ||
-      !encode_tmap_rows(&wm, w, row_bytes, (uint64_t)p.n, stride, BN / 2))
+  if (!encode_tmap_rows(&am, ra.at, ra.bytes, (uint64_t)p.m, ra.pitch, kRowsA) ||
+      !encode_tmap_rows(&wm, rw.at, rw.bytes, (uint64_t)p.n, rw.pitch, BN / 2))
     return cudaErrorInvalidValue;
-  TcArgs t = {p.as, p.ws, p.bias, p.out, p.status, p.m, p.n, (int)((p.m + 255) / 256), (int)((p.n + BN - 1) / BN),
-              (int)((row_bytes + 127) / 128)};
+  PairArgs t = {p, (int)((p.m + 255) / 256), (int)((p.n + BN - 1) / BN), (int)((ra.bytes + 127) / 128), clear};
   const long long tiles = (long long)t.mt * t.nt;
   const int pairs = device_sm_count() / 2;
   const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
-  constexpr int smem = TcSmem<BN>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(pair_matmul_kernel<kFp8, O, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = PairSmem<BN>::kBytes;
+  auto kernel = pair_matmul_kernel<kFp8, O, BN>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   set_kernel_name("scaled_matmul_pairs");
-  pair_matmul_kernel<kFp8, O, BN><<<grid, kTcThreads, smem, s>>>(am, wm, t);
+  kernel<<<grid, kPairThreads, smem, s>>>(am, wm, t);
   return cudaGetLastError();
 }
 template <bool kFp8, typename O>
-cudaError_t launch_pairs(const MatmulArgs& p, const void* a, const void* w, uint64_t row_bytes, uint64_t stride,
-                         cudaStream_t s) {
+cudaError_t launch_pairs(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear) {
   const long long mt = (p.m + 255) / 256;
   const int pairs = device_sm_count() / 2;
-  if (mt * ((p.n + 255) / 256) >= pairs) return launch_pairs_t<kFp8, O, 256>(p, a, w, row_bytes, stride, s);
-  if (mt * ((p.n + 127) / 128) >= pairs) return launch_pairs_t<kFp8, O, 128>(p, a, w, row_bytes, stride, s);
-  return launch_pairs_t<kFp8, O, 64>(p, a, w, row_bytes, stride, s);
+  if (mt * ((p.n + 255) / 256) >= pairs) return launch_pairs_t<kFp8, O, 256>(p, ra, rw, s, clear);
+  return launch_pairs_t<kFp8, O, 128>(p, ra, rw, s, clear);
 }
 
 // ---- plan -------------------------------------------------------------------
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct MatmulPlan {
-  bool few, pack, half;   // which kernel; rows written out first; as fp16
-  long long pitch;        // bytes of a written row
+  bool few, some;
+  // which operand is written out first (as fp16), with what pitch, and where
+  bool out_a, out_w, half_a, half_w;
+  long long pitch_a, pitch_w;
   size_t off_a, off_w, bytes;
 };
 
-int check(const ssd_matmul_problem* pr, MatmulPlan* p) {
+int check(const ssd_matmul_problem* pr, MatmulPlan* pl) {
   if (!pr || pr->m < 1 || pr->n < 1 || pr->k < 1 || pr->flags != 0) return SSD_ERR_INVALID_ARGUMENT;
   if (pr->format != SSD_CACHE_INT8 && pr->format != SSD_CACHE_E4M3) return SSD_ERR_INVALID_ARGUMENT;
   if (pr->out_dtype != SSD_F32 && pr->out_dtype != SSD_BF16) return SSD_ERR_INVALID_ARGUMENT;
   // 2^40 elements per tensor; rows and tiles in 32 bits
   const int64_t cap = 1LL << 22;
-  if (pr->m > cap || pr->n > cap || pr->k > cap || (double)pr->m * (double)pr->n >= (double)(1LL << 40) ||
+  if (pr->m > cap || pr->n > cap || pr->k > (1LL << 20) || (double)pr->m * (double)pr->n >= (double)(1LL << 40) ||
       (double)pr->m * (double)pr->k >= (double)(1LL << 40) || (double)pr->n * (double)pr->k >= (double)(1LL << 40))
     return SSD_ERR_UNSUPPORTED;
-  p->few = pr->m <= kFewTokens;
-  p->half = !p->few && pr->format == SSD_CACHE_INT8;
-  p->pack = p->half || pr->k % 16 != 0;
-  p->pitch = p->half ? (pr->k + 63) / 64 * 128 : (pr->k + 15) / 16 * 16;
-  p->off_a = p->off_w = 256;
-  p->bytes = 256;
-  if (p->pack) {
-    p->off_w = 256 + align256((size_t)pr->m * p->pitch);
-    p->bytes = p->off_w + align256((size_t)pr->n * p->pitch);
-  }
+  const bool whole = pr->k % 16 == 0, int8 = pr->format == SSD_CACHE_INT8;
+  pl->few = pr->m <= kFewTokens;
+  pl->some = !pl->few && pr->m <= kSomeTokens;
+  pl->half_a = int8 && !pl->few;
+  pl->half_w = int8 && !pl->few && !pl->some;
+  pl->out_a = pl->half_a || !whole;
+  pl->out_w = pl->half_w || !whole;
+  const long long codes = (pr->k + 15) / 16 * 16;
+  pl->pitch_a = codes << pl->half_a;
+  pl->pitch_w = codes << pl->half_w;
+  pl->off_a = 256;
+  pl->off_w = 256 + (pl->out_a ? align256((size_t)pr->m * pl->pitch_a) : 0);
+  pl->bytes = pl->off_w + (pl->out_w ? align256((size_t)pr->n * pl->pitch_w) : 0);
   return SSD_OK;
 }
 bool misaligned16(const void* ptr) { return ptr && (reinterpret_cast<uintptr_t>(ptr) & 15u); }
 
 template <bool kFp8, typename O>
-cudaError_t launch_product(const MatmulPlan& pl, const MatmulArgs& p, const void* a, const void* w, cudaStream_t s) {
-  if (pl.few) return launch_skinny<kFp8, O>(p, s);
-  return launch_pairs<kFp8, O>(p, a, w, pl.half ? (uint64_t)pl.pitch : (uint64_t)p.k, pl.pack ? pl.pitch : p.k, s);
+cudaError_t launch_product(const MatmulPlan& pl, MatmulArgs p, const Rows& ra, const Rows& rw, cudaStream_t s) {
+  const bool clear = !pl.out_a && !pl.out_w;
+  if (pl.few) {
+    p.a = static_cast<const uint8_t*>(ra.at);
+    p.w = static_cast<const uint8_t*>(rw.at);
+    p.k = (long long)ra.pitch;  // (zeros behind the last code)
+    return launch_skinny<kFp8, O>(p, s);
+  }
+  if (pl.some) return launch_some<kFp8, O>(p, ra, rw, s, clear, pl.out_a && !pl.out_w);
+  return launch_pairs<kFp8, O>(p, ra, rw, s, clear);
 }
 
 }  // namespace
@@ -598,40 +1000,36 @@ int ssd_scaled_matmul(const ssd_matmul_problem* pr, const void* a, const float* 
   if (rc != SSD_OK) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  MatmulArgs p = {static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(w), a_scales, w_scales, bias, out,
-                  reinterpret_cast<int*>(ws), pr->m, pr->n, pr->k};
+  const MatmulArgs p = {static_cast<const uint8_t*>(a), static_cast<const uint8_t*>(w), a_scales, w_scales, bias, out,
+                        reinterpret_cast<int*>(ws), pr->m, pr->n, pr->k};
+  const Rows ra = {pl.out_a ? ws + pl.off_a : a, (uint64_t)pr->k << pl.half_a,
+                   (uint64_t)(pl.out_a ? pl.pitch_a : pr->k)},
+             rw = {pl.out_w ? ws + pl.off_w : w, (uint64_t)pr->k << pl.half_w,
+                   (uint64_t)(pl.out_w ? pl.pitch_w : pr->k)};
   cudaError_t e;
-  if (pl.pack) {
+  if (pl.out_a || pl.out_w) {
     PackArgs q;
     memset(&q, 0, sizeof(q));
-    q.src[0] = p.a; q.src[1] = p.w;
-    q.dst[0] = ws + pl.off_a; q.dst[1] = ws + pl.off_w;
     q.k = (int)pr->k;
-    q.per_row = (int)(pl.half ? pl.pitch / 32 : pl.pitch / 16);
-    q.groups[0] = pr->m * q.per_row; q.groups[1] = pr->n * q.per_row;
-    q.bytes[0] = pr->m * pr->k; q.bytes[1] = pr->n * pr->k;
     q.status = p.status;
-    long long grid = (q.groups[0] + q.groups[1] + 255) / 256;
+    const int per_row = (int)((pr->k + 15) / 16);
+    if (pl.out_a) q.part[0] = {p.a, ws + pl.off_a, pr->m * per_row, pr->m * pr->k, per_row, pl.half_a};
+    if (pl.out_w) q.part[1] = {p.w, ws + pl.off_w, pr->n * per_row, pr->n * pr->k, per_row, pl.half_w};
+    long long grid = (q.part[0].groups + q.part[1].groups + 255) / 256;
     const long long most = (long long)device_sm_count() * 16;
     if (grid > most) grid = most;
     set_kernel_name("scaled_matmul_pack");
     prof_before(s);
-    if (pl.half) pack_rows_kernel<true><<<(unsigned)grid, 256, 0, s>>>(q);
-    else pack_rows_kernel<false><<<(unsigned)grid, 256, 0, s>>>(q);
+    pack_rows_kernel<<<(unsigned)grid, 256, 0, s>>>(q);
     e = cudaGetLastError();
     prof_after(s);
     if (e != cudaSuccess) return SSD_ERR_CUDA;
-    p.a = ws + pl.off_a;
-    p.w = ws + pl.off_w;
-    if (!pl.half) p.k = pl.pitch;
-  } else if (!pl.few) {
-    if (cudaMemsetAsync(p.status, 0, sizeof(int), s) != cudaSuccess) return SSD_ERR_CUDA;
   }
   const bool fp8 = pr->format == SSD_CACHE_E4M3, b16 = pr->out_dtype == SSD_BF16;
   prof_before(s);
-  e = fp8 ? (b16 ? launch_product<true, __nv_bfloat16>(pl, p, p.a, p.w, s) : launch_product<true, float>(pl, p, p.a, p.w, s))
-          : (b16 ? launch_product<false, __nv_bfloat16>(pl, p, p.a, p.w, s)
-                 : launch_product<false, float>(pl, p, p.a, p.w, s));
+  e = fp8 ? (b16 ? launch_product<true, __nv_bfloat16>(pl, p, ra, rw, s) : launch_product<true, float>(pl, p, ra, rw, s))
+          : (b16 ? launch_product<false, __nv_bfloat16>(pl, p, ra, rw, s)
+                 : launch_product<false, float>(pl, p, ra, rw, s));
   prof_after(s);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }

@@ -9,15 +9,18 @@
 // Forward: one pass over the logits, bound by HBM where there are many rows.  A
 // CTA, or a cluster of up to eight where rows are few, takes a row; each thread
 // keeps the largest logit that it has met and the two sums relative to it, in
-// units of log 2, and they are joined in a fixed order.
+// units of log 2, and they are joined in a fixed order.  A CTA goes on to its
+// next row while the joins of the last one are under way: the first vectors of
+// that row are in flight by then.
 //
 // Alternatives.  The k-th largest of the maxima of 64 groups of threads is at
 // most the row's k-th largest logit: every alternative is at or above that
-// bound, so only threads whose maximum is have any.  Their words are read once
-// more (one vector to a lane), what reaches the bound is put on a list, and
-// counting who is ahead of whom sorts the list.  A list that overflows (many
-// equal logits) is replaced by k passes over the words that find the next
-// largest each.
+// bound.  Each thread also keeps the largest logit of every run of its vectors
+// in shared memory, so only the runs that reach the bound (about k of them) are
+// read once more, all at a time; what reaches the bound is put on a list, and
+// counting who is ahead of whom sorts the list.  A list that overflows
+// (many equal logits) is replaced by k passes over those words that find the
+// next largest each.
 #include <cooperative_groups.h>
 
 #include "ssd_internal.cuh"
@@ -32,11 +35,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBwdThreads = 256;
+constexpr int kAhead = 4;        // 16-byte vectors of a thread in flight
 constexpr int kGroups = 64;      // groups of threads whose maxima give the bound
 constexpr int kMaxTop = 32;      // alternatives
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;       // words that may reach the bound
+constexpr int kLong = 96;        // a list that is shortened first
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -101,37 +106,22 @@ struct Sums {
     s += o.s;
     t += o.t;
   }
+  // words of which none is above m; kNear: by_product(m c2)
+  template <bool kNear, int K>
+  __device__ __forceinline__ void add(const float (&x)[K], float mc, float c2) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const float d = floored(kNear ? fmaf(x[i], c2, -mc) : (x[i] - m) * c2), e = ex2(d);
+      s += e;
+      t = fmaf(e, d, t);
+    }
+  }
+  // nothing but excluded words so far: is one a NaN?
   template <int K>
-  __device__ __forceinline__ void meet(const float (&x)[K], float c2) {
-    float b = x[0];
+  __device__ __forceinline__ void add_none(const float (&x)[K]) {
 #pragma unroll
-    for (int i = 1; i < K; ++i) b = fmaxf(b, x[i]);
-    if (b > m) {
-      rebase(b, c2);
-      m = b;
-    }
-    if (m == kNegInf) {  // nothing but excluded words, or NaN
-#pragma unroll
-      for (int i = 0; i < K; ++i)
-        if (x[i] != x[i]) s = x[i];
-      return;
-    }
-    const float mc = __fmul_rn(m, c2);
-    if (by_product(mc)) {
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const float d = floored(fmaf(x[i], c2, -mc)), e = ex2(d);
-        s += e;
-        t = fmaf(e, d, t);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const float d = floored((x[i] - m) * c2), e = ex2(d);
-        s += e;
-        t = fmaf(e, d, t);
-      }
-    }
+    for (int i = 0; i < K; ++i)
+      if (x[i] != x[i]) s = x[i];
   }
 };
 
@@ -141,16 +131,64 @@ template <typename T>
 struct Row {
   static constexpr int n = 16 / sizeof(T);
   const T* base;      // the row's first word
-  const uint4* vec;   // the first whole vector
   unsigned V, head, nvec, tail;
   __device__ __forceinline__ Row(const void* p, long long row, long long stride, long long words) {
     base = static_cast<const T*>(p) + row * stride;
     V = (unsigned)words;
     const unsigned off = (unsigned)((reinterpret_cast<uintptr_t>(base) & 15u) / sizeof(T));
     head = min(off ? n - off : 0u, V);
-    vec = reinterpret_cast<const uint4*>(base + head);
     nvec = (V - head) / n;
     tail = V - head - nvec * n;
+  }
+  __device__ __forceinline__ Row() {}
+  // the first whole vector
+  __device__ __forceinline__ const uint4* vec() const { return reinterpret_cast<const uint4*>(base + head); }
+  // The largest word of some vectors (NaN passed over)
+  template <int K>
+  static __device__ __forceinline__ float largest(const uint4 (&u)[K]) {
+    if constexpr (sizeof(T) == 2) {
+      uint32_t b = u[0].x;
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm("max.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(w[j]));
+      }
+      return fmaxf(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    } else {
+      float b = kNegInf;
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        b = fmaxf(fmaxf(fmaxf(b, __uint_as_float(u[i].x)), fmaxf(__uint_as_float(u[i].y), __uint_as_float(u[i].z))),
+                  __uint_as_float(u[i].w));
+      return b;
+    }
+  }
+  template <int K>
+  static __device__ __forceinline__ float meet(Sums& sum, const uint4 (&u)[K], float c2) {
+    const float b = largest(u);
+    if (b > sum.m) {
+      sum.rebase(b, c2);
+      sum.m = b;
+    }
+    const float mc = __fmul_rn(sum.m, c2);
+    if (by_product(mc)) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        float x[n];
+        unpack(u[i], x);
+        sum.template add<true>(x, mc, c2);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; ++i) {
+        float x[n];
+        unpack(u[i], x);
+        if (sum.m == kNegInf) sum.add_none(x);
+        else sum.template add<false>(x, mc, c2);
+      }
+    }
+    return b;
   }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -176,199 +214,326 @@ __device__ __forceinline__ float key_logit(unsigned long long k) {
   return __uint_as_float(b ^ ((int)b < 0 ? 0x80000000u : 0xffffffffu));
 }
 
-struct TopShared {
-  float group[kGroups];
-  unsigned long long list[kList];
-  unsigned long long warp[kWarps];
-  int count;
+template <int kThreads>
+struct Shared {
+  static constexpr int kRuns = kThreads > 256 ? 8 : 16;  // runs of a thread's vectors
+  alignas(16) float group[kGroups];  // (read four at a time)
+  float warp[kThreads / 32][3];     // m, s, t of the warps
+  float all[3];                     // of the CTA
+  float cta[kMaxCluster][3];        // of the cluster's CTAs
+  unsigned long long best[kThreads / 32];
+  alignas(16) unsigned long long list[kList];
+  alignas(16) unsigned long long list2[kList];
+  alignas(16) unsigned long long part[kGroups];
+  unsigned long long near;
+  unsigned long long top[kMaxCluster * kMaxTop];
+  float run[kRuns][kThreads];       // the largest of each thread's runs
+  unsigned short owner[kRuns * kThreads];  // runs that have an alternative
+  float bound;
+  int owners, count;
 };
 
-// The words of thread `of` of this CTA, one vector to a lane at a time: f(logit, index)
-template <typename T, typename F>
-__device__ __forceinline__ void words_of(const Row<T>& r, unsigned lo, unsigned hi, bool first, int of, int lane, F f) {
-  constexpr int n = Row<T>::n;
-  for (unsigned v = lo + of + lane * kThreads; v < hi; v += 32 * kThreads) {
-    float x[n];
-    Row<T>::unpack(r.vec[v], x);
+// Sums of a warp's first `lanes` lanes (a power of two), in every one of them
+template <int lanes>
+__device__ __forceinline__ void join_lanes(Sums& sum, float c2) {
+  const unsigned b = __float_as_uint(sum.m);
+  const unsigned key = __reduce_max_sync(0xffffffffu, b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u));
+  const float m = __uint_as_float(key ^ ((int)key < 0 ? 0x80000000u : 0xffffffffu));
+  if (m > sum.m) sum.rebase(m, c2);
+  sum.m = m;
 #pragma unroll
-    for (int i = 0; i < n; ++i) f(x[i], r.head + v * n + i);
+  for (int o = lanes / 2; o; o >>= 1) {
+    sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
+    sum.t += __shfl_xor_sync(0xffffffffu, sum.t, o);
   }
-  if (first && of == 0 && (unsigned)lane < r.head) f(to_f(r.base[lane]), (unsigned)lane);
-  if (first && of == 1 && (unsigned)lane < r.tail) f(to_f(r.base[r.V - r.tail + lane]), r.V - r.tail + lane);
 }
 
-// This CTA's k largest words, in order, to `to` (0 where there is none)
-template <typename T>
-__device__ void cta_top(const Row<T>& r, unsigned lo, unsigned hi, bool first, float mine, int k, TopShared& sh,
-                        unsigned long long* to) {
-  const int lane = threadIdx.x & 31;
-  float g = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((threadIdx.x & 3) == 0) sh.group[threadIdx.x >> 2] = g;
-  if (threadIdx.x == 0) sh.count = 0;
-  if (threadIdx.x < kMaxTop) to[threadIdx.x] = 0;
-  __syncthreads();
-  // (every warp finds the bound for itself)
-  const float a = sh.group[lane], b = sh.group[lane + 32];
-  int ra = 0, rb = 0;
-#pragma unroll 16
-  for (int i = 0; i < kGroups; ++i) {
-    const float o = sh.group[i];
-    ra += o > a || (o == a && i < lane);
-    rb += o > b || (o == b && i < lane + 32);
-  }
-  const unsigned ha = __ballot_sync(0xffffffffu, ra == k - 1), hb = __ballot_sync(0xffffffffu, rb == k - 1);
-  const float bound = ha ? __shfl_sync(0xffffffffu, a, __ffs(ha) - 1) : __shfl_sync(0xffffffffu, b, __ffs(hb) - 1);
-  for (unsigned has = __ballot_sync(0xffffffffu, mine >= bound && mine > kNegInf); has; has &= has - 1)
-    words_of(r, lo, hi, first, (int)(threadIdx.x & ~31u) + __ffs(has) - 1, lane, [&](float x, unsigned v) {
-      if (x >= bound && x > kNegInf) {
-        const int at = atomicAdd(&sh.count, 1);  // (the list's order does not matter)
-        if (at < kList) sh.list[at] = word_key(x, v);
-      }
-    });
-  __syncthreads();
-  const int count = sh.count;
-  if (count <= kList) {
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-      const unsigned long long key = sh.list[i];
-      int rank = 0;
-      for (int j = 0; j < count; ++j) rank += sh.list[j] > key;
-      if (rank < k) to[rank] = key;
-    }
-  } else {
-    unsigned long long last = ~0ull;
-    for (int i = 0; i < k && last; ++i) {
-      unsigned long long best = 0;
-      for (int of = (int)(threadIdx.x & ~31u), end = of + 32; of < end; ++of)
-        words_of(r, lo, hi, first, of, lane, [&](float x, unsigned v) {
-          if (x >= bound && x > kNegInf) {
-            const unsigned long long key = word_key(x, v);
-            if (key < last && key > best) best = key;
-          }
-        });
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-        best = other > best ? other : best;
-      }
-      if (lane == 0) sh.warp[threadIdx.x >> 5] = best;
-      __syncthreads();
-      best = 0;
-      for (int w = 0; w < kWarps; ++w) best = sh.warp[w] > best ? sh.warp[w] : best;
-      if (threadIdx.x == 0) to[i] = best;
-      last = best;
-      __syncthreads();
-    }
-  }
-  __syncthreads();
-}
+// CTAs to an SM: 80 registers to a thread (with 64 what is kept across a row is
+// spilled: 4096 rows of 32,000 bf16 words 62 us instead of 51)
+constexpr int resident(int threads) { return threads > 256 ? 1 : 768 / threads; }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) token_logprobs_kernel(LogpArgs a) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_kernel(LogpArgs a) {
+  constexpr int n = Row<T>::n, kWarps = kThreads / 32, kTile = kAhead * kThreads, kRuns = Shared<kThreads>::kRuns;
   cg::cluster_group cluster = cg::this_cluster();
+  const unsigned ncta = cluster.num_blocks(), rank = cluster.block_rank();
   // Another CTA's shared memory may be written only once that CTA is known to
   // have started: each says so here, and the wait comes before the first such write.
-  cluster.barrier_arrive();
-  const unsigned ncta = cluster.num_blocks(), rank = cluster.block_rank();
-  const long long row = blockIdx.x / ncta;
-  __shared__ TopShared sh;
-  __shared__ float warp_sums[kWarps][3], cta_sums[kMaxCluster][3];
-  __shared__ unsigned long long mine[kMaxTop], all[kMaxCluster * kMaxTop];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int n = Row<T>::n, kAhead = 4;
-  const Row<T> r(a.logits, row, a.stride, a.V);
+  if (ncta > 1) cluster.barrier_arrive();
+  __shared__ Shared<kThreads> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool first = rank == 0;
-  const int tok = a.tokens ? a.tokens[row] : -1;
-  const bool known = tok >= 0 && tok < a.V;
-  float tok_x = 0.f;
-  if (first && known) tok_x = to_f(r.base[tok]);
-  const unsigned per = (r.nvec + ncta - 1) / ncta, lo = min(rank * per, r.nvec), hi = min(lo + per, r.nvec);
-  Sums sum;
-  float top = kNegInf;
-  auto tile = [&](unsigned v0, auto whole) {
-    uint4 u[kAhead];
-    const uint4* at = r.vec + v0 + threadIdx.x;
+  const long long step = gridDim.x / ncta;
+  unsigned lo = 0, hi = 0;
+  auto take = [&](long long row) {
+    const Row<T> r(a.logits, row, a.stride, a.V);
+    const unsigned per = (r.nvec + ncta - 1) / ncta;
+    lo = min(rank * per, r.nvec);
+    hi = min(lo + per, r.nvec);
+    return r;
+  };
+  uint4 u[kAhead];
+  auto fetch = [&](const Row<T>& r, unsigned v0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (decltype(whole)::value || v0 + threadIdx.x + i * kThreads < hi) {
-        u[i] = __ldg(at + i * kThreads);
-      } else {  // nothing there: excluded words
-        const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-        u[i] = make_uint4(none, none, none, none);
+      // nothing there: excluded words
+      constexpr uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+      u[i] = make_uint4(none, none, none, none);
+      if (v0 + i * kThreads + tid < hi) u[i] = __ldg(r.vec() + v0 + i * kThreads + tid);
+    }
+  };
+  Row<T> r = take(blockIdx.x / ncta);
+  fetch(r, lo);
+  for (long long row = blockIdx.x / ncta; row < a.rows; row += step) {
+    const int tok = a.tokens ? a.tokens[row] : -1;
+    const bool known = tok >= 0 && tok < a.V;
+    float tok_x = 0.f;
+    if (known) tok_x = to_f(r.base[tok]);
+    const Row<T> now = r;
+    const unsigned from = lo, to = hi;
+    Sums sum;
+    unsigned shift = 0;  // tiles to a run: 1 << shift
+    while ((to - from) > ((unsigned)(kRuns * kTile) << shift)) ++shift;
+    float run = kNegInf;
+    unsigned tile = 0;
+#pragma unroll 1
+    for (unsigned v0 = from; v0 < to; v0 += kTile, ++tile) {
+      uint4 w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) w[i] = u[i];
+      if (v0 + kTile < to) fetch(now, v0 + kTile);
+      const float b = Row<T>::meet(sum, w, a.c2);
+      if (a.ntop) {
+        run = (tile & ((1u << shift) - 1)) == 0 ? b : fmaxf(run, b);
+        sh.run[tile >> shift][tid] = run;
       }
     }
-    float x[kAhead * n];
+    const unsigned runs = (tile + (1u << shift) - 1) >> shift;
+    if (row + step < a.rows) {
+      r = take(row + step);
+      fetch(r, lo);
+    }
+    if (first && tid < 2) {  // the words before and behind the whole vectors
+      const unsigned cnt = tid == 0 ? now.head : now.tail, at = tid == 0 ? 0 : now.V - now.tail;
+      float x[n], b = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) Row<T>::unpack(u[i], x + i * n);
-    sum.meet(x, a.c2);
-  };
-  constexpr unsigned kTile = kAhead * kThreads;
-  unsigned v0 = lo;
-  for (; v0 < hi && hi - v0 >= kTile; v0 += kTile) tile(v0, std::true_type());
-  if (v0 < hi) tile(v0, std::false_type());
-  if (first && threadIdx.x < 2) {
-    const unsigned cnt = threadIdx.x == 0 ? r.head : r.tail, from = threadIdx.x == 0 ? 0 : r.V - r.tail;
-    float x[n];
+      for (int i = 0; i < n; ++i) {
+        x[i] = (unsigned)i < cnt ? to_f(now.base[at + i]) : kNegInf;
+        b = fmaxf(b, x[i]);
+      }
+      if (b > sum.m) {
+        sum.rebase(b, a.c2);
+        sum.m = b;
+      }
+      const float mc = __fmul_rn(sum.m, a.c2);
+      if (sum.m == kNegInf) sum.add_none(x);
+      else if (by_product(mc)) sum.template add<true>(x, mc, a.c2);
+      else sum.template add<false>(x, mc, a.c2);
+    }
+    const float top = sum.m;
+    if (a.ntop) {
+      float g = top;
 #pragma unroll
-    for (int i = 0; i < n; ++i) x[i] = (unsigned)i < cnt ? to_f(r.base[from + i]) : kNegInf;
-    sum.meet(x, a.c2);
-  }
-  top = sum.m;
+      for (int o = 1; o < kThreads / kGroups; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+      if (tid % (kThreads / kGroups) == 0) sh.group[tid / (kThreads / kGroups)] = g;
+      if (tid == 0) sh.owners = sh.count = 0;
+    }
+    join_lanes<32>(sum, a.c2);
+    if (lane == 0) {
+      sh.warp[warp][0] = sum.m;
+      sh.warp[warp][1] = sum.s;
+      sh.warp[warp][2] = sum.t;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      Sums c;
+      if (lane < kWarps) {
+        c.m = sh.warp[lane][0];
+        c.s = sh.warp[lane][1];
+        c.t = sh.warp[lane][2];
+      }
+      join_lanes<kWarps>(c, a.c2);
+      if (lane == 0) {
+        sh.all[0] = c.m;
+        sh.all[1] = c.s;
+        sh.all[2] = c.t;
+      }
+    } else if (warp == 1 && a.ntop) {
+      // the ntop-th largest of the groups' maxima
+      const float x = sh.group[lane], y = sh.group[lane + 32];
+      int rx = 0, ry = 0;
+#pragma unroll 4
+      for (int i = 0; i < kGroups; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(&sh.group[i]);
+        const float v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
-    sum.join(__shfl_down_sync(0xffffffffu, sum.m, o), __shfl_down_sync(0xffffffffu, sum.s, o),
-             __shfl_down_sync(0xffffffffu, sum.t, o), a.c2);
-  if (lane == 0) {
-    warp_sums[warp][0] = sum.m;
-    warp_sums[warp][1] = sum.s;
-    warp_sums[warp][2] = sum.t;
-  }
-  if (a.ntop) cta_top<T>(r, lo, hi, first, top, a.ntop, sh, mine);
-  else __syncthreads();
-  cluster.barrier_wait();
-  if (threadIdx.x == 0) {
+        for (int j = 0; j < 4; ++j) {
+          rx += v[j] > x || (v[j] == x && i + j < lane);
+          ry += v[j] > y || (v[j] == y && i + j < lane + 32);
+        }
+      }
+      if (rx == a.ntop - 1) sh.bound = x;
+      if (ry == a.ntop - 1) sh.bound = y;
+    }
+    __syncthreads();
+    if (a.ntop) {
+      const float bound = sh.bound;
+      auto in = [&](float x) { return x >= bound && x > kNegInf; };
+      if (in(top))
+        for (unsigned i = 0; i < runs; ++i)  // (their order does not matter)
+          if (in(sh.run[i][tid])) sh.owner[atomicAdd(&sh.owners, 1)] = (unsigned short)(i * kThreads + tid);
+      __syncthreads();
+      const unsigned all = (unsigned)sh.owners * kAhead << shift;
+      // every word of those runs: f(logit, index)
+      auto scan = [&](auto f) {
+        constexpr int kScan = 2;
+#pragma unroll 1
+        for (unsigned i0 = tid; i0 < all; i0 += kScan * kThreads) {
+          uint4 w[kScan];
+          unsigned at[kScan];
+#pragma unroll
+          for (int i = 0; i < kScan; ++i) {
+            const unsigned j = i0 + i * kThreads;
+            at[i] = to;
+            if (j < all) {
+              const unsigned o = sh.owner[j / kAhead >> shift], in_run = j & ((kAhead << shift) - 1);
+              at[i] = from + (((o / kThreads) << shift) * kAhead + in_run) * kThreads + o % kThreads;
+            }
+            if (at[i] < to) w[i] = __ldg(now.vec() + at[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kScan; ++i) {
+            if (at[i] >= to) continue;
+            float x[n];
+            Row<T>::unpack(w[i], x);
+#pragma unroll
+            for (int j = 0; j < n; ++j) f(x[j], now.head + at[i] * n + j);
+          }
+        }
+        if (first && (unsigned)tid < now.head) f(to_f(now.base[tid]), (unsigned)tid);
+        if (first && (unsigned)tid < now.tail) f(to_f(now.base[now.V - now.tail + tid]), now.V - now.tail + tid);
+      };
+      scan([&](float x, unsigned v) {
+        if (in(x)) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kList) sh.list[at] = word_key(x, v);
+        }
+      });
+      if (tid < a.ntop) sh.top[tid] = 0;
+      __syncthreads();
+      int count = sh.count;
+      if (count <= kList) {
+        const unsigned long long* list = sh.list;
+        if (count > kLong) {
+          // a nearer bound: the ntop-th largest of the maxima of 64 parts of the list
+          for (int g = tid; g < kGroups; g += kThreads) {
+            unsigned long long best = 0;
+            for (int i = g; i < count; i += kGroups) best = sh.list[i] > best ? sh.list[i] : best;
+            sh.part[g] = best;
+          }
+          if (tid == 0) sh.count = 0;
+          __syncthreads();
+          for (int g = tid; g < kGroups; g += kThreads) {
+            const unsigned long long key = sh.part[g];
+            int ahead = 0;
+#pragma unroll 8
+            for (int j = 0; j < kGroups; j += 2) {
+              const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&sh.part[j]);
+              ahead += (o.x > key) + (o.y > key);
+            }
+            if (ahead == a.ntop - 1) sh.near = key;  // (the keys are all different)
+          }
+          __syncthreads();
+          const unsigned long long near = sh.near;
+          for (int i = tid; i < count; i += kThreads)
+            if (sh.list[i] >= near) sh.list2[atomicAdd(&sh.count, 1)] = sh.list[i];
+          __syncthreads();
+          count = sh.count;
+          list = sh.list2;
+        }
+        if (tid == 0 && (count & 1)) const_cast<unsigned long long*>(list)[count] = 0;  // (they are compared in pairs)
+        __syncthreads();
+        for (int i = tid; i < count; i += kThreads) {
+          const unsigned long long key = list[i];
+          int ahead = 0;
+#pragma unroll 4
+          for (int j = 0; j < count; j += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&list[j]);
+            ahead += (o.x > key) + (o.y > key);
+          }
+          if (ahead < a.ntop) sh.top[ahead] = key;
+        }
+      } else {
+        unsigned long long last = ~0ull;
+        for (int i = 0; i < a.ntop && last; ++i) {
+          unsigned long long best = 0;
+          scan([&](float x, unsigned v) {
+            if (in(x)) {
+              const unsigned long long key = word_key(x, v);
+              if (key < last && key > best) best = key;
+            }
+          });
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+            const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
+            best = other > best ? other : best;
+          }
+          if (lane == 0) sh.best[warp] = best;
+          __syncthreads();
+          best = 0;
+          for (int w = 0; w < kWarps; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+          if (tid == 0) sh.top[i] = best;
+          last = best;
+          __syncthreads();
+        }
+      }
+      __syncthreads();
+    }
     Sums c;
-    for (int w = 0; w < kWarps; ++w) c.join(warp_sums[w][0], warp_sums[w][1], warp_sums[w][2], a.c2);
-    float* to = cluster.map_shared_rank(&cta_sums[rank][0], 0);
-    to[0] = c.m;
-    to[1] = c.s;
-    to[2] = c.t;
-  }
-  if ((int)threadIdx.x < a.ntop) *cluster.map_shared_rank(&all[rank * a.ntop + threadIdx.x], 0) = mine[threadIdx.x];
-  cluster.sync();
-  if (!first) return;
-  Sums c;
-  for (unsigned w = 0; w < ncta; ++w) c.join(cta_sums[w][0], cta_sums[w][1], cta_sums[w][2], a.c2);
-  const bool nothing = c.m == kNegInf && c.s == 0.f;  // every word is excluded
-  const float ln_s = logf(c.s) - off_of(c.m, a.c2) * kLn2;  // ln sum e^(z - m)
-  if (threadIdx.x == 0) {
-    if (a.lse) a.lse[row] = nothing ? kNegInf : fmaf(c.m, a.scale, ln_s);
-    if (a.entropy) a.entropy[row] = nothing ? 0.f : logf(c.s) - kLn2 * (c.t / c.s);
-    if (a.logprobs) a.logprobs[row] = !known ? 0.f : nothing ? kNegInf : (tok_x - c.m) * a.scale - ln_s;
-  }
-  const int have = (int)ncta * a.ntop;
-  for (int i = threadIdx.x; i < have; i += kThreads) {
-    const unsigned long long key = all[i];
-    int at = 0;
+    c.m = sh.all[0];
+    c.s = sh.all[1];
+    c.t = sh.all[2];
     if (ncta > 1) {
-      for (int j = 0; j < have; ++j) at += all[j] > key || (all[j] == key && j < i);
-    } else {
-      at = i;
+      cluster.barrier_wait();
+      if (tid < 3) *cluster.map_shared_rank(&sh.cta[rank][tid], 0) = sh.all[tid];
+      if (!first && tid < a.ntop) *cluster.map_shared_rank(&sh.top[rank * a.ntop + tid], 0) = sh.top[tid];
+      cluster.sync();
+      if (!first) return;
+      c.m = kNegInf;
+      c.s = c.t = 0.f;
+      for (unsigned w = 0; w < ncta; ++w) c.join(sh.cta[w][0], sh.cta[w][1], sh.cta[w][2], a.c2);
     }
-    if (at < a.ntop) {
-      const long long o = row * a.ntop + at;
-      a.top_tok[o] = key ? (int)(0xffffffffu - (unsigned)key) : -1;
-      a.top_lp[o] = key ? (key_logit(key) - c.m) * a.scale - ln_s : kNegInf;
+    const bool nothing = c.m == kNegInf && c.s == 0.f;  // every word is excluded
+    const float ln_s = logf(c.s) - off_of(c.m, a.c2) * kLn2;  // ln sum e^(z - m)
+    if (tid == 0) {
+      if (a.lse) a.lse[row] = nothing ? kNegInf : fmaf(c.m, a.scale, ln_s);
+      if (a.entropy) a.entropy[row] = nothing ? 0.f : logf(c.s) - kLn2 * (c.t / c.s);
+      if (a.logprobs) a.logprobs[row] = !known ? 0.f : nothing ? kNegInf : (tok_x - c.m) * a.scale - ln_s;
     }
+    const int have = (int)ncta * a.ntop;
+    for (int i = tid; i < have; i += kThreads) {
+      const unsigned long long key = sh.top[i];
+      int at = i;
+      if (ncta > 1) {
+        at = 0;
+        for (int j = 0; j < have; ++j) at += sh.top[j] > key || (sh.top[j] == key && j < i);
+      }
+      if (at < a.ntop) {
+        const long long o = row * a.ntop + at;
+        a.top_tok[o] = key ? (int)(0xffffffffu - (unsigned)key) : -1;
+        a.top_lp[o] = key ? (key_logit(key) - c.m) * a.scale - ln_s : kNegInf;
+      }
+    }
+    __syncthreads();  // the next row writes over what this one has read
   }
 }
 
 // One CTA to a row's run of vectors.  kSame: the gradient's rows lie in their
 // vectors as the logits' do.
 template <typename T, bool kSame>
-__global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(LogpArgs a, unsigned per) {
+__global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(LogpArgs a, unsigned per) {
   const long long row = blockIdx.x;
-  constexpr int n = Row<T>::n, kAhead = 4;
+  constexpr int n = Row<T>::n;
   const Row<T> r(a.logits, row, a.stride, a.V);
   T* out = static_cast<T*>(a.dlogits) + row * a.gstride;
   const float lse = a.lse_in[row], H = a.ent_in ? a.ent_in[row] : 0.f;
@@ -390,14 +555,14 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(LogpArgs a
   }
   for (unsigned b = blockIdx.y * per; b < r.nvec; b += gridDim.y * per) {
     const unsigned hi = min(b + per, r.nvec);
-    for (unsigned v0 = b + threadIdx.x; v0 < hi; v0 += kAhead * kThreads) {
+    for (unsigned v0 = b + threadIdx.x; v0 < hi; v0 += kAhead * kBwdThreads) {
       uint4 u[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (v0 + i * kThreads < hi) u[i] = r.vec[v0 + i * kThreads];
+        if (v0 + i * kBwdThreads < hi) u[i] = r.vec()[v0 + i * kBwdThreads];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const unsigned v = v0 + i * kThreads;
+        const unsigned v = v0 + i * kBwdThreads;
         if (v >= hi) break;
         float x[n];
         Row<T>::unpack(u[i], x);
@@ -423,15 +588,11 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_bwd_kernel(LogpArgs a
   }
 }
 
-template <typename T>
-cudaError_t launch_fwd(const LogpArgs& a, cudaStream_t s) {
-  // CTAs to a row: more, in powers of two up to the portable cluster size, while all of them are resident at once and
-  // each has more than 2048 words.
-  const int sms = device_sm_count();
-  int ncta = 1;
-  while (ncta < kMaxCluster && (long long)ncta * 2048 < a.V && a.rows * ncta * 2 <= 4 * sms) ncta *= 2;
+template <typename T, int kThreads>
+cudaError_t launch_fwd_t(const LogpArgs& a, int ncta, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.rows * ncta));
+  const long long most = (long long)device_sm_count() * resident(kThreads);
+  cfg.gridDim = dim3((unsigned)(ncta > 1 ? a.rows * ncta : a.rows < most ? a.rows : most));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -440,16 +601,30 @@ cudaError_t launch_fwd(const LogpArgs& a, cudaStream_t s) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ncta > 1 ? 1 : 0;
   set_kernel_name("token_logprobs");
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kThreads>, a);
+}
+template <typename T>
+cudaError_t launch_fwd(const LogpArgs& a, cudaStream_t s) {
+  // CTAs to a row: more, in powers of two up to the portable cluster size, while each has an SM of its own and more than
+  // 2048 words; they are wide, for the shortest way through the row.
+  const int sms = device_sm_count();
+  int ncta = 1;
+  while (ncta < kMaxCluster && (long long)ncta * 2048 < a.V && a.rows * ncta * 2 <= sms) ncta *= 2;
+  if (ncta > 1) return launch_fwd_t<T, 512>(a, ncta, s);
+  // Else narrow ones, whose joins leave the SM to others (4096 rows of 32,000 bf16 words: 51 us with 128 threads, 62 with
+  // 256, 56 with 64), the narrowest for rows of up to 8 vectors to each of their threads (rows of 300 with 20
+  // alternatives: 25 us with 64 threads, 40 with 128).
+  if (a.V * (long long)sizeof(T) <= 64 * 8 * 16) return launch_fwd_t<T, 64>(a, 1, s);
+  return launch_fwd_t<T, 128>(a, 1, s);
 }
 
 template <typename T>
 cudaError_t launch_bwd(const LogpArgs& a, cudaStream_t s) {
   // runs of 4 tiles where there are rows enough, else of one
   const long long vecs = (a.V * (long long)sizeof(T) + 15) / 16;
-  const unsigned per = 4 * kThreads * (a.rows >= 4 * device_sm_count() ? 4 : 1);
+  const unsigned per = 4 * kBwdThreads * (a.rows >= 4 * device_sm_count() ? 4 : 1);
   long long runs = (vecs + per - 1) / per;
   if (runs < 1) runs = 1;
   if (runs > 65535) runs = 65535;
@@ -457,8 +632,8 @@ cudaError_t launch_bwd(const LogpArgs& a, cudaStream_t s) {
                     ((a.stride - a.gstride) * (long long)sizeof(T)) % 16 == 0;
   const dim3 grid((unsigned)a.rows, (unsigned)runs);
   set_kernel_name("token_logprobs_bwd");
-  if (same) token_logprobs_bwd_kernel<T, true><<<grid, kThreads, 0, s>>>(a, per);
-  else token_logprobs_bwd_kernel<T, false><<<grid, kThreads, 0, s>>>(a, per);
+  if (same) token_logprobs_bwd_kernel<T, true><<<grid, kBwdThreads, 0, s>>>(a, per);
+  else token_logprobs_bwd_kernel<T, false><<<grid, kBwdThreads, 0, s>>>(a, per);
   return cudaGetLastError();
 }
 

@@ -469,9 +469,6 @@ class AddNormDevice:
                                         check=check)
 
 
-_matmul_problem = functools.lru_cache(maxsize=256)(_lib.make_matmul_problem)
-
-
 class Linear8:
     """A linear map whose weights are 8-bit codes (n, k), int8 or e4m3, with a
     scale for each output channel; it takes tokens in the same codes with a
@@ -489,6 +486,9 @@ class Linear8:
         _dense(bias, (n,), torch.float32, "bias", codes.device)
         self.codes, self.scales, self.bias, self.out_dtype = codes, scales, bias, out_dtype
         self.format = StateCache.FORMATS["int8" if codes.dtype is torch.int8 else "e4m3"]
+        self._plans = {}
+        # the status word of calls that need no more (calls that overlap share it)
+        self._status = self.workspace = torch.zeros(256, dtype=torch.uint8, device=codes.device)
 
     @classmethod
     def from_weight(cls, weight, form="int8", bias=None, out_dtype=torch.bfloat16):
@@ -510,25 +510,49 @@ class Linear8:
         """out (m, n) of the tokens' codes (m, k) and scales (m); a new tensor
         unless given (``stream``'s: another stream waits for it before it reads
         it)."""
+        plan = self._plans.get(codes.shape) or self._plan(codes.shape)
+        prob, ws, scales_shape, out_shape = plan
+        dev, index = self.codes.device, self.codes.get_device()
+        if index != torch.cuda.current_device():
+            _on_gpu(dev, "Linear8")
+        # (single tokens: these comparisons are the cheap ones)
+        if codes.dtype is not self.codes.dtype or codes.get_device() != index or not codes.is_contiguous():
+            _dense(codes, codes.shape, self.codes.dtype, "codes", dev)
+        if (scales.dtype is not torch.float32 or scales.get_device() != index or scales.shape != scales_shape
+                or not scales.is_contiguous()):
+            _dense(scales, scales_shape, torch.float32, "scales", dev)
+        if out is None:
+            if stream is None:
+                out = torch.empty(out_shape, dtype=self.out_dtype, device=dev)
+            else:
+                with _allocating_on(stream):
+                    out = torch.empty(out_shape, dtype=self.out_dtype, device=dev)
+        else:
+            _dense(out, out_shape, self.out_dtype, "out", dev)
+        work = self._status
+        if ws:
+            with _allocating_on(stream):
+                work = torch.empty(ws, dtype=torch.uint8, device=dev)
+        _lib.ssd_scaled_matmul(prob, codes, scales, self.codes, self.scales, self.bias, out, work,
+                               ws or 256, stream=stream, check=check)
+        self.workspace = work
+        return out
+
+    def _plan(self, shape):
+        """The problem of tokens (m, k), the bytes of its workspace where it needs
+        more than the status word, and its tensors' shapes; kept for shapes that
+        come again."""
         n, k = self.codes.shape
-        if codes.dim() != 2 or codes.shape[1] != k:
+        if len(shape) != 2 or shape[1] != k:
             raise ValueError(f"codes: expected (m, {k})")
-        m, dev = codes.shape[0], self.codes.device
-        _on_gpu(dev, "Linear8")
-        _dense(codes, (m, k), self.codes.dtype, "codes", dev)
-        _dense(scales, (m,), torch.float32, "scales", dev)
-        _dense(out, (m, n), self.out_dtype, "out", dev)
-        prob = _matmul_problem(m, n, k, self.format, self.out_dtype)
+        prob = _lib.make_matmul_problem(shape[0], n, k, self.format, self.out_dtype)
         ws = _lib.ssd_scaled_matmul_workspace_bytes(prob)
         if ws == 0:
             raise _lib.SSDError(_lib.SSD_ERR_INVALID_ARGUMENT, "matmul problem")
-        with _allocating_on(stream):
-            if out is None:
-                out = torch.empty((m, n), dtype=self.out_dtype, device=dev)
-            self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
-        _lib.ssd_scaled_matmul(prob, codes, scales, self.codes, self.scales, self.bias, out,
-                               self.workspace, ws, stream=stream, check=check)
-        return out
+        if len(self._plans) >= 256:
+            self._plans.clear()
+        self._plans[shape] = plan = (prob, ws if ws > 256 else 0, torch.Size(shape[:1]), (shape[0], n))
+        return plan
 
     def device_status(self, stream=None):
         """Synchronises; the status word of the last call."""
