@@ -8,17 +8,18 @@
 // exactly; sums are fp32.  e4m3 codes go to the tensor cores as they are.
 //
 // Three kernels, by the number of tokens:
-//  * up to 16: bound by the weights' bytes.  Warps read 16 channels' codes in
+//  * up to 16 or 24: bound by the weights' bytes.  Warps read 16 channels' codes in
 //    16-byte pieces, turn them into fp16 in registers and multiply them with
 //    the tokens' by warp-level products; the order of k inside a product is
 //    free, so a lane's 16 neighbouring codes serve four products as they lie.
-//  * up to 256: the channels are the rows of tensor-memory products with all
-//    tokens.  int8 weights stay int8 up to shared memory; warps turn them into
-//    fp16 on their way to tensor memory, from where the products take them.
+//  * some hundreds: tensor-memory products of 128 tokens x up to 256 channels, k
+//    shared by the CTAs of a cluster.  An instruction with 128 rows takes about 136
+//    cycles whether it has 32 columns or 256, so the weights are the columns.  int8
+//    codes stay int8 up to shared memory; warps turn them into fp16 there.
 //  * more: products of 256 tokens x up to 256 channels by pairs of CTAs,
 //    persistent, the epilogue of one tile under the products of the next.
-// A launch before them writes out what they cannot read as it is: int8 tokens (and
-// with many tokens the weights) as fp16, rows that are not whole 16-byte vectors.
+// A launch before them writes out what they cannot read as it is: int8 codes as
+// fp16 for the last one, rows that are not whole 16-byte vectors for all.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -33,7 +34,7 @@ int device_check();
 
 namespace {
 
-constexpr int kFewTokens = 16, kSomeTokens = 256;
+constexpr int kFewTokens[2] = {24, 16};  // of int8, e4m3 (10304 x 4096, 24 int8 tokens: 15 us, by the next kernel 18)
 
 struct MatmulArgs {
   const uint8_t *a, *w;
@@ -111,6 +112,7 @@ __device__ __forceinline__ uint4 load16(const uint8_t* base, long long at, int c
 }
 
 __global__ void __launch_bounds__(256) pack_rows_kernel(PackArgs p) {
+  // (the pairs' launch may come up; it waits for this one's end before it reads)
   asm volatile("griddepcontrol.launch_dependents;");
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   const long long total = p.part[0].groups + p.part[1].groups;
@@ -147,7 +149,7 @@ constexpr int kSkWarps = 8;
 // CT: tiles of 16 channels to a CTA; MT: groups of 8 tokens.  The warps split k,
 // 64 codes at a time; k is a multiple of 16.
 template <bool kFp8, typename O, int CT, int MT>
-__global__ void __launch_bounds__(kSkWarps * 32, MT == 1 ? 5 : 4) skinny_kernel(MatmulArgs p) {
+__global__ void __launch_bounds__(kSkWarps * 32, MT == 1 ? 5 : MT == 2 ? 4 : 2) skinny_kernel(MatmulArgs p) {
   constexpr int kCh = CT * 16, kTok = MT * 8, kPitch = kCh + 1;
   extern __shared__ float part[];  // [warp][token][channel]
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -239,7 +241,8 @@ cudaError_t launch_skinny_t(const MatmulArgs& p, cudaStream_t s) {
 template <bool kFp8, typename O>
 cudaError_t launch_skinny(const MatmulArgs& p, cudaStream_t s) {
   if (p.m <= 8) return launch_skinny_t<kFp8, O, 1, 1>(p, s);
-  return launch_skinny_t<kFp8, O, 1, 2>(p, s);
+  if (p.m <= 16) return launch_skinny_t<kFp8, O, 1, 2>(p, s);
+  return launch_skinny_t<kFp8, O, 2, 3>(p, s);
 }
 
 template <bool kFp8, int kPair>
@@ -298,35 +301,37 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
 }
 
 // ---- some tokens ------------------------------------------------------------
-// A CTA multiplies up to 128 channels (the products' rows) with up to NT tokens
-// over its share of k, 128 codes to a stage.  int8: four warps, a lane to a
-// channel, turn a stage's codes into fp16, into one of the operand's places in
-// tensor memory, four others the next stage's; shared memory then carries the
-// weights once, as int8, and the tokens as fp16.  e4m3: both
-// operands are taken from shared memory as they are.  The CTAs of a cluster
-// share k; they leave their sums in shared memory and each joins and writes some
-// of the tokens, in the order of the shares.
-constexpr int kTurners = 8;                                // warps that turn codes into fp16, and write results
-constexpr int kSomeThreads = kTurners * 32 + 64;           // and one that copies, one for the products
+// A CTA multiplies 128 tokens' rows with up to 256 channels over its share of k,
+// 128 codes to a stage.  e4m3: the products take both from the stage.  int8: two
+// groups of eight warps turn the weights into fp16, each 64 codes of every stage,
+// in a place of its own, so that one group writes under the other's products (one
+// group for both places: 2100 cycles a stage); four warps turn the tokens, a lane
+// to a row, and put them into tensor memory.  The CTAs of a cluster share k; they leave their sums in shared memory
+// and each joins and writes some of the tokens, in the order of the shares.
+constexpr int kRows = 128;                                  // tokens of a CTA
+constexpr int kWide = 256;                                  // channels of a CTA, at most
+constexpr int kGroup = 8, kTurners = 2 * kGroup, kTokTurners = 4;
+constexpr int kSomeThreads = (kTurners + kTokTurners + 2) * 32;
 
-template <bool kFp8, int NT>
+template <bool kFp8>
 struct SomeShape {
-  static constexpr int kTok = (kFp8 ? 1 : 2) * NT * 128;   // bytes of a stage's tokens
-  static constexpr int kStageBytes = 128 * 128 + kTok;
-  static constexpr int kStages = 196608 / kStageBytes < 8 ? 196608 / kStageBytes : 8;
-  static constexpr int kBytes = kStages * kStageBytes + 1024;
-  static constexpr int kPlaces = kFp8 ? 0 : 4;             // of the operand in tensor memory, 64 columns each
-  static constexpr uint32_t kCols = NT + 64 * kPlaces <= 64 ? 64 : NT + 64 * kPlaces <= 128 ? 128 : NT + 64 * kPlaces <= 256 ? 256 : 512;
-  static_assert(NT * 128 * 4 <= kStages * kStageBytes, "the sums fit into the stages");
+  static constexpr int kW = kWide * 128, kA = kRows * 128, kStageBytes = kW + kA;
+  static constexpr int kStages = kFp8 ? 4 : 3;
+  static constexpr int kTurned = kFp8 ? 0 : 2 * kWide * 128;  // two places of 64 codes as fp16
+  static constexpr int kBytes = kStages * kStageBytes + kTurned + 1024;
+  static constexpr int kPlaces = 4;                           // of the tokens in tensor memory, 64 columns each
+  static constexpr uint32_t kCols = kFp8 ? kWide : kWide + 64 * kPlaces;
+  static_assert(kRows * kWide * 4 <= kStages * kStageBytes, "the sums fit into the stages");
 };
 
 struct SomeArgs {
   MatmulArgs p;
-  int ch, kb, per;  // channels of a CTA (a multiple of 8); stages of k in all; of a CTA
+  int ch, kb, per;  // channels of a CTA (a multiple of 16); stages of k in all; of a CTA
+  int nt;           // tiles of channels
   int clear;        // no launch before this one has cleared the status word
 };
 
-// 16 codes of a lane's row at a time to 8 columns of tensor memory
+// 32 columns of a lane's row of tensor memory
 __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
@@ -338,9 +343,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// The launch before this one has ended and what it wrote is there (nothing, where
-// this one did not start early)
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // D (+)= A B^T with A in tensor memory: lane i is row i, a column two neighbouring k
 __device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -356,26 +358,54 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ uint4 shared_load(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+  return u;
+}
+__device__ __forceinline__ void shared_store(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// A place in a ring, and the parity of the round that it is in
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      ph ^= 1;
+    }
+  }
+};
 
-template <bool kFp8, typename O, int NT>
+template <bool kFp8, typename O>
 __global__ void __launch_bounds__(kSomeThreads)
     some_tokens_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap, SomeArgs s) {
-  using S = SomeShape<kFp8, NT>;
-  constexpr int kStages = S::kStages, kPlaces = S::kPlaces ? S::kPlaces : 1;
+  using S = SomeShape<kFp8>;
+  constexpr int kStages = S::kStages, kPlaces = S::kPlaces;
   extern __shared__ uint8_t raw[];
   const MatmulArgs& p = s.p;
   const uint32_t pad = (1024u - (tc::smem_u32(raw) & 1023u)) & 1023u, smem = tc::smem_u32(raw) + pad;
-  __shared__ uint64_t full[kStages], empty[kStages], turned[kPlaces], taken[kPlaces], done;
+  const uint32_t wbuf = smem + kStages * S::kStageBytes;
+  __shared__ uint64_t full[kStages], empty[kStages], wfull[2], wempty[2], turned[kPlaces], taken[kPlaces], done;
   __shared__ uint32_t tmem_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cta_rank();
   uint32_t ncta;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
-  const int quarters = (s.ch + 31) / 32;  // lane quarters that hold channels
+  const int tile = (int)(blockIdx.x / ncta);
+  const long long n0 = (long long)(tile % s.nt) * s.ch;
+  const int m0 = tile / s.nt * kRows, rows = (int)min(p.m - m0, (long long)kRows);
+  const int quarters = (rows + 31) / 32;  // lane quarters that hold tokens
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], kFp8 ? 1 : kTurners + quarters);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&wfull[i], kGroup);
+      tc::mbar_init(&wempty[i], 1);
     }
     for (int i = 0; i < kPlaces; ++i) {
       tc::mbar_init(&turned[i], quarters);
@@ -385,148 +415,143 @@ __global__ void __launch_bounds__(kSomeThreads)
     tc::mbar_fence_init();
     if (s.clear && blockIdx.x == 0) *p.status = 0;  // (a wait that expires does so a second later)
   }
-  if (warp == kTurners + 1 && lane == 0) {
+  constexpr int kMmaWarp = kTurners + kTokTurners, kCopyWarp = kMmaWarp + 1;
+  if (warp == kCopyWarp && lane == 0) {
     tc::prefetch_tmap(&amap);
     tc::prefetch_tmap(&wmap);
   }
-  if (warp == kTurners) tc::tmem_alloc(&tmem_s, S::kCols);
+  if (warp == kMmaWarp) tc::tmem_alloc(&tmem_s, S::kCols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_s;
-  const long long n0 = (long long)(blockIdx.x / ncta) * s.ch;
   const int b0 = (int)rank * s.per, nb = min(s.per, s.kb - b0);
   bool ok = true;
 
-  if (warp == kTurners + 1) {
+  if (warp == kCopyWarp) {
     if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      for (int b = 0; b < nb; ++b) {
-        tc::mbar_wait_flag(&empty[st], ph ^ 1, ok);
-        const uint32_t to = smem + st * S::kStageBytes;
-        tc::mbar_expect_tx(&full[st], s.ch * 128 + S::kTok);
-        box_load(to, &wmap, &full[st], (b0 + b) * 128, (int)n0);
-        if (b == 0) grid_wait();  // the tokens, written out by the launch before
-        if constexpr (kFp8) {
-          box_load(to + 128 * 128, &amap, &full[st], (b0 + b) * 128, 0);
-        } else {
-          box_load(to + 128 * 128, &amap, &full[st], (b0 + b) * 256, 0);
-          box_load(to + 128 * 128 + NT * 128, &amap, &full[st], (b0 + b) * 256 + 128, 0);
-        }
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1;
-        }
+      Ring<kStages> st;
+      for (int b = 0; b < nb; ++b, st.next()) {
+        tc::mbar_wait_flag(&empty[st.at], st.ph ^ 1, ok);
+        const uint32_t to = smem + st.at * S::kStageBytes;
+        tc::mbar_expect_tx(&full[st.at], s.ch * 128 + S::kA);
+        box_load(to, &wmap, &full[st.at], (b0 + b) * 128, (int)n0);
+        box_load(to + S::kW, &amap, &full[st.at], (b0 + b) * 128, m0);
       }
     }
-  } else if (warp == kTurners) {
+  } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      int st = 0, pl = 0;
-      uint32_t ph = 0, pph = 0;
+      const uint32_t idesc = idesc_of(kRows, s.ch);
+      Ring<kStages> st;
+      Ring<kPlaces> pl;
       for (int b = 0; b < nb; ++b) {
-        tc::mbar_wait_flag(&full[st], ph, ok);
-        const uint32_t w = smem + st * S::kStageBytes, a = w + 128 * 128;
         if constexpr (kFp8) {
+          tc::mbar_wait_flag(&full[st.at], st.ph, ok);
           tc::tc_fence_after();
+          const uint32_t w = smem + st.at * S::kStageBytes, a = w + S::kW;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            block_mma<true, false>(tmem, tc::smem_desc(w + j * 32, 16, 1024, tc::kSwz128),
-                                   tc::smem_desc(a + j * 32, 16, 1024, tc::kSwz128), idesc_of(128, NT), b | j);
+            block_mma<true, false>(tmem, tc::smem_desc(a + j * 32, 16, 1024, tc::kSwz128),
+                                   tc::smem_desc(w + j * 32, 16, 1024, tc::kSwz128), idesc, b | j);
+          tc::mma_commit(&empty[st.at]);
+          st.next();
         } else {
-          tc::mbar_wait_flag(&turned[pl], pph, ok);
-          tc::tc_fence_after();
+          tc::mbar_wait_flag(&turned[pl.at], pl.ph, ok);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            mma_from_tmem(tmem, tmem + NT + pl * 64 + j * 8,
-                          tc::smem_desc(a + (j >> 2) * NT * 128 + (j & 3) * 32, 16, 1024, tc::kSwz128),
-                          idesc_of(128, NT), b | j);
-          tc::mma_commit(&taken[pl]);
-          if (++pl == kPlaces) {
-            pl = 0;
-            pph ^= 1;
+          for (int h = 0; h < 2; ++h) {
+            tc::mbar_wait_flag(&wfull[h], (uint32_t)b & 1u, ok);
+            tc::tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_from_tmem(tmem, tmem + kWide + pl.at * 64 + h * 32 + j * 8,
+                            tc::smem_desc(wbuf + h * (kWide * 128) + j * 32, 16, 1024, tc::kSwz128), idesc, b | h | j);
+            tc::mma_commit(&wempty[h]);
           }
-        }
-        tc::mma_commit(&empty[st]);
-        if (++st == kStages) {
-          st = 0;
-          ph ^= 1;
+          tc::mma_commit(&taken[pl.at]);
+          pl.next();
         }
       }
       tc::mma_commit(&done);
     }
-  } else if (!kFp8 && (warp & 3) < quarters) {
-    const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane;
-    uint4 u[8];
-    // a stage's codes of this lane's channel, and the stage after the next
-    int st = half % kStages;
-    uint32_t ph = 0;
-    auto read = [&]() {
-      tc::mbar_wait_flag(&full[st], ph, ok);
-      const uint32_t row = smem + st * S::kStageBytes + r * 128;
+  } else if (!kFp8 && warp < kTurners) {
+    // A unit is 16 codes of a channel, 32 bytes as fp16.  Eight lanes read the
+    // units of rows x and x ^ 5, so that neither their reads nor their writes meet in
+    // a bank.
+    const int unit = lane & 3, g = lane >> 2, x = (g >> 1) ^ (g & 1 ? 5 : 0);
+    const int half = warp / kGroup, row0 = (warp % kGroup) * 8 + x;
+    const uint32_t from = row0 * 128, read0 = from + (((half * 4 + unit) ^ x) << 4);
+    const uint32_t put0 = wbuf + half * (kWide * 128) + from + ((2 * unit ^ x) << 4),
+                   put1 = wbuf + half * (kWide * 128) + from + (((2 * unit + 1) ^ x) << 4);
+    const int units = (s.ch - row0 + 63) / 64;  // rows row0, row0 + 64, ... of this tile (at most four)
+    Ring<kStages> st;
+    for (int b = 0; b < nb; ++b, st.next()) {
+      tc::mbar_wait_flag(&full[st.at], st.ph, ok);
+      uint32_t v[4][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u[j].x), "=r"(u[j].y), "=r"(u[j].z), "=r"(u[j].w)
-                     : "r"(row + ((j ^ (r & 7)) << 4))
-                     : "memory");
-      st += 2;
-      if (st >= kStages) {
-        st -= kStages;
-        ph ^= 1;
+      for (int i = 0; i < 4; ++i)
+        if (i < units) to_half<false>(shared_load(smem + st.at * S::kStageBytes + read0 + i * 64 * 128), v[i]);
+      tc::mbar_wait_flag(&wempty[half], (uint32_t)(b & 1) ^ 1u, ok);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < units) {
+          shared_store(put0 + i * 64 * 128, v[i][0], v[i][1], v[i][2], v[i][3]);
+          shared_store(put1 + i * 64 * 128, v[i][4], v[i][5], v[i][6], v[i][7]);
+        }
+      tc::fence_async_smem();  // written here, read by the products; the stage: read here, written by a copy
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&wfull[half]);
+        tc::mbar_arrive(&empty[st.at]);
       }
-    };
-    if (half < nb) read();
-    const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + NT;
-    for (int b = half; b < nb; b += 2) {
+    }
+  } else if (!kFp8 && warp - kTurners < quarters) {
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    Ring<kStages> st;
+    Ring<kPlaces> pl;
+    for (int b = 0; b < nb; ++b) {
+      tc::mbar_wait_flag(&full[st.at], st.ph, ok);
+      const uint32_t row = smem + st.at * S::kStageBytes + S::kW + r * 128;
       uint32_t h[2][32];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint32_t x[8];
-        to_half<false>(u[j], x);
+        uint32_t v[8];
+        to_half<false>(shared_load(row + ((j ^ (r & 7)) << 4)), v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[j >> 2][(j & 3) * 8 + i] = x[i];
+        for (int i = 0; i < 8; ++i) h[j >> 2][(j & 3) * 8 + i] = v[i];
       }
-      tc::fence_async_smem();  // (read here, written by the next copy)
-      // (with two stages the next but one waits for this one's product)
-      if (kStages > 2 && b + 2 < nb) read();
-      const int pl = b % kPlaces;
-      tc::mbar_wait_flag(&taken[pl], (uint32_t)(b / kPlaces & 1) ^ 1u, ok);
+      tc::fence_async_smem();  // read here, written by a copy
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[st.at]);
+      tc::mbar_wait_flag(&taken[pl.at], pl.ph ^ 1, ok);
       tc::tc_fence_after();
       __syncwarp();
-      tmem_store32(to + pl * 64, h[0]);
-      tmem_store32(to + pl * 64 + 32, h[1]);
+      const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + kWide + pl.at * 64;
+      tmem_store32(to, h[0]);
+      tmem_store32(to + 32, h[1]);
       tmem_store_wait();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&turned[pl]);
-      if (kStages == 2 && b + 2 < nb) read();
+      if (lane == 0) tc::mbar_arrive(&turned[pl.at]);
+      st.next();
+      pl.next();
     }
   }
   __syncwarp();
-  const int share = ((int)p.m + (int)ncta - 1) / (int)ncta, lo = (int)rank * share, hi = min(lo + share, (int)p.m);
-  const int ch = lane * 4;
-  const long long n = n0 + ch;
-  const int cols = (int)min(min(p.n - n, (long long)(s.ch - ch)), 4LL);  // of this lane; may be negative
-  float ws[4], bias[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ws[i] = i < cols ? __ldg(p.ws + n + i) : 0.f;
-    bias[i] = i < cols && p.bias ? __ldg(p.bias + n + i) : 0.f;
-  }
-  // every product is done: the stages become the sums, [token][channel]
+  // Every product is done: the stages become the sums, a row of kWide fp32 to a
+  // token, whose 16-byte pieces are swapped by the row, so that neither a column's
+  // writes nor a row's reads meet in a bank.
   tc::mbar_wait_flag(&done, 0, ok);
   tc::tc_fence_after();
   __syncwarp();
-  float* sums = reinterpret_cast<float*>(raw + pad);
-  if (warp < kTurners && (warp & 3) < quarters) {
-    const int quarter = warp & 3, half = warp >> 2;
-#pragma unroll 2
-    for (int c = half * (NT / 2); c < (half + 1) * (NT / 2) && c < p.m; c += 16) {
+  if (warp < kMmaWarp && (warp & 3) < quarters) {
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    for (int c = (warp >> 2) * 16; c < s.ch; c += (kMmaWarp / 4) * 16) {
       float v[16];
       tc::tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + c, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sums[(c + i) * 128 + quarter * 32 + lane] = v[i];
+      for (int i = 0; i < 4; ++i)
+        shared_store(smem + r * (kWide * 4) + (((c / 4 + i) ^ (r & 7)) << 4), __float_as_uint(v[4 * i]),
+                     __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
     }
   }
   tc::tc_fence_before();
@@ -534,41 +559,45 @@ __global__ void __launch_bounds__(kSomeThreads)
   if (ncta > 1) cluster_sync_all();
   else __syncthreads();
   tc::tc_fence_after();
-  if (warp == kTurners) {
-    tc::tmem_dealloc(tmem, S::kCols);
-  } else if (warp < kTurners) {
-    for (int t = lo + warp; t < hi; t += kTurners) {
-      const float as = __ldg(p.as + t);
-      const uint32_t at = tc::smem_u32(sums + t * 128 + ch);
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (uint32_t r = 0; r < ncta; ++r) {
-        float x[4];
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
-                     : "r"(at_rank(at, r))
-                     : "memory");
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, S::kCols);
+  const int share = (rows + (int)ncta - 1) / (int)ncta, lo = (int)rank * share, hi = min(lo + share, rows);
+  const int pieces = s.ch / 4;
+  for (int i = lo * pieces + (int)threadIdx.x; i < hi * pieces; i += kSomeThreads) {
+    const int t = i / pieces, c = i - t * pieces;
+    const long long n = n0 + c * 4;
+    if (n >= p.n) continue;
+    const int cols = (int)min(p.n - n, 4LL);
+    const uint32_t at = smem + t * (kWide * 4) + ((c ^ (t & 7)) << 4);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t r = 0; r < ncta; ++r) {
+      float x[4];
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                   : "r"(at_rank(at, r))
+                   : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += x[i];
-      }
-      O* out = static_cast<O*>(p.out) + t * p.n + n;
+      for (int j = 0; j < 4; ++j) v[j] += x[j];
+    }
+    const float as = __ldg(p.as + m0 + t);
+    O* out = static_cast<O*>(p.out) + (m0 + t) * p.n + n;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = v[i] * as * ws[i];
-        if (p.bias) v[i] += bias[i];
+    for (int j = 0; j < 4; ++j)
+      if (j < cols) {
+        v[j] = v[j] * as * __ldg(p.ws + n + j);
+        if (p.bias) v[j] += __ldg(p.bias + n + j);
       }
-      if (p.n % 4 == 0 && cols >= 4) {
-        if constexpr (sizeof(O) == 2) {
-          const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
-          *reinterpret_cast<uint2*>(out) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-        } else {
-          *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+    if (p.n % 4 == 0) {  // (then there are four)
+      if constexpr (sizeof(O) == 2) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < cols) out[i] = from_f<O>(v[i]);
+        *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < cols) out[j] = from_f<O>(v[j]);
     }
   }
   if (!ok) atomicOr(p.status, kDevTimeout);
@@ -576,23 +605,34 @@ __global__ void __launch_bounds__(kSomeThreads)
   if (ncta > 1) cluster_sync_all();  // other CTAs read this one's sums until here
 }
 
-// How the products' rows and k are shared out: k over as many CTAs of a cluster as
-// 128 channels to a CTA leave SMs free for (each with four stages at least), then
-// the channels evenly over the CTAs of as few waves as they need.
-void share_out(const MatmulArgs& p, int sms, SomeArgs* a, int* split, int* tiles) {
-  a->kb = (int)((p.k + 127) / 128);
-  const long long wide = (p.n + 127) / 128;
-  int x = (int)(sms / wide);
-  if (x > 8) x = 8;
-  if (x > a->kb / 4) x = a->kb / 4;
-  if (x < 1) x = 1;
-  a->per = (a->kb + x - 1) / x;
-  x = (a->kb + a->per - 1) / a->per;  // every share has a stage
-  const long long room = sms / x, waves = (wide + room - 1) / room;
-  a->ch = (int)((p.n + room * waves - 1) / (room * waves));
-  a->ch = (a->ch + 7) / 8 * 8;
-  *split = x;
-  *tiles = (int)((p.n + a->ch - 1) / a->ch);
+// Clusters of 1 .. 8 CTAs that this chip holds at once, one CTA to an SM (they only
+// decide how the work is shared out).
+constexpr int kClusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+
+// Channels to a CTA and CTAs to a cluster: what costs least by the cycles of a
+// stage (measured: about 1500 and one for each channel with int8, 800 with e4m3),
+// the stages of a share, the waves of clusters, and what a CTA takes beside its
+// stages.  Few channels make no stage shorter, so they are as many as leave no
+// wave more.  Returns the cycles.
+double share_out(bool fp8, int64_t m, int64_t n, int64_t k, SomeArgs* a, int* split) {
+  a->kb = (int)((k + 127) / 128);
+  const long long mt = (m + kRows - 1) / kRows, wide = (n + kWide - 1) / kWide;
+  double best = 0;
+  for (int x = 1; x <= 8 && x <= a->kb; ++x) {
+    const int per = (a->kb + x - 1) / x;
+    if ((long long)per * (x - 1) >= a->kb) continue;  // a share without a stage
+    const long long waves = (wide * mt + kClusters[x] - 1) / kClusters[x], tiles = waves * kClusters[x] / mt;
+    const int ch = (int)((n + tiles - 1) / tiles + 15) / 16 * 16;
+    const double cost = (double)waves * (1.15 * (per * ((fp8 ? 800.0 : 1500.0) + ch) + 7000 + (x > 1 ? 2000 : 0)));
+    if (best == 0 || cost < best) {
+      best = cost;
+      a->ch = ch < 32 ? 32 : ch;
+      a->per = per;
+      *split = x;
+    }
+  }
+  a->nt = (int)((n + a->ch - 1) / a->ch);
+  return best;
 }
 
 // a, w: rows as the copies read them, of bytes in all and in memory
@@ -601,45 +641,36 @@ struct Rows {
   uint64_t bytes, pitch;
 };
 
-template <bool kFp8, typename O, int NT>
-cudaError_t launch_some_t(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear, bool early) {
-  using S = SomeShape<kFp8, NT>;
+template <bool kFp8, typename O>
+cudaError_t launch_some(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear) {
+  auto kernel = some_tokens_kernel<kFp8, O>;
+  constexpr int smem = SomeShape<kFp8>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   SomeArgs a;
+  memset(&a, 0, sizeof(a));
   a.p = p;
   a.clear = clear;
-  int split, tiles;
-  share_out(p, device_sm_count(), &a, &split, &tiles);
+  int split = 1;
+  share_out(kFp8, p.m, p.n, p.k, &a, &split);
   CUtensorMap am, wm;
-  if (!encode_tmap_rows(&am, ra.at, ra.bytes, (uint64_t)p.m, ra.pitch, NT) ||
+  if (!encode_tmap_rows(&am, ra.at, ra.bytes, (uint64_t)p.m, ra.pitch, kRows) ||
       !encode_tmap_rows(&wm, rw.at, rw.bytes, (uint64_t)p.n, rw.pitch, (uint32_t)a.ch))
     return cudaErrorInvalidValue;
-  auto kernel = some_tokens_kernel<kFp8, O, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.gridDim = dim3((unsigned)(a.nt * ((p.m + kRows - 1) / kRows) * split));
   cfg.blockDim = dim3(kSomeThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = split;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
-  // Behind the launch that writes out the tokens this one starts early: the weights' first stages are under way by then.
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = early ? 2 : 1;
+  cfg.numAttrs = 1;
   set_kernel_name("scaled_matmul_some");
   return cudaLaunchKernelEx(&cfg, kernel, am, wm, a);
-}
-template <bool kFp8, typename O>
-cudaError_t launch_some(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear, bool early) {
-  if (p.m <= 32) return launch_some_t<kFp8, O, 32>(p, ra, rw, s, clear, early);
-  if (p.m <= 64) return launch_some_t<kFp8, O, 64>(p, ra, rw, s, clear, early);
-  if (p.m <= 128) return launch_some_t<kFp8, O, 128>(p, ra, rw, s, clear, early);
-  return launch_some_t<kFp8, O, 256>(p, ra, rw, s, clear, early);
 }
 
 // ---- many tokens: tensor-memory products by pairs of CTAs -------------------
@@ -649,7 +680,7 @@ cudaError_t launch_some(const MatmulArgs& p, const Rows& ra, const Rows& rw, cud
 // own tensor memory, twice.  The leader (even rank) issues the products for
 // both; its `full` barriers take the bytes of both CTAs' copies.  Commits arrive in both CTAs.
 constexpr int kStages = 6;
-constexpr int kRowsA = 128;
+constexpr int kRowsA = 128;  // tokens of one of its CTAs
 
 template <int BN>
 struct PairSmem {
@@ -784,6 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     if (lane == 0) {
       tc::prefetch_tmap(&amap);
       tc::prefetch_tmap(&wmap);
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // what the launch before this one has written is there
       int st = 0;
       uint32_t ph = 0;
       for (long long t = pair; t < tiles; t += pairs) {
@@ -912,15 +944,37 @@ cudaError_t launch_pairs_t(const MatmulArgs& p, const Rows& ra, const Rows& rw, 
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   set_kernel_name("scaled_matmul_pairs");
-  kernel<<<grid, kPairThreads, smem, s>>>(am, wm, t);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  // Behind the launch that writes out the rows this one comes up early, and waits for it before its first copy.
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = clear ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, am, wm, t);
 }
+// Waves of tiles of the pairs' products with tiles of bn channels, and whether
+// narrow tiles take no wave more: their products take as long as the wide ones',
+// but their ends are shorter.
+long long pair_waves(int64_t m, int64_t n, int bn) { return ((m + 255) / 256 * ((n + bn - 1) / bn) + 75) / 76; }
+bool narrow_pairs(int64_t m, int64_t n) { return pair_waves(m, n, 128) <= pair_waves(m, n, 256); }
+
 template <bool kFp8, typename O>
 cudaError_t launch_pairs(const MatmulArgs& p, const Rows& ra, const Rows& rw, cudaStream_t s, bool clear) {
-  const long long mt = (p.m + 255) / 256;
-  const int pairs = device_sm_count() / 2;
-  if (mt * ((p.n + 255) / 256) >= pairs) return launch_pairs_t<kFp8, O, 256>(p, ra, rw, s, clear);
-  return launch_pairs_t<kFp8, O, 128>(p, ra, rw, s, clear);
+  if (narrow_pairs(p.m, p.n)) return launch_pairs_t<kFp8, O, 128>(p, ra, rw, s, clear);
+  return launch_pairs_t<kFp8, O, 256>(p, ra, rw, s, clear);
+}
+
+// The cycles of the products by pairs: waves of tiles by the stages of 128 bytes
+// (four products of about 175 cycles), what writing int8 codes out as fp16 takes at
+// 2600 bytes a cycle, and a tile's beginning and end.
+double pairs_cost(bool fp8, int64_t m, int64_t n, int64_t k) {
+  return (double)pair_waves(m, n, 256) * (double)((k * (fp8 ? 1 : 2) + 127) / 128) * 700 + 12000 +
+         (fp8 ? 0 : (double)(m + n) * (double)k * 3 / 2600);
 }
 
 // ---- plan -------------------------------------------------------------------
@@ -944,10 +998,12 @@ int check(const ssd_matmul_problem* pr, MatmulPlan* pl) {
       (double)pr->m * (double)pr->k >= (double)(1LL << 40) || (double)pr->n * (double)pr->k >= (double)(1LL << 40))
     return SSD_ERR_UNSUPPORTED;
   const bool whole = pr->k % 16 == 0, int8 = pr->format == SSD_CACHE_INT8;
-  pl->few = pr->m <= kFewTokens;
-  pl->some = !pl->few && pr->m <= kSomeTokens;
-  pl->half_a = int8 && !pl->few;
-  pl->half_w = int8 && !pl->few && !pl->some;
+  pl->few = pr->m <= kFewTokens[!int8];
+  SomeArgs share;
+  int split;
+  pl->some = !pl->few &&
+             share_out(!int8, pr->m, pr->n, pr->k, &share, &split) <= pairs_cost(!int8, pr->m, pr->n, pr->k);
+  pl->half_a = pl->half_w = int8 && !pl->few && !pl->some;
   pl->out_a = pl->half_a || !whole;
   pl->out_w = pl->half_w || !whole;
   const long long codes = (pr->k + 15) / 16 * 16;
@@ -969,7 +1025,7 @@ cudaError_t launch_product(const MatmulPlan& pl, MatmulArgs p, const Rows& ra, c
     p.k = (long long)ra.pitch;  // (zeros behind the last code)
     return launch_skinny<kFp8, O>(p, s);
   }
-  if (pl.some) return launch_some<kFp8, O>(p, ra, rw, s, clear, pl.out_a && !pl.out_w);
+  if (pl.some) return launch_some<kFp8, O>(p, ra, rw, s, clear);
   return launch_pairs<kFp8, O>(p, ra, rw, s, clear);
 }
 
