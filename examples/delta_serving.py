@@ -13,6 +13,12 @@ cheaper readout.  What the library does:
   drafted     DeltaStepDevice   outputs of the drafted tokens, states left alone
   verified    verify_draft      which of them the target keeps, and the token after
   advanced    DeltaStepDevice   the states moved on by the kept tokens only
+
+and, for what was generated, the readout in 8 bits:
+
+  scored      AddNormDevice     the outputs as int8 codes of their normed rows
+              Linear8           against the embeddings in int8: the logits
+              LogProbsDevice    the next tokens' log probabilities, entropies, alternatives
 """
 import argparse
 import os
@@ -100,6 +106,24 @@ def generate(layer, prompt, batch, new, draft, seed=1):
     return out, pool.states, kept
 
 
+def score(layer, tokens, top=3):
+    """The log probability of each token of a sequence (L,) after those before it,
+    with the entropies and the top alternatives (L - 1 rows): the model's readout
+    with outputs and embeddings in 8 bits."""
+    pre = runner.DeltaDevice(*layer.inputs(tokens[None, :-1]))
+    pre.fwd()
+    h = (pre.y[0].float().flatten(1) @ layer.wo).bfloat16()
+    eps = 1e-5
+    norm = runner.AddNormDevice(h, torch.ones(h.shape[1], device=h.device), eps=eps, form="int8")
+    norm.fwd()
+    # this readout takes its input as it is: the rows' sizes go back into their scales
+    size = (h.float().square().mean(-1) + eps).sqrt()
+    readout = runner.Linear8.from_weight(layer.embed, out_dtype=torch.float32)
+    answer = runner.LogProbsDevice(readout(norm.codes, norm.scales * size), tokens[1:].clone(), ntop=top)
+    answer.fwd()
+    return answer
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--batch", type=int, default=8)
@@ -114,7 +138,9 @@ def main():
     total = sum(len(o) for o in out)
     print(f"{total} tokens in {a.batch} sequences, {kept} of them drafted and kept")
     for i, o in enumerate(out[:4]):
-        print(f"  sequence {i}: {o[:12]} ...")
+        got = score(layer, torch.cat((prompt, torch.tensor(o, device="cuda", dtype=torch.int32))))
+        print(f"  sequence {i}: {o[:12]} ... mean log probability {got.logprobs[-len(o):].mean():.2f}, "
+              f"entropy {got.entropy[-len(o):].mean():.2f}")
 
 
 if __name__ == "__main__":

@@ -328,6 +328,7 @@ struct SomeArgs {
   MatmulArgs p;
   int ch, kb, per;  // channels of a CTA (a multiple of 16); stages of k in all; of a CTA
   int nt;           // tiles of channels
+  int box;          // rows of a tile's tokens that are copied (a multiple of 8)
   int clear;        // no launch before this one has cleared the status word
 };
 
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(kSomeThreads)
       for (int b = 0; b < nb; ++b, st.next()) {
         tc::mbar_wait_flag(&empty[st.at], st.ph ^ 1, ok);
         const uint32_t to = smem + st.at * S::kStageBytes;
-        tc::mbar_expect_tx(&full[st.at], s.ch * 128 + S::kA);
+        tc::mbar_expect_tx(&full[st.at], (s.ch + s.box) * 128);
         box_load(to, &wmap, &full[st.at], (b0 + b) * 128, (int)n0);
         box_load(to + S::kW, &amap, &full[st.at], (b0 + b) * 128, m0);
       }
@@ -653,8 +654,10 @@ cudaError_t launch_some(const MatmulArgs& p, const Rows& ra, const Rows& rw, cud
   a.clear = clear;
   int split = 1;
   share_out(kFp8, p.m, p.n, p.k, &a, &split);
+  // (the rows behind the tokens' last are whatever shared memory holds: their sums are not written)
+  a.box = p.m < kRows ? (int)(p.m + 7) / 8 * 8 : kRows;
   CUtensorMap am, wm;
-  if (!encode_tmap_rows(&am, ra.at, ra.bytes, (uint64_t)p.m, ra.pitch, kRows) ||
+  if (!encode_tmap_rows(&am, ra.at, ra.bytes, (uint64_t)p.m, ra.pitch, (uint32_t)a.box) ||
       !encode_tmap_rows(&wm, rw.at, rw.bytes, (uint64_t)p.n, rw.pitch, (uint32_t)a.ch))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};

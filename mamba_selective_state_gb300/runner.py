@@ -4,6 +4,7 @@ C ABI.  Allocation and argument marshalling only; the layer runs in libssd.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import functools
 
 import torch
@@ -388,6 +389,22 @@ class StateCache:
                                          out, stream=stream, check=check)
 
 
+def _here(device, what, stream):
+    """The stream's handle for a call of a single token's size, after _on_gpu's
+    check of the tensors' device."""
+    if torch.cuda.current_device() != device.index:
+        _on_gpu(device, what)
+    if stream is None and _lib._raw_stream is not None:
+        return _lib._raw_stream(device.index)
+    return _lib._stream(stream)
+
+
+def _raise(rc, check, what):
+    if check and rc != _lib.SSD_OK:
+        raise _lib.SSDError(rc, what)
+    return rc
+
+
 # torch's types of the 8-bit codes
 CODE_TYPES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 
@@ -435,6 +452,7 @@ class AddNormDevice:
         self.x, self.weight, self.residual, self.dout, self.dh = x, weight, residual, dout, dh
         self.prob = _lib.make_add_norm_problem(rows, dim, eps, x.dtype, rt, self.FORMATS[form],
                                                residual is not None, stride)
+        self._ref = ctypes.byref(self.prob)
         ws = _lib.ssd_add_rmsnorm_bwd_workspace_bytes(self.prob)
         if ws == 0:
             raise _lib.SSDError(_lib.SSD_ERR_INVALID_ARGUMENT, "add_norm problem")
@@ -454,10 +472,12 @@ class AddNormDevice:
             self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
 
     def fwd(self, stream=None, check=True):
-        _on_gpu(self.x.device, "AddNormDevice")
-        return _lib.ssd_add_rmsnorm_fwd(self.prob, self.x, self.residual, self.weight, self._h,
-                                        self.codes if self.out is None else self.out, self.scales,
-                                        stream=stream, check=check)
+        handle = _here(self.x.device, "AddNormDevice", stream)
+        out, p = self.codes if self.out is None else self.out, _lib._p
+        rc = _lib.LIB.ssd_add_rmsnorm_fwd(self._ref, self.x.data_ptr(), p(self.residual),
+                                          self.weight.data_ptr(), p(self._h), out.data_ptr(),
+                                          p(self.scales), handle)
+        return _raise(rc, check, "ssd_add_rmsnorm_fwd")
 
     def bwd(self, stream=None, check=True):
         if self.dout is None:
@@ -513,8 +533,7 @@ class Linear8:
         plan = self._plans.get(codes.shape) or self._plan(codes.shape)
         prob, ws, scales_shape, out_shape = plan
         dev, index = self.codes.device, self.codes.get_device()
-        if index != torch.cuda.current_device():
-            _on_gpu(dev, "Linear8")
+        handle = _here(dev, "Linear8", stream)
         # (single tokens: these comparisons are the cheap ones)
         if codes.dtype is not self.codes.dtype or codes.get_device() != index or not codes.is_contiguous():
             _dense(codes, codes.shape, self.codes.dtype, "codes", dev)
@@ -533,9 +552,12 @@ class Linear8:
         if ws:
             with _allocating_on(stream):
                 work = torch.empty(ws, dtype=torch.uint8, device=dev)
-        _lib.ssd_scaled_matmul(prob, codes, scales, self.codes, self.scales, self.bias, out, work,
-                               ws or 256, stream=stream, check=check)
+        rc = _lib.LIB.ssd_scaled_matmul(ctypes.byref(prob), codes.data_ptr(), scales.data_ptr(),
+                                        self.codes.data_ptr(), self.scales.data_ptr(),
+                                        _lib._p(self.bias), out.data_ptr(), work.data_ptr(),
+                                        ws or 256, handle)
         self.workspace = work
+        _raise(rc, check, "ssd_scaled_matmul")
         return out
 
     def _plan(self, shape):
@@ -596,16 +618,19 @@ class LogProbsDevice:
             self.dlogits = torch.empty((rows, vocab), dtype=logits.dtype, device=dev)
         self.prob = _lib.make_logprob_problem(rows, vocab, scale, ntop, logits.dtype, spaced(logits),
                                               spaced(self.dlogits) if self.back else 0)
+        self._ref = ctypes.byref(self.prob)
         new = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
         self.logprobs, self.entropy, self.lse = new(rows), new(rows), new(rows)
         self.top_tokens = new(rows, ntop, dt=torch.int32) if ntop else None
         self.top_logprobs = new(rows, ntop) if ntop else None
 
     def fwd(self, stream=None, check=True):
-        _on_gpu(self.logits.device, "LogProbsDevice")
-        return _lib.ssd_token_logprobs(self.prob, self.logits, self.tokens, self.logprobs,
-                                       self.entropy, self.lse, self.top_tokens, self.top_logprobs,
-                                       stream=stream, check=check)
+        handle, p = _here(self.logits.device, "LogProbsDevice", stream), _lib._p
+        rc = _lib.LIB.ssd_token_logprobs(self._ref, self.logits.data_ptr(), self.tokens.data_ptr(),
+                                         self.logprobs.data_ptr(), self.entropy.data_ptr(),
+                                         self.lse.data_ptr(), p(self.top_tokens),
+                                         p(self.top_logprobs), handle)
+        return _raise(rc, check, "ssd_token_logprobs")
 
     def bwd(self, stream=None, check=True):
         if not self.back:

@@ -504,3 +504,179 @@ def test_from_the_residual_to_the_answer(rows):
     out = lin(norm.codes, norm.scales, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(out, first[3])
+
+
+# each way that a product can go: few tokens, some, pairs of CTAs with and without rows written out before
+WAYS = [(5, 300, 256, "int8"), (5, 300, 250, "int8"), (20, 300, 256, "e4m3"), (100, 500, 512, "int8"),
+        (100, 500, 500, "e4m3"), (9000, 1100, 256, "int8"), (9000, 1100, 250, "e4m3"), (9000, 1100, 256, "e4m3")]
+
+
+@pytest.mark.parametrize("m,n,k,form", WAYS)
+def test_product_captured_and_on_two_streams(m, n, k, form):
+    """Replays with new inputs, and two calls of one map at once on two streams,
+    give the bits of calls one by one."""
+    from mamba_selective_state_gb300 import runner
+    g = gen(m + k)
+    w, sw = some_codes(g, n, k, form), torch.rand(n, generator=g, device="cuda")
+    ins = [(some_codes(g, m, k, form), torch.rand(m, generator=g, device="cuda")) for _ in range(2)]
+    lin = runner.Linear8(w, sw)
+    want = [lin(a, s).clone() for a, s in ins]
+    check_product(*ins[0], w, sw, None, want[0], BF16)
+    assert not torch.equal(*want)
+    a, s = ins[0][0].clone(), ins[0][1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lin(a, s)
+    for i in (1, 0):
+        a.copy_(ins[i][0])
+        s.copy_(ins[i][1])
+        graph.replay()
+        assert torch.equal(out, want[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(5):
+        for i in (0, 1):
+            outs[i].append(lin(*ins[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i in (0, 1) for o in outs[i])
+    assert lin.device_status() == 0
+
+
+def test_product_reproducible_and_rowwise():
+    """A token's result does not depend on the tokens around it where the same
+    kernel takes them, and the same call gives the same bits."""
+    from mamba_selective_state_gb300 import runner
+    g = gen(5)
+    for form, m in (("int8", 20), ("e4m3", 100), ("int8", 100), ("int8", 3000), ("e4m3", 3000)):
+        w, a = some_codes(g, 700, 640, form), some_codes(g, m, 640, form)
+        lin = runner.Linear8(w, torch.ones(700, device="cuda"), out_dtype=F32)
+        one = lin(a, torch.ones(m, device="cuda"))
+        assert torch.equal(one, lin(a, torch.ones(m, device="cuda")))
+        b = a.clone()
+        tail = b[m // 2:].view(torch.uint8)
+        tail.copy_(tail.roll(1, 0))
+        assert torch.equal(one[:m // 2], lin(b, torch.ones(m, device="cuda"))[:m // 2])
+
+
+def test_offsets_beyond_32_bits():
+    """The last rows of tensors of more than 2^31 elements."""
+    from mamba_selective_state_gb300 import runner
+    g = gen(11)
+    rows, V = 21500, 100003
+    logits = torch.zeros(rows, V, dtype=BF16, device="cuda")
+    logits[-2:] = (3 * rn(g, 2, V)).to(BF16)
+    tok = torch.full((rows,), 77, dtype=torch.int32, device="cuda")
+    dl, dH = rn(g, rows), rn(g, rows)
+    dev = runner.LogProbsDevice(logits, tok, ntop=3, dlogprobs=dl, dentropy=dH)
+    dev.fwd()
+    dev.bwd()
+    small = runner.LogProbsDevice(logits[-2:].clone(), tok[-2:].clone(), ntop=3, dlogprobs=dl[-2:].clone(),
+                                  dentropy=dH[-2:].clone())
+    small.fwd()
+    small.bwd()
+    check_logp(small, small.logits, small.tokens, 1.0, 3)
+    assert torch.equal(dev.top_tokens[-2:], small.top_tokens)
+    assert torch.allclose(dev.logprobs[-2:], small.logprobs, rtol=1e-5)
+    assert torch.allclose(dev.dlogits[-2:].float(), small.dlogits.float(), rtol=2.0 ** -7, atol=1e-12)
+    assert torch.equal(dev.top_tokens[:-2], torch.tensor([0, 1, 2], device="cuda", dtype=torch.int32).expand(rows - 2, 3))
+    del logits, dev
+    rows, dim = 135000, 16384
+    x = torch.zeros(rows, dim, dtype=BF16, device="cuda")
+    x[-3:] = rn(g, 3, dim).to(BF16)
+    w = 1 + 0.1 * rn(g, dim)
+    dev = runner.AddNormDevice(x, w, form="int8")
+    dev.fwd()
+    out, _ = ro.add_rmsnorm_fwd(f64(x[-3:]), f64(w), 1e-5)
+    got = ro.code_values(raw(dev.codes[-3:]), "int8") * f64(dev.scales[-3:])[:, None]
+    assert np.abs(got - out).max() <= 0.51 / 127 * np.abs(out).max()
+    assert not dev.scales[:-3].any() and not dev.codes[0].any()
+    del x, dev
+    torch.cuda.empty_cache()
+    m, n, k = 210000, 10304, 64
+    a, wc = some_codes(g, m, k, "int8"), some_codes(g, n, k, "int8")
+    lin = runner.Linear8(wc, torch.ones(n, device="cuda"))
+    out = lin(a, torch.ones(m, device="cuda"))
+    check_product(a[-300:], torch.ones(300, device="cuda"), wc, lin.scales, None, out[-300:], BF16)
+
+
+def test_gradients_through_the_chain():
+    """A training step's chain -- norm on the residual stream, readout, log
+    probabilities and entropy of sampled tokens, and back -- against float64
+    differentiation, in fp32."""
+    from mamba_selective_state_gb300 import runner
+    g = gen(21)
+    rows, dim, V, eps = 33, 96, 500, 1e-5
+    x, r, w = norm_case(rows, dim, F32, F32, 21)
+    E = rn(g, V, dim) * dim ** -0.5
+    tok = torch.randint(0, V, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    tok[3] = -1
+    adv, dH, dh = rn(g, rows), 0.1 * rn(g, rows), rn(g, rows, dim)
+    dout = torch.empty(rows, dim, device="cuda")
+    norm = runner.AddNormDevice(x, w, residual=r, eps=eps, dout=dout, dh=dh)
+    norm.fwd()
+    logits = norm.out @ E.T
+    lp = runner.LogProbsDevice(logits, tok, dlogprobs=adv, dentropy=dH)
+    lp.fwd()
+    lp.bwd()
+    dout.copy_(lp.dlogits @ E)
+    norm.bwd()
+    xd, rd, wd, Ed = (t.detach().double().cpu().requires_grad_() for t in (x, r, w, E))
+    h = xd + rd
+    z = (h / torch.sqrt((h * h).mean(-1, keepdim=True) + eps) * wd) @ Ed.T
+    logp = torch.log_softmax(z, -1)
+    t = tok.cpu().long()
+    loss = ((logp.gather(1, t.clamp(min=0)[:, None])[:, 0] * (t >= 0)) * adv.cpu().double()).sum()
+    loss = loss - ((logp.exp() * logp).sum(-1) * dH.cpu().double()).sum() + (h * dh.cpu().double()).sum()
+    loss.backward()
+    # five steps in fp32, sums of at most 500 terms: 1e-4 of the largest is 1600 roundings
+    for got, want in ((norm.dx, xd.grad), (norm.dweight, wd.grad), (norm.dresidual, rd.grad)):
+        assert np.abs(f64(got) - want.numpy()).max() < 1e-4 * np.abs(want.numpy()).max()
+
+
+def test_refusals_of_misaligned_tensors():
+    from mamba_selective_state_gb300 import _lib, runner
+    x = torch.zeros(5, 7, device="cuda")
+    with pytest.raises(_lib.SSDError):
+        runner.AddNormDevice(x[1:], torch.ones(7, device="cuda")).fwd()
+    with pytest.raises(_lib.SSDError):
+        runner.LogProbsDevice(x[1:], torch.zeros(4, dtype=torch.int32, device="cuda")).fwd()
+    c = torch.zeros(5, 7, dtype=torch.int8, device="cuda")
+    lin = runner.Linear8(c, torch.ones(5, device="cuda"))
+    with pytest.raises(_lib.SSDError):
+        lin(c[1:], torch.ones(4, device="cuda"))
+    for bad in (dict(codes=c.float()), dict(codes=c.cpu()), dict(codes=c[:, :5]), dict(codes=c[0]),
+                dict(scales=torch.ones(4, device="cuda")), dict(scales=torch.ones(5)),
+                dict(out=torch.zeros(5, 5, device="cuda"))):
+        with pytest.raises(ValueError):
+            lin(**dict(dict(codes=c, scales=torch.ones(5, device="cuda")), **bad))
+
+
+def test_serving_example_scores_what_it_generated():
+    """The example's 8-bit scores against the same readout in float64: 8 bits of
+    the outputs (a row's largest over 254) and of the embeddings weigh in the
+    logits as independent errors of half a step each."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "delta_serving.py")
+    spec = importlib.util.spec_from_file_location("delta_serving", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    layer = ex.Layer(vocab=64, width=64, nheads=4, headdim=64, dstate=64)
+    tokens = torch.randint(0, 64, (90,), generator=gen(1), device="cuda", dtype=torch.int32)
+    got = ex.score(layer, tokens, top=4)
+    pre = ex.runner.DeltaDevice(*layer.inputs(tokens[None, :-1]))
+    pre.fwd()
+    h = f64((pre.y[0].float().flatten(1) @ layer.wo).bfloat16())
+    out, E = h, f64(layer.embed)
+    z = out @ E.T
+    want = ro.token_logprobs(z, tokens[1:].cpu().numpy(), 1.0)
+    # (1 % more for what fp32 rounds)
+    # |z - z8| <= half a step of one operand on the sum of the other's sizes, and the product of both
+    so, se = np.abs(out).max(-1) / 254, np.abs(E).max(-1) / 254
+    tol = so[:, None] * np.abs(E).sum(-1) + se * np.abs(out).sum(-1)[:, None] + 64 * so[:, None] * se
+    worst = tol.max(-1) * 1.01
+    assert (np.abs(f64(got.logits) - z) <= tol * 1.01).all()
+    # a log probability moves by at most the largest error of its row, twice
+    assert (np.abs(f64(got.logprobs) - want["logprobs"]) <= 2 * worst).all()
+    assert (got.top_logprobs[:, :-1] >= got.top_logprobs[:, 1:]).all() and (got.logprobs <= 0).all()
