@@ -560,17 +560,18 @@ int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float
  * lower index, with their log probabilities.
  *
  * logits (rows, vocab) dtype, logit_stride elements from row to row (0:
- * dense); tokens (rows) int32; logprobs, entropy, lse (rows) fp32; top_tokens
- * int32 and top_logprobs fp32 (rows, ntop).  A token outside [0, vocab) is
+ * dense); tokens (rows) int32; logprobs, entropy, lse (rows) fp32; stats
+ * (rows, 2) fp32, what the backward needs of the rows: the largest logit m, and
+ * log sum exp(z - scale m); top_tokens int32 and top_logprobs fp32 (rows, ntop).  A token outside [0, vocab) is
  * padding: its logprob is 0 and has no gradient.  A logit of -inf excludes its
  * word: its log probability is -inf, its gradient 0, and it is no alternative;
  * places for which no word is left hold -1 and -inf.  A row that excludes every
  * word has lse -inf, logprob -inf, entropy 0 and no gradient.  A NaN or +inf in
  * a row makes its lse, logprobs, entropy and gradient NaN; the alternatives are
  * then those of the values that are not NaN.  Of logprobs (given with tokens),
- * entropy, lse and the alternatives each may be NULL, but not all.
+ * entropy, lse, stats and the alternatives each may be NULL, but not all.
  *
- * The backward takes lse and, for dentropy, entropy from the forward, and the
+ * The backward takes stats and, for dentropy, entropy from the forward, and the
  * upstream gradients dlogprobs (given with tokens) and dentropy (rows) fp32 --
  * either may be NULL -- and writes dlogits (rows, vocab) dtype, grad_stride
  * elements from row to row (0: dense):
@@ -592,10 +593,10 @@ typedef struct {
 } ssd_logprob_problem;
 
 int ssd_token_logprobs(const ssd_logprob_problem* prob, const void* logits, const int32_t* tokens,
-                       float* logprobs, float* entropy, float* lse, int32_t* top_tokens,
-                       float* top_logprobs, ssd_stream_t stream);
+                       float* logprobs, float* entropy, float* lse, float* stats,
+                       int32_t* top_tokens, float* top_logprobs, ssd_stream_t stream);
 int ssd_token_logprobs_bwd(const ssd_logprob_problem* prob, const void* logits,
-                           const int32_t* tokens, const float* lse, const float* entropy,
+                           const int32_t* tokens, const float* stats, const float* entropy,
                            const float* dlogprobs, const float* dentropy, void* dlogits,
                            ssd_stream_t stream);
 

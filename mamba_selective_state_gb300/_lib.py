@@ -188,7 +188,7 @@ def _load():
     lib.ssd_scaled_matmul.argtypes = [mpp] + [vp] * 7 + [sz, vp]
     lib.ssd_scaled_matmul.restype = i32
     lpp = ctypes.POINTER(ssd_logprob_problem)
-    lib.ssd_token_logprobs.argtypes = [lpp] + [vp] * 7 + [vp]
+    lib.ssd_token_logprobs.argtypes = [lpp] + [vp] * 8 + [vp]
     lib.ssd_token_logprobs.restype = i32
     lib.ssd_token_logprobs_bwd.argtypes = [lpp] + [vp] * 7 + [vp]
     lib.ssd_token_logprobs_bwd.restype = i32
@@ -535,21 +535,21 @@ def make_logprob_problem(rows, vocab, scale, ntop, dtype, logit_stride=0,
                                _dtype_code(dtype), 0)
 
 
-def ssd_token_logprobs(prob, logits, tokens, logprobs, entropy, lse, top_tokens=None,
+def ssd_token_logprobs(prob, logits, tokens, logprobs, entropy, lse, stats=None, top_tokens=None,
                        top_logprobs=None, stream=None, check=True) -> int:
     """Enqueue the tokens' log probabilities on ``stream``."""
     rc = LIB.ssd_token_logprobs(ctypes.byref(prob), _p(logits), _p(tokens), _p(logprobs),
-                                _p(entropy), _p(lse), _p(top_tokens), _p(top_logprobs),
-                                _stream(stream))
+                                _p(entropy), _p(lse), _p(stats), _p(top_tokens),
+                                _p(top_logprobs), _stream(stream))
     if check and rc != SSD_OK:
         raise SSDError(rc, "ssd_token_logprobs")
     return rc
 
 
-def ssd_token_logprobs_bwd(prob, logits, tokens, lse, entropy, dlogprobs, dentropy, dlogits,
+def ssd_token_logprobs_bwd(prob, logits, tokens, stats, entropy, dlogprobs, dentropy, dlogits,
                            stream=None, check=True) -> int:
     """Enqueue the gradient to the logits on ``stream``."""
-    rc = LIB.ssd_token_logprobs_bwd(ctypes.byref(prob), _p(logits), _p(tokens), _p(lse),
+    rc = LIB.ssd_token_logprobs_bwd(ctypes.byref(prob), _p(logits), _p(tokens), _p(stats),
                                     _p(entropy), _p(dlogprobs), _p(dentropy), _p(dlogits),
                                     _stream(stream))
     if check and rc != SSD_OK:

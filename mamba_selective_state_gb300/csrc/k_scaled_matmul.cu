@@ -624,6 +624,7 @@ double share_out(bool fp8, int64_t m, int64_t n, int64_t k, SomeArgs* a, int* sp
     if ((long long)per * (x - 1) >= a->kb) continue;  // a share without a stage
     const long long waves = (wide * mt + kClusters[x] - 1) / kClusters[x], tiles = waves * kClusters[x] / mt;
     const int ch = (int)((n + tiles - 1) / tiles + 15) / 16 * 16;
+    if (waves * kClusters[x] * x > (1LL << 30)) continue;  // (CTAs of a grid)
     const double cost = (double)waves * (1.15 * (per * ((fp8 ? 800.0 : 1500.0) + ch) + 7000 + (x > 1 ? 2000 : 0)));
     if (best == 0 || cost < best) {
       best = cost;
@@ -632,8 +633,8 @@ double share_out(bool fp8, int64_t m, int64_t n, int64_t k, SomeArgs* a, int* sp
       *split = x;
     }
   }
-  a->nt = (int)((n + a->ch - 1) / a->ch);
-  return best;
+  if (best > 0) a->nt = (int)((n + a->ch - 1) / a->ch);
+  return best;  // (0: too many)
 }
 
 // a, w: rows as the copies read them, of bytes in all and in memory
@@ -1004,8 +1005,10 @@ int check(const ssd_matmul_problem* pr, MatmulPlan* pl) {
   pl->few = pr->m <= kFewTokens[!int8];
   SomeArgs share;
   int split;
+  double cost;
   pl->some = !pl->few &&
-             share_out(!int8, pr->m, pr->n, pr->k, &share, &split) <= pairs_cost(!int8, pr->m, pr->n, pr->k);
+             0 < (cost = share_out(!int8, pr->m, pr->n, pr->k, &share, &split)) &&
+             cost <= pairs_cost(!int8, pr->m, pr->n, pr->k);
   pl->half_a = pl->half_w = int8 && !pl->few && !pl->some;
   pl->out_a = pl->half_a || !whole;
   pl->out_w = pl->half_w || !whole;

@@ -49,9 +49,11 @@ struct LogpArgs {
   const void* logits;
   const int32_t* tokens;
   float *logprobs, *entropy, *lse;
+  float2* stats;
   int32_t* top_tok;
   float* top_lp;
-  const float *lse_in, *ent_in, *dlogp, *dent;
+  const float2* stats_in;
+  const float *ent_in, *dlogp, *dent;
   void* dlogits;
   long long rows, V, stride, gstride;
   float scale, c2;  // c2 = scale log2(e)
@@ -506,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
     const bool nothing = c.m == kNegInf && c.s == 0.f;  // every word is excluded
     const float ln_s = logf(c.s) - off_of(c.m, a.c2) * kLn2;  // ln sum e^(z - m)
     if (tid == 0) {
+      if (a.stats) a.stats[row] = make_float2(c.m, nothing ? kNegInf : ln_s);
       if (a.lse) a.lse[row] = nothing ? kNegInf : fmaf(c.m, a.scale, ln_s);
       if (a.entropy) a.entropy[row] = nothing ? 0.f : logf(c.s) - kLn2 * (c.t / c.s);
       if (a.logprobs) a.logprobs[row] = !known ? 0.f : nothing ? kNegInf : (tok_x - c.m) * a.scale - ln_s;
@@ -536,14 +539,16 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(LogpArg
   constexpr int n = Row<T>::n;
   const Row<T> r(a.logits, row, a.stride, a.V);
   T* out = static_cast<T*>(a.dlogits) + row * a.gstride;
-  const float lse = a.lse_in[row], H = a.ent_in ? a.ent_in[row] : 0.f;
+  const float2 st = a.stats_in[row];  // the largest logit m, and ln sum e^(z - scale m)
+  const float m = st.x, ln_s = st.y, H = a.ent_in ? a.ent_in[row] : 0.f;
   const int t = a.tokens ? a.tokens[row] : -1;
   const unsigned tok = t >= 0 && t < a.V ? (unsigned)t : 0xffffffffu;
   const float dl = tok != 0xffffffffu && a.dlogp ? a.dlogp[row] : 0.f, dH = a.dent ? a.dent[row] : 0.f;
-  const bool nothing = lse == kNegInf;
-  // p (-dl - dH (log p + H)) with log p = z - lse
+  const bool nothing = ln_s == kNegInf;
+  // p (-dl - dH (log p + H)) with log p = scale (x - m) - ln_s: the difference keeps
+  // its digits where the logits are large
   auto grad = [&](float x, unsigned v) {
-    const float lp = floored(fmaf(x, a.scale, -lse)), p = ex2(lp * kLog2e);
+    const float lp = floored(fmaf(x - m, a.scale, -ln_s)), p = ex2(lp * kLog2e);
     float g = -p * fmaf(dH, lp + H, dl);
     if (v == tok) g += dl;
     return nothing ? 0.f : g * a.scale;
@@ -668,20 +673,22 @@ using namespace ssd;
 extern "C" {
 
 int ssd_token_logprobs(const ssd_logprob_problem* pr, const void* logits, const int32_t* tokens, float* logprobs,
-                       float* entropy, float* lse, int32_t* top_tokens, float* top_logprobs, ssd_stream_t stream) {
+                       float* entropy, float* lse, float* stats, int32_t* top_tokens, float* top_logprobs,
+                       ssd_stream_t stream) {
   LogpArgs a;
   int rc = check(pr, &a);
   if (rc != SSD_OK) return rc;
   if (!logits || (logprobs != nullptr) != (tokens != nullptr)) return SSD_ERR_INVALID_ARGUMENT;
   if ((pr->ntop > 0) != (top_tokens != nullptr) || (pr->ntop > 0) != (top_logprobs != nullptr))
     return SSD_ERR_INVALID_ARGUMENT;
-  if (!logprobs && !entropy && !lse && !top_tokens) return SSD_ERR_INVALID_ARGUMENT;
-  const void* ptrs[] = {logits, tokens, logprobs, entropy, lse, top_tokens, top_logprobs};
+  if (!logprobs && !entropy && !lse && !stats && !top_tokens) return SSD_ERR_INVALID_ARGUMENT;
+  const void* ptrs[] = {logits, tokens, logprobs, entropy, lse, stats, top_tokens, top_logprobs};
   for (const void* q : ptrs)
     if (misaligned16(q)) return SSD_ERR_INVALID_ARGUMENT;
   rc = device_check();
   if (rc != SSD_OK) return rc;
   a.logits = logits; a.tokens = tokens; a.logprobs = logprobs; a.entropy = entropy; a.lse = lse;
+  a.stats = reinterpret_cast<float2*>(stats);
   a.top_tok = top_tokens; a.top_lp = top_logprobs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_before(s);
@@ -690,22 +697,22 @@ int ssd_token_logprobs(const ssd_logprob_problem* pr, const void* logits, const 
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
-int ssd_token_logprobs_bwd(const ssd_logprob_problem* pr, const void* logits, const int32_t* tokens, const float* lse,
-                           const float* entropy, const float* dlogprobs, const float* dentropy, void* dlogits,
+int ssd_token_logprobs_bwd(const ssd_logprob_problem* pr, const void* logits, const int32_t* tokens,
+                           const float* stats, const float* entropy, const float* dlogprobs, const float* dentropy, void* dlogits,
                            ssd_stream_t stream) {
   LogpArgs a;
   int rc = check(pr, &a);
   if (rc != SSD_OK) return rc;
-  if (!logits || !lse || !dlogits || (!dlogprobs && !dentropy)) return SSD_ERR_INVALID_ARGUMENT;
+  if (!logits || !stats || !dlogits || (!dlogprobs && !dentropy)) return SSD_ERR_INVALID_ARGUMENT;
   if ((dlogprobs != nullptr) != (tokens != nullptr) || (dentropy != nullptr) != (entropy != nullptr))
     return SSD_ERR_INVALID_ARGUMENT;
   if (dlogits == logits && a.stride != a.gstride) return SSD_ERR_INVALID_ARGUMENT;
-  const void* ptrs[] = {logits, tokens, lse, entropy, dlogprobs, dentropy, dlogits};
+  const void* ptrs[] = {logits, tokens, stats, entropy, dlogprobs, dentropy, dlogits};
   for (const void* q : ptrs)
     if (misaligned16(q)) return SSD_ERR_INVALID_ARGUMENT;
   rc = device_check();
   if (rc != SSD_OK) return rc;
-  a.logits = logits; a.tokens = tokens; a.lse_in = lse; a.ent_in = entropy; a.dlogp = dlogprobs; a.dent = dentropy;
+  a.logits = logits; a.tokens = tokens; a.stats_in = reinterpret_cast<const float2*>(stats); a.ent_in = entropy; a.dlogp = dlogprobs; a.dent = dentropy;
   a.dlogits = dlogits;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_before(s);

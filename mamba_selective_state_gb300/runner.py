@@ -621,6 +621,7 @@ class LogProbsDevice:
         self._ref = ctypes.byref(self.prob)
         new = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
         self.logprobs, self.entropy, self.lse = new(rows), new(rows), new(rows)
+        self.stats = new(rows, 2) if self.back else None
         self.top_tokens = new(rows, ntop, dt=torch.int32) if ntop else None
         self.top_logprobs = new(rows, ntop) if ntop else None
 
@@ -628,7 +629,7 @@ class LogProbsDevice:
         handle, p = _here(self.logits.device, "LogProbsDevice", stream), _lib._p
         rc = _lib.LIB.ssd_token_logprobs(self._ref, self.logits.data_ptr(), self.tokens.data_ptr(),
                                          self.logprobs.data_ptr(), self.entropy.data_ptr(),
-                                         self.lse.data_ptr(), p(self.top_tokens),
+                                         self.lse.data_ptr(), p(self.stats), p(self.top_tokens),
                                          p(self.top_logprobs), handle)
         return _raise(rc, check, "ssd_token_logprobs")
 
@@ -637,7 +638,7 @@ class LogProbsDevice:
             raise ValueError("built without dlogprobs and dentropy: there is no backward")
         _on_gpu(self.logits.device, "LogProbsDevice")
         return _lib.ssd_token_logprobs_bwd(self.prob, self.logits,
-                                           None if self.dlogprobs is None else self.tokens, self.lse,
+                                           None if self.dlogprobs is None else self.tokens, self.stats,
                                            None if self.dentropy is None else self.entropy,
                                            self.dlogprobs, self.dentropy, self.dlogits,
                                            stream=stream, check=check)

@@ -90,6 +90,7 @@ def test_matmul_refusals(lib):
             assert call(**{n: None}) == bad, n
         assert call(**{n: FAKE + 8}) == bad, n
     assert call(nb=8) == lib.SSD_ERR_WORKSPACE_TOO_SMALL
+    assert call(k=(1 << 20) + 1) == uns
     for dims in ((1, 1, 1), (1, 10304, 4096), (64, 8, 17), (65, 8, 17), (4001, 2048, 4096), (1000, 1, 1)):
         for fmt in (0, 1):
             assert lib.ssd_scaled_matmul_workspace_bytes(lib.make_matmul_problem(*dims, fmt, 0)) >= 256
@@ -98,8 +99,9 @@ def test_matmul_refusals(lib):
 
 def test_logprob_refusals(lib):
     bad, uns = lib.SSD_ERR_INVALID_ARGUMENT, lib.SSD_ERR_UNSUPPORTED
-    base = dict(logits=FAKE, tokens=FAKE, logprobs=FAKE, entropy=FAKE, lse=FAKE, top_tokens=FAKE, top_logprobs=FAKE)
-    base2 = dict(logits=FAKE, tokens=FAKE, lse=FAKE, entropy=FAKE, dlogprobs=FAKE, dentropy=FAKE, dlogits=2 * FAKE)
+    base = dict(logits=FAKE, tokens=FAKE, logprobs=FAKE, entropy=FAKE, lse=FAKE, stats=FAKE, top_tokens=FAKE,
+                top_logprobs=FAKE)
+    base2 = dict(logits=FAKE, tokens=FAKE, stats=FAKE, entropy=FAKE, dlogprobs=FAKE, dentropy=FAKE, dlogits=2 * FAKE)
 
     def prob(rows=4, vocab=100, scale=1.0, ntop=3, dtype=1, **kw):
         return lib.make_logprob_problem(rows, vocab, scale, ntop, dtype, **kw)
@@ -117,16 +119,16 @@ def test_logprob_refusals(lib):
         assert fwd(**{n: FAKE + 4}) == bad, n
     assert fwd(prob(ntop=0)) == bad                          # alternatives without a number
     assert fwd(prob(ntop=0), logprobs=None) == bad           # tokens without logprobs
-    assert fwd(prob(ntop=0), logprobs=None, tokens=None, entropy=None, lse=None, top_tokens=None,
+    assert fwd(prob(ntop=0), logprobs=None, tokens=None, entropy=None, lse=None, stats=None, top_tokens=None,
                top_logprobs=None) == bad                     # nothing to do
-    for n in ("logits", "lse", "dlogits", "tokens", "entropy"):
+    for n in ("logits", "stats", "dlogits", "tokens", "entropy"):
         assert bwd(**{n: None}) == bad, n
     for n in base2:
         assert bwd(**{n: FAKE + 4}) == bad, n
     assert bwd(dlogprobs=None) == bad and bwd(dentropy=None) == bad
     assert bwd(dlogprobs=None, tokens=None, dentropy=None, entropy=None) == bad
     assert bwd(prob(logit_stride=128), dlogits=FAKE) == bad  # in place with other strides
-    assert lib.LIB.ssd_token_logprobs(None, *([None] * 7), None) == bad
+    assert lib.LIB.ssd_token_logprobs(None, *([None] * 8), None) == bad
     assert lib.LIB.ssd_token_logprobs_bwd(None, *([None] * 7), None) == bad
 
 

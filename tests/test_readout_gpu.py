@@ -227,7 +227,8 @@ def values(t):
 MATS = [(1, 1, 1), (1, 10304, 4096), (1, 17, 100), (2, 5, 3), (3, 300, 64), (4, 1000, 1000), (7, 130, 4096),
         (8, 64, 16), (9, 64, 48), (16, 777, 80), (17, 129, 272), (31, 100, 1040), (33, 2048, 512), (61, 515, 4096),
         (64, 256, 128), (65, 256, 128), (100, 1, 64), (128, 100, 192), (129, 257, 63), (200, 640, 2048),
-        (255, 33, 4096), (257, 513, 129), (300, 1000, 1000), (520, 776, 384), (1000, 4100, 256), (2049, 300, 64)]
+        (255, 33, 4096), (257, 513, 129), (300, 1000, 1000), (520, 776, 384), (1000, 4100, 256), (2049, 300, 64), (40, 50, 1),
+        (3000, 40, 1), (9000, 1030, 3)]
 
 
 def check_product(a, sa, w, sw, bias, out, out_dtype):
@@ -398,6 +399,47 @@ def test_logprobs_backward(dt, stride, which):
     assert dev.dlogits.shape == (rows, V)
     want, rel = check_logp(dev, logits, tok, scale, 0)
     check_grad(dev.dlogits, logits, tok, scale, rel, want, dt, **kw)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_logprobs_of_large_logits(dt):
+    """Rows whose logits are large, or all of them the type's lowest value: the
+    sums are relative to the row's largest, in the gradient too."""
+    from mamba_selective_state_gb300 import runner
+    rows, V = 4, 700
+    logits, tok = logp_case(rows, V, dt, 3)
+    logits[0] = torch.finfo(dt).min
+    logits[1] = (logits[1].float() + 30000).to(dt)
+    logits[2] = -1e30
+    dl, dH = rn(gen(1), rows), rn(gen(2), rows)
+    dev = runner.LogProbsDevice(logits, tok, dlogprobs=dl, dentropy=dH)
+    dev.fwd()
+    dev.bwd()
+    x, got = f64(logits), f64(dev.dlogits)
+    for i in range(rows):
+        z = x[i] - x[i].max()
+        lp = z - np.log(np.exp(z).sum())
+        p, t = np.exp(lp), int(tok[i])
+        H = -(p * lp).sum()
+        d = -p * (float(dl[i]) + float(dH[i]) * (lp + H))
+        d[t] += float(dl[i])
+        # (V / 256 + 96 roundings of the sum, 4 of an exponent of at most 32)
+        tol = (V / 256 + 96 + 128) * U * p * (abs(float(dl[i])) + abs(float(dH[i])) * (np.abs(lp) + H + 1))
+        tol = tol + 2 * U * abs(float(dl[i])) + HALF[dt] * np.abs(d) + 1e-40
+        assert (np.abs(got[i] - d) <= tol).all(), i
+
+
+def test_logprobs_without_tokens():
+    """Only what is asked for is written."""
+    from mamba_selective_state_gb300 import _lib
+    logits, _ = logp_case(7, 900, F32, 4)
+    prob = _lib.make_logprob_problem(7, 900, 1.0, 0, F32)
+    lse = torch.zeros(7, device="cuda")
+    _lib.ssd_token_logprobs(prob, logits, None, None, None, lse)
+    assert torch.allclose(lse, torch.logsumexp(logits, -1))
+    top, val = torch.zeros(7, 2, dtype=torch.int32, device="cuda"), torch.zeros(7, 2, device="cuda")
+    _lib.ssd_token_logprobs(_lib.make_logprob_problem(7, 900, 1.0, 2, F32), logits, None, None, None, None, None, top, val)
+    assert torch.equal(top[:, 0].long(), logits.argmax(-1))
 
 
 def check_grad(got, logits, tok, scale, rel, want, dt, dlogprobs, dentropy):
