@@ -315,13 +315,15 @@ constexpr int kSomeThreads = (kTurners + kTokTurners + 2) * 32;
 
 template <bool kFp8>
 struct SomeShape {
-  static constexpr int kW = kWide * 128, kA = kRows * 128, kStageBytes = kW + kA;
-  static constexpr int kStages = kFp8 ? 4 : 3;
-  static constexpr int kTurned = kFp8 ? 0 : 2 * kWide * 128;  // two places of 64 codes as fp16
-  static constexpr int kBytes = kStages * kStageBytes + kTurned + 1024;
+  // The stages: as many of (ch + box) 128-byte rows as there is room for
+  static constexpr int kRing = kFp8 ? 196608 : 147456, kStages = 8;
+  // behind them two places of 64 codes as fp16, or the rows up to the 128th that products of the last stage's tokens read
+  // (whatever they hold; their sums are not written)
+  static constexpr int kTurned = kFp8 ? kRows * 128 : 2 * kWide * 128;
+  static constexpr int kBytes = kRing + kTurned + 1024;
   static constexpr int kPlaces = 4;                           // of the tokens in tensor memory, 64 columns each
   static constexpr uint32_t kCols = kFp8 ? kWide : kWide + 64 * kPlaces;
-  static_assert(kRows * kWide * 4 <= kStages * kStageBytes, "the sums fit into the stages");
+  static_assert(kRows * kWide * 4 <= kRing && 3 * (kWide + kRows) * 128 <= kRing, "the sums, and three stages, fit into the ring");
 };
 
 struct SomeArgs {
@@ -367,13 +369,13 @@ __device__ __forceinline__ uint4 shared_load(uint32_t at) {
 __device__ __forceinline__ void shared_store(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// A place in a ring, and the parity of the round that it is in
-template <int N>
+// A place in a ring of n, and the parity of the round that it is in
 struct Ring {
-  int at = 0;
+  int n, at = 0;
   uint32_t ph = 0;
+  __device__ __forceinline__ explicit Ring(int places) : n(places) {}
   __device__ __forceinline__ void next() {
-    if (++at == N) {
+    if (++at == n) {
       at = 0;
       ph ^= 1;
     }
@@ -388,7 +390,8 @@ __global__ void __launch_bounds__(kSomeThreads)
   extern __shared__ uint8_t raw[];
   const MatmulArgs& p = s.p;
   const uint32_t pad = (1024u - (tc::smem_u32(raw) & 1023u)) & 1023u, smem = tc::smem_u32(raw) + pad;
-  const uint32_t wbuf = smem + kStages * S::kStageBytes;
+  const uint32_t wbuf = smem + S::kRing, w_bytes = s.ch * 128, stage_bytes = w_bytes + s.box * 128;
+  const int stages = min(S::kRing / (int)stage_bytes, kStages);
   __shared__ uint64_t full[kStages], empty[kStages], wfull[2], wempty[2], turned[kPlaces], taken[kPlaces], done;
   __shared__ uint32_t tmem_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -431,25 +434,25 @@ __global__ void __launch_bounds__(kSomeThreads)
 
   if (warp == kCopyWarp) {
     if (lane == 0) {
-      Ring<kStages> st;
+      Ring st(stages);
       for (int b = 0; b < nb; ++b, st.next()) {
         tc::mbar_wait_flag(&empty[st.at], st.ph ^ 1, ok);
-        const uint32_t to = smem + st.at * S::kStageBytes;
-        tc::mbar_expect_tx(&full[st.at], (s.ch + s.box) * 128);
+        const uint32_t to = smem + st.at * stage_bytes;
+        tc::mbar_expect_tx(&full[st.at], stage_bytes);
         box_load(to, &wmap, &full[st.at], (b0 + b) * 128, (int)n0);
-        box_load(to + S::kW, &amap, &full[st.at], (b0 + b) * 128, m0);
+        box_load(to + w_bytes, &amap, &full[st.at], (b0 + b) * 128, m0);
       }
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
       const uint32_t idesc = idesc_of(kRows, s.ch);
-      Ring<kStages> st;
-      Ring<kPlaces> pl;
+      Ring st(stages);
+      Ring pl(kPlaces);
       for (int b = 0; b < nb; ++b) {
         if constexpr (kFp8) {
           tc::mbar_wait_flag(&full[st.at], st.ph, ok);
           tc::tc_fence_after();
-          const uint32_t w = smem + st.at * S::kStageBytes, a = w + S::kW;
+          const uint32_t w = smem + st.at * stage_bytes, a = w + w_bytes;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             block_mma<true, false>(tmem, tc::smem_desc(a + j * 32, 16, 1024, tc::kSwz128),
@@ -484,13 +487,16 @@ __global__ void __launch_bounds__(kSomeThreads)
     const uint32_t put0 = wbuf + half * (kWide * 128) + from + ((2 * unit ^ x) << 4),
                    put1 = wbuf + half * (kWide * 128) + from + (((2 * unit + 1) ^ x) << 4);
     const int units = (s.ch - row0 + 63) / 64;  // rows row0, row0 + 64, ... of this tile (at most four)
-    Ring<kStages> st;
+    Ring st(stages);
     for (int b = 0; b < nb; ++b, st.next()) {
       tc::mbar_wait_flag(&full[st.at], st.ph, ok);
       uint32_t v[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < units) to_half<false>(shared_load(smem + st.at * S::kStageBytes + read0 + i * 64 * 128), v[i]);
+        if (i < units) to_half<false>(shared_load(smem + st.at * stage_bytes + read0 + i * 64 * 128), v[i]);
+      tc::fence_async_smem();  // read here, written by a copy
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[st.at]);
       tc::mbar_wait_flag(&wempty[half], (uint32_t)(b & 1) ^ 1u, ok);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -498,20 +504,17 @@ __global__ void __launch_bounds__(kSomeThreads)
           shared_store(put0 + i * 64 * 128, v[i][0], v[i][1], v[i][2], v[i][3]);
           shared_store(put1 + i * 64 * 128, v[i][4], v[i][5], v[i][6], v[i][7]);
         }
-      tc::fence_async_smem();  // written here, read by the products; the stage: read here, written by a copy
+      tc::fence_async_smem();  // written here, read by the products
       __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&wfull[half]);
-        tc::mbar_arrive(&empty[st.at]);
-      }
+      if (lane == 0) tc::mbar_arrive(&wfull[half]);
     }
   } else if (!kFp8 && warp - kTurners < quarters) {
     const int quarter = warp & 3, r = quarter * 32 + lane;
-    Ring<kStages> st;
-    Ring<kPlaces> pl;
+    Ring st(stages);
+    Ring pl(kPlaces);
     for (int b = 0; b < nb; ++b) {
       tc::mbar_wait_flag(&full[st.at], st.ph, ok);
-      const uint32_t row = smem + st.at * S::kStageBytes + S::kW + r * 128;
+      const uint32_t row = smem + st.at * stage_bytes + w_bytes + r * 128;
       uint32_t h[2][32];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

@@ -447,7 +447,7 @@ class AddNormDevice:
         _dense(dh, (rows, dim), rt, "dh", dev)
         if dh is not None and dout is None:
             raise ValueError("dh needs dout")
-        if residual is None and dout is not None and not x.is_contiguous():
+        if residual is None and h_out is None and dout is not None and not x.is_contiguous():
             raise ValueError("the backward reads x as h: it must be dense")
         self.x, self.weight, self.residual, self.dout, self.dh = x, weight, residual, dout, dh
         self.prob = _lib.make_add_norm_problem(rows, dim, eps, x.dtype, rt, self.FORMATS[form],
@@ -482,11 +482,13 @@ class AddNormDevice:
     def bwd(self, stream=None, check=True):
         if self.dout is None:
             raise ValueError("built without dout: there is no backward")
-        _on_gpu(self.x.device, "AddNormDevice")
+        handle, p = _here(self.x.device, "AddNormDevice", stream), _lib._p
         own = None if self.dresidual is self.dx else self.dresidual
-        return _lib.ssd_add_rmsnorm_bwd(self.prob, self.h, self.weight, self.dout, self.dh,
-                                        self.dx, own, self.dweight, self.workspace, stream=stream,
-                                        check=check)
+        rc = _lib.LIB.ssd_add_rmsnorm_bwd(self._ref, self.h.data_ptr(), self.weight.data_ptr(),
+                                          self.dout.data_ptr(), p(self.dh), self.dx.data_ptr(),
+                                          p(own), self.dweight.data_ptr(),
+                                          self.workspace.data_ptr(), self.workspace.numel(), handle)
+        return _raise(rc, check, "ssd_add_rmsnorm_bwd")
 
 
 class Linear8:
@@ -636,9 +638,9 @@ class LogProbsDevice:
     def bwd(self, stream=None, check=True):
         if not self.back:
             raise ValueError("built without dlogprobs and dentropy: there is no backward")
-        _on_gpu(self.logits.device, "LogProbsDevice")
-        return _lib.ssd_token_logprobs_bwd(self.prob, self.logits,
-                                           None if self.dlogprobs is None else self.tokens, self.stats,
-                                           None if self.dentropy is None else self.entropy,
-                                           self.dlogprobs, self.dentropy, self.dlogits,
-                                           stream=stream, check=check)
+        handle, p = _here(self.logits.device, "LogProbsDevice", stream), _lib._p
+        rc = _lib.LIB.ssd_token_logprobs_bwd(
+            self._ref, self.logits.data_ptr(), None if self.dlogprobs is None else self.tokens.data_ptr(),
+            self.stats.data_ptr(), None if self.dentropy is None else self.entropy.data_ptr(),
+            p(self.dlogprobs), p(self.dentropy), self.dlogits.data_ptr(), handle)
+        return _raise(rc, check, "ssd_token_logprobs_bwd")
