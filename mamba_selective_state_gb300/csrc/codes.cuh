@@ -35,8 +35,8 @@ __device__ __forceinline__ float decode(uint8_t v) {
 template <bool kFp8>
 __device__ __forceinline__ uint32_t encode4(float4 v, float inv) {
   if (kFp8)
-    return (uint32_t)encode<true>(v.x * inv) | (uint32_t)encode<true>(v.y * inv) << 8 |
-           (uint32_t)encode<true>(v.z * inv) << 16 | (uint32_t)encode<true>(v.w * inv) << 24;
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v.x * inv, v.y * inv), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v.z * inv, v.w * inv), __NV_SATFINITE, __NV_E4M3) << 16;
   // |v inv| <= 127 (1 + 2^-22): the sum with 1.5 * 2^23 rounds it to an integer, ties to even, in its low byte
   // (float-to-integer conversions run at a quarter of the rate)
   const float magic = 12582912.f;
