@@ -8,7 +8,7 @@
 // exactly; sums are fp32.  e4m3 codes go to the tensor cores as they are.
 //
 // Three kernels, by the number of tokens:
-//  * up to 16 or 24: bound by the weights' bytes.  Warps read 16 channels' codes in
+//  * up to 16 (e4m3) or 24 (int8): bound by the weights' bytes.  Warps read 16 channels' codes in
 //    16-byte pieces, turn them into fp16 in registers and multiply them with
 //    the tokens' by warp-level products; the order of k inside a product is
 //    free, so a lane's 16 neighbouring codes serve four products as they lie.
@@ -34,7 +34,7 @@ int device_check();
 
 namespace {
 
-constexpr int kFewTokens[2] = {24, 16};  // of int8, e4m3 (10304 x 4096, 24 int8 tokens: 15 us, by the next kernel 18)
+constexpr int kFewTokens[2] = {24, 16};  // of int8, e4m3: what the first kernel takes
 
 struct MatmulArgs {
   const uint8_t *a, *w;
@@ -168,11 +168,12 @@ __global__ void __launch_bounds__(kSkWarps * 32, MT == 1 ? 5 : MT == 2 ? 4 : 2) 
   float acc[CT][MT][4] = {};
   constexpr int kAhead = 2;
   const int k = (int)p.k;
-  for (int k0 = warp * 64; k0 < k; k0 += kSkWarps * 64 * kAhead) {
+  // (a warp's kAhead pieces of a row are neighbours: whole lines of memory)
+  for (int k0 = warp * 64 * kAhead; k0 < k; k0 += kSkWarps * 64 * kAhead) {
     uint4 w[kAhead][CT][2], tok_codes[kAhead][MT];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int kk = k0 + u * kSkWarps * 64;
+      const int kk = k0 + u * 64;
       const bool in = kk + q * 16 < k;
 #pragma unroll
       for (int c = 0; c < CT; ++c)
@@ -976,6 +977,14 @@ cudaError_t launch_pairs(const MatmulArgs& p, const Rows& ra, const Rows& rw, cu
   return launch_pairs_t<kFp8, O, 256>(p, ra, rw, s, clear);
 }
 
+// The cycles of the products of few tokens: a short launch, and the weights at so
+// many bytes a cycle (e4m3 codes become fp16 at a lower rate).  One token, 10304 x
+// 4096: int8 8.7 us, by the next kernel 17; e4m3 11.6 and 10; 2048 x 4096: 5.6 and 7.7.
+double few_cost(bool fp8, int64_t m, int64_t n, int64_t k) {
+  const double rate = fp8 ? (m <= 8 ? 2000 : 1500) : m <= 8 ? 2900 : m <= 16 ? 2100 : 1600;
+  return 5000 + (double)n * (double)k / rate;
+}
+
 // The cycles of the products by pairs: waves of tiles by the stages of 128 bytes
 // (four products of about 175 cycles), what writing int8 codes out as fp16 takes at
 // 2600 bytes a cycle, and a tile's beginning and end.
@@ -1005,13 +1014,11 @@ int check(const ssd_matmul_problem* pr, MatmulPlan* pl) {
       (double)pr->m * (double)pr->k >= (double)(1LL << 40) || (double)pr->n * (double)pr->k >= (double)(1LL << 40))
     return SSD_ERR_UNSUPPORTED;
   const bool whole = pr->k % 16 == 0, int8 = pr->format == SSD_CACHE_INT8;
-  pl->few = pr->m <= kFewTokens[!int8];
   SomeArgs share;
   int split;
-  double cost;
-  pl->some = !pl->few &&
-             0 < (cost = share_out(!int8, pr->m, pr->n, pr->k, &share, &split)) &&
-             cost <= pairs_cost(!int8, pr->m, pr->n, pr->k);
+  const double some = share_out(!int8, pr->m, pr->n, pr->k, &share, &split);  // (0: too many CTAs)
+  pl->few = pr->m <= kFewTokens[!int8] && (some == 0 || few_cost(!int8, pr->m, pr->n, pr->k) <= some);
+  pl->some = !pl->few && some > 0 && some <= pairs_cost(!int8, pr->m, pr->n, pr->k);
   pl->half_a = pl->half_w = int8 && !pl->few && !pl->some;
   pl->out_a = pl->half_a || !whole;
   pl->out_w = pl->half_w || !whole;
