@@ -44,31 +44,48 @@ struct AddNormArgs {
   float inv_dim, eps;
 };
 
-// Eight values of a row: neighbours where rows are whole 16-byte vectors, else
-// columns a CTA's width apart.  They are fetched as they lie and turned into
-// fp32 when they are wanted, so that a row ahead costs few registers.
-template <typename T, bool kVec>
+// Which eight values of a row a thread takes at a time.
+enum How {
+  kApart,   // columns a CTA's width apart, one by one
+  kWhole,   // neighbours: rows are whole 16-byte vectors
+  kAligned  // neighbours in memory's vectors, in which a row of dense tensors begins `shift` values late; a row's first and
+            // last vectors are shared with other rows: they are read whole but at the tensor's end, what is another row's
+            // is masked, and their own values are written one by one
+};
+
+// Eight values of a row.  They are fetched as they lie and turned into fp32 when
+// they are wanted, so that a row ahead costs few registers.
+template <typename T, How kHow>
 struct Cols {
   struct Raw {
     uint4 u[sizeof(T) / 2];
   };
-  static __device__ __forceinline__ int col(int i, int j) {
-    return kVec ? (i * (int)blockDim.x + (int)threadIdx.x) * 8 + j : (i * 8 + j) * (int)blockDim.x + (int)threadIdx.x;
+  static __device__ __forceinline__ int col(int i, int j, int shift) {
+    return kHow == kApart ? (i * 8 + j) * (int)blockDim.x + (int)threadIdx.x
+                          : (i * (int)blockDim.x + (int)threadIdx.x) * 8 + j - (kHow == kAligned ? shift : 0);
   }
-  static __device__ __forceinline__ void fetch(const T* row, int i, int dim, Raw& r) {
-    if constexpr (kVec) {
-      const int c = col(i, 0);
+  // whether the eight are a vector of this row
+  static __device__ __forceinline__ bool whole(int c, int dim) {
+    return kHow == kWhole ? c < dim : kHow == kAligned && c >= 0 && c + 8 <= dim;
+  }
+  static __device__ __forceinline__ bool inside(int c, int dim) { return (kHow != kAligned || c >= 0) && c < dim; }
+  // reach: how many values of the tensor there are from the row's first on, or 8 past the row if there are more.  (Before
+  // it there are `shift`, for the tensor begins with a whole vector.)
+  static __device__ __forceinline__ void fetch(const T* row, int i, int dim, int shift, int reach, Raw& r) {
+    const int c = col(i, 0, shift);
 #pragma unroll
-      for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-        r.u[j] = c < dim ? __ldcs(reinterpret_cast<const uint4*>(row + c) + j) : make_uint4(0, 0, 0, 0);
-    } else {
+    for (int j = 0; j < (int)sizeof(T) / 2; ++j) r.u[j] = make_uint4(0, 0, 0, 0);
+    if (kHow == kAligned ? c < dim && c + 8 <= reach : whole(c, dim)) {
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(T) / 2; ++j) r.u[j] = __ldcs(reinterpret_cast<const uint4*>(row + c) + j);
+    } else if (kHow == kApart || (kHow == kAligned && c < dim)) {
       uint32_t w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         w[j] = 0;
-        if (col(i, j) < dim) {
-          if constexpr (sizeof(T) == 2) w[j] = __ldcs(reinterpret_cast<const unsigned short*>(row) + col(i, j));
-          else w[j] = __ldcs(reinterpret_cast<const uint32_t*>(row) + col(i, j));
+        if (inside(col(i, j, shift), dim)) {
+          if constexpr (sizeof(T) == 2) w[j] = __ldcs(reinterpret_cast<const unsigned short*>(row) + col(i, j, shift));
+          else w[j] = __ldcs(reinterpret_cast<const uint32_t*>(row) + col(i, j, shift));
         }
       }
       if constexpr (sizeof(T) == 2) {
@@ -95,48 +112,63 @@ struct Cols {
       v[6] = __uint_as_float(x.z); v[7] = __uint_as_float(x.w);
     }
   }
-  static __device__ __forceinline__ void store(T* row, int i, int dim, const float (&v)[8]) {
-    if constexpr (kVec) {
-      const int c = col(i, 0);
-      if (c < dim) {
-        if constexpr (sizeof(T) == 2) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&p);
-          }
-          __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
-          __stcs(reinterpret_cast<float4*>(row + c), make_float4(v[0], v[1], v[2], v[3]));
-          __stcs(reinterpret_cast<float4*>(row + c) + 1, make_float4(v[4], v[5], v[6], v[7]));
-        }
-      }
-    } else {
+  // Nothing of other rows' values
+  static __device__ __forceinline__ void mask(int i, int dim, int shift, float (&v)[8]) {
+    if constexpr (kHow == kAligned) {
+      if (whole(col(i, 0, shift), dim)) return;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (col(i, j) < dim) row[col(i, j)] = from_f<T>(v[j]);
+        if (!inside(col(i, j, shift), dim)) v[j] = 0.f;
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int i, int dim, int shift, const float (&v)[8]) {
+    const int c = col(i, 0, shift);
+    if (whole(c, dim)) {
+      if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[0], w[1], w[2], w[3]));
+      } else {
+        __stcs(reinterpret_cast<float4*>(row + c), make_float4(v[0], v[1], v[2], v[3]));
+        __stcs(reinterpret_cast<float4*>(row + c) + 1, make_float4(v[4], v[5], v[6], v[7]));
+      }
+    } else if (kHow != kWhole) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (inside(col(i, j, shift), dim)) row[col(i, j, shift)] = from_f<T>(v[j]);
     }
   }
 };
 
 // The weight's values stay in the caches: every row reads them.
-template <bool kVec>
-__device__ __forceinline__ void load_weight(const float* w, int i, int dim, float (&v)[8]) {
-  using C = Cols<float, kVec>;
-  if constexpr (kVec) {
-    const int c = C::col(i, 0);
-    if (c < dim) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
+template <How kHow>
+__device__ __forceinline__ void load_weight(const float* w, int i, int dim, int shift, float (&v)[8]) {
+  using C = Cols<float, kHow>;
+  const int c = C::col(i, 0, shift), c4 = c & ~3;
+  if (kHow == kWhole && c < dim) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else if (kHow == kAligned && c >= 0 && c4 + 12 <= dim) {
+    // three vectors hold them, from the same place on for the whole row
+    float x[12];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    for (int j = 0; j < 3; ++j) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(w + c4) + j);
+      x[4 * j] = q.x; x[4 * j + 1] = q.y; x[4 * j + 2] = q.z; x[4 * j + 3] = q.w;
     }
+    const int late = -shift & 3;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = late == 0 ? x[j] : late == 1 ? x[j + 1] : late == 2 ? x[j + 2] : x[j + 3];
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = C::col(i, j) < dim ? __ldg(w + C::col(i, j)) : 0.f;
+    for (int j = 0; j < 8; ++j)
+      v[j] = kHow != kWhole && C::inside(C::col(i, j, shift), dim) ? __ldg(w + C::col(i, j, shift)) : 0.f;
   }
 }
 
@@ -157,48 +189,51 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return v;
 }
 
-template <bool kFp8, bool kVec>
-__device__ __forceinline__ void store_codes(uint8_t* row, int i, int dim, const float (&v)[8], float inv, bool zero) {
-  using C = Cols<float, kVec>;
-  if constexpr (kVec) {
-    const int c = C::col(i, 0);
-    if (c < dim) {
-      uint2 u = make_uint2(0, 0);
-      if (!zero)
-        u = make_uint2(encode4<kFp8>(make_float4(v[0], v[1], v[2], v[3]), inv),
-                       encode4<kFp8>(make_float4(v[4], v[5], v[6], v[7]), inv));
-      *reinterpret_cast<uint2*>(row + c) = u;
-    }
-  } else {
+template <bool kFp8, How kHow>
+__device__ __forceinline__ void store_codes(uint8_t* row, int i, int dim, int shift, const float (&v)[8], float inv,
+                                            bool zero) {
+  using C = Cols<float, kHow>;
+  const int c = C::col(i, 0, shift);
+  if (C::whole(c, dim)) {
+    uint2 u = make_uint2(0, 0);
+    if (!zero)
+      u = make_uint2(encode4<kFp8>(make_float4(v[0], v[1], v[2], v[3]), inv),
+                     encode4<kFp8>(make_float4(v[4], v[5], v[6], v[7]), inv));
+    *reinterpret_cast<uint2*>(row + c) = u;
+  } else if (kHow != kWhole) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (C::col(i, j) < dim) row[C::col(i, j)] = zero ? 0 : encode<kFp8>(v[j] * inv);
+      if (C::inside(C::col(i, j, shift), dim)) row[C::col(i, j, shift)] = zero ? 0 : encode<kFp8>(v[j] * inv);
   }
 }
 
 // NP: pieces of 8 columns to a thread.  The next row of a CTA is on its way
 // while this one is summed, rounded and written.
-template <typename T, typename R, int NP, bool kVec>
+template <typename T, typename R, int NP, How kHow>
 __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a) {
-  using X = Cols<T, kVec>;
-  using H = Cols<R, kVec>;
+  using X = Cols<T, kHow>;
+  using H = Cols<R, kHow>;
   __shared__ float red[2][kMaxThreads / 32], big_s[2][kMaxThreads / 32];
   typename X::Raw x[NP];
   typename H::Raw y[NP];
+  auto shift_of = [&](long long row) { return kHow == kAligned ? (int)((row * a.dim) & 7) : 0; };
   auto fetch = [&](long long row) {
+    const int shift = shift_of(row);
+    const int reach = a.dim + (int)min((a.rows - 1 - row) * a.dim, 8LL);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      X::fetch(static_cast<const T*>(a.x) + row * a.xs, i, a.dim, x[i]);
-      if (a.res) H::fetch(static_cast<const R*>(a.res) + row * a.dim, i, a.dim, y[i]);
+      X::fetch(static_cast<const T*>(a.x) + row * a.xs, i, a.dim, shift, reach, x[i]);
+      if (a.res) H::fetch(static_cast<const R*>(a.res) + row * a.dim, i, a.dim, shift, reach, y[i]);
     }
   };
   fetch(blockIdx.x);
   float w0[8];  // the weight of a single piece stays in registers
-  if (NP == 1) load_weight<kVec>(a.w, 0, a.dim, w0);
+  if (NP == 1 && kHow != kAligned) load_weight<kHow>(a.w, 0, a.dim, 0, w0);
   int par = 0;
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
     float v[NP][8];
     float ss = 0.f;
+    const int shift = shift_of(row);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       X::values(x[i], v[i]);
@@ -208,11 +243,12 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = to_f(from_f<R>(v[i][j] + u[j]));
       }
+      X::mask(i, a.dim, shift, v[i]);
     }
     if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      if (a.h) H::store(static_cast<R*>(a.h) + row * a.dim, i, a.dim, v[i]);
+      if (a.h) H::store(static_cast<R*>(a.h) + row * a.dim, i, a.dim, shift, v[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
     }
@@ -221,17 +257,17 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       float w[8];
-      if (NP > 1) load_weight<kVec>(a.w, i, a.dim, w);
+      if (NP > 1 || kHow == kAligned) load_weight<kHow>(a.w, i, a.dim, shift, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[i][j] = v[i][j] * r * (NP == 1 ? w0[j] : w[j]);
+        v[i][j] = v[i][j] * r * (NP == 1 && kHow != kAligned ? w0[j] : w[j]);
         // what is not finite makes the row's largest an infinity
         big = fmaxf(big, fabsf(v[i][j]) <= 3.402823466e38f ? fabsf(v[i][j]) : __int_as_float(0x7f800000));
       }
     }
     if (a.codes == 0) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) X::store(static_cast<T*>(a.out) + row * a.dim, i, a.dim, v[i]);
+      for (int i = 0; i < NP; ++i) X::store(static_cast<T*>(a.out) + row * a.dim, i, a.dim, shift, v[i]);
       continue;
     }
     // (values that are not negative order as integers)
@@ -247,18 +283,18 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_fwd_kernel(AddNormArgs a
     uint8_t* to = static_cast<uint8_t*>(a.out) + row * a.dim;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      if (fp8) store_codes<true, kVec>(to, i, a.dim, v[i], inv, zero);
-      else store_codes<false, kVec>(to, i, a.dim, v[i], inv, zero);
+      if (fp8) store_codes<true, kHow>(to, i, a.dim, shift, v[i], inv, zero);
+      else store_codes<false, kHow>(to, i, a.dim, shift, v[i], inv, zero);
     }
     if (threadIdx.x == 0)
       a.scales[row] = bad ? __int_as_float(0x7fc00000) : zero ? 0.f : fp8 ? scale_of<true>(big) : scale_of<false>(big);
   }
 }
 
-template <typename T, typename R, int NP, bool kVec>
+template <typename T, typename R, int NP, How kHow>
 __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a) {
-  using X = Cols<T, kVec>;
-  using H = Cols<R, kVec>;
+  using X = Cols<T, kHow>;
+  using H = Cols<R, kHow>;
   __shared__ float red[2][2][kMaxThreads / 32];
   float dw[NP][8];
 #pragma unroll
@@ -270,8 +306,8 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
   auto fetch = [&](long long row) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      H::fetch(static_cast<const R*>(a.h) + row * a.dim, i, a.dim, h[i]);
-      X::fetch(static_cast<const T*>(a.dout) + row * a.dim, i, a.dim, dout[i]);
+      H::fetch(static_cast<const R*>(a.h) + row * a.dim, i, a.dim, 0, a.dim, h[i]);
+      X::fetch(static_cast<const T*>(a.dout) + row * a.dim, i, a.dim, 0, a.dim, dout[i]);
     }
   };
   constexpr bool kNext = NP <= 2;  // (four pieces leave no registers for another row)
@@ -283,7 +319,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
     if (!kNext) fetch(row);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      if (a.dh && kNext) H::fetch(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, dh[i]);
+      if (a.dh && kNext) H::fetch(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, 0, a.dim, dh[i]);
       H::values(h[i], v[i]);
       X::values(dout[i], d[i]);
     }
@@ -291,7 +327,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       float w[8];
-      load_weight<kVec>(a.w, i, a.dim, w);
+      load_weight<kHow>(a.w, i, a.dim, 0, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         ss = fmaf(v[i][j], v[i][j], ss);
@@ -317,11 +353,11 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       float w[8], u[8];
-      load_weight<kVec>(a.w, i, a.dim, w);
+      load_weight<kHow>(a.w, i, a.dim, 0, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] = 0.f;
       if (a.dh) {
-        if (!kNext) H::fetch(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, dh[i]);
+        if (!kNext) H::fetch(static_cast<const R*>(a.dh) + row * a.dim, i, a.dim, 0, a.dim, dh[i]);
         H::values(dh[i], u);
       }
 #pragma unroll
@@ -330,8 +366,8 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
         dw[i][j] = fmaf(d[i][j], n, dw[i][j]);
         u[j] += r * (d[i][j] * w[j] - n * proj);
       }
-      X::store(static_cast<T*>(a.dx) + row * a.dim, i, a.dim, u);
-      if (a.dres) H::store(static_cast<R*>(a.dres) + row * a.dim, i, a.dim, u);
+      X::store(static_cast<T*>(a.dx) + row * a.dim, i, a.dim, 0, u);
+      if (a.dres) H::store(static_cast<R*>(a.dres) + row * a.dim, i, a.dim, 0, u);
     }
   }
   // (the launch that joins the partial sums comes up while the last of them are written)
@@ -341,7 +377,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_norm_bwd_kernel(AddNormArgs a
   for (int i = 0; i < NP; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (X::col(i, j) < a.dim) part[X::col(i, j)] = dw[i][j];
+      if (X::col(i, j, 0) < a.dim) part[X::col(i, j, 0)] = dw[i][j];
 }
 
 // dweight[c] = sum of the slices' partials: 32 columns to a CTA, each warp a
@@ -377,8 +413,8 @@ __global__ void __launch_bounds__(kFoldWarps * 32) add_norm_fold_kernel(const fl
 struct Shape {
   int threads, np;
 };
-Shape shape_of(int dim, long long rows, int sms) {
-  const int pieces = (dim + 7) / 8;
+Shape shape_of(int dim, long long rows, int sms, How how) {
+  const int pieces = how == kAligned ? (dim + 7) / 8 + 1 : (dim + 7) / 8;
   int np = rows > 8 * sms && pieces >= 64 ? 2 : 1;
   while (pieces > np * kMaxThreads) np *= 2;
   const int t = ((pieces + np - 1) / np + 31) / 32 * 32;
@@ -396,34 +432,40 @@ long long grid_of(long long rows, int threads, int sms, bool bwd) {
   return bwd && grid > kMaxSlices ? kMaxSlices : grid;
 }
 
-template <typename T, typename R, int NP, bool kVec>
-cudaError_t launch_np(const AddNormArgs& a, int threads, unsigned grid, bool bwd, cudaStream_t s) {
+template <typename T, typename R, int NP>
+cudaError_t launch_np(const AddNormArgs& a, int threads, unsigned grid, How how, bool bwd, cudaStream_t s) {
   if (bwd) {
     set_kernel_name("add_norm_bwd");
-    add_norm_bwd_kernel<T, R, NP, kVec><<<grid, threads, 0, s>>>(a);
+    if (how == kWhole) add_norm_bwd_kernel<T, R, NP, kWhole><<<grid, threads, 0, s>>>(a);
+    else add_norm_bwd_kernel<T, R, NP, kApart><<<grid, threads, 0, s>>>(a);
   } else {
     set_kernel_name("add_norm_fwd");
-    add_norm_fwd_kernel<T, R, NP, kVec><<<grid, threads, 0, s>>>(a);
+    if (how == kWhole) add_norm_fwd_kernel<T, R, NP, kWhole><<<grid, threads, 0, s>>>(a);
+    else if (sizeof(T) == 2 && how == kAligned)
+      add_norm_fwd_kernel<T, R, NP, sizeof(T) == 2 ? kAligned : kApart><<<grid, threads, 0, s>>>(a);
+    else add_norm_fwd_kernel<T, R, NP, kApart><<<grid, threads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }
 template <typename T, typename R>
-cudaError_t launch_t(const AddNormArgs& a, const Shape& sh, bool vec, unsigned grid, bool bwd, cudaStream_t s) {
-  if (vec) {
-    if (sh.np == 1) return launch_np<T, R, 1, true>(a, sh.threads, grid, bwd, s);
-    if (sh.np == 2) return launch_np<T, R, 2, true>(a, sh.threads, grid, bwd, s);
-    return launch_np<T, R, 4, true>(a, sh.threads, grid, bwd, s);
-  }
-  if (sh.np == 1) return launch_np<T, R, 1, false>(a, sh.threads, grid, bwd, s);
-  if (sh.np == 2) return launch_np<T, R, 2, false>(a, sh.threads, grid, bwd, s);
-  return launch_np<T, R, 4, false>(a, sh.threads, grid, bwd, s);
+cudaError_t launch_t(const AddNormArgs& a, const Shape& sh, How how, unsigned grid, bool bwd, cudaStream_t s) {
+  if (sh.np == 1) return launch_np<T, R, 1>(a, sh.threads, grid, how, bwd, s);
+  if (sh.np == 2) return launch_np<T, R, 2>(a, sh.threads, grid, how, bwd, s);
+  return launch_np<T, R, 4>(a, sh.threads, grid, how, bwd, s);
 }
-cudaError_t launch(const ssd_add_norm_problem& pr, const AddNormArgs& a, const Shape& sh, unsigned grid, bool bwd,
-                   cudaStream_t s) {
-  const bool vec = a.dim % 8 == 0 && (bwd || a.xs % 8 == 0);
-  if (pr.dtype == SSD_F32) return launch_t<float, float>(a, sh, vec, grid, bwd, s);
-  if (pr.residual_dtype == SSD_F32) return launch_t<__nv_bfloat16, float>(a, sh, vec, grid, bwd, s);
-  return launch_t<__nv_bfloat16, __nv_bfloat16>(a, sh, vec, grid, bwd, s);
+cudaError_t launch(const ssd_add_norm_problem& pr, const AddNormArgs& a, const Shape& sh, How how, unsigned grid,
+                   bool bwd, cudaStream_t s) {
+  if (pr.dtype == SSD_F32) return launch_t<float, float>(a, sh, how, grid, bwd, s);
+  if (pr.residual_dtype == SSD_F32) return launch_t<__nv_bfloat16, float>(a, sh, how, grid, bwd, s);
+  return launch_t<__nv_bfloat16, __nv_bfloat16>(a, sh, how, grid, bwd, s);
+}
+// The forward of many dense odd rows of bf16 goes by memory's vectors, of which a
+// row may touch one more than it fills (16,384 x 4095 to e4m3: 125 us, column by
+// column 267; fp32 rows are no faster so, few rows slower).  The backward's threads
+// keep their columns' dweight, which a row's shift would move.
+How how_of(int dim, long long xs, long long rows, bool bf16, bool bwd, int sms) {
+  if (dim % 8 == 0 && xs % 8 == 0) return kWhole;
+  return !bwd && bf16 && xs == dim && rows > 8 * sms && dim / 8 + 2 <= kMaxThreads * 4 ? kAligned : kApart;
 }
 
 int check(const ssd_add_norm_problem* pr) {
@@ -473,11 +515,12 @@ int ssd_add_rmsnorm_fwd(const ssd_add_norm_problem* pr, const void* x, const voi
   a.inv_dim = 1.f / (float)pr->dim;
   a.eps = pr->eps;
   const int sms = device_sm_count();
-  const Shape sh = shape_of(a.dim, a.rows, sms);
+  const How how = how_of(a.dim, a.xs, a.rows, pr->dtype == SSD_BF16, false, sms);
+  const Shape sh = shape_of(a.dim, a.rows, sms, how);
   const long long grid = grid_of(a.rows, sh.threads, sms, false);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_before(s);
-  const cudaError_t e = launch(*pr, a, sh, (unsigned)grid, false, s);
+  const cudaError_t e = launch(*pr, a, sh, how, (unsigned)grid, false, s);
   prof_after(s);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -511,11 +554,12 @@ int ssd_add_rmsnorm_bwd(const ssd_add_norm_problem* pr, const void* h, const flo
   a.inv_dim = 1.f / (float)pr->dim;
   a.eps = pr->eps;
   const int sms = device_sm_count();
-  const Shape sh = shape_of(a.dim, a.rows, sms);
+  const How how = how_of(a.dim, a.dim, a.rows, false, true, sms);
+  const Shape sh = shape_of(a.dim, a.rows, sms, how);
   const long long grid = grid_of(a.rows, sh.threads, sms, true);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   prof_before(s);
-  cudaError_t e = launch(*pr, a, sh, (unsigned)grid, true, s);
+  cudaError_t e = launch(*pr, a, sh, how, (unsigned)grid, true, s);
   prof_after(s);
   if (e != cudaSuccess) return SSD_ERR_CUDA;
   prof_before(s);

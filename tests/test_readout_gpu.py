@@ -107,6 +107,40 @@ def test_norm_without_residual_and_strided():
         close(dev.out, want, (NORM + HALF[BF16]) * np.abs(want))
 
 
+# Many rows whose ends are not those of 16-byte vectors: each row but the first
+# begins inside a vector that holds other rows' values too.
+@pytest.mark.parametrize("form", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("rt", [BF16, F32])
+@pytest.mark.parametrize("rows,dim", [(2003, 1), (2001, 3), (1500, 7), (1501, 9), (1237, 100), (1300, 1237), (1250, 4095),
+                                      (1221, 16367), (1221, 16371)])
+def test_norm_many_odd_rows(rows, dim, rt, form):
+    from mamba_selective_state_gb300 import runner
+    x, r, w = norm_case(rows, dim, BF16, rt, rows * 5 + dim)
+    x[11, dim // 2], r[rows - 3, 0], x[rows - 1, dim - 1] = float("nan"), float("inf"), float("-inf")
+    room = rows * dim                                # the stream in place, with room behind it that stays as it was
+    buf = torch.full((room + 64,), 3.0, dtype=rt, device="cuda")
+    buf[:room] = r.flatten()
+    inplace = buf[:room].view(rows, dim)
+    dev = runner.AddNormDevice(x, w, residual=inplace, h_out=inplace, form=form)
+    want_h = stored(x.cpu(), r.cpu())
+    fine = torch.ones(rows, dtype=torch.bool)
+    fine[[11, rows - 3, rows - 1]] = False
+    dev.fwd()
+    torch.testing.assert_close(dev.h.cpu(), want_h, rtol=0, atol=0, equal_nan=True)
+    assert bool((buf[room:] == 3).all())
+    want, _ = ro.add_rmsnorm_fwd(f64(want_h[fine]), f64(w), 1e-5)
+    if form is None:
+        close(dev.out.cpu()[fine], want, (NORM + HALF[BF16]) * np.abs(want))
+        return
+    scales = np.abs(want).max(-1) / ro.TOP[form]
+    got = dev.scales.cpu()
+    close(got[fine], scales, (NORM + 2 * U) * scales)
+    assert bool(got[11].isnan()) and bool(got[rows - 1].isnan())
+    y = want / np.where(scales > 0, scales, 1)[:, None]
+    codes = ro.code_values(raw(dev.codes), form)[fine.numpy()]
+    close(codes, y, ro.half_steps(y, form) + (2 * NORM + 4 * U) * np.abs(y))
+
+
 def test_norm_updates_the_residual_in_place():
     from mamba_selective_state_gb300 import runner
     x, r, w = norm_case(500, 1024, BF16, F32, 5)
