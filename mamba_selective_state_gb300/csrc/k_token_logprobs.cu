@@ -11,8 +11,8 @@
 // keeps the largest logit that it has met and the two sums relative to it, in
 // units of log 2, and they are joined in a fixed order.  A CTA goes on to its
 // next row while the joins of the last one are under way: the first vectors of
-// that row are in flight by then.  4096 rows of 100,003 bf16 words: 139 us (5.9
-// TB/s), with 20 alternatives 167.  The gradient reads and writes once: 4096 rows
+// that row are in flight by then.  4096 rows of 100,003 bf16 words: 146 us (5.6
+// TB/s), with 20 alternatives 175.  The gradient reads and writes once: 4096 rows
 // of 32,000 words 81 us (6.5 TB/s).
 //
 // Alternatives.  The k-th largest of the maxima of 64 groups of threads is at
@@ -58,7 +58,8 @@ struct LogpArgs {
   const float *ent_in, *dlogp, *dent;
   void* dlogits;
   long long rows, V, stride, gstride;
-  float scale, c2;  // c2 = scale log2(e)
+  float scale, c2;  // c2 = scale log2(e), rounded:
+  float c2_less;    // by this part of itself it is too small, times ln 2
   int ntop;
 };
 
@@ -90,42 +91,63 @@ __device__ __forceinline__ float apart(float a, float b, float c2) {
 }
 
 // What has been met of a row: the largest logit m, and the sums of 2^d and of
-// 2^d d over its words, d = (x - m) c2.
+// 2^d d over its words, d = (x - m) c2.  Those are added up from sums of a batch
+// of words each, which keeps the chains of roundings short.
+//
+// A row that is nearly all one word has log probabilities and an entropy that are
+// as small as what the other words leave, which a sum with that word's 1 would
+// round away.  So the batch that holds the first m is kept out of s, in q; a row
+// whose sum comes out below 1.5 reads that batch once more and leaves s without
+// the word itself (q = kAlone).
+constexpr float kAlone = -1.f;
 struct Sums {
-  float m = kNegInf, s = 0.f, t = 0.f;
+  float m = kNegInf, s = 0.f, q = 0.f, t = 0.f;
+  // q as a sum: the word alone has 2^off
+  __device__ __forceinline__ float batch(float c2) const {
+    return q == kAlone ? fmaf(off_of(m, c2), kLn2, 1.f) : q;
+  }
   __device__ __forceinline__ void rebase(float m2, float c2) {
     if (m == kNegInf) return;  // (s may be a NaN: it stays)
-    const float d = floored(apart(m, m2, c2)), f = ex2(d);
-    t = f * (t + s * d);
-    s = f * s;
+    const float d = floored(apart(m, m2, c2)), f = ex2(d), all = s + batch(c2);
+    t = f * (t + all * d);
+    s = f * all;
+    q = 0.f;
     m = m2;
   }
-  __device__ __forceinline__ void join(float m2, float s2, float t2, float c2) {
+  __device__ __forceinline__ void join(float m2, float s2, float t2, float q2, float c2) {
     Sums o;
-    o.m = m2; o.s = s2; o.t = t2;
+    o.m = m2; o.s = s2; o.t = t2; o.q = q2;
     const float top = fmaxf(m, m2);
     if (top > m) rebase(top, c2);
     if (top > m2) o.rebase(top, c2);
     m = top;
     s += o.s;
     t += o.t;
+    if (q == 0.f) q = o.q;
+    else if (o.q != 0.f) s += o.batch(c2);
+  }
+  // A batch's sums; fresh: it holds the first m
+  __device__ __forceinline__ void take(bool fresh, float es, float et) {
+    if (fresh) q = es;
+    else s += es;
+    t += et;
   }
   // words of which none is above m; kNear: by_product(m c2)
   template <bool kNear, int K>
-  __device__ __forceinline__ void add(const float (&x)[K], float mc, float c2) {
+  __device__ __forceinline__ void add(const float (&x)[K], float mc, float c2, float& es, float& et) const {
 #pragma unroll
     for (int i = 0; i < K; ++i) {
       const float d = floored(kNear ? fmaf(x[i], c2, -mc) : (x[i] - m) * c2), e = ex2(d);
-      s += e;
-      t = fmaf(e, d, t);
+      es += e;
+      et = fmaf(e, d, et);
     }
   }
   // nothing but excluded words so far: is one a NaN?
   template <int K>
-  __device__ __forceinline__ void add_none(const float (&x)[K]) {
+  __device__ __forceinline__ void add_none(const float (&x)[K], float& es) const {
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      if (x[i] != x[i]) s = x[i];
+      if (x[i] != x[i]) es = x[i];
   }
 };
 
@@ -169,29 +191,33 @@ struct Row {
     }
   }
   template <int K>
-  static __device__ __forceinline__ float meet(Sums& sum, const uint4 (&u)[K], float c2) {
+  static __device__ __forceinline__ float meet(Sums& sum, const uint4 (&u)[K], float c2, unsigned here, unsigned& at) {
     const float b = largest(u);
-    if (b > sum.m) {
+    const bool fresh = b > sum.m;
+    if (fresh) {
       sum.rebase(b, c2);
       sum.m = b;
+      at = here;
     }
     const float mc = __fmul_rn(sum.m, c2);
+    float es[2] = {0.f, 0.f}, et[2] = {0.f, 0.f};
     if (by_product(mc)) {
 #pragma unroll
       for (int i = 0; i < K; ++i) {
         float x[n];
         unpack(u[i], x);
-        sum.template add<true>(x, mc, c2);
+        sum.template add<true>(x, mc, c2, es[i & 1], et[i & 1]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < K; ++i) {
         float x[n];
         unpack(u[i], x);
-        if (sum.m == kNegInf) sum.add_none(x);
-        else sum.template add<false>(x, mc, c2);
+        if (sum.m == kNegInf) sum.add_none(x, es[0]);
+        else sum.template add<false>(x, mc, c2, es[0], et[0]);
       }
     }
+    sum.take(fresh, es[0] + es[1], et[0] + et[1]);
     return b;
   }
   static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
@@ -222,9 +248,11 @@ template <int kThreads>
 struct Shared {
   static constexpr int kRuns = kThreads > 256 ? 8 : 16;  // runs of a thread's vectors
   alignas(16) float group[kGroups];  // (read four at a time)
-  float warp[kThreads / 32][3];     // m, s, t of the warps
-  float all[3];                     // of the CTA
-  float cta[kMaxCluster][3];        // of the cluster's CTAs
+  float warp[kThreads / 32][4];     // m, s, t, q of the warps
+  float all[4];                     // of the CTA
+  float alone;                      // s without the largest word, where it is wanted
+  int first;                        // the warp whose q is the CTA's
+  float cta[kMaxCluster][4];        // of the cluster's CTAs
   unsigned long long best[kThreads / 32];
   alignas(16) unsigned long long list[kList];
   alignas(16) unsigned long long list2[kList];
@@ -237,19 +265,24 @@ struct Shared {
   int owners, count;
 };
 
-// Sums of a warp's first `lanes` lanes (a power of two), in every one of them
+// Sums of a warp's first `lanes` lanes (a power of two), in every one of them.
+// Returns the lane whose q is theirs, -1 if there is none.
 template <int lanes>
-__device__ __forceinline__ void join_lanes(Sums& sum, float c2) {
+__device__ __forceinline__ int join_lanes(Sums& sum, float c2) {
   const unsigned b = __float_as_uint(sum.m);
   const unsigned key = __reduce_max_sync(0xffffffffu, b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u));
   const float m = __uint_as_float(key ^ ((int)key < 0 ? 0x80000000u : 0xffffffffu));
   if (m > sum.m) sum.rebase(m, c2);
   sum.m = m;
+  const int first = __ffs(__ballot_sync(0xffffffffu, sum.q != 0.f)) - 1;
+  if ((int)(threadIdx.x & 31) != first) sum.s += sum.q;
+  sum.q = first < 0 ? 0.f : __shfl_sync(0xffffffffu, sum.q, first);
 #pragma unroll
   for (int o = lanes / 2; o; o >>= 1) {
     sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
     sum.t += __shfl_xor_sync(0xffffffffu, sum.t, o);
   }
+  return first;
 }
 
 // CTAs to an SM: 80 registers to a thread (with 64 what is kept across a row is
@@ -296,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
     const Row<T> now = r;
     const unsigned from = lo, to = hi;
     Sums sum;
+    constexpr unsigned kEdge = ~0u;
+    unsigned at = 0;     // the first vector of the batch in q, or kEdge
     unsigned shift = 0;  // tiles to a run: 1 << shift
     while ((to - from) > ((unsigned)(kRuns * kTile) << shift)) ++shift;
     float run = kNegInf;
@@ -306,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) w[i] = u[i];
       if (v0 + kTile < to) fetch(now, v0 + kTile);
-      const float b = Row<T>::meet(sum, w, a.c2);
+      const float b = Row<T>::meet(sum, w, a.c2, v0, at);
       if (a.ntop) {
         run = (tile & ((1u << shift) - 1)) == 0 ? b : fmaxf(run, b);
         sh.run[tile >> shift][tid] = run;
@@ -317,22 +352,29 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
       r = take(row + step);
       fetch(r, lo);
     }
-    if (first && tid < 2) {  // the words before and behind the whole vectors
-      const unsigned cnt = tid == 0 ? now.head : now.tail, at = tid == 0 ? 0 : now.V - now.tail;
-      float x[n], b = kNegInf;
+    // the words before (0) and behind (1) the whole vectors
+    auto edge = [&](int which, float (&x)[n]) {
+      const unsigned cnt = which == 0 ? now.head : now.tail, off = which == 0 ? 0 : now.V - now.tail;
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        x[i] = (unsigned)i < cnt ? to_f(now.base[at + i]) : kNegInf;
-        b = fmaxf(b, x[i]);
-      }
-      if (b > sum.m) {
+      for (int i = 0; i < n; ++i) x[i] = (unsigned)i < cnt ? to_f(now.base[off + i]) : kNegInf;
+    };
+    if (first && tid < 2) {
+      float x[n], b = kNegInf;
+      edge(tid, x);
+#pragma unroll
+      for (int i = 0; i < n; ++i) b = fmaxf(b, x[i]);
+      const bool fresh = b > sum.m;
+      if (fresh) {
         sum.rebase(b, a.c2);
         sum.m = b;
+        at = kEdge;
       }
       const float mc = __fmul_rn(sum.m, a.c2);
-      if (sum.m == kNegInf) sum.add_none(x);
-      else if (by_product(mc)) sum.template add<true>(x, mc, a.c2);
-      else sum.template add<false>(x, mc, a.c2);
+      float es = 0.f, et = 0.f;
+      if (sum.m == kNegInf) sum.add_none(x, es);
+      else if (by_product(mc)) sum.template add<true>(x, mc, a.c2, es, et);
+      else sum.template add<false>(x, mc, a.c2, es, et);
+      sum.take(fresh, es, et);
     }
     const float top = sum.m;
     if (a.ntop) {
@@ -342,11 +384,12 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
       if (tid % (kThreads / kGroups) == 0) sh.group[tid / (kThreads / kGroups)] = g;
       if (tid == 0) sh.owners = sh.count = 0;
     }
-    join_lanes<32>(sum, a.c2);
+    const int holder = join_lanes<32>(sum, a.c2);
     if (lane == 0) {
       sh.warp[warp][0] = sum.m;
       sh.warp[warp][1] = sum.s;
       sh.warp[warp][2] = sum.t;
+      sh.warp[warp][3] = sum.q;
     }
     __syncthreads();
     if (warp == 0) {
@@ -355,12 +398,15 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
         c.m = sh.warp[lane][0];
         c.s = sh.warp[lane][1];
         c.t = sh.warp[lane][2];
+        c.q = sh.warp[lane][3];
       }
-      join_lanes<kWarps>(c, a.c2);
+      const int w = join_lanes<kWarps>(c, a.c2);
       if (lane == 0) {
         sh.all[0] = c.m;
         sh.all[1] = c.s;
         sh.all[2] = c.t;
+        sh.all[3] = c.q;
+        sh.first = w;
       }
     } else if (warp == 1 && a.ntop) {
       // the ntop-th largest of the groups' maxima
@@ -380,6 +426,36 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
       if (ry == a.ntop - 1) sh.bound = y;
     }
     __syncthreads();
+    const bool alone = sh.all[1] + sh.all[3] < 1.5f && sh.all[3] > 0.f;
+    if (alone && warp == sh.first) {
+      // that batch again, a vector to a lane, without the first of its words that is m
+      const float m = sh.all[0], mc = __fmul_rn(m, a.c2);
+      const unsigned v0 = __shfl_sync(0xffffffffu, at, holder);
+      float x[n];
+#pragma unroll
+      for (int i = 0; i < n; ++i) x[i] = kNegInf;
+      if (v0 == kEdge) {
+        if (lane == 0) edge(holder, x);
+      } else if (lane < kAhead) {
+        const unsigned v = v0 + lane * kThreads + warp * 32 + holder;
+        if (v < to) Row<T>::unpack(__ldg(now.vec() + v), x);
+      }
+      bool is = false;
+#pragma unroll
+      for (int i = 0; i < n; ++i) is |= x[i] == m;
+      bool skip = lane == __ffs(__ballot_sync(0xffffffffu, is)) - 1;
+      float es = 0.f;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float d = by_product(mc) ? fmaf(x[i], a.c2, -mc) : (x[i] - m) * a.c2;
+        if (skip && x[i] == m) skip = false;
+        else es += ex2(floored(d));
+      }
+#pragma unroll
+      for (int o = kAhead / 2; o; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
+      if (lane == 0) sh.alone = sh.all[1] + es;
+    }
+    if (alone && !a.ntop) __syncthreads();  // (with alternatives there are others before it is read)
     if (a.ntop) {
       const float bound = sh.bound;
       auto in = [&](float x) { return x >= bound && x > kNegInf; };
@@ -495,24 +571,33 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
     }
     Sums c;
     c.m = sh.all[0];
-    c.s = sh.all[1];
+    c.s = alone ? sh.alone : sh.all[1];
     c.t = sh.all[2];
+    c.q = alone ? kAlone : sh.all[3];
     if (ncta > 1) {
       cluster.barrier_wait();
-      if (tid < 3) *cluster.map_shared_rank(&sh.cta[rank][tid], 0) = sh.all[tid];
+      if (tid < 4) *cluster.map_shared_rank(&sh.cta[rank][tid], 0) = tid == 0 ? c.m : tid == 1 ? c.s : tid == 2 ? c.t : c.q;
       if (!first && tid < a.ntop) *cluster.map_shared_rank(&sh.top[rank * a.ntop + tid], 0) = sh.top[tid];
       cluster.sync();
       if (!first) return;
-      c.m = kNegInf;
-      c.s = c.t = 0.f;
-      for (unsigned w = 0; w < ncta; ++w) c.join(sh.cta[w][0], sh.cta[w][1], sh.cta[w][2], a.c2);
+      c = Sums();
+      for (unsigned w = 0; w < ncta; ++w) c.join(sh.cta[w][0], sh.cta[w][1], sh.cta[w][2], sh.cta[w][3], a.c2);
     }
     const bool nothing = c.m == kNegInf && c.s == 0.f;  // every word is excluded
-    const float ln_s = logf(c.s) - off_of(c.m, a.c2) * kLn2;  // ln sum e^(z - m)
+    const float off = off_of(c.m, a.c2);
+    // ln of such a sum, under m itself
+    auto ln_of = [&](float s) {
+      return c.q == kAlone ? log1pf(fmaf(s, -off * kLn2, s)) : logf(s + c.q) - off * kLn2;
+    };
+    // ln sum e^(z - scale m): c2's rounding, to first order
+    const float ln_s = ln_of(fmaf(c.t, a.c2_less, c.s));
     if (tid == 0) {
       if (a.stats) a.stats[row] = make_float2(c.m, nothing ? kNegInf : ln_s);
       if (a.lse) a.lse[row] = nothing ? kNegInf : fmaf(c.m, a.scale, ln_s);
-      if (a.entropy) a.entropy[row] = nothing ? 0.f : logf(c.s) - kLn2 * (c.t / c.s);
+      if (a.entropy) {
+        const float all = c.s + c.batch(a.c2);
+        a.entropy[row] = nothing ? 0.f : ln_of(c.s) - kLn2 * (fmaf(-off, all, c.t) / all);
+      }
       if (a.logprobs) a.logprobs[row] = !known ? 0.f : nothing ? kNegInf : (tok_x - c.m) * a.scale - ln_s;
     }
     const int have = (int)ncta * a.ntop;
@@ -662,6 +747,8 @@ int check(const ssd_logprob_problem* pr, LogpArgs* a) {
   a->gstride = gs;
   a->scale = pr->scale;
   a->c2 = pr->scale * kLog2e;
+  const double less = (double)pr->scale * 1.4426950408889634 / (double)a->c2 - 1.0;
+  a->c2_less = less > -1e-6 && less < 1e-6 ? (float)(less * 0.6931471805599453) : 0.f;
   a->ntop = pr->ntop;
   return SSD_OK;
 }

@@ -463,6 +463,45 @@ def test_logprobs_of_large_logits(dt):
         assert (np.abs(got[i] - d) <= tol).all(), i
 
 
+# Rows that are nearly all one word: their log probabilities and entropies keep
+# their digits, however small.  In roundings relative to each: a word's exponent d,
+# below 64 here, and the exponent of each rebasing (64 at most in all) put 0.7 d on
+# its exponential, 45 each, as does the factor log2(e) scale for the entropy; an
+# exponential is within 4 and there are fewer than 10 rebasings; the chains of sums
+# are 16 + 13 + 5 + 4 + 8 long: under 256.  Rows whose sum is 1.5 or more have
+# logarithms from 0.4 on and lose a factor of 2.5 to it: 640.
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("rows,V,ntop", [(3, 1, 0), (50, 2, 1), (200, 7, 0), (400, 300, 5), (300, 5003, 0), (1000, 5003, 3),
+                                         (300, 40001, 0), (4, 40001, 2), (1, 100003, 0)])
+def test_logprobs_of_likely_words(rows, V, ntop, dt):
+    from mamba_selective_state_gb300 import runner
+    for turn in range(4 if rows < 10 else 1):
+        g = gen(rows + V + turn)
+        logits = 2 * rn(g, rows, V)
+        # the word anywhere in the row: in its first and last vectors, in the middle
+        tok = torch.randint(0, V, (rows,), generator=g, device="cuda", dtype=torch.int32)
+        tok[::5] = torch.randint(0, min(V, 4), (len(tok[::5]),), generator=g, device="cuda", dtype=torch.int32)
+        tok[1::5] = V - 1
+        lift = 8 + 17 * torch.rand(rows, generator=g, device="cuda")
+        logits[torch.arange(rows, device="cuda"), tok.long()] = lift
+        if V > 7:
+            logits[2::7, 3] = logits[2::7].max(-1).values       # one more as likely, or the same word
+            logits[4::7, :2] = -math.inf
+            logits[4::7, 2] = 24.0
+            tok[4::7] = 2
+        logits = logits.to(dt)
+        dev = runner.LogProbsDevice(logits, tok, scale=1.25, ntop=ntop)
+        dev.fwd()
+        want = ro.token_logprobs(f64(logits), tok.cpu().numpy(), 1.25, ntop)
+        near = lambda x: 640 * U * np.abs(x) + 1e-14    # (64 bits lose what they add to 1)  # noqa: E731
+        close(dev.logprobs, want["logprobs"], near(want["logprobs"]), "logprobs")
+        # the likely word's own exponent is the rounding of its product with log2(e) scale (below 64: 64 U at most), and it is
+        # taken back times a sum within 8 U
+        close(dev.entropy, want["entropy"], near(want["entropy"]) + 512 * U * U, "entropy")
+        if ntop:
+            close(dev.top_logprobs[:, 0], want["top_logprobs"][:, 0], near(want["top_logprobs"][:, 0]), "top")
+
+
 def test_logprobs_without_tokens():
     """Only what is asked for is written."""
     from mamba_selective_state_gb300 import _lib
