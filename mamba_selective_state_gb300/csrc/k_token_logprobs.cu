@@ -672,13 +672,18 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(LogpArg
   const bool nothing = ln_s == kNegInf;
   // p (-dl - dH (log p + H)) with log p = scale (x - m) - ln_s: the difference keeps
   // its digits where the logits are large
-  auto grad = [&](float x, unsigned v) {
+  auto grad = [&](float x) {
     const float lp = floored(fmaf(x - m, a.scale, -ln_s)), p = ex2(lp * kLog2e);
-    float g = -p * fmaf(dH, lp + H, dl);
-    if (v == tok) g += dl;
+    const float g = -p * fmaf(dH, lp + H, dl);
     return nothing ? 0.f : g * a.scale;
   };
-  auto one = [&](unsigned v) { out[v] = from_f<T>(grad(to_f(r.base[v]), v)); };
+  // the token's, with 1 - p whole however near p is to 1
+  auto chosen = [&](float x) {
+    const float lp = floored(fmaf(x - m, a.scale, -ln_s)), p = ex2(lp * kLog2e);
+    const float g = -p * dH * (lp + H) - dl * expm1f(lp);
+    return nothing ? 0.f : g * a.scale;
+  };
+  auto one = [&](unsigned v) { out[v] = from_f<T>(v == tok ? chosen(to_f(r.base[v])) : grad(to_f(r.base[v]))); };
   if (blockIdx.y == 0) {
     if (threadIdx.x < r.head) one(threadIdx.x);
     if (threadIdx.x < r.tail) one(r.V - r.tail + threadIdx.x);
@@ -698,7 +703,18 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(LogpArg
         Row<T>::unpack(u[i], x);
         const unsigned w = r.head + v * n;
 #pragma unroll
-        for (int j = 0; j < n; ++j) x[j] = grad(x[j], w + j);
+        for (int j = 0; j < n; ++j) x[j] = grad(x[j]);
+        if (tok - w < n) {
+          float y[n], c = 0.f;
+          Row<T>::unpack(u[i], y);
+#pragma unroll
+          for (int j = 0; j < n; ++j)
+            if (w + j == tok) c = y[j];
+          c = chosen(c);
+#pragma unroll
+          for (int j = 0; j < n; ++j)
+            if (w + j == tok) x[j] = c;
+        }
         if (!kSame) {
 #pragma unroll
           for (int j = 0; j < n; ++j) out[w + j] = from_f<T>(x[j]);

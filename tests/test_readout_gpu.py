@@ -490,9 +490,12 @@ def test_logprobs_of_likely_words(rows, V, ntop, dt):
             logits[4::7, 2] = 24.0
             tok[4::7] = 2
         logits = logits.to(dt)
-        dev = runner.LogProbsDevice(logits, tok, scale=1.25, ntop=ntop)
+        dl, dH = rn(g, rows), rn(g, rows)
+        dev = runner.LogProbsDevice(logits, tok, scale=1.25, ntop=ntop, dlogprobs=dl, dentropy=dH)
         dev.fwd()
-        want = ro.token_logprobs(f64(logits), tok.cpu().numpy(), 1.25, ntop)
+        dev.bwd()
+        t = tok.cpu().numpy()
+        want = ro.token_logprobs(f64(logits), t, 1.25, ntop)
         near = lambda x: 640 * U * np.abs(x) + 1e-14    # (64 bits lose what they add to 1)  # noqa: E731
         close(dev.logprobs, want["logprobs"], near(want["logprobs"]), "logprobs")
         # the likely word's own exponent is the rounding of its product with log2(e) scale (below 64: 64 U at most), and it is
@@ -500,6 +503,16 @@ def test_logprobs_of_likely_words(rows, V, ntop, dt):
         close(dev.entropy, want["entropy"], near(want["entropy"]) + 512 * U * U, "entropy")
         if ntop:
             close(dev.top_logprobs[:, 0], want["top_logprobs"][:, 0], near(want["top_logprobs"][:, 0]), "top")
+        # the gradient: a word's p with its exponent's roundings (64 of them and the exponential's), the token's 1 - p with
+        # those of its log probability
+        lp = 1.25 * f64(logits) - want["lse"][:, None]
+        with np.errstate(invalid="ignore"):
+            p, off = np.exp(lp), np.where(lp > -np.inf, np.abs(lp), 0) + want["entropy"][:, None]
+        size = p * (np.abs(f64(dl))[:, None] + np.abs(f64(dH))[:, None] * off)
+        at = np.arange(rows), t
+        size[at] = np.abs(f64(dl) * np.expm1(want["logprobs"])) + np.abs(f64(dH)) * p[at] * off[at]
+        d = ro.token_logprobs_bwd(f64(logits), t, 1.25, f64(dl), f64(dH))
+        close(dev.dlogits, d, 1.25 * (1300 * U * size + 1e-11) + HALF[dt] * np.abs(d), "dlogits")
 
 
 def test_logprobs_without_tokens():
