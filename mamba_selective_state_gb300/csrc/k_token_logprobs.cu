@@ -300,7 +300,7 @@ struct Shared {
   float run[kRuns][kThreads];       // the largest of each thread's runs
   unsigned short owner[kRuns * kThreads];  // runs that have an alternative
   float bound;
-  int owners, count;
+  int owners, count, kept;         // lengths: of owner, of list, of list2
 };
 
 // Sums of a warp's first `lanes` lanes (a power of two), in every one of them.
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
 #pragma unroll
       for (int o = 1; o < kThreads / kGroups; o *= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
       if (tid % (kThreads / kGroups) == 0) sh.group[tid / (kThreads / kGroups)] = g;
-      if (tid == 0) sh.owners = sh.count = 0;
+      if (tid == 0) sh.owners = sh.count = sh.kept = 0;
     }
     const int holder = join_lanes<32>(sum, a.c2);
     if (lane == 0) {
@@ -549,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
             for (int i = g; i < count; i += kGroups) best = sh.list[i] > best ? sh.list[i] : best;
             sh.part[g] = best;
           }
-          if (tid == 0) sh.count = 0;
           __syncthreads();
           for (int g = tid; g < kGroups; g += kThreads) {
             const unsigned long long key = sh.part[g];
@@ -564,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
           __syncthreads();
           const unsigned long long near = sh.near;
           for (int i = tid; i < count; i += kThreads)
-            if (sh.list[i] >= near) sh.list2[atomicAdd(&sh.count, 1)] = sh.list[i];
+            if (sh.list[i] >= near) sh.list2[atomicAdd(&sh.kept, 1)] = sh.list[i];
           __syncthreads();
-          count = sh.count;
+          count = sh.kept;
           list = sh.list2;
         }
         if (tid == 0 && (count & 1)) const_cast<unsigned long long*>(list)[count] = 0;  // (they are compared in pairs)
