@@ -10,7 +10,7 @@ F32, BF16 = torch.float32, torch.bfloat16
 
 def tops(logits, ntop):
     """The largest first, equal ones by their index."""
-    return (logits.float() + 0.0).sort(1, descending=True, stable=True).indices[:, :ntop].int()
+    return (logits.float() + 0.0).sort(dim=1, descending=True, stable=True).indices[:, :ntop].int()
 
 
 # few words to a row: fewer than ntop of the groups of threads have any, so that all are listed (one CTA to a row, of 64
