@@ -579,10 +579,10 @@ int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float
  *                        - dentropy * p_v * (log p_v + entropy))
  * dlogits may be logits itself (then with the same stride).
  *
- * Device memory, 16-byte aligned (strides are free).  scale > 0; ntop <= 32;
- * 1 <= vocab < 2^31.  All sums are fp32.  Ownership, errors and stream
- * semantics as above; no workspace.  Results are bitwise reproducible run to
- * run. */
+ * Device memory, 16-byte aligned (strides are free).  scale > 0, and
+ * scale * log2(e) finite (scale <= 2.358e38); ntop <= 32; 1 <= vocab < 2^31.
+ * All sums are fp32.  Ownership, errors and stream semantics as above; no
+ * workspace.  Results are bitwise reproducible run to run. */
 typedef struct {
   int64_t rows, vocab;
   int64_t logit_stride, grad_stride; /* elements from row to row; 0 = dense */

@@ -793,6 +793,7 @@ int check(const ssd_logprob_problem* pr, LogpArgs* a) {
   if (pr->ntop > kMaxTop || pr->vocab >= (1LL << 31) || pr->rows >= (1LL << 28) ||
       (double)pr->rows * (double)wide >= (double)(1LL << 40))
     return SSD_ERR_UNSUPPORTED;
+  if (!(pr->scale * kLog2e <= 3.402823466e38f)) return SSD_ERR_UNSUPPORTED;
   *a = LogpArgs();
   a->rows = pr->rows;
   a->V = pr->vocab;
