@@ -567,8 +567,8 @@ int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float
  * word: its log probability is -inf, its gradient 0, and it is no alternative;
  * places for which no word is left hold -1 and -inf.  A row that excludes every
  * word has lse -inf, logprob -inf, entropy 0 and no gradient.  A NaN or +inf in
- * a row makes its lse, logprobs, entropy and gradient NaN; the alternatives are
- * then those of the values that are not NaN.  Of logprobs (given with tokens),
+ * a row makes its lse, logprob (of a token), entropy and gradient NaN; the
+ * alternatives are then those of the values that are not NaN.  Of logprobs (given with tokens),
  * entropy, lse, stats and the alternatives each may be NULL, but not all.
  *
  * The backward takes stats and, for dentropy, entropy from the forward, and the
@@ -577,7 +577,9 @@ int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float
  * elements from row to row (0: dense):
  *   dlogits_v = scale * (dlogprob * (1[v = token] - p_v)
  *                        - dentropy * p_v * (log p_v + entropy))
- * dlogits may be logits itself (then with the same stride).
+ * A row into which no gradient comes -- padding, or no dlogprobs, with dentropy 0
+ * or NULL -- has dlogits 0, whatever its logits hold.  dlogits may be logits
+ * itself (then with the same stride).
  *
  * Device memory, 16-byte aligned (strides are free).  scale > 0, and
  * scale * log2(e) finite (scale <= 2.358e38); ntop <= 32; 1 <= vocab < 2^31.

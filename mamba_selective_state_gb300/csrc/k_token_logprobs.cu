@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(kBwdThreads) token_logprobs_bwd_kernel(LogpArg
   const int t = a.tokens ? a.tokens[row] : -1;
   const unsigned tok = t >= 0 && t < a.V ? (unsigned)t : 0xffffffffu;
   const float dl = tok != 0xffffffffu && a.dlogp ? a.dlogp[row] : 0.f, dH = a.dent ? a.dent[row] : 0.f;
-  const bool nothing = ln_s == kNegInf;
+  // every word is excluded, or nothing comes in (padding): zeros, whatever the row holds
+  const bool nothing = ln_s == kNegInf || (tok == 0xffffffffu && dH == 0.f);
   // p (-dl - dH (log p + H)) with log p = scale (x - m) - ln_s: the difference keeps
   // its digits where the logits are large
   auto grad = [&](float x) {

@@ -591,8 +591,9 @@ class LogProbsDevice:
     (outside the vocabulary: padding).  ``fwd`` fills logprobs, entropy, lse
     (rows) and, with ``ntop``, top_tokens and top_logprobs (rows, ntop).  With
     ``dlogprobs`` and/or ``dentropy`` (rows), ``bwd`` after a ``fwd`` fills
-    dlogits, laid out as logits; ``dlogits=logits`` overwrites them.  The tensors
-    may be refilled between calls.  All are on the current CUDA device; the
+    dlogits, laid out as logits; ``dlogits=logits`` overwrites them.  A row of
+    padding whose dentropy is 0 or not given gets zeros, whatever its logits hold.
+    The tensors may be refilled between calls.  All are on the current CUDA device; the
     buffers belong to the stream that is current here, and calls on another one
     come after its work."""
 

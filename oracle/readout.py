@@ -100,14 +100,14 @@ def token_logprobs_bwd(logits, tokens, scale, dlogprobs=None, dentropy=None):
     f = token_logprobs(x, tokens, scale)
     d = np.zeros_like(x)
     for i in range(rows):
-        if f["lse"][i] == -np.inf:
-            continue
+        t = int(tokens[i]) if tokens is not None and dlogprobs is not None else -1
+        dl = float(dlogprobs[i]) if 0 <= t < V else 0.0
+        dH = float(dentropy[i]) if dentropy is not None else 0.0
+        if f["lse"][i] == -np.inf or (not 0 <= t < V and dH == 0):
+            continue                # nothing is left, or nothing comes in
         if np.isnan(f["lse"][i]):
             d[i] = np.nan
             continue
-        t = int(tokens[i]) if tokens is not None else -1
-        dl = float(dlogprobs[i]) if dlogprobs is not None and 0 <= t < V else 0.0
-        dH = float(dentropy[i]) if dentropy is not None else 0.0
         lp = np.maximum(scale * x[i] - f["lse"][i], -1e4)
         p = np.exp(lp)
         d[i] = -p * (dl + dH * (lp + f["entropy"][i]))
