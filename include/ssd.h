@@ -562,14 +562,16 @@ int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float
  * logits (rows, vocab) dtype, logit_stride elements from row to row (0:
  * dense); tokens (rows) int32; logprobs, entropy, lse (rows) fp32; stats
  * (rows, 2) fp32, what the backward needs of the rows: the largest logit m, and
- * log sum exp(z - scale m); top_tokens int32 and top_logprobs fp32 (rows, ntop).  A token outside [0, vocab) is
- * padding: its logprob is 0 and has no gradient.  A logit of -inf excludes its
- * word: its log probability is -inf, its gradient 0, and it is no alternative;
- * places for which no word is left hold -1 and -inf.  A row that excludes every
- * word has lse -inf, logprob -inf, entropy 0 and no gradient.  A NaN or +inf in
- * a row makes its lse, logprob (of a token), entropy and gradient NaN; the
- * alternatives are then those of the values that are not NaN.  Of logprobs (given with tokens),
- * entropy, lse, stats and the alternatives each may be NULL, but not all.
+ * log sum exp(z - scale m); top_tokens int32 and top_logprobs fp32 (rows, ntop).
+ * A token outside [0, vocab) is padding: its logprob is 0 and has no gradient.
+ * A logit of -inf excludes its word: it is no alternative, its log probability
+ * is -inf, and its gradient 0 unless it is the given token (then the formula's
+ * below with p = 0, scale * dlogprob: such a row wants a dlogprob of 0); places
+ * for which no word is left hold -1 and -inf.  A row that excludes every word
+ * has lse -inf, logprob -inf, entropy 0 and no gradient.  A NaN or +inf in a row
+ * makes its lse, logprob (of a token), entropy and gradient NaN; the alternatives
+ * are then those of the values that are not NaN.  Of logprobs (given with
+ * tokens), entropy, lse, stats and the alternatives each may be NULL, but not all.
  *
  * The backward takes stats and, for dentropy, entropy from the forward, and the
  * upstream gradients dlogprobs (given with tokens) and dentropy (rows) fp32 --
