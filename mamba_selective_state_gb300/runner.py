@@ -509,8 +509,9 @@ class Linear8:
         self.codes, self.scales, self.bias, self.out_dtype = codes, scales, bias, out_dtype
         self.format = StateCache.FORMATS["int8" if codes.dtype is torch.int8 else "e4m3"]
         self._plans = {}
-        # the status word of calls that need no more (calls that overlap share it)
-        self._status = self.workspace = torch.zeros(256, dtype=torch.uint8, device=codes.device)
+        # the status words of calls that need no more: one to a stream, whose calls follow one another
+        self._words = {}
+        self.workspace = torch.zeros(256, dtype=torch.uint8, device=codes.device)
 
     @classmethod
     def from_weight(cls, weight, form="int8", bias=None, out_dtype=torch.bfloat16):
@@ -550,10 +551,13 @@ class Linear8:
                     out = torch.empty(out_shape, dtype=self.out_dtype, device=dev)
         else:
             _dense(out, out_shape, self.out_dtype, "out", dev)
-        work = self._status
-        if ws:
+        # (a call that is being captured has its own memory: graphs may be replayed side by side)
+        work = None if ws or torch.cuda.is_current_stream_capturing() else self._words.get(handle)
+        if work is None:
             with _allocating_on(stream):
-                work = torch.empty(ws, dtype=torch.uint8, device=dev)
+                work = torch.empty(ws or 256, dtype=torch.uint8, device=dev)
+            if not ws and not torch.cuda.is_current_stream_capturing():
+                self._words[handle] = work
         rc = _lib.LIB.ssd_scaled_matmul(ctypes.byref(prob), codes.data_ptr(), scales.data_ptr(),
                                         self.codes.data_ptr(), self.scales.data_ptr(),
                                         _lib._p(self.bias), out.data_ptr(), work.data_ptr(),
