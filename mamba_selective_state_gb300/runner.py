@@ -512,6 +512,7 @@ class Linear8:
         # the status words of calls that need no more: one to a stream, whose calls follow one another
         self._words = {}
         self.workspace = torch.zeros(256, dtype=torch.uint8, device=codes.device)
+        self._last = None       # the stream's handle of the last call
 
     @classmethod
     def from_weight(cls, weight, form="int8", bias=None, out_dtype=torch.bfloat16):
@@ -562,7 +563,7 @@ class Linear8:
                                         self.codes.data_ptr(), self.scales.data_ptr(),
                                         _lib._p(self.bias), out.data_ptr(), work.data_ptr(),
                                         ws or 256, handle)
-        self.workspace = work
+        self.workspace, self._last = work, handle
         _raise(rc, check, "ssd_scaled_matmul")
         return out
 
@@ -583,7 +584,10 @@ class Linear8:
         return plan
 
     def device_status(self, stream=None):
-        """Synchronises; the status word of the last call."""
+        """The status word of the last call, behind that call -- or behind
+        ``stream``'s work, where a graph that holds the call was replayed there."""
+        if stream is None and self._last not in (None, _here(self.codes.device, "Linear8", None)):
+            torch.cuda.synchronize(self.codes.device)
         return _lib.ssd_read_device_status(self.workspace, stream)
 
 

@@ -66,3 +66,23 @@ def test_graphs_have_their_own(m):
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
     assert _lib.ssd_read_device_status(eager) == _lib.SSD_ERR_TIMEOUT
+
+
+def test_the_last_call_is_waited_for_wherever_it_ran():
+    """The status is read behind the last call, also where that was given a stream
+    and none is named here: the word that is found holds what the call left."""
+    from mamba_selective_state_gb300 import _lib
+    lin, a, s = maps(9000)                      # (needs more memory than the word)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    lin(a, s, stream=side)
+    word = lin.workspace[:4].view(torch.int32)
+    for value, n in ((0, 1), (1, 20)):          # (once before, so that every kernel is loaded)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            wait = torch.randn(6000, 6000, device="cuda")
+            for _ in range(n):                  # some milliseconds of work ahead of the word's writer
+                wait = wait @ wait
+                wait = wait / wait.abs().max()
+            word.fill_(value)
+    assert lin.device_status() == _lib.SSD_ERR_TIMEOUT
