@@ -520,7 +520,9 @@ class Linear8:
         state cache's rule, once."""
         if form not in CODE_TYPES:
             raise ValueError(f"form must be one of {sorted(CODE_TYPES)}")
-        w = weight.detach().float()
+        if weight.dim() != 2 or weight.numel() == 0:
+            raise ValueError("weight must be (n, k)")
+        w = weight.detach().float().contiguous()
         top = 127.0 if form == "int8" else 448.0
         big = w.abs().amax(1, keepdim=True)
         bad = ~torch.isfinite(w).all(1, keepdim=True)
