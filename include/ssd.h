@@ -583,7 +583,7 @@ int ssd_scaled_matmul(const ssd_matmul_problem* prob, const void* a, const float
  * or NULL -- has dlogits 0, whatever its logits hold.  dlogits may be logits
  * itself (then with the same stride).
  *
- * Device memory, 16-byte aligned (strides are free).  scale > 0, and
+ * Device memory, 16-byte aligned (strides are free).  scale from 2^-120 on, with
  * scale * log2(e) finite (scale <= 2.358e38); ntop <= 32; 1 <= vocab < 2^31.
  * All sums are fp32.  Ownership, errors and stream semantics as above; no
  * workspace.  Results are bitwise reproducible run to run. */

@@ -45,6 +45,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kList = 512;       // words that may reach the bound
 constexpr int kLong = 96;        // a list that is shortened first
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLeastScale = 7.52316385e-37f;  // 2^-120: 2^128 of it is an exponent of 256
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct LogpArgs {
@@ -109,6 +110,12 @@ __device__ __forceinline__ float off_of(float m, float c2) {
 // The factor's exponent from sums under a to sums under b
 __device__ __forceinline__ float apart(float a, float b, float c2) {
   return fmaf(a - b, c2, off_of(b, c2) - off_of(a, c2));
+}
+
+// scale (x - m), also of values that are farther apart than fp32's largest
+__device__ __forceinline__ float below(float x, float m, float scale) {
+  const float d = x - m;
+  return fabsf(d) <= 3.402823466e38f ? d * scale : (0.5f * x - 0.5f * m) * scale * 2.f;
 }
 
 // What has been met of a row: the largest logit m, and the sums of 2^d and of
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
         const float all = c.s + c.batch(a.c2);
         a.entropy[row] = nothing ? 0.f : ln_of(c.s) - kLn2 * (fmaf(-off, all, c.t) / all);
       }
-      if (a.logprobs) a.logprobs[row] = !known ? 0.f : nothing ? kNegInf : (tok_x - c.m) * a.scale - ln_s;
+      if (a.logprobs) a.logprobs[row] = !known ? 0.f : nothing ? kNegInf : below(tok_x, c.m, a.scale) - ln_s;
     }
     const int have = (int)ncta * a.ntop;
     for (int i = tid; i < have; i += kThreads) {
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, resident(kThreads)) token_logprobs_k
       if (at < a.ntop) {
         const long long o = row * a.ntop + at;
         a.top_tok[o] = key ? (int)(0xffffffffu - (unsigned)key) : -1;
-        a.top_lp[o] = key ? (key_logit(key) - c.m) * a.scale - ln_s : kNegInf;
+        a.top_lp[o] = key ? below(key_logit(key), c.m, a.scale) - ln_s : kNegInf;
       }
     }
     __syncthreads();  // the next row writes over what this one has read
@@ -794,7 +801,8 @@ int check(const ssd_logprob_problem* pr, LogpArgs* a) {
   if (pr->ntop > kMaxTop || pr->vocab >= (1LL << 31) || pr->rows >= (1LL << 28) ||
       (double)pr->rows * (double)wide >= (double)(1LL << 40))
     return SSD_ERR_UNSUPPORTED;
-  if (!(pr->scale * kLog2e <= 3.402823466e38f)) return SSD_ERR_UNSUPPORTED;
+  // exponents' factors are finite; a difference of logits that is not has the exponential 0
+  if (!(pr->scale * kLog2e <= 3.402823466e38f) || pr->scale < kLeastScale) return SSD_ERR_UNSUPPORTED;
   *a = LogpArgs();
   a->rows = pr->rows;
   a->V = pr->vocab;
