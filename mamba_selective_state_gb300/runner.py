@@ -554,12 +554,13 @@ class Linear8:
                     out = torch.empty(out_shape, dtype=self.out_dtype, device=dev)
         else:
             _dense(out, out_shape, self.out_dtype, "out", dev)
-        # (a call that is being captured has its own memory: graphs may be replayed side by side)
-        work = None if ws or torch.cuda.is_current_stream_capturing() else self._words.get(handle)
+        # a call that is being captured (never on the default stream) has its own memory: graphs may be replayed side by side
+        own = ws or (handle and torch.cuda.is_current_stream_capturing())
+        work = None if own else self._words.get(handle)
         if work is None:
             with _allocating_on(stream):
                 work = torch.empty(ws or 256, dtype=torch.uint8, device=dev)
-            if not ws and not torch.cuda.is_current_stream_capturing():
+            if not own:
                 self._words[handle] = work
         rc = _lib.LIB.ssd_scaled_matmul(ctypes.byref(prob), codes.data_ptr(), scales.data_ptr(),
                                         self.codes.data_ptr(), self.scales.data_ptr(),
