@@ -12,12 +12,14 @@
 //    channels' codes in 16-byte pieces, turn them into fp16 in registers and
 //    multiply them with the tokens' by warp-level products; the order of k inside
 //    a product is free, so a lane's 16 neighbouring codes serve four products as
-//    they lie.  One token, 10304 x 4096 int8: 8.7 us (4.9 TB/s).
+//    they lie.  One token, 10304 x 4096 int8: 10 us (4.2 TB/s), 7.7 with the weights in L2.
 //  * some hundreds: tensor-memory products of 128 tokens x up to 256 channels, k
 //    shared by the CTAs of a cluster.  An instruction with 128 rows takes about 136
 //    cycles whether it has 32 columns or 256, so the weights are the columns.  int8
 //    codes stay int8 up to shared memory; warps turn them into fp16 there, and the
-//    chain of copy, turn and product bounds it.  61 tokens: int8 18 us, e4m3 11.7.
+//    chain of copy, turn and product bounds it.  61 tokens: int8 20 us, e4m3 14.7 (17 and 11
+//    with the weights in L2); from 129 tokens on the weights are read and turned again
+//    for every 128: int8 22 us at 128, 37 at 129, 69 at 512.
 //  * more: products of 256 tokens x up to 256 channels by pairs of CTAs,
 //    persistent, the epilogue of one tile under the products of the next, bound by
 //    the tensor cores.  16,384 tokens: int8 0.83 ms (1,650 TFLOP/s, 1,790 without
@@ -973,7 +975,8 @@ cudaError_t launch_pairs_t(const MatmulArgs& p, const Rows& ra, const Rows& rw, 
   cfg.numAttrs = clear ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, am, wm, t);
 }
-// Waves of tiles of the pairs' products with tiles of bn channels, and whether
+// Waves of tiles of the pairs' products with tiles of bn channels (by this chip's 76
+// pairs of SMs: they only choose the plan, without a device at hand), and whether
 // narrow tiles take no wave more: their products take as long as the wide ones',
 // but their ends are shorter.
 long long pair_waves(int64_t m, int64_t n, int bn) { return ((m + 255) / 256 * ((n + bn - 1) / bn) + 75) / 76; }
@@ -987,7 +990,8 @@ cudaError_t launch_pairs(const MatmulArgs& p, const Rows& ra, const Rows& rw, cu
 
 // The cycles of the products of few tokens: a short launch, and the weights at so
 // many bytes a cycle (e4m3 codes become fp16 at a lower rate).  One token, 10304 x
-// 4096: int8 8.7 us, by the next kernel 17; e4m3 11.6 and 10; 2048 x 4096: 5.6 and 7.7.
+// 4096, weights in L2: int8 8.7 us, by the next kernel 17; e4m3 11.6 and 10; 2048 x
+// 4096: 5.6 and 7.7.
 double few_cost(bool fp8, int64_t m, int64_t n, int64_t k) {
   const double rate = fp8 ? (m <= 8 ? 2000 : 1500) : m <= 8 ? 2900 : m <= 16 ? 2100 : 1600;
   return 5000 + (double)n * (double)k / rate;

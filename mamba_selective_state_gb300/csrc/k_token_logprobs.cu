@@ -769,6 +769,8 @@ cudaError_t launch_fwd(const LogpArgs& a, cudaStream_t s) {
   // Else narrow ones, whose joins leave the SM to others (4096 rows of 32,000 bf16 words: 51 us with 128 threads, 62 with
   // 256, 56 with 64), the narrowest for rows of up to 8 vectors to each of their threads (rows of 300 with 20
   // alternatives: 25 us with 64 threads, 40 with 128).
+  // Between 77 and some 900 rows they leave an SM little in flight: rows of 128,000 fp32 words take 12 us at 76 rows
+  // (two CTAs to a row), 45 at 77, 50 at 256 and 76 at 912, where HBM takes 69.
   if (a.V * (long long)sizeof(T) <= 64 * 8 * 16) return launch_fwd_t<T, 64>(a, 1, s);
   return launch_fwd_t<T, 128>(a, 1, s);
 }

@@ -599,7 +599,8 @@ class LogProbsDevice:
     outputs and the calls through the C ABI.
 
     logits (rows, vocab), fp32 or bf16, rows evenly spaced; tokens (rows) int32
-    (outside the vocabulary: padding).  ``fwd`` fills logprobs, entropy, lse
+    (outside the vocabulary: padding).  Tensors begin on 16-byte boundaries
+    (clone a slice such as ``tokens[1:]``).  ``fwd`` fills logprobs, entropy, lse
     (rows) and, with ``ntop``, top_tokens and top_logprobs (rows, ntop).  With
     ``dlogprobs`` and/or ``dentropy`` (rows), ``bwd`` after a ``fwd`` fills
     dlogits, laid out as logits; ``dlogits=logits`` overwrites them.  A row of
