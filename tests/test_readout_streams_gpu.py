@@ -93,3 +93,48 @@ def test_norm_writes_its_rows_and_no_more(rows, dim, rt, form):
         s = scales[2].cpu().numpy()
         assert np.isnan(s[bad]).all() and np.isnan(s).sum() == len(bad)
         assert not out[2].view(torch.uint8).view(rows, dim)[bad].any()
+
+
+def test_training_step_captured_and_replayed():
+    """Forward and backward of the norm and of the log probabilities in one graph:
+    replays with new inputs give the bits of eager calls."""
+    from mamba_selective_state_gb300 import runner
+    rows, dim, V = 400, 264, 1003
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x, r, w, E = rn(rows, dim).to(BF16), rn(rows, dim), 1 + 0.1 * rn(dim), rn(V, dim) * dim ** -0.5
+    tok = torch.randint(0, V, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    dout, logits = torch.empty(rows, dim, dtype=BF16, device="cuda"), torch.empty(rows, V, device="cuda")
+    norm = runner.AddNormDevice(x, w, residual=r, dout=dout, dh=rn(rows, dim))
+    lp = runner.LogProbsDevice(logits, tok, dlogprobs=rn(rows), dentropy=rn(rows), dlogits=logits)
+
+    def step():
+        norm.fwd()
+        torch.matmul(norm.out.float(), E.T, out=logits)
+        lp.fwd()
+        lp.bwd()
+        dout.copy_(logits @ E)
+        norm.bwd()
+
+    def results():
+        return [t.clone() for t in (norm.out, norm.dx, norm.dresidual, norm.dweight, lp.logprobs, lp.entropy, logits)]
+    first, second = (rn(rows, dim).to(BF16), rn(rows, dim)), (rn(rows, dim).to(BF16), rn(rows, dim))
+    want = []
+    for xs, rs in (first, second):
+        x.copy_(xs)
+        r.copy_(rs)
+        step()
+        want.append(results())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (0, 1, 0):
+        x.copy_((first, second)[i][0])
+        r.copy_((first, second)[i][1])
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want[i], results()))
